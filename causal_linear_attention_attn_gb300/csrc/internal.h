@@ -162,8 +162,8 @@ class LaunchTimer {
 };
 
 // Opt a kernel in to `bytes` of dynamic shared memory on the current device.
-// The attribute lives in each device's context, so it is set once per
-// (device, kernel, size) and the result is remembered for that device only.
+// The attribute lives in each device's context, so it is kept per (device,
+// kernel): the largest size asked for so far.
 cudaError_t ensure_smem_optin(const void *kernel, int bytes);
 
 // Per-device attributes, read once per device (dev < 0: the current device;

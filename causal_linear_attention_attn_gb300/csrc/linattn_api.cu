@@ -132,15 +132,32 @@ void LaunchTimer::done(cudaError_t launch_error) {
 }
 
 cudaError_t ensure_smem_optin(const void *kernel, int bytes) {
-  static PerDeviceCache<std::pair<const void *, int>, cudaError_t> cache;
+  // the opt-in is a maximum: a kernel launched at several sizes keeps the largest one asked for
+  struct Entry {
+    int dev;
+    const void *kernel;
+    int bytes;
+  };
+  static std::mutex mu;
+  static std::vector<Entry> set;
   int dev = 0;
-  const cudaError_t e = cudaGetDevice(&dev);
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  return cache.get(dev, std::make_pair(kernel, bytes), [&] {
-    const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (r != cudaSuccess) cudaGetLastError();
-    return r;
-  });
+  std::lock_guard<std::mutex> lk(mu);
+  Entry *at = nullptr;
+  for (Entry &x : set)
+    if (x.dev == dev && x.kernel == kernel) at = &x;
+  if (at && at->bytes >= bytes) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return e;
+  }
+  if (at)
+    at->bytes = bytes;
+  else
+    set.push_back({dev, kernel, bytes});
+  return cudaSuccess;
 }
 
 DeviceInfo device_info(int dev) {
