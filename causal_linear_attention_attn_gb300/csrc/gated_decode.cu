@@ -1,0 +1,122 @@
+// One recurrent step of gated linear attention per (batch row, head):
+//   S = e^g S + k v^T,   out = q^T S
+// on the row's state in a pool of states (slots[b]; the pool holds the sequences being served, the
+// batch is any subset of them in any order).
+//
+// A pure read-modify-write of the states: 2 x 4 dk dv bytes per head against 5 dk dv flops, so HBM
+// bounds it.  Every thread loads all of its rows of the state (one float4 column quad over a strided
+// set of rows) before it stores any; the state is touched once, with streaming hints.  q, k, v and
+// the decay meet the state in registers, the column sums of the read meet in shared memory.
+// A slot out of range, or one that an earlier row of the batch already has, leaves its state alone:
+// two rows on one state would race.  The check reads the batch's slots while the state loads.
+#include "gated.cuh"
+#include "internal.h"
+
+namespace la {
+
+__device__ unsigned int g_gated_step_status;
+
+namespace {
+
+constexpr int kThreads = 256;
+
+template <typename Tin, int DK, int DV>
+__global__ void __launch_bounds__(kThreads) gated_decode_kernel(const __grid_constant__ GatedStepProblem p) {
+  constexpr int kQuads = DV / 4;
+  constexpr int kGroups = kThreads / kQuads;
+  constexpr int kRows = DK / kGroups;
+  static_assert(kRows >= 1 && kRows * kGroups == DK, "rows must split evenly over the row groups");
+  __shared__ float fk[DK], fq[DK], vv[DV];
+  __shared__ float4 part[kThreads];
+  const long bh = blockIdx.x;
+  const int b = (int)(bh / p.H), h = (int)(bh - (long)b * p.H);
+  const int tid = threadIdx.x, cq = tid % kQuads, g = tid / kQuads;
+  Tin *out = (Tin *)p.out + bh * DV;
+  const int slot = p.slots ? p.slots[b] : b;
+  if (slot < 0 || slot >= p.n_slots) {  // negative: an unused row of a fixed-size batch
+    if (slot >= 0 && tid == 0) atomicOr(&g_gated_step_status, kStatusBadSlot);
+    if (tid < DV / 4) st4(out + 4 * tid, 0.f, 0.f, 0.f, 0.f);
+    return;
+  }
+  float4 *S4 = reinterpret_cast<float4 *>(p.S + ((long)slot * p.H + h) * (DK * DV));
+  float4 s[kRows];
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) s[r] = __ldcs(S4 + (g + r * kGroups) * kQuads + cq);
+  int again = 0;
+  if (p.slots)
+    for (int o = tid; o < b; o += kThreads) again |= p.slots[o] == slot;
+  if (tid < DK) {
+    fk[tid] = ldf((const Tin *)p.k + bh * DK + tid);
+    fq[tid] = ldf((const Tin *)p.q + bh * DK + tid);
+  }
+  if (tid < DV) vv[tid] = ldf((const Tin *)p.v + bh * DV + tid);
+  const float a = expf(p.g[bh]);
+  if (__syncthreads_or(again)) {
+    if (tid == 0) atomicOr(&g_gated_step_status, kStatusBadSlot);
+    if (tid < DV / 4) st4(out + 4 * tid, 0.f, 0.f, 0.f, 0.f);
+    return;
+  }
+  const float4 vq = reinterpret_cast<const float4 *>(vv)[cq];
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    const int i = g + r * kGroups;
+    const float kk = fk[i], qq = fq[i];
+    float4 x = s[r];
+    x.x = fmaf(kk, vq.x, a * x.x);
+    x.y = fmaf(kk, vq.y, a * x.y);
+    x.z = fmaf(kk, vq.z, a * x.z);
+    x.w = fmaf(kk, vq.w, a * x.w);
+    __stcs(S4 + i * kQuads + cq, x);
+    acc.x = fmaf(qq, x.x, acc.x);
+    acc.y = fmaf(qq, x.y, acc.y);
+    acc.z = fmaf(qq, x.z, acc.z);
+    acc.w = fmaf(qq, x.w, acc.w);
+  }
+  part[g * kQuads + cq] = acc;
+  __syncthreads();
+  if (tid < DV / 4) {
+    float4 n = part[tid];
+#pragma unroll
+    for (int gg = 1; gg < kGroups; ++gg) {
+      const float4 y = part[gg * kQuads + tid];
+      n = make_float4(n.x + y.x, n.y + y.y, n.z + y.z, n.w + y.w);
+    }
+    st4(out + 4 * tid, n.x, n.y, n.z, n.w);
+  }
+}
+
+template <typename Tin, int DK, int DV>
+cudaError_t launch_t(const GatedStepProblem &p) {
+  LaunchTimer timer(kKGatedDecode, p.stream);
+  gated_decode_kernel<Tin, DK, DV><<<(unsigned)((long)p.B * p.H), kThreads, 0, p.stream>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  timer.done(e);
+  if (e == cudaSuccess) count_launch();
+  return e;
+}
+
+template <typename Tin, int DK>
+cudaError_t launch_dv(const GatedStepProblem &p) {
+  return p.dv == 32 ? launch_t<Tin, DK, 32>(p) : p.dv == 64 ? launch_t<Tin, DK, 64>(p) : launch_t<Tin, DK, 128>(p);
+}
+
+template <typename Tin>
+cudaError_t launch_dk(const GatedStepProblem &p) {
+  return p.dk == 32 ? launch_dv<Tin, 32>(p) : p.dk == 64 ? launch_dv<Tin, 64>(p) : launch_dv<Tin, 128>(p);
+}
+
+}  // namespace
+
+cudaError_t launch_gated_decode(const GatedStepProblem &p) {
+  return p.dt == LA_F32 ? launch_dk<float>(p) : launch_dk<__nv_bfloat16>(p);
+}
+
+cudaError_t read_and_clear_gated_step_status(unsigned int *value) {
+  unsigned int zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(value, g_gated_step_status, sizeof(unsigned int));
+  if (e == cudaSuccess && *value) e = cudaMemcpyToSymbol(g_gated_step_status, &zero, sizeof(unsigned int));
+  return e;
+}
+
+}  // namespace la

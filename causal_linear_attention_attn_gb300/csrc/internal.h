@@ -126,6 +126,81 @@ cudaError_t launch_retention_decode(const Problem &p, const float *gamma, int H)
 // (host array, head bh decays by gamma[bh % H], H <= 128).
 cudaError_t launch_retention_simt(const Problem &p, bool from_state, const float *gamma, int H);
 
+// Gated linear attention: S_t = e^{g_t} S_{t-1} + k_t v_t^T, out_t = q_t^T S_t, with a log decay
+// per token and head (g: [BH][N]).  lengths (nullable, [B]): tokens of batch row b past
+// lengths[b] take no part.  S0 (nullable): initial state, not overlapping S.
+struct GatedProblem {
+  const void *q, *k, *v;
+  const float *g;
+  const int *lengths;
+  const float *S0;
+  void *out;  // dtype dt
+  float *S;
+  int B, H;
+  long N;
+  int dk, dv;
+  la_dtype dt;
+  void *ws;  // device workspace of the size the matching *_workspace function gives
+  cudaStream_t stream;
+  long BH() const { return (long)B * H; }
+};
+// Its gradient: dout, dq, dk, dv have dtype dt; dS (gradient of the final state) and dS0 are nullable.
+struct GatedGradProblem {
+  GatedProblem p;
+  const void *dout;
+  const float *dS;
+  void *dq, *dk, *dv;
+  float *dg, *dS0;
+};
+// Exact fp32 CUDA-core kernels for every supported type and head size.
+size_t gated_simt_workspace(long BH, long N, int dk, int dv, bool grad);
+cudaError_t launch_gated_simt(const GatedProblem &p);
+cudaError_t launch_gated_grad_simt(const GatedGradProblem &b);
+
+// One recurrent step of the gated form per (row, head): row b works on state slots[b] of the
+// pool S ([n_slots][H][dk][dv]); see la_gated_decode_step.
+struct GatedStepProblem {
+  const void *q, *k, *v;
+  const float *g;
+  float *S;
+  const int *slots;
+  void *out;
+  int B, H, n_slots, dk, dv;
+  la_dtype dt;
+  cudaStream_t stream;
+};
+cudaError_t launch_gated_decode(const GatedStepProblem &p);
+cudaError_t read_and_clear_gated_step_status(unsigned int *value);
+constexpr unsigned kStatusBadSlot = 4u;  // device status bit: a slot out of range or given twice
+
+// Group norm of each head's channels with a SiLU gate, [B][H][N][d] -> [B][N][H*d], and its gradient.
+struct NormProblem {
+  const void *x, *gate;
+  const float *weight, *bias;  // [H*d], nullable
+  void *y;
+  int B, H;
+  long N;
+  int d;
+  float eps;
+  la_dtype dt;
+  cudaStream_t stream;
+};
+struct NormGradProblem {
+  NormProblem p;
+  const void *dy;
+  void *dx, *dgate;
+  float *dweight, *dbias;  // nullable
+  float *ws;               // norm_grad_workspace bytes
+};
+cudaError_t launch_group_norm(const NormProblem &p);
+size_t norm_grad_workspace(int B, int H, long N, int d);
+cudaError_t launch_group_norm_grad(const NormGradProblem &b);
+
+// For the entry points: whether a current device exists, and the status of a CUDA result (whose
+// detail la_last_error_detail then gives).
+la_status api_device();
+la_status api_status(cudaError_t e);
+
 // Count one successful kernel launch (reported by la_kernel_launches).
 void count_launch(unsigned n = 1);
 
@@ -144,7 +219,13 @@ enum KernelId : int {
   kKBackward = 10,
   kKFavor = 11,
   kKGlobalFused = 12,
-  kKNumKernels = 13
+  kKGated = 13,
+  kKGatedState = 14,
+  kKGatedBackward = 15,
+  kKGatedDecode = 16,
+  kKGroupNorm = 17,
+  kKGroupNormBackward = 18,
+  kKNumKernels = 19
 };
 
 // While profiling is on (la_profile_enable), brackets one launch with a CUDA

@@ -72,6 +72,12 @@ la_status current_device(int *dev) {
 
 }  // namespace
 
+la_status api_device() {
+  int dev;
+  return current_device(&dev);
+}
+la_status api_status(cudaError_t e) { return from_cuda(e); }
+
 void count_launch(unsigned n) { g_launches.fetch_add(n, std::memory_order_relaxed); }
 
 // --- device-time diagnostics --------------------------------------------------------
@@ -204,9 +210,12 @@ la_status la_device_status(void *stream) {
   unsigned int vb = 0;
   if (e == cudaSuccess) e = la::read_and_clear_favor_status(&vf);
   if (e == cudaSuccess) e = la::read_and_clear_backward_status(&vb);
+  unsigned int vs = 0;
+  if (e == cudaSuccess) e = la::read_and_clear_gated_step_status(&vs);
   if (e != cudaSuccess) return la::from_cuda(e);
   v |= vg | vf | vb;
   if (v & 1u) return LA_ERR_TIMEOUT;
+  if (!v && (vs & la::kStatusBadSlot)) return LA_ERR_INVALID_VALUE;
   return v ? LA_ERR_LAUNCH : LA_OK;  // other bits: a kernel refused to run (e.g. misaligned shared memory)
 }
 

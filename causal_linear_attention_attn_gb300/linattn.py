@@ -41,6 +41,22 @@ lib.la_causal_backward.argtypes = [_vp] * 13 + [_i, _i, _i, _i, _i, _f, _i, _vp]
 lib.la_causal_backward.restype = _i
 lib.la_favor_features.argtypes = [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp]
 lib.la_favor_features.restype = _i
+_sz = ctypes.c_size_t
+for _name in ("la_gated", "la_gated_with_state"):
+    getattr(lib, _name).argtypes = [_vp] * 7 + [_i] * 6 + [_vp, _sz, _vp]
+    getattr(lib, _name).restype = _i
+lib.la_gated_workspace.argtypes = [_i] * 7
+lib.la_gated_workspace.restype = _sz
+lib.la_gated_backward.argtypes = [_vp] * 13 + [_i] * 6 + [_vp, _sz, _vp]
+lib.la_gated_backward.restype = _i
+lib.la_gated_decode_step.argtypes = [_vp] * 7 + [_i] * 6 + [_vp]
+lib.la_gated_decode_step.restype = _i
+lib.la_group_norm.argtypes = [_vp] * 5 + [_i] * 4 + [_f, _i, _vp]
+lib.la_group_norm.restype = _i
+lib.la_group_norm_workspace.argtypes = [_i] * 4
+lib.la_group_norm_workspace.restype = _sz
+lib.la_group_norm_backward.argtypes = [_vp] * 9 + [_i] * 4 + [_f, _i, _vp, _sz, _vp]
+lib.la_group_norm_backward.restype = _i
 lib.la_decode_step.restype = _i
 lib.la_status_string.argtypes = [_i]
 lib.la_status_string.restype = ctypes.c_char_p
@@ -64,7 +80,8 @@ lib.la_profile_read.restype = _i
 # la_kernel ids of the device-time diagnostics
 KERNELS = {"causal_main": 0, "causal_state": 1, "exact_head": 2, "causal_simt": 3, "global_state": 4,
            "global_read": 5, "decode": 6, "retention_main": 7, "retention_state": 8, "retention_decode": 9,
-           "backward": 10, "favor": 11, "global_fused": 12}
+           "backward": 10, "favor": 11, "global_fused": 12, "gated": 13, "gated_state": 14, "gated_backward": 15,
+           "gated_decode": 16, "group_norm": 17, "group_norm_backward": 18}
 
 
 class LinAttnError(RuntimeError):
@@ -291,6 +308,193 @@ def la_causal_backward(q, k, v, dout, S0=None, z0=None, dS=None, dz=None, need_s
     if rc != 0:
         raise LinAttnError("la_causal_backward", rc)
     return (dq, dkk, dvv, dS0, dz0) if need_state_grad else (dq, dkk, dvv)
+
+
+class _On:
+    """The device and stream a call runs on: the tensors' device, and the given stream or that device's
+    current one.  Outputs and workspaces are allocated inside, so that they belong to that stream."""
+
+    def __init__(self, device, stream):
+        if stream is None:
+            self.stream = torch.cuda.current_stream(device)
+        elif isinstance(stream, torch.cuda.Stream):
+            self.stream = stream
+        elif int(stream) == 0:
+            self.stream = torch.cuda.default_stream(device)
+        else:
+            self.stream = torch.cuda.ExternalStream(int(stream), device=device)
+        if self.stream.device != device:
+            raise ValueError(f"the stream belongs to {self.stream.device}, the tensors to {device}")
+        # entering the stream also makes its device current; not needed for a call on the current pair
+        self._ctx = None
+        if stream is not None or torch.cuda.current_device() != device.index:
+            self._ctx = torch.cuda.stream(self.stream)
+
+    def __enter__(self):
+        if self._ctx is not None:
+            self._ctx.__enter__()
+        return self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
+
+
+def _need(name, t, shape, dtype, device):
+    """t itself, after checking that it is a contiguous CUDA tensor of that shape, dtype and device."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    return t
+
+
+def _opt(name, t, shape, dtype, device):
+    return None if t is None else _need(name, t, shape, dtype, device)
+
+
+def _out(name, t, shape, dtype, device):
+    return torch.empty(shape, dtype=dtype, device=device) if t is None else _need(name, t, shape, dtype, device)
+
+
+def _gated_inputs(q, k, v, g, nd):
+    """(lead, d_k, d_v, dtype code) of gated inputs whose leading dims are [B, H, N] (nd = 4) or [B, H] (nd = 3)."""
+    if not isinstance(q, torch.Tensor) or q.dim() != nd or not isinstance(v, torch.Tensor) or v.dim() != nd:
+        raise ValueError(f"q and v must be {nd}-d tensors")
+    dt, lead, dev = _dt(q), tuple(q.shape[:-1]), q.device
+    dk, dv = q.shape[-1], v.shape[-1]
+    _need("q", q, (*lead, dk), q.dtype, dev)
+    _need("k", k, (*lead, dk), q.dtype, dev)
+    _need("v", v, (*lead, dv), q.dtype, dev)
+    _need("g", g, lead, torch.float32, dev)
+    return lead, dk, dv, dt
+
+
+def _gated_call(fn, q, k, v, g, lengths, out, S, stream):
+    (B, H, N), dk, dv, dt = _gated_inputs(q, k, v, g, 4)
+    dev = q.device
+    _opt("lengths", lengths, (B,), torch.int32, dev)
+    with _On(dev, stream) as s:
+        out = _out("out", out, (B, H, N, dv), q.dtype, dev)
+        S = _out("S", S, (B, H, dk, dv), torch.float32, dev)
+        need = lib.la_gated_workspace(B, H, N, dk, dv, dt, 0)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        rc = getattr(lib, fn)(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(lengths), _ptr(out), _ptr(S), B, H, N, dk, dv, dt,
+                              _ptr(ws), need, s)
+    if rc != 0:
+        raise LinAttnError(fn, rc)
+    return out, S
+
+
+def la_gated(q, k, v, g, lengths=None, out=None, S=None, stream=None):
+    """Gated linear attention S_t = e^{g_t} S_{t-1} + k_t v_t^T, out_t = q_t^T S_t from the zero state.
+
+    q, k [B, H, N, d_k], v [B, H, N, d_v] (float32 or bfloat16); g [B, H, N] float32 log decays (<= 0; -inf resets).
+    lengths [B] int32: tokens past a row's length take no part and their ``out`` rows are not written.
+    Returns (out in q's dtype, final state S float32).
+    """
+    return _gated_call("la_gated", q, k, v, g, lengths, out, S, stream)
+
+
+def la_gated_with_state(q, k, v, g, S, lengths=None, out=None, stream=None):
+    """Gated linear attention continuing from S, which is updated in place; returns (out, S)."""
+    if S is None:
+        raise ValueError("la_gated_with_state needs the initial state S")
+    return _gated_call("la_gated_with_state", q, k, v, g, lengths, out, S, stream)
+
+
+def la_gated_backward(q, k, v, g, dout, S0=None, dS=None, lengths=None, need_state_grad: bool = False, stream=None):
+    """Gradients of la_gated (la_gated_with_state when S0 is given) for the upstream gradient ``dout`` of its output
+    (q's dtype) and, optionally, ``dS`` of its final state.  Returns (dq, dk, dv, dg), plus dS0 when
+    ``need_state_grad``; dq, dk, dv in q's dtype, dg and dS0 float32."""
+    (B, H, N), dk, dv, dt = _gated_inputs(q, k, v, g, 4)
+    dev = q.device
+    _need("dout", dout, (B, H, N, dv), q.dtype, dev)
+    _opt("lengths", lengths, (B,), torch.int32, dev)
+    _opt("S0", S0, (B, H, dk, dv), torch.float32, dev)
+    _opt("dS", dS, (B, H, dk, dv), torch.float32, dev)
+    with _On(dev, stream) as s:
+        dq, dkk, dvv, dg = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v), torch.empty_like(g)
+        dS0 = torch.empty(B, H, dk, dv, dtype=torch.float32, device=dev) if need_state_grad else None
+        need = lib.la_gated_workspace(B, H, N, dk, dv, dt, 1)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        rc = lib.la_gated_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(lengths), _ptr(dout), _ptr(S0), _ptr(dS),
+                                   _ptr(dq), _ptr(dkk), _ptr(dvv), _ptr(dg), _ptr(dS0), B, H, N, dk, dv, dt, _ptr(ws),
+                                   need, s)
+    if rc != 0:
+        raise LinAttnError("la_gated_backward", rc)
+    return (dq, dkk, dvv, dg, dS0) if need_state_grad else (dq, dkk, dvv, dg)
+
+
+def la_gated_decode_step(q, k, v, g, S, slots=None, out=None, stream=None):
+    """One gated step; q, k [B, H, d_k], v [B, H, d_v], g [B, H]; returns out [B, H, d_v] in q's dtype.
+
+    S [n_slots, H, d_k, d_v] is a pool of states: row b works in place on S[slots[b]] (slots [B] int32; without it,
+    row b on S[b]).  A negative slot marks an unused row (out zero).  A slot out of range or repeated in the batch
+    is skipped too, and the next device_status() is 1.
+    """
+    (B, H), dk, dv, dt = _gated_inputs(q, k, v, g, 3)
+    dev = q.device
+    if not isinstance(S, torch.Tensor) or S.dim() != 4:
+        raise ValueError("S must be a [n_slots, H, d_k, d_v] tensor")
+    n_slots = S.shape[0]
+    _need("S", S, (n_slots, H, dk, dv), torch.float32, dev)
+    _opt("slots", slots, (B,), torch.int32, dev)
+    if slots is None and n_slots < B:
+        raise ValueError(f"S holds {n_slots} states for {B} rows")
+    with _On(dev, stream) as s:
+        out = _out("out", out, (B, H, dv), q.dtype, dev)
+        rc = lib.la_gated_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S), _ptr(slots), _ptr(out), B, H, n_slots,
+                                      dk, dv, dt, s)
+    if rc != 0:
+        raise LinAttnError("la_gated_decode_step", rc)
+    return out
+
+
+def _norm_inputs(x, gate, weight, bias):
+    if not isinstance(x, torch.Tensor) or x.dim() != 4:
+        raise ValueError("x must be a 4-d tensor")
+    B, H, N, d = x.shape
+    _need("x", x, (B, H, N, d), x.dtype, x.device)
+    dt = _dt(x)
+    _opt("gate", gate, (B, N, H * d), x.dtype, x.device)
+    _opt("weight", weight, (H * d,), torch.float32, x.device)
+    _opt("bias", bias, (H * d,), torch.float32, x.device)
+    return B, H, N, d, dt
+
+
+def la_group_norm(x, gate=None, weight=None, bias=None, eps: float = 1e-5, out=None, stream=None):
+    """Group norm of each head's channels times silu(gate): x [B, H, N, d] -> [B, N, H*d], x's dtype.
+
+    gate [B, N, H*d] (x's dtype); weight, bias [H*d] float32; each may be None.
+    """
+    B, H, N, d, dt = _norm_inputs(x, gate, weight, bias)
+    with _On(x.device, stream) as s:
+        out = _out("out", out, (B, N, H * d), x.dtype, x.device)
+        rc = lib.la_group_norm(_ptr(x), _ptr(gate), _ptr(weight), _ptr(bias), _ptr(out), B, H, N, d, float(eps), dt, s)
+    if rc != 0:
+        raise LinAttnError("la_group_norm", rc)
+    return out
+
+
+def la_group_norm_backward(x, dy, gate=None, weight=None, bias=None, eps: float = 1e-5, stream=None):
+    """Gradients of la_group_norm for dy [B, N, H*d]: (dx, dgate, dweight, dbias), None for an argument not given."""
+    B, H, N, d, dt = _norm_inputs(x, gate, weight, bias)
+    _need("dy", dy, (B, N, H * d), x.dtype, x.device)
+    with _On(x.device, stream) as s:
+        dx = torch.empty_like(x)
+        dgate, dw, db = (None if t is None else torch.empty_like(t) for t in (gate, weight, bias))
+        need = 0 if dw is None and db is None else lib.la_group_norm_workspace(B, H, N, d)
+        ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+        rc = lib.la_group_norm_backward(_ptr(x), _ptr(dy), _ptr(gate), _ptr(weight), _ptr(bias), _ptr(dx), _ptr(dgate),
+                                        _ptr(dw), _ptr(db), B, H, N, d, float(eps), dt, _ptr(ws), need, s)
+    if rc != 0:
+        raise LinAttnError("la_group_norm_backward", rc)
+    return dx, dgate, dw, db
 
 
 def device_status(stream=None) -> int:

@@ -50,6 +50,8 @@
 #ifndef LINATTN_H
 #define LINATTN_H
 
+#include <stddef.h>
+
 #if defined(__GNUC__)
 #define LA_API __attribute__((visibility("default")))
 #else
@@ -318,13 +320,128 @@ LA_API la_status la_retention_decode_step(const void *q, const void *k, const vo
                                           void *stream);
 
 /*
+ * Gated linear attention: retention whose decay is data, one per token and
+ * head,
+ *     S_t = e^{g_t} S_{t-1} + k_t v_t^T,   out_t = q_t^T S_t,   S_{-1} = 0,
+ * q and k used as given, the read taken after the update.  Source: "Linear
+ * Attention Math", "The kernel cousins: SSMs and RetNet" (the decayed update
+ * without a denominator); "Linear Attention: From Pairwise Reads to a
+ * Recurrent State" (gated unnormalized states).  la_group_norm is the
+ * normalization that takes the denominator's place.
+ *
+ * q, k: [B,H,N,d_k]; v, out: [B,H,N,d_v], all of dtype dt (out too, unlike
+ * the normalized forms: the next layer takes the inputs' type).  g:
+ * [B,H,N] float32 DEVICE array of natural-log decays, meant to be <= 0; -inf
+ * resets the state (nothing before the token is read at or after it), and a
+ * positive value grows it.  S: [B,H,d_k,d_v] float32, OVERWRITTEN with the
+ * final state.  lengths: [B] int32 DEVICE array or NULL (every row has N
+ * tokens): tokens t >= lengths[b] of batch row b take no part, whatever they
+ * hold; out is left as it was there and S is the state after the last token
+ * that does.  Values outside [0, N] are taken as the nearer bound.
+ *
+ * workspace: at least la_gated_workspace(..., 0) bytes of device memory, free
+ * for other use when the call's work on `stream` is done; calls that may run
+ * at the same time (two streams, two graphs) need one each.  Nothing is
+ * allocated.  d_k, d_v in {32, 64, 128}; dt LA_F32 or LA_BF16; LA_ERR_MISALIGNED
+ * for g or lengths off 4 bytes or another pointer off 16; LA_ERR_INVALID_VALUE
+ * for a workspace that is NULL or too small; other errors as la_causal.
+ * N == 0 zeroes S.
+ */
+LA_API la_status la_gated(const void *q, const void *k, const void *v, const float *g, const int *lengths,
+                          void *out, float *S, int B, int H, int N, int d_k, int d_v, la_dtype dt,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gated linear attention continuing from a given state: as la_gated, but the
+ * recurrence starts from the caller's S, which is read and then OVERWRITTEN
+ * with the state after the new tokens (unchanged for a row without any).
+ */
+LA_API la_status la_gated_with_state(const void *q, const void *k, const void *v, const float *g,
+                                     const int *lengths, void *out, float *S, int B, int H, int N, int d_k,
+                                     int d_v, la_dtype dt, void *workspace, size_t workspace_bytes,
+                                     void *stream);
+
+/*
+ * Workspace bytes of la_gated / la_gated_with_state (backward == 0) or of
+ * la_gated_backward (backward != 0) on the current device; 0 when the sizes
+ * are invalid or there is nothing to do.
+ */
+LA_API size_t la_gated_workspace(int B, int H, int N, int d_k, int d_v, la_dtype dt, int backward);
+
+/*
+ * Gradient of la_gated / la_gated_with_state: with R_t the gradient of S_t,
+ *     R_t = q_t dout_t^T + e^{g_{t+1}} R_{t+1},   R_{N-1} = q dout^T + dS,
+ *     dq_t = S_t dout_t,  dk_t = R_t v_t,  dv_t = R_t^T k_t,
+ *     dg_t = e^{g_t} <S_{t-1}, R_t>,  dS0 = e^{g_0} R_0.
+ * q, k, v, g, lengths: the forward's inputs.  dout: [B,H,N,d_v] of dtype dt.
+ * S0 (NULL = zero): the forward's initial state.  dS (NULL = zero): gradient
+ * of its final state.  Written: dq, dk: [B,H,N,d_k], dv: [B,H,N,d_v], dtype
+ * dt; dg: [B,H,N] float32; dS0 (nullable): [B,H,d_k,d_v] float32, gradient of
+ * the initial state, which may be dS itself.  Rows t >= lengths[b] get zero
+ * gradients.  Workspace, sizes and errors as la_gated, with
+ * la_gated_workspace(..., 1).
+ */
+LA_API la_status la_gated_backward(const void *q, const void *k, const void *v, const float *g,
+                                   const int *lengths, const void *dout, const float *S0, const float *dS,
+                                   void *dq, void *dk, void *dv, float *dg, float *dS0, int B, int H, int N,
+                                   int d_k, int d_v, la_dtype dt, void *workspace, size_t workspace_bytes,
+                                   void *stream);
+
+/*
+ * One recurrent step of gated linear attention per (row, head), on states
+ * that live in a pool:
+ *     S = e^{g} S + k v^T;   out = q^T S,   S the state of row b's slot.
+ * q, k: [B,H,d_k]; v, out: [B,H,d_v], dtype dt; g: [B,H] float32.  S:
+ * [n_slots,H,d_k,d_v] float32, the slots of this batch read and written IN
+ * PLACE, the others untouched.  slots: [B] int32 DEVICE array or NULL (row b
+ * uses slot b; n_slots >= B).  A negative slot marks an unused row: no state
+ * is touched and its out is zero.  A slot >= n_slots, or one that an earlier
+ * row of the batch has, is treated the same way and also makes the next
+ * la_device_status return LA_ERR_INVALID_VALUE (two rows on one state have no
+ * defined order).  Allocates nothing.  Sizes and errors as la_gated.
+ */
+LA_API la_status la_gated_decode_step(const void *q, const void *k, const void *v, const float *g, float *S,
+                                      const int *slots, void *out, int B, int H, int n_slots, int d_k, int d_v,
+                                      la_dtype dt, void *stream);
+
+/*
+ * Group norm of each head's channels with an affine map and a SiLU gate, the
+ * "gated normalization" that replaces retention's denominator ("Linear
+ * Attention Math", "The kernel cousins: SSMs and RetNet"): per token and
+ * head, over its d channels,
+ *     y = ((x - mean) / sqrt(var + eps) * weight + bias) * gate * sigmoid(gate),
+ * var the mean squared deviation.  x: [B,H,N,d] (the attention output's
+ * layout); gate (nullable: no gating), y: [B,N,H*d], channels last; all of
+ * dtype dt.  weight, bias: [H*d] float32, each nullable (1 and 0).  d in
+ * {32, 64, 128}, eps >= 0.  Statistics in fp32.  Every pointer 16-byte
+ * aligned; y must not overlap an input.  B*H*N == 0 is a no-op.
+ */
+LA_API la_status la_group_norm(const void *x, const void *gate, const float *weight, const float *bias, void *y,
+                               int B, int H, int N, int d, float eps, la_dtype dt, void *stream);
+
+/*
+ * Gradient of la_group_norm for dy ([B,N,H*d], dtype dt).  Written: dx
+ * [B,H,N,d] and dgate [B,N,H*d] (given exactly when gate is) of dtype dt;
+ * dweight, dbias [H*d] float32, each nullable, whether or not the forward had
+ * weight and bias.  The column sums are added in a fixed order.  workspace:
+ * la_group_norm_workspace bytes when dweight or dbias is wanted (NULL
+ * otherwise); calls that may run at the same time need one each.
+ */
+LA_API la_status la_group_norm_backward(const void *x, const void *dy, const void *gate, const float *weight,
+                                        const float *bias, void *dx, void *dgate, float *dweight, float *dbias,
+                                        int B, int H, int N, int d, float eps, la_dtype dt, void *workspace,
+                                        size_t workspace_bytes, void *stream);
+LA_API size_t la_group_norm_workspace(int B, int H, int N, int d);
+
+/*
  * Synchronizes `stream`, then reads and clears the library's device status
  * word on the current device.  Returns LA_ERR_TIMEOUT if a bounded
  * device-side wait inside one of the library's kernels gave up since the
  * last check, LA_ERR_LAUNCH if a kernel refused to run on this device
  * configuration (its shared-memory base was not 1024-byte aligned); in both
- * cases that call's outputs are not valid.  LA_OK otherwise, or the error
- * of the synchronization itself.
+ * cases that call's outputs are not valid.  LA_ERR_INVALID_VALUE if a
+ * la_gated_decode_step skipped a row whose slot was out of range or repeated.
+ * LA_OK otherwise, or the error of the synchronization itself.
  */
 LA_API la_status la_device_status(void *stream);
 
@@ -392,7 +509,13 @@ typedef enum {
   LA_KERNEL_RETENTION_DECODE = 9, /* recurrent retention step */
   LA_KERNEL_BACKWARD = 10,        /* causal backward */
   LA_KERNEL_FAVOR = 11,           /* positive random features */
-  LA_KERNEL_GLOBAL_FUSED = 12     /* global form in one pass: a CTA per head (d = 64, heads >= 80 % of SMs) */
+  LA_KERNEL_GLOBAL_FUSED = 12,    /* global form in one pass: a CTA per head (d = 64, heads >= 80 % of SMs) */
+  LA_KERNEL_GATED = 13,           /* gated linear attention: outputs */
+  LA_KERNEL_GATED_STATE = 14,     /* its passes over chunk states, forward and backward */
+  LA_KERNEL_GATED_BACKWARD = 15,  /* its gradient */
+  LA_KERNEL_GATED_DECODE = 16,    /* its recurrent step */
+  LA_KERNEL_GROUP_NORM = 17,      /* gated group norm */
+  LA_KERNEL_GROUP_NORM_BACKWARD = 18 /* its gradient */
 } la_kernel;
 
 /*
