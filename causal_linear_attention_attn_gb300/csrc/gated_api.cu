@@ -30,7 +30,9 @@ la_status sizes(int B, int H, long N, int dk, int dv, la_dtype dt) {
 }
 
 size_t workspace(int B, int H, long N, int dk, int dv, la_dtype dt, bool grad) {
-  return gated_simt_workspace((long)B * H, N, dk, dv, grad);
+  const long BH = (long)B * H;
+  if (!grad && gated_tc_supported(dk, dv, dt)) return gated_tc_prefill_workspace(BH, N, dk);
+  return gated_simt_workspace(BH, N, dk, dv, grad);
 }
 
 la_status gated(const void *q, const void *k, const void *v, const float *g, const int *lengths, void *out, float *S,
@@ -49,7 +51,7 @@ la_status gated(const void *q, const void *k, const void *v, const float *g, con
   }
   if ((st = api_device()) != LA_OK) return st;
   if (!ws || ws_bytes < workspace(B, H, N, dk, dv, dt, false)) return LA_ERR_INVALID_VALUE;
-  return api_status(launch_gated_simt(p));
+  return api_status(gated_tc_supported(dk, dv, dt) ? launch_gated_tc(p) : launch_gated_simt(p));
 }
 
 }  // namespace

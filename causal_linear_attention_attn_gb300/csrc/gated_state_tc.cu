@@ -1,0 +1,376 @@
+// States of gated linear attention at chunk borders, on the sm_103a tensor cores.
+//
+//   X <- 2^{c_T} X + sum_t w_t a_t b_t^T      over chunks of 128 tokens,
+// forward: a = k, b = v, w_t = 2^{c_T - c_t} (the state); backward, from the last chunk: a = q,
+// b = dout, w_t = 2^{c_t} (the gradient of the state).  The state stays fp32 in tensor memory.  The
+// weighted a_t reach the MMAs as a bf16 pair (hi + lo, 2^-17 relative): the state is an fp32 result
+// and feeds the decays' gradient, and one bf16 rounding (2^-9) would show in both.
+//
+// A CTA owns 64 of the state's columns for one segment of one head and direction, so that 64 heads
+// make 256 CTAs at D = 128, two to an SM, all resident at once: the recurrence over chunks is a
+// chain, and only independent chains hide its latency.  (The a tile is read once per column slice;
+// the second read comes from L2.)  Loads come in 64-token stages so that two CTAs fit an SM.
+// At D = 64 hi and lo make up the 128 rows of one MMA, [hi | lo]^T b, and meet when the state is read.
+// HBM bounds it: per token 4 D bytes in and, when tiles are written, 4 D bytes out per direction.
+//
+// Warps: 0 TMA, 1 MMA and TMEM owner, 2-5 weights (hi in place, lo beside it), 6-9 state (store,
+// decay, write back), 10 running sums of the decays.  Every wait is bounded (tc_ptx.cuh).
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+
+#include "gated_tc.cuh"
+
+namespace la {
+
+namespace {
+using namespace gtc;
+
+constexpr int kThreads = 352;
+constexpr int kWarpXform = 2, kWarpState = 6, kWarpGate = 10;
+constexpr uint32_t kBarState = 1;
+constexpr int kSub = 64;  // tokens per stage
+constexpr uint32_t kHalf = 8192;  // [64 rows x 128 bytes]
+
+template <int D>
+struct Lay {
+  static constexpr int kStages = D == 128 ? 3 : 4;
+  static constexpr uint32_t kA = D / 64 * kHalf;  // one stage of a (or of its low parts)
+  static constexpr uint32_t A = 0;
+  static constexpr uint32_t Lo = A + kStages * kA;  // 2 buffers
+  static constexpr uint32_t B = Lo + 2 * kA;
+  static constexpr uint32_t Sum = B + kStages * kHalf;  // D = 64: low rows of the state [64][65] fp32
+  static constexpr uint32_t Gate = Sum + (D == 64 ? 64 * 65 * 4 : 0);  // [2][hi 128, lo 128]
+  static constexpr uint32_t Bars = Gate + 2 * 2 * kC * 4;
+  static constexpr int kNumBars = 3 * kStages + 2 + 4 + 3;
+  static constexpr uint32_t Misc = Bars + kNumBars * 8;
+  static constexpr uint32_t Bytes = Misc + 16;
+};
+static_assert(Lay<128>::Bytes <= 115712 && Lay<64>::Bytes <= 115712, "two CTAs per SM");
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2) gated_state_tc_kernel(const __grid_constant__ GatedStateParams p) {
+  using L = Lay<D>;
+  constexpr int kStages = L::kStages, kSlices = D / 64;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  if (smem_u32(sm) & 1023u) {
+    if (threadIdx.x == 0) atomicOr(&g_gated_status, kAbortMisaligned);
+    return;
+  }
+  uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::Bars);
+  uint64_t *full = bars, *done = full + kStages, *empty = done + kStages, *lo_free = empty + kStages,
+           *gate_full = lo_free + 2, *gate_free = gate_full + 2, *x_ready = gate_free + 2, *x_full = x_ready + 1,
+           *drain = x_full + 1;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::Misc);
+  volatile uint32_t *abort_word = reinterpret_cast<volatile uint32_t *>(sm + L::Misc + 4);
+  unsigned int *status = &g_gated_status;
+  float *gate = reinterpret_cast<float *>(sm + L::Gate);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int dir = blockIdx.y;
+  const int slice = blockIdx.x % kSlices;
+  const long item = blockIdx.x / kSlices;
+  const long bh = item / p.run_segs;
+  const int seg = (int)(item - bh * p.run_segs);
+  const long len = row_length(p.lengths, bh / p.H, p.N);
+  const long nb = (len + kC - 1) / kC;  // the row's chunks
+  const long c_lo = min(nb, (long)seg * p.seg_chunks), c_hi = min(nb, c_lo + p.seg_chunks);
+  const int nc = (int)(c_hi - c_lo);
+  uint8_t *tiles = p.tiles[dir];
+  float *fin = p.fin[dir];
+  // the last chunk is folded in only if the state behind it is wanted
+  const int run = fin ? nc : max(0, nc - 1);
+  auto chunk = [&](int i) -> long { return dir ? c_hi - 1 - i : c_lo + i; };
+  auto valid = [&](int i) -> int { return (int)min((long)kC, len - chunk(i) * kC); };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&done[s], 128);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&lo_free[b], 1);
+      mbar_init(&gate_full[b], 32);
+      mbar_init(&gate_free[b], 256);
+    }
+    mbar_init(x_ready, 128);
+    mbar_init(x_full, 1);
+    mbar_init(drain, 1);
+    *abort_word = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, 64);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // after the tensor-memory allocation: the next kernel's CTAs, which allocate too and wait for this
+  // grid, must not take columns that a CTA of this grid still needs
+  if (threadIdx.x == 0) pdl_trigger();
+  pdl_wait();  // init may be the previous kernel's
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int issued = 0;
+      for (int u = 0; u < 2 * run; ++u) {
+        const int s = u % kStages;
+        if (u >= kStages && !mbar_wait(&empty[s], (u / kStages - 1) & 1, abort_word, status)) break;
+        const int tok = (int)(chunk(u >> 1) * kC) + (u & 1) * kSub;
+        mbar_arrive_expect_tx(&full[s], L::kA + kHalf);
+        for (int b = 0; b < D / 64; ++b) tma_load_3d(sm + L::A + s * L::kA + b * kHalf, &p.ta[dir], &full[s], 64 * b, tok, (int)bh);
+        tma_load_3d(sm + L::B + s * kHalf, &p.tb[dir], &full[s], 64 * slice, tok, (int)bh);
+        issued = u + 1;
+      }
+      for (int u = max(0, issued - kStages); u < issued; ++u) wait_drain(&full[u % kStages], (u / kStages) & 1, status);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t iMM = idesc_bf16_f32(128, 64, 1, 1);
+      const uint32_t sA = smem_u32(sm + L::A), sLo = smem_u32(sm + L::Lo), sB = smem_u32(sm + L::B);
+      for (int u = 0; u < 2 * run; ++u) {
+        const int s = u % kStages;
+        if (!mbar_wait(&done[s], (u / kStages) & 1, abort_word, status)) break;
+        if (!(u & 1) && !mbar_wait(x_ready, (u >> 1) & 1, abort_word, status)) break;
+        tc_fence_after();
+        const uint32_t a = sA + s * L::kA, lo = sLo + (u & 1) * L::kA, b = sB + s * kHalf;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+          if (D == 128) {
+            mma_bf16(tmem, mndesc(a, ks, kHalf), mndesc(b, ks, kHalf), iMM, 1);
+            mma_bf16(tmem, mndesc(lo, ks, kHalf), mndesc(b, ks, kHalf), iMM, 1);
+          } else {
+            mma_bf16(tmem, mndesc(a, ks, lo - a), mndesc(b, ks, kHalf), iMM, 1);  // rows: hi, then lo
+          }
+        }
+        mma_commit(&empty[s]);
+        mma_commit(&lo_free[u & 1]);
+        if (u & 1) mma_commit(x_full);
+      }
+      mma_commit(drain);
+      wait_drain(drain, 0, status);
+    }
+  } else if (warp < kWarpState) {
+    // weights: row r of the stage, half of its features (D = 128: one 64-wide block)
+    const int r = (threadIdx.x - kWarpXform * 32) & 63, half = (threadIdx.x - kWarpXform * 32) >> 6;
+    for (int u = 0; u < 2 * run; ++u) {
+      const int s = u % kStages, i = u >> 1;
+      bool ok = mbar_wait(&gate_full[i & 1], (i >> 1) & 1, abort_word, status);
+      ok = ok && mbar_wait(&full[s], (u / kStages) & 1, abort_word, status);
+      if (ok && u >= 2) ok = mbar_wait(&lo_free[u & 1], ((u >> 1) - 1) & 1, abort_word, status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const float *hi = gate + (i & 1) * 2 * kC, *lo = hi + kC;
+      const int t = (u & 1) * kSub + r;
+      const bool in = t < valid(i);
+      const float w = dir ? exp2f(hi[t] + lo[t]) : exp2f((hi[kC - 1] - hi[t]) + (lo[kC - 1] - lo[t]));
+      if (u & 1) mbar_arrive(&gate_free[i & 1]);
+      constexpr int kChunks = D / 16;  // 16-byte chunks per thread
+      const int blk = D == 128 ? half * kHalf : 0, c0 = D == 128 ? 0 : half * 4;
+      uint8_t *A = sm + L::A + s * L::kA + blk, *Lo = sm + L::Lo + (u & 1) * L::kA + blk;
+#pragma unroll
+      for (int e = 0; e < kChunks; ++e) {
+        const uint32_t off = sw128_offset(r, (c0 + e) * 8);
+        uint4 h = make_uint4(0u, 0u, 0u, 0u), l = h;
+        if (in) split8(*reinterpret_cast<const uint4 *>(A + off), w, h, l);
+        *reinterpret_cast<uint4 *>(A + off) = h;
+        *reinterpret_cast<uint4 *>(Lo + off) = l;
+      }
+      if (!in) {  // padding tokens: a zero weight does not clear a NaN of the other operand
+        uint8_t *B = sm + L::B + s * kHalf;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4 *>(B + sw128_offset(r, (half * 4 + e) * 8)) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_async_smem();
+      mbar_arrive(&done[s]);
+    }
+  } else if (warp < kWarpGate) {
+    const int q = warp & 3, T = q * 32 + lane;  // tensor-memory lane: a row of the state (D = 64: from 64 on, its low part)
+    const uint32_t tx = tmem + ((uint32_t)(q * 32) << 16);
+    const int row = D == 64 ? T & 63 : T;
+    const bool main_row = D == 128 || q < 2;
+    float *sum = reinterpret_cast<float *>(sm + L::Sum);
+    uint32_t r[32];
+    const long dd = (long)D * D;
+    const float *init = p.init[dir] ? p.init[dir] + (bh * p.segs + seg) * dd + (long)row * D + slice * 64 : nullptr;
+#pragma unroll
+    for (int cb = 0; cb < 2; ++cb) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (init && main_row) x = reinterpret_cast<const float4 *>(init + cb * 32)[e];
+        r[4 * e] = __float_as_uint(x.x), r[4 * e + 1] = __float_as_uint(x.y);
+        r[4 * e + 2] = __float_as_uint(x.z), r[4 * e + 3] = __float_as_uint(x.w);
+      }
+      tmem_st32(tx + cb * 32, r);
+    }
+    // D = 64: the two parts of columns [32 cb, 32 cb + 32) meet in the rows of the first two warps
+    auto join = [&](int cb) {
+      if (D == 128) return;
+      if (!main_row)
+#pragma unroll
+        for (int e = 0; e < 32; ++e) sum[row * 65 + cb * 32 + e] = __uint_as_float(r[e]);
+      named_bar(kBarState, 128);
+      if (main_row)
+#pragma unroll
+        for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) + sum[row * 65 + cb * 32 + e]);
+    };
+    bool ok = true;
+    for (int i = 0; i < nc && ok; ++i) {
+      bool w = i == 0 || mbar_wait(x_full, (i - 1) & 1, abort_word, status);
+      if (w && i < run) w = mbar_wait(&gate_full[i & 1], (i >> 1) & 1, abort_word, status);
+      if (bar_or(kBarState, 128, !w)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      float f = 1.f;
+      if (i < run) {
+        const float *hi = gate + (i & 1) * 2 * kC;
+        f = exp2f(hi[kC - 1] + hi[2 * kC - 1]);
+        mbar_arrive(&gate_free[i & 1]);
+      }
+#pragma unroll 1
+      for (int cb = 0; cb < 2; ++cb) {
+        tmem_ld32(tx + cb * 32, r);
+        if (i < run) {
+          uint32_t y[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) y[e] = r[e];
+          scale32(y, f);
+          tmem_st32(tx + cb * 32, y);
+        }
+        if (cb == 1 && i < run) {
+          tc_fence_before();
+          mbar_arrive(x_ready);
+        }
+        if (tiles) {
+          join(cb);
+          if (main_row) {
+            uint4 h[4], l[4];
+            split_bf16x32(r, h, l);
+            uint8_t *t = tiles + (bh * p.n + chunk(i)) * (size_t)(D * D * 4) + slice * (D * 128);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t off = sw128_offset(row, cb * 32 + e * 8);
+              *reinterpret_cast<uint4 *>(t + off) = h[e];
+              *reinterpret_cast<uint4 *>(t + D * D * 2 + off) = l[e];
+            }
+          }
+          if (D == 64) named_bar(kBarState, 128);  // the joined columns are read
+        }
+      }
+    }
+    if (fin && ok) {
+      const bool w = run == 0 || mbar_wait(x_full, (run - 1) & 1, abort_word, status);
+      if (!bar_or(kBarState, 128, !w)) {
+        tc_fence_after();
+        float *dst = fin + (bh * p.segs + seg) * dd + (long)row * D + slice * 64;
+#pragma unroll 1
+        for (int cb = 0; cb < 2; ++cb) {
+          tmem_ld32(tx + cb * 32, r);
+          join(cb);
+          if (main_row)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              reinterpret_cast<float4 *>(dst + cb * 32)[e] =
+                  make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]), __uint_as_float(r[4 * e + 2]),
+                              __uint_as_float(r[4 * e + 3]));
+        }
+      }
+    }
+  } else {
+    double total = 0.0;
+    for (int i = 0; i < run; ++i) {
+      if (i >= 2 && !warp_wait(&gate_free[i & 1], ((i >> 1) - 1) & 1, abort_word)) break;
+      float *hi = gate + (i & 1) * 2 * kC;
+      scan_gates(p.g + bh * p.N + chunk(i) * kC, valid(i), lane, hi, hi + kC);
+      __syncwarp();
+      total += (double)hi[kC - 1] + (double)hi[2 * kC - 1];
+      mbar_arrive(&gate_full[i & 1]);
+    }
+    if (p.seg_tot && fin && dir == 0 && slice == 0 && lane == 0) p.seg_tot[bh * p.segs + seg] = (float)total;
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 64);
+  }
+}
+
+__global__ void __launch_bounds__(128) gated_seg_scan_kernel(const __grid_constant__ GatedSegScan a) {
+  pdl_wait();
+  const int dir = blockIdx.z, parts = (a.dd / 4 + 127) / 128;
+  const long bh = blockIdx.x / parts;
+  const long e = ((blockIdx.x - bh * parts) * 128 + threadIdx.x) * 4L;
+  if (e >= a.dd) return;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (a.first[dir]) s = *reinterpret_cast<const float4 *>(a.first[dir] + bh * a.dd + e);
+  for (int i = 0; i < a.segs; ++i) {
+    const int g = dir ? a.segs - 1 - i : i;
+    float4 *at = reinterpret_cast<float4 *>(a.sums[dir] + (bh * a.segs + g) * a.dd + e);
+    const bool has = !(a.skip_last && i == a.segs - 1);
+    const float4 x = has ? *at : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float w = has ? exp2f(a.tot[bh * a.segs + g]) : 1.f;
+    *at = s;
+    s = make_float4(fmaf(w, s.x, x.x), fmaf(w, s.y, x.y), fmaf(w, s.z, x.z), fmaf(w, s.w, x.w));
+  }
+  if (a.last[dir]) *reinterpret_cast<float4 *>(a.last[dir] + bh * a.dd + e) = s;
+}
+
+template <int D>
+cudaError_t launch_t(const GatedStateParams &sp, long BH, int dirs, bool pdl, cudaStream_t stream) {
+  cudaError_t e = ensure_smem_optin((const void *)gated_state_tc_kernel<D>, (int)Lay<D>::Bytes);
+  if (e != cudaSuccess) return e;
+  LaunchTimer timer(kKGatedState, stream);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)(BH * sp.run_segs * (D / 64)), (unsigned)dirs);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Lay<D>::Bytes;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, gated_state_tc_kernel<D>, sp);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  timer.done(e);
+  if (e == cudaSuccess) count_launch();
+  return e;
+}
+
+}  // namespace
+
+bool gated_map(CUtensorMap *m, const void *base, long BH, long N, int D, uint32_t rows) {
+  auto fn = tensor_map_encoder();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)N, (cuuint64_t)BH};
+  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)N * D * 2};
+  cuuint32_t box[3] = {64, rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t launch_gated_states(const GatedStateParams &sp, int D, long BH, int dirs, bool pdl, cudaStream_t stream) {
+  return D == 64 ? launch_t<64>(sp, BH, dirs, pdl, stream) : launch_t<128>(sp, BH, dirs, pdl, stream);
+}
+
+cudaError_t read_and_clear_gated_state_status(unsigned int *value) {
+  return read_and_clear_status_word((const void *)&g_gated_status, value);
+}
+
+cudaError_t launch_gated_seg_scan(const GatedSegScan &a, long BH, int dirs, cudaStream_t stream) {
+  LaunchTimer timer(kKGatedState, stream);
+  gated_seg_scan_kernel<<<dim3((unsigned)(BH * ((a.dd / 4 + 127) / 128)), 1, (unsigned)dirs), 128, 0, stream>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  timer.done(e);
+  if (e == cudaSuccess) count_launch();
+  return e;
+}
+
+}  // namespace la

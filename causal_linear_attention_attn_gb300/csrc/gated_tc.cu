@@ -1,0 +1,489 @@
+// Gated linear attention on the sm_103a tensor cores (bf16, d_k = d_v = D in {64, 128}).
+//
+// A CTA owns a segment of one head and carries its state S through chunks of 128 tokens.  Per chunk
+// (local rows i, j; c the inclusive running sum of log2 decays, kept as hi + lo, see gated.cuh):
+//   P   = Q K^T                             fp32 in tensor memory
+//   P'  = bf16(2^{c_i - c_j} P), j <= i     one rounding; written back as the A operand
+//   O   = 2^{c_i} (Q bf16(S)) + P' V        two accumulators, joined when they are read
+//   S  <- 2^{c_T} S + (w k)^T V             w_j = 2^{c_T - c_j}; w k as a bf16 pair, S fp32
+// The outputs are bf16, so one rounding of the weights and of the state the queries read keeps their
+// error near the outputs' own; S is an fp32 result and takes its keys as a pair (2^-17).  Weighting
+// scores by differences of running sums (not queries and keys by their own) costs an exponential per
+// score, half of them masked, and holds for every decay: no factor exceeds 1.
+//
+// Long sequences with few heads are cut into segments; the state before each comes from the state
+// pass (gated_state_tc.cu) over the earlier ones and a scan over their sums.
+//
+// HBM bounds it (8 D bytes per token in and out, 40 flops a byte at D = 128): a chunk's loads take
+// about 5000 cycles of an SM's share, its longest chain (P, weights, P' V) about 2800.
+//
+// Warps: 0 TMA, 1 MMA and TMEM owner, 2-5 weights of the scores, 6-9 weighted keys, 10-13 state
+// (bf16 copy, decay), 14-17 outputs, 18 running sums.  Every wait is bounded (tc_ptx.cuh).
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "gated_tc.cuh"
+
+namespace la {
+namespace {
+using namespace gtc;
+
+constexpr int kThreads = 608;
+constexpr int kWarpK = 6, kWarpS = 10, kWarpO = 14, kWarpGate = 18;
+constexpr uint32_t kBarS = 1;
+
+template <int D>
+struct Lay {
+  static constexpr uint32_t kTile = D / 64 * kBlk;  // 128 tokens
+  static constexpr uint32_t Q = 0;
+  static constexpr uint32_t K = Q + kTile;
+  static constexpr uint32_t Klo = K + 2 * kTile;
+  static constexpr uint32_t V = Klo + kTile;
+  static constexpr uint32_t Sb = V + 2 * kTile;
+  static constexpr uint32_t Sum = Sb + D * D * 2;  // D = 64: low rows of the state [64][65] fp32
+  static constexpr uint32_t Gate = Sum + (D == 64 ? 64 * 65 * 4 : 0);
+  static constexpr uint32_t Bars = Gate + 2 * 2 * kC * 4;
+  static constexpr int kNumBars = 20;
+  static constexpr uint32_t Misc = Bars + kNumBars * 8;
+  static constexpr uint32_t Bytes = Misc + 16;
+};
+static_assert(Lay<128>::Bytes <= 232448, "shared memory budget");
+constexpr uint32_t kColS = 0, kColP = 128, kColI = 256, kColA = 384;  // state, scores, Q S, P' V
+
+struct Params {
+  CUtensorMap tq, tk, tv;  // boxes of 64 x 128
+  const float *g;
+  const int *lengths;
+  const float *init;  // state before each segment: [BH][init_segs][D][D], segment s at s * init_step; null: zero
+  __nv_bfloat16 *out;
+  float *S;
+  long N;
+  int H, segs, seg_chunks, init_segs, init_step;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_constant__ Params p) {
+  using L = Lay<D>;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  if (smem_u32(sm) & 1023u) {
+    if (threadIdx.x == 0) atomicOr(&g_gated_status, kAbortMisaligned);
+    return;
+  }
+  uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::Bars);
+  uint64_t *full_k = bars, *full_v = bars + 2, *kv_free = bars + 4, *gate_full = bars + 6, *gate_free = bars + 8,
+           *full_q = bars + 10, *q_free = bars + 11, *p_full = bars + 12, *k_ready = bars + 13, *pp_ready = bars + 14,
+           *sb_ready = bars + 15, *s_full = bars + 16, *o_full = bars + 17, *o_free = bars + 18, *drain = bars + 19;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::Misc);
+  volatile uint32_t *abort_word = reinterpret_cast<volatile uint32_t *>(sm + L::Misc + 4);
+  unsigned int *status = &g_gated_status;
+  float *gate = reinterpret_cast<float *>(sm + L::Gate);  // [2][hi 128, lo 128]
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long bh = blockIdx.x / p.segs;
+  const int seg = (int)(blockIdx.x - bh * p.segs);
+  const long len = row_length(p.lengths, bh / p.H, p.N);
+  const long nb = (len + kC - 1) / kC;
+  const long c_lo = min(nb, (long)seg * p.seg_chunks);
+  const int nc = (int)(min(nb, c_lo + p.seg_chunks) - c_lo);
+  auto valid = [&](int c) -> int { return (int)min((long)kC, len - (c_lo + c) * kC); };
+
+  if (threadIdx.x == 0) {
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&full_k[b], 1);
+      mbar_init(&full_v[b], 1);
+      mbar_init(&kv_free[b], 1);
+      mbar_init(&gate_full[b], 32);
+      mbar_init(&gate_free[b], 512);
+    }
+    mbar_init(full_q, 1);
+    mbar_init(q_free, 1);
+    mbar_init(p_full, 1);
+    mbar_init(k_ready, 128);
+    mbar_init(pp_ready, 128);
+    mbar_init(sb_ready, 128);
+    mbar_init(s_full, 1);
+    mbar_init(o_full, 1);
+    mbar_init(o_free, 128);
+    mbar_init(drain, 1);
+    *abort_word = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      prefetch_tmap(&p.tq);
+      prefetch_tmap(&p.tk);
+      prefetch_tmap(&p.tv);
+      auto load = [&](uint32_t at, const CUtensorMap *map, uint64_t *bar, int tok) {
+        mbar_arrive_expect_tx(bar, L::kTile);
+        for (int b = 0; b < D / 64; ++b) tma_load_3d(sm + at + b * kBlk, map, bar, 64 * b, tok, (int)bh);
+      };
+      int k_issued = 0, q_issued = 0;
+      for (int c = 0; c < nc; ++c) {
+        const int s = c & 1, tok = (int)((c_lo + c) * kC);
+        if (c >= 2 && !mbar_wait(&kv_free[s], ((c >> 1) - 1) & 1, abort_word, status)) break;
+        load(L::K + s * L::kTile, &p.tk, &full_k[s], tok);
+        load(L::V + s * L::kTile, &p.tv, &full_v[s], tok);
+        k_issued = c + 1;
+        if (c >= 1 && !mbar_wait(q_free, (c - 1) & 1, abort_word, status)) break;
+        load(L::Q, &p.tq, full_q, tok);
+        q_issued = c + 1;
+      }
+      for (int c = max(0, k_issued - 2); c < k_issued; ++c) {
+        wait_drain(&full_k[c & 1], (c >> 1) & 1, status);
+        wait_drain(&full_v[c & 1], (c >> 1) & 1, status);
+      }
+      if (q_issued) wait_drain(full_q, (q_issued - 1) & 1, status);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t iP = idesc_bf16_f32(128, 128, 0, 0), iO = idesc_bf16_f32(128, D, 0, 1),
+                         iS = idesc_bf16_f32(128, D, 1, 1);
+      constexpr int kDs = D / 16;
+      const uint32_t tS = tmem + kColS, tP = tmem + kColP, tI = tmem + kColI, tA = tmem + kColA;
+      const uint32_t sQ = smem_u32(sm + L::Q), sSb = smem_u32(sm + L::Sb), sKlo = smem_u32(sm + L::Klo);
+      for (int c = 0; c < nc; ++c) {
+        const int s = c & 1;
+        const uint32_t k = smem_u32(sm + L::K) + s * L::kTile, v = smem_u32(sm + L::V) + s * L::kTile;
+        if (!mbar_wait(full_q, c & 1, abort_word, status)) break;
+        if (!mbar_wait(&full_k[s], (c >> 1) & 1, abort_word, status)) break;
+        tc_fence_after();
+        // the scores' columns are free: the previous P' V reads them before, in issue order
+#pragma unroll 4
+        for (int ks = 0; ks < kDs; ++ks) mma_bf16(tP, kdesc(sQ, ks), kdesc(k, ks), iP, ks > 0);
+        mma_commit(p_full);
+        if (!mbar_wait(sb_ready, c & 1, abort_word, status)) break;
+        if (c > 0 && !mbar_wait(o_free, (c - 1) & 1, abort_word, status)) break;
+        tc_fence_after();
+#pragma unroll 4
+        for (int ks = 0; ks < kDs; ++ks) mma_bf16(tI, kdesc(sQ, ks), mndesc(sSb, ks), iO, ks > 0);
+        mma_commit(q_free);
+        if (!mbar_wait(k_ready, c & 1, abort_word, status)) break;
+        if (!mbar_wait(&full_v[s], (c >> 1) & 1, abort_word, status)) break;
+        tc_fence_after();
+#pragma unroll 4
+        for (int ks = 0; ks < 8; ++ks) {
+          if (D == 128) {
+            mma_bf16(tS, mndesc(k, ks), mndesc(v, ks), iS, 1);
+            mma_bf16(tS, mndesc(sKlo, ks), mndesc(v, ks), iS, 1);
+          } else {
+            mma_bf16(tS, mndesc(k, ks, sKlo - k), mndesc(v, ks), iS, 1);  // rows: hi, then lo
+          }
+        }
+        mma_commit(s_full);
+        if (!mbar_wait(pp_ready, c & 1, abort_word, status)) break;
+        tc_fence_after();
+#pragma unroll 4
+        for (int ks = 0; ks < 8; ++ks) mma_bf16_ts(tA, tP + 8 * ks, mndesc(v, ks), iO, ks > 0);
+        mma_commit(&kv_free[s]);
+        mma_commit(o_full);
+      }
+      mma_commit(drain);
+      wait_drain(drain, 0, status);
+    }
+  } else if (warp < kWarpK) {
+    // ---- weights of the scores: row i of this thread, keys in blocks of 32 ----
+    const int q = warp & 3, i = q * 32 + lane;
+    const uint32_t tP = tmem + ((uint32_t)(q * 32) << 16) + kColP;
+    for (int c = 0; c < nc; ++c) {
+      if (!warp_wait(&gate_full[c & 1], (c >> 1) & 1, abort_word)) break;
+      if (!warp_wait(p_full, c & 1, abort_word)) break;
+      tc_fence_after();
+      const float *hi = gate + (c & 1) * 2 * kC, *lo = hi + kC;
+      const float hi_i = hi[i], lo_i = lo[i];
+#pragma unroll 1
+      for (int cb = 0; cb < 4; ++cb) {
+        uint32_t o[16];
+        if (cb > q) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = 0u;
+        } else {
+          uint32_t r[32];
+          tmem_ld32(tP + cb * 32, r);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int j = cb * 32 + 4 * e;
+            const float4 h = *reinterpret_cast<const float4 *>(hi + j), l = *reinterpret_cast<const float4 *>(lo + j);
+            const float w[4] = {(hi_i - h.x) + (lo_i - l.x), (hi_i - h.y) + (lo_i - l.y), (hi_i - h.z) + (lo_i - l.z),
+                                (hi_i - h.w) + (lo_i - l.w)};
+            float x[4];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) x[m] = j + m <= i ? __uint_as_float(r[4 * e + m]) * ex2_approx(w[m]) : 0.f;
+            o[2 * e] = pack_bf16(x[0], x[1]);
+            o[2 * e + 1] = pack_bf16(x[2], x[3]);
+          }
+        }
+        tmem_st16(tP + cb * 16, o);
+      }
+      tc_fence_before();
+      mbar_arrive(pp_ready);
+      mbar_arrive(&gate_free[c & 1]);
+    }
+  } else if (warp < kWarpS) {
+    // ---- weighted keys as a pair: hi in place once Q K^T has read them, lo beside them ----
+    const int r = threadIdx.x - kWarpK * 32;
+    for (int c = 0; c < nc; ++c) {
+      const int s = c & 1;
+      if (!warp_wait(&gate_full[c & 1], (c >> 1) & 1, abort_word)) break;
+      const float *hi = gate + (c & 1) * 2 * kC, *lo = hi + kC;
+      const float w = exp2f((hi[kC - 1] - hi[r]) + (lo[kC - 1] - lo[r]));
+      const int tv = valid(c);
+      mbar_arrive(&gate_free[c & 1]);
+      if (!warp_wait(&full_k[s], (c >> 1) & 1, abort_word)) break;
+      if (!warp_wait(p_full, c & 1, abort_word)) break;
+      if (c > 0 && !warp_wait(s_full, (c - 1) & 1, abort_word)) break;  // the last low parts are read
+      uint8_t *K = sm + L::K + s * L::kTile, *Klo = sm + L::Klo;
+#pragma unroll 4
+      for (int e = 0; e < D / 8; ++e) {
+        const uint32_t off = (e >> 3) * kBlk + sw128_offset(r, (e & 7) * 8);
+        uint4 h = make_uint4(0u, 0u, 0u, 0u), l = h;
+        if (r < tv) split8(*reinterpret_cast<const uint4 *>(K + off), w, h, l);
+        *reinterpret_cast<uint4 *>(K + off) = h;
+        *reinterpret_cast<uint4 *>(Klo + off) = l;
+      }
+      if (tv < kC) {  // padding tokens: a zero weight does not clear a NaN of the values
+        if (!warp_wait(&full_v[s], (c >> 1) & 1, abort_word)) break;
+        uint8_t *V = sm + L::V + s * L::kTile;
+        if (r >= tv)
+          for (int e = 0; e < D / 8; ++e)
+            *reinterpret_cast<uint4 *>(V + (e >> 3) * kBlk + sw128_offset(r, (e & 7) * 8)) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_async_smem();
+      mbar_arrive(k_ready);
+    }
+  } else if (warp < kWarpO) {
+    // ---- state: bf16 copy for the queries, then decayed in place for the update ----
+    const int q = warp & 3, T = q * 32 + lane;
+    const int row = D == 64 ? T & 63 : T;
+    const bool main_row = D == 128 || q < 2;  // D = 64: lanes from 64 on hold the low keys' part
+    const uint32_t tS = tmem + ((uint32_t)(q * 32) << 16) + kColS;
+    float *sum = reinterpret_cast<float *>(sm + L::Sum);
+    uint32_t r[32];
+    const long dd = (long)D * D;
+    const float *init = p.init ? p.init + (bh * p.init_segs + (long)seg * p.init_step) * dd + (long)row * D : nullptr;
+    auto load_init = [&](int cb) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (init && main_row) x = reinterpret_cast<const float4 *>(init + cb * 32)[e];
+        r[4 * e] = __float_as_uint(x.x), r[4 * e + 1] = __float_as_uint(x.y);
+        r[4 * e + 2] = __float_as_uint(x.z), r[4 * e + 3] = __float_as_uint(x.w);
+      }
+    };
+    auto join = [&]() {  // D = 64: the two parts of 32 columns meet in the rows of the first two warps
+      if (D == 128) return;
+      if (!main_row)
+#pragma unroll
+        for (int e = 0; e < 32; ++e) sum[row * 65 + e] = __uint_as_float(r[e]);
+      named_bar(kBarS, 128);
+      if (main_row)
+#pragma unroll
+        for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) + sum[row * 65 + e]);
+      named_bar(kBarS, 128);
+    };
+    bool ok = true;
+    for (int c = 0; c < nc; ++c) {
+      bool w = mbar_wait(&gate_full[c & 1], (c >> 1) & 1, abort_word, status);
+      if (w && c > 0) w = mbar_wait(s_full, (c - 1) & 1, abort_word, status);
+      if (bar_or(kBarS, 128, !w)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const float *hi = gate + (c & 1) * 2 * kC;
+      const float f = exp2f(hi[kC - 1] + hi[2 * kC - 1]);
+      mbar_arrive(&gate_free[c & 1]);
+#pragma unroll 1
+      for (int cb = 0; cb < D / 32; ++cb) {
+        if (c == 0)
+          load_init(cb);
+        else
+          tmem_ld32(tS + cb * 32, r);
+        uint32_t y[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) y[e] = r[e];
+        scale32(y, f);
+        tmem_st32(tS + cb * 32, y);
+        join();
+        if (main_row) {
+          uint4 h[4];
+          to_bf16x32(r, h);
+          uint8_t *Sb = sm + L::Sb + (cb >> 1) * kBlk;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint4 *>(Sb + sw128_offset(row, (cb & 1) * 32 + 8 * e)) = h[e];
+        }
+      }
+      fence_async_smem();
+      tc_fence_before();
+      mbar_arrive(sb_ready);
+    }
+    if (seg == p.segs - 1 && ok) {
+      const bool w = nc == 0 || mbar_wait(s_full, (nc - 1) & 1, abort_word, status);
+      if (!bar_or(kBarS, 128, !w)) {
+        tc_fence_after();
+        float *dst = p.S + bh * dd + (long)row * D;
+#pragma unroll 1
+        for (int cb = 0; cb < D / 32; ++cb) {
+          if (nc == 0)
+            load_init(cb);
+          else
+            tmem_ld32(tS + cb * 32, r);
+          join();
+          if (main_row)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              reinterpret_cast<float4 *>(dst + cb * 32)[e] =
+                  make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]), __uint_as_float(r[4 * e + 2]),
+                              __uint_as_float(r[4 * e + 3]));
+        }
+      }
+    }
+  } else if (warp < kWarpGate) {
+    // ---- outputs: row i, 2^{c_i} (Q S) + P' V ----
+    const int q = warp & 3, i = q * 32 + lane;
+    const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16);
+    for (int c = 0; c < nc; ++c) {
+      if (!warp_wait(&gate_full[c & 1], (c >> 1) & 1, abort_word)) break;
+      const float *hi = gate + (c & 1) * 2 * kC;
+      const float f = exp2f(hi[i] + hi[kC + i]);
+      mbar_arrive(&gate_free[c & 1]);
+      if (!warp_wait(o_full, c & 1, abort_word)) break;
+      tc_fence_after();
+      const bool in = i < valid(c);
+      __nv_bfloat16 *dst = p.out + (bh * p.N + (c_lo + c) * kC + i) * D;
+#pragma unroll 1
+      for (int cb = 0; cb < D / 32; ++cb) {
+        uint32_t x[32], y[32];
+        tmem_ld32x2(tl + kColI + cb * 32, tl + kColA + cb * 32, x, y);
+        if (cb == D / 32 - 1) {
+          tc_fence_before();
+          mbar_arrive(o_free);
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float2 z = __ffma2_rn(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), make_float2(f, f),
+                                      make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])));
+          x[e] = pack_bf16(z.x, z.y);
+        }
+        if (in)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            reinterpret_cast<uint4 *>(dst + cb * 32)[e] = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+      }
+    }
+  } else {
+    for (int c = 0; c < nc; ++c) {
+      if (c >= 2 && !warp_wait(&gate_free[c & 1], ((c >> 1) - 1) & 1, abort_word)) break;
+      float *hi = gate + (c & 1) * 2 * kC;
+      scan_gates(p.g + bh * p.N + (c_lo + c) * kC, valid(c), lane, hi, hi + kC);
+      mbar_arrive(&gate_full[c & 1]);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// How a prefill is cut: G segments of seg_chunks chunks per head in the main pass; the states before
+// them come from sub-segments of seg_chunks / step chunks (the state pass's CTAs).
+struct Plan {
+  long n, G, seg_chunks, step;
+  long init_segs() const { return (G - 1) * step + 1; }
+  bool split() const { return G > 1; }
+};
+Plan make_plan(long BH, long N, int D) {
+  const long sms = std::max(1, device_info(-1).sm_count);
+  Plan t;
+  t.n = (N + kC - 1) / kC;
+  // enough CTAs to cover the SMs once, at least four chunks each: a segment costs a second reading of
+  // its keys and values
+  t.G = std::max(1L, std::min(sms / std::max(1L, BH), t.n / 4));
+  t.seg_chunks = (t.n + t.G - 1) / t.G;
+  // the state pass has two CTAs an SM: cut its segments finer while that fills them
+  t.step = 1;
+  if (t.G > 1) {
+    const long per = BH * (t.G - 1) * (D / 64);
+    while (per * t.step * 2 <= 2 * sms && t.seg_chunks / (t.step * 2) >= 2) t.step *= 2;
+    t.seg_chunks = (t.seg_chunks + t.step - 1) / t.step * t.step;
+    t.G = (t.n + t.seg_chunks - 1) / t.seg_chunks;
+    if (t.G == 1) t.step = 1;
+  }
+  return t;
+}
+
+template <int D>
+cudaError_t launch_main(const Params &mp, long BH, cudaStream_t stream) {
+  cudaError_t e = ensure_smem_optin((const void *)gated_tc_kernel<D>, (int)Lay<D>::Bytes);
+  if (e != cudaSuccess) return e;
+  LaunchTimer timer(kKGated, stream);
+  gated_tc_kernel<D><<<(unsigned)(BH * mp.segs), kThreads, Lay<D>::Bytes, stream>>>(mp);
+  e = cudaGetLastError();
+  timer.done(e);
+  if (e == cudaSuccess) count_launch();
+  return e;
+}
+
+}  // namespace
+
+bool gated_tc_supported(int dk, int dv, la_dtype dt) {
+  if (dt != LA_BF16 || dk != dv || (dk != 64 && dk != 128)) return false;
+  const DeviceInfo di = device_info(-1);
+  return di.cc_major == 10 && di.cc_minor == 3 && tensor_map_encoder() != nullptr;
+}
+
+cudaError_t read_and_clear_gated_status(unsigned int *value) {
+  return read_and_clear_status_word((const void *)&g_gated_status, value);
+}
+
+size_t gated_tc_prefill_workspace(long BH, long N, int D) {
+  const Plan t = make_plan(BH, N, D);
+  return t.split() ? sizeof(float) * (size_t)BH * t.init_segs() * ((size_t)D * D + 1) : 16;
+}
+
+cudaError_t launch_gated_tc(const GatedProblem &p) {
+  const int D = p.dk;
+  const long BH = p.BH();
+  const Plan t = make_plan(BH, p.N, D);
+  Params mp;
+  memset(&mp, 0, sizeof mp);
+  if (!gated_map(&mp.tq, p.q, BH, p.N, D, kC) || !gated_map(&mp.tk, p.k, BH, p.N, D, kC) ||
+      !gated_map(&mp.tv, p.v, BH, p.N, D, kC))
+    return cudaErrorInvalidValue;
+  mp.g = p.g, mp.lengths = p.lengths, mp.out = (__nv_bfloat16 *)p.out, mp.S = p.S, mp.N = p.N, mp.H = p.H;
+  mp.segs = (int)t.G, mp.seg_chunks = (int)t.seg_chunks, mp.init_segs = 1, mp.init_step = 0;
+  mp.init = p.S0;
+  cudaError_t e = cudaSuccess;
+  if (t.split()) {
+    float *sums = (float *)p.ws, *tot = sums + (size_t)BH * t.init_segs() * D * D;
+    GatedStateParams sp;
+    memset(&sp, 0, sizeof sp);
+    if (!gated_map(&sp.ta[0], p.k, BH, p.N, D, 64) || !gated_map(&sp.tb[0], p.v, BH, p.N, D, 64))
+      return cudaErrorInvalidValue;
+    sp.g = p.g, sp.lengths = p.lengths, sp.N = p.N, sp.n = t.n, sp.H = p.H;
+    sp.segs = (int)t.init_segs(), sp.run_segs = sp.segs - 1, sp.seg_chunks = (int)(t.seg_chunks / t.step);
+    sp.fin[0] = sums, sp.seg_tot = tot;
+    e = launch_gated_states(sp, D, BH, 1, false, p.stream);
+    if (e != cudaSuccess) return e;
+    GatedSegScan sc = {};
+    sc.sums[0] = sums, sc.tot = tot, sc.first[0] = p.S0, sc.segs = sp.segs, sc.dd = D * D, sc.skip_last = true;
+    e = launch_gated_seg_scan(sc, BH, 1, p.stream);
+    if (e != cudaSuccess) return e;
+    mp.init = sums, mp.init_segs = sp.segs, mp.init_step = (int)t.step;
+  }
+  return D == 64 ? launch_main<64>(mp, BH, p.stream) : launch_main<128>(mp, BH, p.stream);
+}
+
+}  // namespace la

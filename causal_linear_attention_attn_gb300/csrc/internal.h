@@ -157,6 +157,16 @@ size_t gated_simt_workspace(long BH, long N, int dk, int dv, bool grad);
 cudaError_t launch_gated_simt(const GatedProblem &p);
 cudaError_t launch_gated_grad_simt(const GatedGradProblem &b);
 
+// The same on the tensor cores (bf16, d_k = d_v in {64, 128}, sm_103).
+bool gated_tc_supported(int dk, int dv, la_dtype dt);
+size_t gated_tc_prefill_workspace(long BH, long N, int d);
+size_t gated_tc_grad_workspace(long BH, long N, int d);
+cudaError_t launch_gated_tc(const GatedProblem &p);
+cudaError_t launch_gated_grad_tc(const GatedGradProblem &b);
+cudaError_t read_and_clear_gated_state_status(unsigned int *value);
+cudaError_t read_and_clear_gated_status(unsigned int *value);
+cudaError_t read_and_clear_gated_grad_status(unsigned int *value);
+
 // One recurrent step of the gated form per (row, head): row b works on state slots[b] of the
 // pool S ([n_slots][H][dk][dv]); see la_gated_decode_step.
 struct GatedStepProblem {
