@@ -1,0 +1,609 @@
+// Gradient of gated linear attention on the sm_103a tensor cores (bf16, d_k = d_v = D in {64, 128}).
+//
+// The state pass (gated_state_tc.cu) leaves, for every chunk of 128 tokens, the state S before it and
+// the gradient R of the state behind it, both as bf16 pairs.  Then every chunk is independent; one
+// CTA takes one chunk at a time.  With W_ij = 2^{c_i - c_j} for j <= i, else 0:
+//   P^T = K Q^T,  D^T = V dO^T                              fp32 in tensor memory, keys in the lanes
+//   dQ  = 2^{c_i} (dO S^T)        + (W D) K
+//   dK  = 2^{c_T - c_j} (V R^T)   + (W D)^T Q
+//   dV  = 2^{c_T - c_j} (K R)     + (W P)^T dO
+//   dg_t = sum_{j < t <= i} W_ij P_ij D_ij + sum_{i >= t} q_i . [2^{c_i} S do_i]
+//          + sum_{j < t} k_j . [2^{c_T - c_j} R v_j] + 2^{c_T} <S, R>
+// dg is an fp32 result: its first term comes from the fp32 products before any rounding, the next
+// two from dQ's and dK's first products, which take S and R as pairs, the last from the stored pairs.
+// No term is a difference of larger ones, and no error is carried from chunk to chunk.  dQ, dK and dV
+// are bf16: W D, W P and dV's R are rounded to bf16 once.
+//
+// Tensor memory holds P^T and D^T, dQ and dK; W P overwrites P^T and dV takes D^T's columns.  The
+// first products are scaled by row in tensor memory, then the second ones accumulate on top.
+// HBM bounds it at 14 D bytes a token of inputs and results plus 8 D of states (D = 128: 8.1 us a
+// chunk at an SM's share); the tensor work is 13 products of 128 x 128 x D.
+//
+// Warps: 0 TMA, 1 MMA and TMEM owner, 2 running sums and dg, 3-6 <S, R>, 7-14 everything elementwise.
+// Every wait is bounded (tc_ptx.cuh).
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "gated_tc.cuh"
+
+namespace la {
+namespace {
+using namespace gtc;
+
+constexpr int kThreads = 480;
+constexpr int kWarpGate = 2, kWarpDot = 3, kWarpEl = 7;
+constexpr int kElThreads = 256;
+constexpr uint32_t kBarEl = 1;
+constexpr int kRing = 3;
+
+template <int D>
+struct Lay {
+  static constexpr uint32_t kTile = D / 64 * kBlk;  // 128 tokens
+  static constexpr uint32_t kState = D * D * 2;     // S or R, hi or lo
+  static constexpr uint32_t Q = 0;
+  static constexpr uint32_t K = Q + kTile;
+  static constexpr uint32_t dO = K + kTile;
+  static constexpr uint32_t V = dO + kTile;
+  static constexpr uint32_t Ring = V + kTile;
+  // W D [keys][queries] bf16: in V's place once V's products are done, if it fits there
+  static constexpr uint32_t WD = D == 128 ? V : Ring + kRing * kState;
+  static constexpr uint32_t Gate = Ring + kRing * kState + (D == 128 ? 0 : 2 * kBlk);  // hi 128, lo 128
+  static constexpr uint32_t Buf = Gate + 2 * kC * 4;                                   // 320 floats
+  static constexpr uint32_t Red = Buf + 320 * 4;                                       // 4 floats
+  static constexpr uint32_t Bars = Red + 16;
+  static constexpr int kNumBars = 2 + 2 * kRing + 13;
+  static constexpr uint32_t Misc = Bars + kNumBars * 8;
+  static constexpr uint32_t Bytes = Misc + 16;
+};
+static_assert(Lay<128>::Bytes <= 232448, "shared memory budget");
+constexpr uint32_t kColP = 0, kColD = 128, kColQ = 256, kColK = 384;  // dV in D's columns
+
+struct Params {
+  CUtensorMap tq, tk, tv, td;  // boxes of 64 x 128
+  const float *g;
+  const int *lengths;
+  const uint8_t *s_tiles, *r_tiles;
+  __nv_bfloat16 *dq, *dk, *dv;
+  float *dg;
+  long N, n, items;
+  int H;
+};
+
+// Partial row sums of key rows [32 q, 32 q + 32) over queries i >= 32 q, packed.
+__device__ __forceinline__ int part_at(int q, int i) { return q * 128 - 16 * q * (q - 1) + i - 32 * q; }
+
+// Sum over the warp's lanes of x[c], returned by lane c.
+__device__ __forceinline__ float column_sums(float (&x)[32], int lane) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < o; ++k) {
+      const bool up = lane & o;
+      const float give = up ? x[k] : x[k + o], keep = up ? x[k + o] : x[k];
+      x[k] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+  return x[0];
+}
+
+// Dot of 32 fp32 values (raw bits) with 32 bf16 values of a swizzled row.
+__device__ __forceinline__ float dot_row32(const uint32_t (&r)[32], const uint8_t *blk, int row, int col0) {
+  float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint4 x = *reinterpret_cast<const uint4 *>(blk + sw128_offset(row, col0 + 8 * e));
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+      s = __ffma2_rn(make_float2(__uint_as_float(w[m] << 16), __uint_as_float(w[m] & 0xffff0000u)),
+                     make_float2(__uint_as_float(r[8 * e + 2 * m]), __uint_as_float(r[8 * e + 2 * m + 1])), s);
+  }
+  return s.x + s.y;
+}
+
+__device__ __forceinline__ float dot_pairs(uint4 ah, uint4 al, uint4 bh, uint4 bl, float s) {
+  const uint32_t a[4] = {ah.x, ah.y, ah.z, ah.w}, b[4] = {al.x, al.y, al.z, al.w}, c[4] = {bh.x, bh.y, bh.z, bh.w},
+                 d[4] = {bl.x, bl.y, bl.z, bl.w};
+  float2 t = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    auto f2 = [](uint32_t w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); };
+    t = __ffma2_rn(__fadd2_rn(f2(a[e]), f2(b[e])), __fadd2_rn(f2(c[e]), f2(d[e])), t);
+  }
+  return s + (t.x + t.y);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid_constant__ Params p) {
+  using L = Lay<D>;
+  constexpr uint32_t kState = L::kState;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  if (smem_u32(sm) & 1023u) {
+    if (threadIdx.x == 0) atomicOr(&g_gated_status, kAbortMisaligned);
+    return;
+  }
+  uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::Bars);
+  uint64_t *full_kq = bars, *full_vd = bars + 1, *ring_full = bars + 2, *ring_free = ring_full + kRing,
+           *b0 = ring_free + kRing, *tok_free = b0, *gate_full = b0 + 1, *e_full = b0 + 2, *el_done = b0 + 3,
+           *q_in = b0 + 4, *k_in = b0 + 5, *v_in = b0 + 6, *x_ready = b0 + 7, *out_full = b0 + 8, *out_free = b0 + 9,
+           *dg_in = b0 + 10, *dot_full = b0 + 11, *dot_free = b0 + 12;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::Misc);
+  volatile uint32_t *abort_word = reinterpret_cast<volatile uint32_t *>(sm + L::Misc + 4);
+  uint64_t *drain = reinterpret_cast<uint64_t *>(sm + L::Misc + 8);
+  unsigned int *status = &g_gated_status;
+  float *hi = reinterpret_cast<float *>(sm + L::Gate), *lo = hi + kC;
+  float *buf = reinterpret_cast<float *>(sm + L::Buf), *red = reinterpret_cast<float *>(sm + L::Red);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    mbar_init(full_kq, 1);
+    mbar_init(full_vd, 1);
+    for (int s = 0; s < kRing; ++s) {
+      mbar_init(&ring_full[s], 1);
+      mbar_init(&ring_free[s], 1);
+    }
+    mbar_init(tok_free, 1);
+    mbar_init(gate_full, 32);
+    mbar_init(e_full, 1);
+    mbar_init(el_done, kElThreads);
+    mbar_init(q_in, 1);
+    mbar_init(k_in, 1);
+    mbar_init(v_in, 1);
+    mbar_init(x_ready, kElThreads);
+    mbar_init(out_full, 1);
+    mbar_init(out_free, kElThreads);
+    mbar_init(dg_in, 128);
+    mbar_init(dot_full, 4);
+    mbar_init(dot_free, 32);
+    mbar_init(drain, 1);
+    *abort_word = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();  // the states are the previous kernel's
+
+  // every role walks over the same chunks; `it` counts those with tokens
+  struct Item {
+    long bh, t0;
+    int tv;
+  };
+  auto item = [&](long x) -> Item {
+    Item r;
+    r.bh = x / p.n;
+    r.t0 = (x - r.bh * p.n) * kC;
+    const long len = row_length(p.lengths, r.bh / p.H, p.N);
+    r.tv = (int)max(0L, min((long)kC, len - r.t0));
+    return r;
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int it = 0, ring = 0;
+      bool kq = false, vd = false, ok = true;
+      auto piece = [&](const uint8_t *src) {
+        const int s = ring % kRing;
+        if (ring >= kRing) ok = ok && mbar_wait(&ring_free[s], (ring / kRing - 1) & 1, abort_word, status);
+        if (!ok) return;
+        mbar_arrive_expect_tx(&ring_full[s], kState);
+        bulk_load(sm + L::Ring + s * kState, src, kState, &ring_full[s]);
+        ++ring;
+      };
+      auto tile = [&](uint32_t at, const CUtensorMap *map, uint64_t *bar, const Item &w) {
+        for (int b = 0; b < D / 64; ++b) tma_load_3d(sm + at + b * kBlk, map, bar, 64 * b, (int)w.t0, (int)w.bh);
+      };
+      for (long x = blockIdx.x; x < p.items && ok; x += gridDim.x) {
+        const Item w = item(x);
+        if (w.tv == 0) continue;
+        const uint8_t *S = p.s_tiles + x * (size_t)(2 * kState), *R = p.r_tiles + x * (size_t)(2 * kState);
+        piece(S);
+        piece(S + kState);
+        piece(R);
+        if (ok && it > 0) ok = mbar_wait(tok_free, (it - 1) & 1, abort_word, status);
+        if (!ok) break;
+        kq = vd = true;
+        mbar_arrive_expect_tx(full_kq, 2 * L::kTile);
+        tile(L::K, &p.tk, full_kq, w);
+        tile(L::Q, &p.tq, full_kq, w);
+        mbar_arrive_expect_tx(full_vd, 2 * L::kTile);
+        tile(L::V, &p.tv, full_vd, w);
+        tile(L::dO, &p.td, full_vd, w);
+        ++it;
+        piece(R + kState);
+      }
+      for (int r = max(0, ring - kRing); r < ring; ++r) wait_drain(&ring_full[r % kRing], (r / kRing) & 1, status);
+      if (kq) wait_drain(full_kq, (it - 1) & 1, status);
+      if (vd) wait_drain(full_vd, (it - 1) & 1, status);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t iE = idesc_bf16_f32(128, 128, 0, 0), iKK = idesc_bf16_f32(128, D, 0, 0),
+                         iKM = idesc_bf16_f32(128, D, 0, 1), iMM = idesc_bf16_f32(128, D, 1, 1);
+      constexpr int kDs = D / 16;
+      const uint32_t tP = tmem + kColP, tD = tmem + kColD, tQ = tmem + kColQ, tK = tmem + kColK;
+      const uint32_t sQ = smem_u32(sm + L::Q), sK = smem_u32(sm + L::K), sV = smem_u32(sm + L::V),
+                     sO = smem_u32(sm + L::dO), sW = smem_u32(sm + L::WD), sR = smem_u32(sm + L::Ring);
+      int it = 0, ring = 0;
+      for (long x = blockIdx.x; x < p.items; x += gridDim.x) {
+        if (item(x).tv == 0) continue;
+        const uint32_t ph = it & 1;
+        auto wait_ring = [&]() { return mbar_wait(&ring_full[ring % kRing], (ring / kRing) & 1, abort_word, status); };
+        if (!mbar_wait(gate_full, ph, abort_word, status)) break;
+        if (it > 0 && !mbar_wait(out_free, ph ^ 1, abort_word, status)) break;
+        if (!mbar_wait(full_kq, ph, abort_word, status)) break;
+        tc_fence_after();
+#pragma unroll 4
+        for (int ks = 0; ks < kDs; ++ks) mma_bf16(tP, kdesc(sK, ks), kdesc(sQ, ks), iE, ks > 0);
+        if (!mbar_wait(full_vd, ph, abort_word, status)) break;
+#pragma unroll 4
+        for (int ks = 0; ks < kDs; ++ks) mma_bf16(tD, kdesc(sV, ks), kdesc(sO, ks), iE, ks > 0);
+        mma_commit(e_full);
+        // dQ = dO S^T, both parts of S
+        bool ok = true;
+        for (int part = 0; part < 2 && ok; ++part) {
+          ok = wait_ring();
+          if (!ok) break;
+          const uint32_t st = sR + (ring % kRing) * kState;
+#pragma unroll 4
+          for (int ks = 0; ks < kDs; ++ks) mma_bf16(tQ, kdesc(sO, ks), kdesc(st, ks, D * 128), iKK, part | (ks > 0));
+          mma_commit(&ring_free[ring % kRing]);
+          ++ring;
+        }
+        if (!ok) break;
+        mma_commit(q_in);
+        // dK = V R^T; R's high part stays for dV
+        if (!wait_ring()) break;
+        const uint32_t r_hi = sR + (ring % kRing) * kState;
+        uint64_t *r_hi_free = &ring_free[ring % kRing];
+        ++ring;
+#pragma unroll 4
+        for (int ks = 0; ks < kDs; ++ks) mma_bf16(tK, kdesc(sV, ks), kdesc(r_hi, ks, D * 128), iKK, ks > 0);
+        if (!wait_ring()) break;
+        const uint32_t r_lo = sR + (ring % kRing) * kState;
+#pragma unroll 4
+        for (int ks = 0; ks < kDs; ++ks) mma_bf16(tK, kdesc(sV, ks), kdesc(r_lo, ks, D * 128), iKK, 1);
+        mma_commit(&ring_free[ring % kRing]);
+        ++ring;
+        mma_commit(k_in);
+        // dV = K R, over D^T once that is read
+        if (!mbar_wait(el_done, ph, abort_word, status)) break;
+        tc_fence_after();
+#pragma unroll 4
+        for (int ks = 0; ks < kDs; ++ks) mma_bf16(tD, kdesc(sK, ks), mndesc(r_hi, ks, D * 128), iKM, ks > 0);
+        mma_commit(r_hi_free);
+        mma_commit(v_in);
+        if (!mbar_wait(x_ready, ph, abort_word, status)) break;
+        tc_fence_after();
+#pragma unroll 4
+        for (int ks = 0; ks < 8; ++ks)  // queries [16 ks, ..): columns 8 ks of the first or the second half
+          mma_bf16_ts(tD, tP + (ks < 4 ? 8 * ks : 32 + 8 * ks), mndesc(sO, ks), iKM, 1);
+#pragma unroll 4
+        for (int ks = 0; ks < 8; ++ks) mma_bf16(tK, kdesc(sW, ks), mndesc(sQ, ks), iKM, 1);
+#pragma unroll 4
+        for (int ks = 0; ks < 8; ++ks) mma_bf16(tQ, mndesc(sW, ks), mndesc(sK, ks), iMM, 1);
+        mma_commit(tok_free);
+        mma_commit(out_full);
+        ++it;
+      }
+      mma_commit(drain);
+      wait_drain(drain, 0, status);
+    }
+  } else if (warp == kWarpGate) {
+    // ---- running sums for the next chunk, dg of the current one ----
+    int it = 0;
+    auto gates = [&](const Item &w) -> bool {
+      scan_gates(p.g + w.bh * p.N + w.t0, w.tv, lane, hi, lo);
+      if (p.lengths && w.tv < kC) {
+        // padding tokens are contracted over: clear whatever they hold
+        if (!warp_wait(full_kq, it & 1, abort_word) || !warp_wait(full_vd, it & 1, abort_word)) return false;
+        for (int e = w.tv * (D / 8) + lane; e < kC * (D / 8); e += 32) {
+          const int row = e / (D / 8), ch = e % (D / 8);
+          const uint32_t off = (ch >> 3) * kBlk + sw128_offset(row, (ch & 7) * 8);
+          const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4 *>(sm + L::Q + off) = z;
+          *reinterpret_cast<uint4 *>(sm + L::K + off) = z;
+          *reinterpret_cast<uint4 *>(sm + L::V + off) = z;
+          *reinterpret_cast<uint4 *>(sm + L::dO + off) = z;
+        }
+        fence_async_smem();
+      }
+      __syncwarp();
+      mbar_arrive(gate_full);
+      return true;
+    };
+    auto next = [&](long x) -> long {
+      while (x < p.items && item(x).tv == 0) x += gridDim.x;
+      return x;
+    };
+    long x = next(blockIdx.x);
+    bool ok = x < p.items && gates(item(x));
+    while (ok && x < p.items) {
+      const Item w = item(x);
+      const float total = exp2f(hi[kC - 1] + lo[kC - 1]);
+      if (!warp_wait(dg_in, it & 1, abort_word) || !warp_wait(dot_full, it & 1, abort_word)) break;
+      const float4 e4 = *reinterpret_cast<const float4 *>(buf + 4 * lane);
+      const float4 r4 = *reinterpret_cast<const float4 *>(buf + kC + 4 * lane);
+      const double over = (double)total * ((red[0] + red[1]) + (red[2] + red[3]));
+      __syncwarp();
+      mbar_arrive(dot_free);
+      // suffix sums of what queries at or behind t add, prefix sums of what keys before t add
+      double e[4] = {e4.x, e4.y, e4.z, e4.w}, r[4] = {r4.x, r4.y, r4.z, r4.w};
+#pragma unroll
+      for (int m = 2; m >= 0; --m) e[m] += e[m + 1];
+      double behind = e[0];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double y = __shfl_down_sync(0xffffffffu, behind, o);
+        if (lane + o < 32) behind += y;
+      }
+      behind -= e[0];
+      const double mine = (r[0] + r[1]) + (r[2] + r[3]);
+      double before = warp_scan(mine, lane) - mine;
+      float *dg = p.dg + w.bh * p.N + w.t0;
+      const int rows = (int)min((long)kC, p.N - w.t0);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const int t = 4 * lane + m;
+        if (t < rows) dg[t] = t < w.tv ? (float)(e[m] + behind + before + over) : 0.f;
+        before += r[m];
+      }
+      ++it;
+      x = next(x + gridDim.x);
+      if (x < p.items) ok = gates(item(x));
+    }
+  } else if (warp < kWarpEl) {
+    // ---- <S, R> of the stored pairs ----
+    int it = 0;
+    for (long x = blockIdx.x; x < p.items; x += gridDim.x) {
+      if (item(x).tv == 0) continue;
+      const uint4 *S = reinterpret_cast<const uint4 *>(p.s_tiles + x * (size_t)(2 * kState));
+      const uint4 *R = reinterpret_cast<const uint4 *>(p.r_tiles + x * (size_t)(2 * kState));
+      constexpr int kQ = kState / 16;
+      float s = 0.f;
+#pragma unroll 4
+      for (int e = threadIdx.x - kWarpDot * 32; e < kQ; e += 128) s = dot_pairs(S[e], S[e + kQ], R[e], R[e + kQ], s);
+      s = warp_sum(s);
+      if (it > 0 && !warp_wait(dot_free, (it - 1) & 1, abort_word)) break;
+      if (lane == 0) {
+        red[warp - kWarpDot] = s;
+        mbar_arrive(dot_full);
+      }
+      ++it;
+    }
+  } else {
+    // ---- elementwise: weights, row scales, results ----
+    const int q = warp & 3, half = (warp - kWarpEl) >> 2, T = q * 32 + lane;
+    const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16);
+    constexpr int kCols = D / 64;  // 32-column blocks of dQ, dK, dV per thread
+    int it = 0;
+    for (long x = blockIdx.x; x < p.items; x += gridDim.x) {
+      const Item w = item(x);
+      const int rows = (int)min((long)kC, p.N - w.t0);
+      const long at = (w.bh * p.N + w.t0 + T) * D + half * (D / 2);
+      auto put = [&](__nv_bfloat16 *dst, int cb, const uint4 (&v)[4], bool in) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          reinterpret_cast<uint4 *>(dst + at + cb * 32)[e] = in ? v[e] : make_uint4(0u, 0u, 0u, 0u);
+      };
+      if (w.tv == 0) {  // padding only
+        const uint4 z[4] = {};
+        if (T < rows)
+          for (int cb = 0; cb < kCols; ++cb) put(p.dq, cb, z, false), put(p.dk, cb, z, false), put(p.dv, cb, z, false);
+        if (half == 0 && T < rows) p.dg[w.bh * p.N + w.t0 + T] = 0.f;
+        continue;
+      }
+      const uint32_t ph = it & 1;
+      bool ok = mbar_wait(gate_full, ph, abort_word, status) && mbar_wait(e_full, ph, abort_word, status);
+      if (bar_or(kBarEl, kElThreads, !ok)) break;
+      tc_fence_after();
+      // key T (lane) against queries i: W P to tensor memory, W D to shared memory, and W P D's sums
+      const float hi_j = hi[T], lo_j = lo[T];
+      float col = 0.f;
+      uint32_t wd[2][16];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int ib = 2 * half + b;
+        uint32_t o[16];
+        if (ib < q) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = wd[b][e] = 0u;
+        } else {
+          uint32_t pr[32], dr[32];
+          tmem_ld32x2(tl + kColP + ib * 32, tl + kColD + ib * 32, pr, dr);
+          float m[32];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int i0 = ib * 32 + 4 * e;
+            const float4 h = *reinterpret_cast<const float4 *>(hi + i0), l = *reinterpret_cast<const float4 *>(lo + i0);
+            const float y[4] = {(h.x - hi_j) + (l.x - lo_j), (h.y - hi_j) + (l.y - lo_j), (h.z - hi_j) + (l.z - lo_j),
+                                (h.w - hi_j) + (l.w - lo_j)};
+            float pw[4], dw[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int i = i0 + k;
+              const float f = ex2_approx(y[k]), pp = __uint_as_float(pr[4 * e + k]);
+              pw[k] = i >= T ? pp * f : 0.f;
+              dw[k] = i >= T ? __uint_as_float(dr[4 * e + k]) * f : 0.f;
+              m[4 * e + k] = i > T ? pp * dw[k] : 0.f;
+              col += m[4 * e + k];
+            }
+            o[2 * e] = pack_bf16(pw[0], pw[1]);
+            o[2 * e + 1] = pack_bf16(pw[2], pw[3]);
+            wd[b][2 * e] = pack_bf16(dw[0], dw[1]);
+            wd[b][2 * e + 1] = pack_bf16(dw[2], dw[3]);
+          }
+          buf[part_at(q, ib * 32 + lane)] = column_sums(m, lane);
+        }
+        tmem_st16(tl + kColP + 64 * half + 16 * b, o);  // over columns this warp alone reads
+      }
+      tc_fence_before();
+      mbar_arrive(el_done);
+      ok = mbar_wait(k_in, ph, abort_word, status) && mbar_wait(q_in, ph, abort_word, status);
+      if (bar_or(kBarEl, kElThreads, !ok)) break;  // and the partial sums are complete
+      tc_fence_after();
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          *reinterpret_cast<uint4 *>(sm + L::WD + half * kBlk + sw128_offset(T, b * 32 + 8 * e)) =
+              make_uint4(wd[b][4 * e], wd[b][4 * e + 1], wd[b][4 * e + 2], wd[b][4 * e + 3]);
+      float ends = -col, rgt = 0.f;  // what this token adds as a query (dg_t, t <= T) and as a key (t > T)
+      if (half == 0)
+        for (int k = 0; k <= q; ++k) ends += buf[part_at(k, T)];
+      const float ec = exp2f(hi_j + lo_j), ew = exp2f((hi[kC - 1] - hi_j) + (lo[kC - 1] - lo_j));
+#pragma unroll
+      for (int cb = 0; cb < kCols; ++cb) {
+        const int c0 = half * (D / 2) + cb * 32;
+        uint32_t r[32];
+        tmem_ld32(tl + kColQ + c0, r);
+        scale32(r, ec);
+        ends += dot_row32(r, sm + L::Q + (c0 >> 6) * kBlk, T, c0 & 63);
+        tmem_st32(tl + kColQ + c0, r);
+        tmem_ld32(tl + kColK + c0, r);
+        scale32(r, ew);
+        rgt += dot_row32(r, sm + L::K + (c0 >> 6) * kBlk, T, c0 & 63);
+        tmem_st32(tl + kColK + c0, r);
+      }
+      ok = mbar_wait(v_in, ph, abort_word, status);
+      if (bar_or(kBarEl, kElThreads, !ok)) break;  // and the partial sums are read
+      tc_fence_after();
+#pragma unroll
+      for (int cb = 0; cb < kCols; ++cb) {
+        uint32_t r[32];
+        tmem_ld32(tl + kColD + half * (D / 2) + cb * 32, r);
+        scale32(r, ew);
+        tmem_st32(tl + kColD + half * (D / 2) + cb * 32, r);
+      }
+      fence_async_smem();
+      tc_fence_before();
+      mbar_arrive(x_ready);
+      if (half == 1) buf[T] = ends, buf[kC + T] = rgt;
+      named_bar(kBarEl, kElThreads);
+      if (half == 0) {
+        buf[T] += ends;
+        buf[kC + T] += rgt;
+        mbar_arrive(dg_in);
+      }
+      ok = mbar_wait(out_full, ph, abort_word, status);
+      if (bar_or(kBarEl, kElThreads, !ok)) break;
+      tc_fence_after();
+      const bool in = T < w.tv;
+#pragma unroll
+      for (int cb = 0; cb < kCols; ++cb) {
+        const uint32_t c0 = half * (D / 2) + cb * 32;
+        uint32_t r[32];
+        uint4 v[4];
+        tmem_ld32(tl + kColQ + c0, r);
+        to_bf16x32(r, v);
+        if (T < rows) put(p.dq, cb, v, in);
+        tmem_ld32(tl + kColK + c0, r);
+        to_bf16x32(r, v);
+        if (T < rows) put(p.dk, cb, v, in);
+        tmem_ld32(tl + kColD + c0, r);
+        to_bf16x32(r, v);
+        if (T < rows) put(p.dv, cb, v, in);
+      }
+      tc_fence_before();
+      mbar_arrive(out_free);
+      ++it;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Segments of the state pass: it has two CTAs an SM, D / 64 per head and direction; few heads are cut
+// further (the sums of the segments first, then the states), down to four chunks a segment.
+struct Plan {
+  long n, segs, seg_chunks;
+};
+Plan make_plan(long BH, long N, int D) {
+  const long slots = 2L * std::max(1, device_info(-1).sm_count), ctas = BH * (D / 64) * 2;
+  Plan t;
+  t.n = (N + kC - 1) / kC;
+  t.segs = std::max(1L, std::min(slots / std::max(1L, ctas), t.n / 4));
+  t.seg_chunks = (t.n + t.segs - 1) / t.segs;
+  t.segs = (t.n + t.seg_chunks - 1) / t.seg_chunks;
+  return t;
+}
+
+template <int D>
+cudaError_t launch_chunks(const Params &cp, cudaStream_t stream) {
+  cudaError_t e = ensure_smem_optin((const void *)gated_grad_tc_kernel<D>, (int)Lay<D>::Bytes);
+  if (e != cudaSuccess) return e;
+  const long sms = std::max(1, device_info(-1).sm_count);
+  LaunchTimer timer(kKGatedBackward, stream);
+  gated_grad_tc_kernel<D><<<(unsigned)std::min(sms, cp.items), kThreads, Lay<D>::Bytes, stream>>>(cp);
+  e = cudaGetLastError();
+  timer.done(e);
+  if (e == cudaSuccess) count_launch();
+  return e;
+}
+
+}  // namespace
+
+cudaError_t read_and_clear_gated_grad_status(unsigned int *value) {
+  return read_and_clear_status_word((const void *)&g_gated_status, value);
+}
+
+size_t gated_tc_grad_workspace(long BH, long N, int D) {
+  const Plan t = make_plan(BH, N, D);
+  const size_t tiles = 2 * (size_t)BH * t.n * gated_tile_bytes(D);
+  return tiles + (t.segs > 1 ? sizeof(float) * (size_t)BH * t.segs * (2 * (size_t)D * D + 1) : 0);
+}
+
+cudaError_t launch_gated_grad_tc(const GatedGradProblem &b) {
+  const GatedProblem &p = b.p;
+  const int D = p.dk;
+  const long BH = p.BH();
+  const Plan t = make_plan(BH, p.N, D);
+  uint8_t *ws = (uint8_t *)p.ws;
+  const size_t tiles = (size_t)BH * t.n * gated_tile_bytes(D);
+  GatedStateParams sp;
+  memset(&sp, 0, sizeof sp);
+  if (!gated_map(&sp.ta[0], p.k, BH, p.N, D, 64) || !gated_map(&sp.tb[0], p.v, BH, p.N, D, 64) ||
+      !gated_map(&sp.ta[1], p.q, BH, p.N, D, 64) || !gated_map(&sp.tb[1], b.dout, BH, p.N, D, 64))
+    return cudaErrorInvalidValue;
+  sp.g = p.g, sp.lengths = p.lengths, sp.N = p.N, sp.n = t.n, sp.H = p.H;
+  sp.segs = sp.run_segs = (int)t.segs, sp.seg_chunks = (int)t.seg_chunks;
+  cudaError_t e;
+  if (t.segs > 1) {
+    float *sums = (float *)(ws + 2 * tiles), *rsums = sums + (size_t)BH * t.segs * D * D,
+          *tot = rsums + (size_t)BH * t.segs * D * D;
+    sp.fin[0] = sums, sp.fin[1] = rsums, sp.seg_tot = tot;
+    e = launch_gated_states(sp, D, BH, 2, false, p.stream);
+    if (e != cudaSuccess) return e;
+    GatedSegScan sc = {};
+    sc.sums[0] = sums, sc.sums[1] = rsums, sc.tot = tot, sc.first[0] = p.S0, sc.first[1] = b.dS;
+    sc.last[1] = b.dS0, sc.segs = (int)t.segs, sc.dd = D * D;
+    e = launch_gated_seg_scan(sc, BH, 2, p.stream);
+    if (e != cudaSuccess) return e;
+    sp.init[0] = sums, sp.init[1] = rsums, sp.fin[0] = sp.fin[1] = nullptr, sp.seg_tot = nullptr;
+  } else {
+    sp.init[0] = p.S0, sp.init[1] = b.dS, sp.fin[1] = b.dS0;
+  }
+  sp.tiles[0] = ws, sp.tiles[1] = ws + tiles;
+  e = launch_gated_states(sp, D, BH, 2, false, p.stream);
+  if (e != cudaSuccess) return e;
+  Params cp;
+  memset(&cp, 0, sizeof cp);
+  if (!gated_map(&cp.tq, p.q, BH, p.N, D, kC) || !gated_map(&cp.tk, p.k, BH, p.N, D, kC) ||
+      !gated_map(&cp.tv, p.v, BH, p.N, D, kC) || !gated_map(&cp.td, b.dout, BH, p.N, D, kC))
+    return cudaErrorInvalidValue;
+  cp.g = p.g, cp.lengths = p.lengths, cp.s_tiles = sp.tiles[0], cp.r_tiles = sp.tiles[1];
+  cp.dq = (__nv_bfloat16 *)b.dq, cp.dk = (__nv_bfloat16 *)b.dk, cp.dv = (__nv_bfloat16 *)b.dv, cp.dg = b.dg;
+  cp.N = p.N, cp.n = t.n, cp.items = BH * t.n, cp.H = p.H;
+  return D == 64 ? launch_chunks<64>(cp, p.stream) : launch_chunks<128>(cp, p.stream);
+}
+
+}  // namespace la

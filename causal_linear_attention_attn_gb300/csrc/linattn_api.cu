@@ -210,12 +210,13 @@ la_status la_device_status(void *stream) {
   unsigned int vb = 0;
   if (e == cudaSuccess) e = la::read_and_clear_favor_status(&vf);
   if (e == cudaSuccess) e = la::read_and_clear_backward_status(&vb);
-  unsigned int vs = 0, vt = 0, vm = 0;
+  unsigned int vs = 0, vt = 0, vm = 0, vd = 0;
   if (e == cudaSuccess) e = la::read_and_clear_gated_state_status(&vt);
   if (e == cudaSuccess) e = la::read_and_clear_gated_status(&vm);
+  if (e == cudaSuccess) e = la::read_and_clear_gated_grad_status(&vd);
   if (e == cudaSuccess) e = la::read_and_clear_gated_step_status(&vs);
   if (e != cudaSuccess) return la::from_cuda(e);
-  v |= vg | vf | vb | vt | vm;
+  v |= vg | vf | vb | vt | vm | vd;
   if (v & 1u) return LA_ERR_TIMEOUT;
   if (!v && (vs & la::kStatusBadSlot)) return LA_ERR_INVALID_VALUE;
   return v ? LA_ERR_LAUNCH : LA_OK;  // other bits: a kernel refused to run (e.g. misaligned shared memory)
