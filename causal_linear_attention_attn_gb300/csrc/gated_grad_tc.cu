@@ -522,13 +522,13 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
   }
 }
 
-// Segments of the state pass: it has two CTAs an SM, D / 64 per head and direction; few heads are cut
-// further (the sums of the segments first, then the states), down to four chunks a segment.
+// Segments of the state pass: one CTA an SM, one per head and direction; few heads are cut further (the
+// sums of the segments first, then the states), down to four chunks a segment.
 struct Plan {
   long n, segs, seg_chunks;
 };
 Plan make_plan(long BH, long N, int D) {
-  const long slots = 2L * std::max(1, device_info(-1).sm_count), ctas = BH * (D / 64) * 2;
+  const long slots = std::max(1, device_info(-1).sm_count), ctas = BH * 2;
   Plan t;
   t.n = (N + kC - 1) / kC;
   t.segs = std::max(1L, std::min(slots / std::max(1L, ctas), t.n / 4));
@@ -571,8 +571,8 @@ cudaError_t launch_gated_grad_tc(const GatedGradProblem &b) {
   const size_t tiles = (size_t)BH * t.n * gated_tile_bytes(D);
   GatedStateParams sp;
   memset(&sp, 0, sizeof sp);
-  if (!gated_map(&sp.ta[0], p.k, BH, p.N, D, 64) || !gated_map(&sp.tb[0], p.v, BH, p.N, D, 64) ||
-      !gated_map(&sp.ta[1], p.q, BH, p.N, D, 64) || !gated_map(&sp.tb[1], b.dout, BH, p.N, D, 64))
+  if (!gated_map(&sp.ta[0], p.k, BH, p.N, D, kC) || !gated_map(&sp.tb[0], p.v, BH, p.N, D, kC) ||
+      !gated_map(&sp.ta[1], p.q, BH, p.N, D, kC) || !gated_map(&sp.tb[1], b.dout, BH, p.N, D, kC))
     return cudaErrorInvalidValue;
   sp.g = p.g, sp.lengths = p.lengths, sp.N = p.N, sp.n = t.n, sp.H = p.H;
   sp.segs = sp.run_segs = (int)t.segs, sp.seg_chunks = (int)t.seg_chunks;

@@ -6,15 +6,14 @@
 // weighted a_t reach the MMAs as a bf16 pair (hi + lo, 2^-17 relative): the state is an fp32 result
 // and feeds the decays' gradient, and one bf16 rounding (2^-9) would show in both.
 //
-// A CTA owns 64 of the state's columns for one segment of one head and direction, so that 64 heads
-// make 256 CTAs at D = 128, two to an SM, all resident at once: the recurrence over chunks is a
-// chain, and only independent chains hide its latency.  (The a tile is read once per column slice;
-// the second read comes from L2.)  Loads come in 64-token stages so that two CTAs fit an SM.
+// A CTA owns one segment of one head and direction.  The chunks are a chain, state -> MMA -> state;
+// what is not on the chain (loads, weights, the bf16 pairs that are stored) runs beside it: the state
+// warps read the state, write it back decayed for the next MMA, and only then split and store it.
 // At D = 64 hi and lo make up the 128 rows of one MMA, [hi | lo]^T b, and meet when the state is read.
 // HBM bounds it: per token 4 D bytes in and, when tiles are written, 4 D bytes out per direction.
 //
-// Warps: 0 TMA, 1 MMA and TMEM owner, 2-5 weights (hi in place, lo beside it), 6-9 state (store,
-// decay, write back), 10 running sums of the decays.  Every wait is bounded (tc_ptx.cuh).
+// Warps: 0 TMA, 1 MMA and TMEM owner, 2-9 weights (hi in place, lo beside it), 10-17 state, 18
+// running sums of the decays.  Every wait is bounded (tc_ptx.cuh).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -27,32 +26,30 @@ namespace la {
 namespace {
 using namespace gtc;
 
-constexpr int kThreads = 352;
-constexpr int kWarpXform = 2, kWarpState = 6, kWarpGate = 10;
+constexpr int kThreads = 608;
+constexpr int kWarpXform = 2, kWarpState = 10, kWarpGate = 18;
 constexpr uint32_t kBarState = 1;
-constexpr int kSub = 64;  // tokens per stage
-constexpr uint32_t kHalf = 8192;  // [64 rows x 128 bytes]
 
 template <int D>
 struct Lay {
-  static constexpr int kStages = D == 128 ? 3 : 4;
-  static constexpr uint32_t kA = D / 64 * kHalf;  // one stage of a (or of its low parts)
+  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr uint32_t kTile = D / 64 * kBlk;  // 128 tokens
   static constexpr uint32_t A = 0;
-  static constexpr uint32_t Lo = A + kStages * kA;  // 2 buffers
-  static constexpr uint32_t B = Lo + 2 * kA;
-  static constexpr uint32_t Sum = B + kStages * kHalf;  // D = 64: low rows of the state [64][65] fp32
+  static constexpr uint32_t Lo = A + kStages * kTile;  // 2 buffers
+  static constexpr uint32_t B = Lo + 2 * kTile;
+  static constexpr uint32_t Sum = B + kStages * kTile;  // D = 64: low rows of the state [64][65] fp32
   static constexpr uint32_t Gate = Sum + (D == 64 ? 64 * 65 * 4 : 0);  // [2][hi 128, lo 128]
   static constexpr uint32_t Bars = Gate + 2 * 2 * kC * 4;
   static constexpr int kNumBars = 3 * kStages + 2 + 4 + 3;
   static constexpr uint32_t Misc = Bars + kNumBars * 8;
   static constexpr uint32_t Bytes = Misc + 16;
 };
-static_assert(Lay<128>::Bytes <= 115712 && Lay<64>::Bytes <= 115712, "two CTAs per SM");
+static_assert(Lay<128>::Bytes <= 232448, "shared memory budget");
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 2) gated_state_tc_kernel(const __grid_constant__ GatedStateParams p) {
+__global__ void __launch_bounds__(kThreads, 1) gated_state_tc_kernel(const __grid_constant__ GatedStateParams p) {
   using L = Lay<D>;
-  constexpr int kStages = L::kStages, kSlices = D / 64;
+  constexpr int kStages = L::kStages;
   extern __shared__ __align__(1024) uint8_t sm[];
   if (smem_u32(sm) & 1023u) {
     if (threadIdx.x == 0) atomicOr(&g_gated_status, kAbortMisaligned);
@@ -69,10 +66,8 @@ __global__ void __launch_bounds__(kThreads, 2) gated_state_tc_kernel(const __gri
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int dir = blockIdx.y;
-  const int slice = blockIdx.x % kSlices;
-  const long item = blockIdx.x / kSlices;
-  const long bh = item / p.run_segs;
-  const int seg = (int)(item - bh * p.run_segs);
+  const long bh = blockIdx.x / p.run_segs;
+  const int seg = (int)(blockIdx.x - bh * p.run_segs);
   const long len = row_length(p.lengths, bh / p.H, p.N);
   const long nb = (len + kC - 1) / kC;  // the row's chunks
   const long c_lo = min(nb, (long)seg * p.seg_chunks), c_hi = min(nb, c_lo + p.seg_chunks);
@@ -87,21 +82,21 @@ __global__ void __launch_bounds__(kThreads, 2) gated_state_tc_kernel(const __gri
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&done[s], 128);
+      mbar_init(&done[s], 256);
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&lo_free[b], 1);
       mbar_init(&gate_full[b], 32);
-      mbar_init(&gate_free[b], 256);
+      mbar_init(&gate_free[b], 512);
     }
-    mbar_init(x_ready, 128);
+    mbar_init(x_ready, 256);
     mbar_init(x_full, 1);
     mbar_init(drain, 1);
     *abort_word = 0;
     fence_barrier_init();
   }
-  if (warp == 1) tmem_alloc(tmem_slot, 64);
+  if (warp == 1) tmem_alloc(tmem_slot, D);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -114,169 +109,178 @@ __global__ void __launch_bounds__(kThreads, 2) gated_state_tc_kernel(const __gri
   if (warp == 0) {
     if (lane == 0) {
       int issued = 0;
-      for (int u = 0; u < 2 * run; ++u) {
-        const int s = u % kStages;
-        if (u >= kStages && !mbar_wait(&empty[s], (u / kStages - 1) & 1, abort_word, status)) break;
-        const int tok = (int)(chunk(u >> 1) * kC) + (u & 1) * kSub;
-        mbar_arrive_expect_tx(&full[s], L::kA + kHalf);
-        for (int b = 0; b < D / 64; ++b) tma_load_3d(sm + L::A + s * L::kA + b * kHalf, &p.ta[dir], &full[s], 64 * b, tok, (int)bh);
-        tma_load_3d(sm + L::B + s * kHalf, &p.tb[dir], &full[s], 64 * slice, tok, (int)bh);
-        issued = u + 1;
+      for (int i = 0; i < run; ++i) {
+        const int s = i % kStages, tok = (int)(chunk(i) * kC);
+        if (i >= kStages && !mbar_wait(&empty[s], (i / kStages - 1) & 1, abort_word, status)) break;
+        mbar_arrive_expect_tx(&full[s], 2 * L::kTile);
+        for (int b = 0; b < D / 64; ++b) {
+          tma_load_3d(sm + L::A + s * L::kTile + b * kBlk, &p.ta[dir], &full[s], 64 * b, tok, (int)bh);
+          tma_load_3d(sm + L::B + s * L::kTile + b * kBlk, &p.tb[dir], &full[s], 64 * b, tok, (int)bh);
+        }
+        issued = i + 1;
       }
-      for (int u = max(0, issued - kStages); u < issued; ++u) wait_drain(&full[u % kStages], (u / kStages) & 1, status);
+      for (int i = max(0, issued - kStages); i < issued; ++i) wait_drain(&full[i % kStages], (i / kStages) & 1, status);
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      constexpr uint32_t iMM = idesc_bf16_f32(128, 64, 1, 1);
+      constexpr uint32_t iMM = idesc_bf16_f32(128, D, 1, 1);
       const uint32_t sA = smem_u32(sm + L::A), sLo = smem_u32(sm + L::Lo), sB = smem_u32(sm + L::B);
-      for (int u = 0; u < 2 * run; ++u) {
-        const int s = u % kStages;
-        if (!mbar_wait(&done[s], (u / kStages) & 1, abort_word, status)) break;
-        if (!(u & 1) && !mbar_wait(x_ready, (u >> 1) & 1, abort_word, status)) break;
+      for (int i = 0; i < run; ++i) {
+        const int s = i % kStages;
+        if (!mbar_wait(&done[s], (i / kStages) & 1, abort_word, status)) break;
+        if (!mbar_wait(x_ready, i & 1, abort_word, status)) break;
         tc_fence_after();
-        const uint32_t a = sA + s * L::kA, lo = sLo + (u & 1) * L::kA, b = sB + s * kHalf;
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
+        const uint32_t a = sA + s * L::kTile, lo = sLo + (i & 1) * L::kTile, b = sB + s * L::kTile;
+#pragma unroll 4
+        for (int ks = 0; ks < 8; ++ks) {
           if (D == 128) {
-            mma_bf16(tmem, mndesc(a, ks, kHalf), mndesc(b, ks, kHalf), iMM, 1);
-            mma_bf16(tmem, mndesc(lo, ks, kHalf), mndesc(b, ks, kHalf), iMM, 1);
+            mma_bf16(tmem, mndesc(a, ks), mndesc(b, ks), iMM, 1);
+            mma_bf16(tmem, mndesc(lo, ks), mndesc(b, ks), iMM, 1);
           } else {
-            mma_bf16(tmem, mndesc(a, ks, lo - a), mndesc(b, ks, kHalf), iMM, 1);  // rows: hi, then lo
+            mma_bf16(tmem, mndesc(a, ks, lo - a), mndesc(b, ks), iMM, 1);  // rows: hi, then lo
           }
         }
         mma_commit(&empty[s]);
-        mma_commit(&lo_free[u & 1]);
-        if (u & 1) mma_commit(x_full);
+        mma_commit(&lo_free[i & 1]);
+        mma_commit(x_full);
       }
       mma_commit(drain);
       wait_drain(drain, 0, status);
     }
   } else if (warp < kWarpState) {
-    // weights: row r of the stage, half of its features (D = 128: one 64-wide block)
-    const int r = (threadIdx.x - kWarpXform * 32) & 63, half = (threadIdx.x - kWarpXform * 32) >> 6;
-    for (int u = 0; u < 2 * run; ++u) {
-      const int s = u % kStages, i = u >> 1;
+    // weights: token r of the chunk, half of its features
+    const int r = (threadIdx.x - kWarpXform * 32) & 127, half = (threadIdx.x - kWarpXform * 32) >> 7;
+    constexpr int kChunks = D / 16;  // 16-byte chunks per thread
+    const int blk = D == 128 ? half * kBlk : 0, c0 = D == 128 ? 0 : half * 4;
+    for (int i = 0; i < run; ++i) {
+      const int s = i % kStages;
       bool ok = mbar_wait(&gate_full[i & 1], (i >> 1) & 1, abort_word, status);
-      ok = ok && mbar_wait(&full[s], (u / kStages) & 1, abort_word, status);
-      if (ok && u >= 2) ok = mbar_wait(&lo_free[u & 1], ((u >> 1) - 1) & 1, abort_word, status);
+      ok = ok && mbar_wait(&full[s], (i / kStages) & 1, abort_word, status);
+      if (ok && i >= 2) ok = mbar_wait(&lo_free[i & 1], ((i >> 1) - 1) & 1, abort_word, status);
       if (!__all_sync(0xffffffffu, ok)) break;
       const float *hi = gate + (i & 1) * 2 * kC, *lo = hi + kC;
-      const int t = (u & 1) * kSub + r;
-      const bool in = t < valid(i);
-      const float w = dir ? exp2f(hi[t] + lo[t]) : exp2f((hi[kC - 1] - hi[t]) + (lo[kC - 1] - lo[t]));
-      if (u & 1) mbar_arrive(&gate_free[i & 1]);
-      constexpr int kChunks = D / 16;  // 16-byte chunks per thread
-      const int blk = D == 128 ? half * kHalf : 0, c0 = D == 128 ? 0 : half * 4;
-      uint8_t *A = sm + L::A + s * L::kA + blk, *Lo = sm + L::Lo + (u & 1) * L::kA + blk;
-#pragma unroll
+      const bool in = r < valid(i);
+      const float w = dir ? exp2f(hi[r] + lo[r]) : exp2f((hi[kC - 1] - hi[r]) + (lo[kC - 1] - lo[r]));
+      mbar_arrive(&gate_free[i & 1]);
+      uint8_t *A = sm + L::A + s * L::kTile + blk, *Lo = sm + L::Lo + (i & 1) * L::kTile + blk;
+#pragma unroll 4
       for (int e = 0; e < kChunks; ++e) {
         const uint32_t off = sw128_offset(r, (c0 + e) * 8);
         uint4 h = make_uint4(0u, 0u, 0u, 0u), l = h;
-        if (in) split8(*reinterpret_cast<const uint4 *>(A + off), w, h, l);
+        if (in) split8p(*reinterpret_cast<const uint4 *>(A + off), w, h, l);
         *reinterpret_cast<uint4 *>(A + off) = h;
         *reinterpret_cast<uint4 *>(Lo + off) = l;
       }
       if (!in) {  // padding tokens: a zero weight does not clear a NaN of the other operand
-        uint8_t *B = sm + L::B + s * kHalf;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4 *>(B + sw128_offset(r, (half * 4 + e) * 8)) = make_uint4(0u, 0u, 0u, 0u);
+        uint8_t *B = sm + L::B + s * L::kTile + blk;
+        for (int e = 0; e < kChunks; ++e)
+          *reinterpret_cast<uint4 *>(B + sw128_offset(r, (c0 + e) * 8)) = make_uint4(0u, 0u, 0u, 0u);
       }
       fence_async_smem();
       mbar_arrive(&done[s]);
     }
   } else if (warp < kWarpGate) {
     const int q = warp & 3, T = q * 32 + lane;  // tensor-memory lane: a row of the state (D = 64: from 64 on, its low part)
-    const uint32_t tx = tmem + ((uint32_t)(q * 32) << 16);
+    const int col0 = ((warp - kWarpState) >> 2) * (D / 2);
+    constexpr int kB = D / 64;  // blocks of 32 columns
+    const uint32_t tx = tmem + ((uint32_t)(q * 32) << 16) + col0;
     const int row = D == 64 ? T & 63 : T;
     const bool main_row = D == 128 || q < 2;
     float *sum = reinterpret_cast<float *>(sm + L::Sum);
-    uint32_t r[32];
+    uint32_t r[kB][32];
     const long dd = (long)D * D;
-    const float *init = p.init[dir] ? p.init[dir] + (bh * p.segs + seg) * dd + (long)row * D + slice * 64 : nullptr;
+    const float *init = p.init[dir] ? p.init[dir] + (bh * p.segs + seg) * dd + (long)row * D + col0 : nullptr;
 #pragma unroll
-    for (int cb = 0; cb < 2; ++cb) {
+    for (int b = 0; b < kB; ++b) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (init && main_row) x = reinterpret_cast<const float4 *>(init + cb * 32)[e];
-        r[4 * e] = __float_as_uint(x.x), r[4 * e + 1] = __float_as_uint(x.y);
-        r[4 * e + 2] = __float_as_uint(x.z), r[4 * e + 3] = __float_as_uint(x.w);
+        if (init && main_row) x = reinterpret_cast<const float4 *>(init + b * 32)[e];
+        r[b][4 * e] = __float_as_uint(x.x), r[b][4 * e + 1] = __float_as_uint(x.y);
+        r[b][4 * e + 2] = __float_as_uint(x.z), r[b][4 * e + 3] = __float_as_uint(x.w);
       }
-      tmem_st32(tx + cb * 32, r);
     }
-    // D = 64: the two parts of columns [32 cb, 32 cb + 32) meet in the rows of the first two warps
-    auto join = [&](int cb) {
+    // D = 64: the two parts meet in the rows of the first two lane quarters
+    auto join = [&]() {
       if (D == 128) return;
       if (!main_row)
 #pragma unroll
-        for (int e = 0; e < 32; ++e) sum[row * 65 + cb * 32 + e] = __uint_as_float(r[e]);
-      named_bar(kBarState, 128);
+        for (int e = 0; e < 32; ++e) sum[row * 65 + col0 + e] = __uint_as_float(r[0][e]);
+      named_bar(kBarState, 256);
       if (main_row)
 #pragma unroll
-        for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) + sum[row * 65 + cb * 32 + e]);
+        for (int e = 0; e < 32; ++e) r[0][e] = __float_as_uint(__uint_as_float(r[0][e]) + sum[row * 65 + col0 + e]);
     };
     bool ok = true;
     for (int i = 0; i < nc && ok; ++i) {
       bool w = i == 0 || mbar_wait(x_full, (i - 1) & 1, abort_word, status);
       if (w && i < run) w = mbar_wait(&gate_full[i & 1], (i >> 1) & 1, abort_word, status);
-      if (bar_or(kBarState, 128, !w)) {
+      if (bar_or(kBarState, 256, !w)) {  // D = 64: also, the last joined columns are read
         ok = false;
         break;
       }
       tc_fence_after();
-      float f = 1.f;
+      if (i > 0) {
+        if constexpr (kB == 2)
+          tmem_ld32x2(tx, tx + 32, r[0], r[kB - 1]);
+        else
+          tmem_ld32(tx, r[0]);
+      }
       if (i < run) {
         const float *hi = gate + (i & 1) * 2 * kC;
-        f = exp2f(hi[kC - 1] + hi[2 * kC - 1]);
+        const float f = exp2f(hi[kC - 1] + hi[2 * kC - 1]);
         mbar_arrive(&gate_free[i & 1]);
-      }
-#pragma unroll 1
-      for (int cb = 0; cb < 2; ++cb) {
-        tmem_ld32(tx + cb * 32, r);
-        if (i < run) {
-          uint32_t y[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) y[e] = r[e];
-          scale32(y, f);
-          tmem_st32(tx + cb * 32, y);
-        }
-        if (cb == 1 && i < run) {
-          tc_fence_before();
-          mbar_arrive(x_ready);
-        }
-        if (tiles) {
-          join(cb);
-          if (main_row) {
+        for (int b = 0; b < kB; ++b)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t y[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(r[b][16 * h + e]) * f);
+            tmem_st16_nowait(tx + 32 * b + 16 * h, y);
+          }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(x_ready);
+      }
+      if (tiles) {
+        join();
+        if (main_row) {
+          uint8_t *t = tiles + (bh * p.n + chunk(i)) * (size_t)(D * D * 4) + (col0 >> 6) * (D * 128);
+#pragma unroll
+          for (int b = 0; b < kB; ++b) {
             uint4 h[4], l[4];
-            split_bf16x32(r, h, l);
-            uint8_t *t = tiles + (bh * p.n + chunk(i)) * (size_t)(D * D * 4) + slice * (D * 128);
+            split_bf16x32(r[b], h, l);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const uint32_t off = sw128_offset(row, cb * 32 + e * 8);
+              const uint32_t off = sw128_offset(row, (col0 & 63) + b * 32 + e * 8);
               *reinterpret_cast<uint4 *>(t + off) = h[e];
               *reinterpret_cast<uint4 *>(t + D * D * 2 + off) = l[e];
             }
           }
-          if (D == 64) named_bar(kBarState, 128);  // the joined columns are read
         }
       }
     }
     if (fin && ok) {
       const bool w = run == 0 || mbar_wait(x_full, (run - 1) & 1, abort_word, status);
-      if (!bar_or(kBarState, 128, !w)) {
+      if (!bar_or(kBarState, 256, !w)) {
         tc_fence_after();
-        float *dst = fin + (bh * p.segs + seg) * dd + (long)row * D + slice * 64;
-#pragma unroll 1
-        for (int cb = 0; cb < 2; ++cb) {
-          tmem_ld32(tx + cb * 32, r);
-          join(cb);
-          if (main_row)
+        if (run > 0) {
+          if constexpr (kB == 2)
+            tmem_ld32x2(tx, tx + 32, r[0], r[kB - 1]);
+          else
+            tmem_ld32(tx, r[0]);
+        }
+        join();
+        float *dst = fin + (bh * p.segs + seg) * dd + (long)row * D + col0;
+        if (main_row)
+#pragma unroll
+          for (int b = 0; b < kB; ++b)
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              reinterpret_cast<float4 *>(dst + cb * 32)[e] =
-                  make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]), __uint_as_float(r[4 * e + 2]),
-                              __uint_as_float(r[4 * e + 3]));
-        }
+              reinterpret_cast<float4 *>(dst + b * 32)[e] =
+                  make_float4(__uint_as_float(r[b][4 * e]), __uint_as_float(r[b][4 * e + 1]),
+                              __uint_as_float(r[b][4 * e + 2]), __uint_as_float(r[b][4 * e + 3]));
       }
     }
   } else {
@@ -289,14 +293,14 @@ __global__ void __launch_bounds__(kThreads, 2) gated_state_tc_kernel(const __gri
       total += (double)hi[kC - 1] + (double)hi[2 * kC - 1];
       mbar_arrive(&gate_full[i & 1]);
     }
-    if (p.seg_tot && fin && dir == 0 && slice == 0 && lane == 0) p.seg_tot[bh * p.segs + seg] = (float)total;
+    if (p.seg_tot && fin && dir == 0 && lane == 0) p.seg_tot[bh * p.segs + seg] = (float)total;
   }
 
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 64);
+    tmem_dealloc(tmem, D);
   }
 }
 
@@ -329,7 +333,7 @@ cudaError_t launch_t(const GatedStateParams &sp, long BH, int dirs, bool pdl, cu
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)(BH * sp.run_segs * (D / 64)), (unsigned)dirs);
+  cfg.gridDim = dim3((unsigned)(BH * sp.run_segs), (unsigned)dirs);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = Lay<D>::Bytes;
   cfg.stream = stream;

@@ -17,8 +17,8 @@
 // HBM bounds it (8 D bytes per token in and out, 40 flops a byte at D = 128): a chunk's loads take
 // about 5000 cycles of an SM's share, its longest chain (P, weights, P' V) about 2800.
 //
-// Warps: 0 TMA, 1 MMA and TMEM owner, 2-5 weights of the scores, 6-9 weighted keys, 10-13 state
-// (bf16 copy, decay), 14-17 outputs, 18 running sums.  Every wait is bounded (tc_ptx.cuh).
+// Warps: 0 TMA, 1 MMA and TMEM owner, 2-9 weights of the scores, 10-13 weighted keys, 14-17 state
+// (bf16 copy, decay), 18-21 outputs, 22 running sums.  Every wait is bounded (tc_ptx.cuh).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -31,8 +31,8 @@ namespace la {
 namespace {
 using namespace gtc;
 
-constexpr int kThreads = 608;
-constexpr int kWarpK = 6, kWarpS = 10, kWarpO = 14, kWarpGate = 18;
+constexpr int kThreads = 736;
+constexpr int kWarpK = 10, kWarpS = 14, kWarpO = 18, kWarpGate = 22;
 constexpr uint32_t kBarS = 1;
 
 template <int D>
@@ -96,13 +96,13 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
       mbar_init(&full_v[b], 1);
       mbar_init(&kv_free[b], 1);
       mbar_init(&gate_full[b], 32);
-      mbar_init(&gate_free[b], 512);
+      mbar_init(&gate_free[b], 640);
     }
     mbar_init(full_q, 1);
     mbar_init(q_free, 1);
     mbar_init(p_full, 1);
     mbar_init(k_ready, 128);
-    mbar_init(pp_ready, 128);
+    mbar_init(pp_ready, 256);
     mbar_init(sb_ready, 128);
     mbar_init(s_full, 1);
     mbar_init(o_full, 1);
@@ -182,7 +182,8 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
         if (!mbar_wait(pp_ready, c & 1, abort_word, status)) break;
         tc_fence_after();
 #pragma unroll 4
-        for (int ks = 0; ks < 8; ++ks) mma_bf16_ts(tA, tP + 8 * ks, mndesc(v, ks), iO, ks > 0);
+        for (int ks = 0; ks < 8; ++ks)  // keys [16 ks, ..): columns 8 ks of the first or the second half
+          mma_bf16_ts(tA, tP + (ks < 4 ? 8 * ks : 32 + 8 * ks), mndesc(v, ks), iO, ks > 0);
         mma_commit(&kv_free[s]);
         mma_commit(o_full);
       }
@@ -190,9 +191,9 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
       wait_drain(drain, 0, status);
     }
   } else if (warp < kWarpK) {
-    // ---- weights of the scores: row i of this thread, keys in blocks of 32 ----
-    const int q = warp & 3, i = q * 32 + lane;
-    const uint32_t tP = tmem + ((uint32_t)(q * 32) << 16) + kColP;
+    // ---- weights of the scores: row i of this thread, keys [64 half, 64 half + 64) ----
+    const int q = warp & 3, i = q * 32 + lane, half = (warp - 2) >> 2;
+    const uint32_t tP = tmem + ((uint32_t)(q * 32) << 16) + kColP + 64 * half;
     for (int c = 0; c < nc; ++c) {
       if (!warp_wait(&gate_full[c & 1], (c >> 1) & 1, abort_word)) break;
       if (!warp_wait(p_full, c & 1, abort_word)) break;
@@ -200,28 +201,33 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
       const float *hi = gate + (c & 1) * 2 * kC, *lo = hi + kC;
       const float hi_i = hi[i], lo_i = lo[i];
 #pragma unroll 1
-      for (int cb = 0; cb < 4; ++cb) {
+      for (int b = 0; b < 2; ++b) {
+        const int cb = 2 * half + b;  // 32 keys: none, all, or (cb == q) those up to the query
         uint32_t o[16];
         if (cb > q) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) o[e] = 0u;
         } else {
           uint32_t r[32];
-          tmem_ld32(tP + cb * 32, r);
+          tmem_ld32(tP + b * 32, r);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const int j = cb * 32 + 4 * e;
-            const float4 h = *reinterpret_cast<const float4 *>(hi + j), l = *reinterpret_cast<const float4 *>(lo + j);
-            const float w[4] = {(hi_i - h.x) + (lo_i - l.x), (hi_i - h.y) + (lo_i - l.y), (hi_i - h.z) + (lo_i - l.z),
-                                (hi_i - h.w) + (lo_i - l.w)};
-            float x[4];
-#pragma unroll
-            for (int m = 0; m < 4; ++m) x[m] = j + m <= i ? __uint_as_float(r[4 * e + m]) * ex2_approx(w[m]) : 0.f;
-            o[2 * e] = pack_bf16(x[0], x[1]);
-            o[2 * e + 1] = pack_bf16(x[2], x[3]);
+            const float4 h = *reinterpret_cast<const float4 *>(hi + cb * 32 + 4 * e),
+                         l = *reinterpret_cast<const float4 *>(lo + cb * 32 + 4 * e);
+            float f[4];
+            decay4(h, l, hi_i, lo_i, -1.f, f);
+            float2 x = __fmul2_rn(make_float2(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1])), make_float2(f[0], f[1]));
+            float2 y = __fmul2_rn(make_float2(__uint_as_float(r[4 * e + 2]), __uint_as_float(r[4 * e + 3])), make_float2(f[2], f[3]));
+            if (cb == q) {
+              const int j = 4 * e;
+              x = make_float2(j <= lane ? x.x : 0.f, j + 1 <= lane ? x.y : 0.f);
+              y = make_float2(j + 2 <= lane ? y.x : 0.f, j + 3 <= lane ? y.y : 0.f);
+            }
+            o[2 * e] = pack_bf16(x.x, x.y);
+            o[2 * e + 1] = pack_bf16(y.x, y.y);
           }
         }
-        tmem_st16(tP + cb * 16, o);
+        tmem_st16(tP + b * 16, o);  // over scores that this warp alone reads
       }
       tc_fence_before();
       mbar_arrive(pp_ready);
@@ -245,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
       for (int e = 0; e < D / 8; ++e) {
         const uint32_t off = (e >> 3) * kBlk + sw128_offset(r, (e & 7) * 8);
         uint4 h = make_uint4(0u, 0u, 0u, 0u), l = h;
-        if (r < tv) split8(*reinterpret_cast<const uint4 *>(K + off), w, h, l);
+        if (r < tv) split8p(*reinterpret_cast<const uint4 *>(K + off), w, h, l);
         *reinterpret_cast<uint4 *>(K + off) = h;
         *reinterpret_cast<uint4 *>(Klo + off) = l;
       }
@@ -361,23 +367,23 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
       const bool in = i < valid(c);
       __nv_bfloat16 *dst = p.out + (bh * p.N + (c_lo + c) * kC + i) * D;
 #pragma unroll 1
-      for (int cb = 0; cb < D / 32; ++cb) {
-        uint32_t x[32], y[32];
-        tmem_ld32x2(tl + kColI + cb * 32, tl + kColA + cb * 32, x, y);
-        if (cb == D / 32 - 1) {
+      for (int cb = 0; cb < D / 16; ++cb) {
+        uint32_t x[16], y[16];
+        tmem_ld16x2(tl + kColI + cb * 16, tl + kColA + cb * 16, x, y);
+        if (cb == D / 16 - 1) {
           tc_fence_before();
           mbar_arrive(o_free);
         }
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
+        for (int e = 0; e < 8; ++e) {
           const float2 z = __ffma2_rn(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), make_float2(f, f),
                                       make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])));
           x[e] = pack_bf16(z.x, z.y);
         }
-        if (in)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            reinterpret_cast<uint4 *>(dst + cb * 32)[e] = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+        if (in) {
+          reinterpret_cast<uint4 *>(dst + cb * 16)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+          reinterpret_cast<uint4 *>(dst + cb * 16)[1] = make_uint4(x[4], x[5], x[6], x[7]);
+        }
       }
     }
   } else {
@@ -412,11 +418,11 @@ Plan make_plan(long BH, long N, int D) {
   // its keys and values
   t.G = std::max(1L, std::min(sms / std::max(1L, BH), t.n / 4));
   t.seg_chunks = (t.n + t.G - 1) / t.G;
-  // the state pass has two CTAs an SM: cut its segments finer while that fills them
+  // the state pass's CTAs: cut its segments finer while one wave of SMs holds them
   t.step = 1;
   if (t.G > 1) {
-    const long per = BH * (t.G - 1) * (D / 64);
-    while (per * t.step * 2 <= 2 * sms && t.seg_chunks / (t.step * 2) >= 2) t.step *= 2;
+    const long per = BH * (t.G - 1);
+    while (per * t.step * 2 <= sms && t.seg_chunks / (t.step * 2) >= 2) t.step *= 2;
     t.seg_chunks = (t.seg_chunks + t.step - 1) / t.step * t.step;
     t.G = (t.n + t.seg_chunks - 1) / t.seg_chunks;
     if (t.G == 1) t.step = 1;
@@ -470,7 +476,7 @@ cudaError_t launch_gated_tc(const GatedProblem &p) {
     float *sums = (float *)p.ws, *tot = sums + (size_t)BH * t.init_segs() * D * D;
     GatedStateParams sp;
     memset(&sp, 0, sizeof sp);
-    if (!gated_map(&sp.ta[0], p.k, BH, p.N, D, 64) || !gated_map(&sp.tb[0], p.v, BH, p.N, D, 64))
+    if (!gated_map(&sp.ta[0], p.k, BH, p.N, D, kC) || !gated_map(&sp.tb[0], p.v, BH, p.N, D, kC))
       return cudaErrorInvalidValue;
     sp.g = p.g, sp.lengths = p.lengths, sp.N = p.N, sp.n = t.n, sp.H = p.H;
     sp.segs = (int)t.init_segs(), sp.run_segs = sp.segs - 1, sp.seg_chunks = (int)(t.seg_chunks / t.step);

@@ -53,6 +53,54 @@ __device__ __forceinline__ void scan_gates(const float *g, int tv, int lane, flo
   *reinterpret_cast<float4 *>(lo + 4 * lane) = make_float4(c[0].lo, c[1].lo, c[2].lo, c[3].lo);
 }
 
+// Two loads of 16 columns with a single wait.
+__device__ __forceinline__ void tmem_ld16x2(uint32_t a, uint32_t b, uint32_t (&r)[16], uint32_t (&s)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(s[0]),
+        "=r"(s[1]), "=r"(s[2]), "=r"(s[3]), "=r"(s[4]), "=r"(s[5]), "=r"(s[6]), "=r"(s[7]), "=r"(s[8]), "=r"(s[9]),
+        "=r"(s[10]), "=r"(s[11]), "=r"(s[12]), "=r"(s[13]), "=r"(s[14]), "=r"(s[15])
+      : "r"(a), "r"(b)
+      : "memory");
+}
+
+// Store 16 consecutive columns of this warp's 32 lanes; a tmem_wait_st() must follow.
+__device__ __forceinline__ void tmem_st16_nowait(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// f = 2^{sign (c_t - c)} for the running sums c_t = h + l of four tokens and c = hi + lo.
+__device__ __forceinline__ void decay4(float4 h, float4 l, float hi, float lo, float sign, float (&f)[4]) {
+  const float2 s = make_float2(sign, sign), a = make_float2(-sign * hi, -sign * hi), b = make_float2(-sign * lo, -sign * lo);
+  const float2 x = __fadd2_rn(__ffma2_rn(make_float2(h.x, h.y), s, a), __ffma2_rn(make_float2(l.x, l.y), s, b));
+  const float2 y = __fadd2_rn(__ffma2_rn(make_float2(h.z, h.w), s, a), __ffma2_rn(make_float2(l.z, l.w), s, b));
+  f[0] = ex2_approx(x.x), f[1] = ex2_approx(x.y), f[2] = ex2_approx(y.x), f[3] = ex2_approx(y.y);
+}
+
+// Eight packed bf16 values times f as a bf16 pair (split8 of tc_ptx.cuh in packed arithmetic).
+__device__ __forceinline__ void split8p(uint4 x, float f, uint4 &hi, uint4 &lo) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 v = __fmul2_rn(make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u)), make_float2(f, f));
+    h[e] = pack_bf16(v.x, v.y);
+    const float2 d = __ffma2_rn(make_float2(__uint_as_float(h[e] << 16), __uint_as_float(h[e] & 0xffff0000u)),
+                                make_float2(-1.f, -1.f), v);
+    l[e] = pack_bf16(d.x, d.y);
+  }
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
 // 32 fp32 values (raw bits) as bf16, four 16-byte chunks.
 __device__ __forceinline__ void to_bf16x32(const uint32_t (&r)[32], uint4 (&o)[4]) {
   const float *v = reinterpret_cast<const float *>(r);
@@ -68,7 +116,9 @@ __device__ __forceinline__ void split_bf16x32(const uint32_t (&r)[32], uint4 (&h
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
     h[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
-    l[e] = pack_bf16(v[2 * e] - __uint_as_float(h[e] << 16), v[2 * e + 1] - __uint_as_float(h[e] & 0xffff0000u));
+    const float2 d = __ffma2_rn(make_float2(__uint_as_float(h[e] << 16), __uint_as_float(h[e] & 0xffff0000u)),
+                                make_float2(-1.f, -1.f), make_float2(v[2 * e], v[2 * e + 1]));
+    l[e] = pack_bf16(d.x, d.y);
   }
 }
 
@@ -100,7 +150,7 @@ bool gated_map(CUtensorMap *m, const void *base, long BH, long N, int D, uint32_
 // (forward) or 2^{c_t} (backward).  tiles: X before each chunk as a bf16 pair in the shared-memory
 // image of the MMAs that read it (gated_tile_bytes a chunk, hi then lo); fin: X behind the segment.
 struct GatedStateParams {
-  CUtensorMap ta[2], tb[2];  // boxes of 64 x 64
+  CUtensorMap ta[2], tb[2];  // boxes of 64 x 128
   const float *g;
   const int *lengths;
   long N, n;  // tokens and chunks per head

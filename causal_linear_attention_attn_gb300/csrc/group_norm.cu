@@ -29,20 +29,6 @@ namespace {
 
 constexpr int kMaxThreads = 256;
 
-__device__ __forceinline__ void st8(float *p, const float (&o)[8]) {
-  st4(p, o[0], o[1], o[2], o[3]);
-  st4(p + 4, o[4], o[5], o[6], o[7]);
-}
-__device__ __forceinline__ void st8(__nv_bfloat16 *p, const float (&o)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const __nv_bfloat162 x = __floats2bfloat162_rn(o[2 * e], o[2 * e + 1]);
-    w[e] = *reinterpret_cast<const uint32_t *>(&x);
-  }
-  *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 // Sum over the aligned group of D / 8 lanes of one head.
 template <int D>
 __device__ __forceinline__ float group_sum(float x) {
@@ -80,150 +66,224 @@ struct Place {  // what a thread owns
   }
 };
 
-template <int D>
-__device__ __forceinline__ void normalize(float (&x)[8], float eps, float &rstd) {
-  float s = 0.f;
+// Eight values as loaded; converted where they are used, so that rows in flight cost few registers.
+template <typename T>
+struct Raw {
+  uint4 a[sizeof(T) / 2];
+  __device__ void load(const T *p) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) s += x[e];
-  const float mean = group_sum<D>(s) * (1.f / D);
-  s = 0.f;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    x[e] -= mean;
-    s = fmaf(x[e], x[e], s);
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) a[i] = reinterpret_cast<const uint4 *>(p)[i];
   }
-  rstd = rsqrtf(group_sum<D>(s) * (1.f / D) + eps);
+  __device__ void zero() {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] *= rstd;
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) a[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  __device__ void get(float2 (&o)[4]) const {
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(a);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      o[e] = sizeof(T) == 2 ? make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u))
+                            : make_float2(__uint_as_float(w[(2 * e) % (2 * sizeof(T))]),
+                                          __uint_as_float(w[(2 * e + 1) % (2 * sizeof(T))]));
+  }
+};
+__device__ __forceinline__ void put8(float *p, const float2 (&o)[4]) {
+  st4(p, o[0].x, o[0].y, o[1].x, o[1].y);
+  st4(p + 4, o[2].x, o[2].y, o[3].x, o[3].y);
+}
+__device__ __forceinline__ void put8(__nv_bfloat16 *p, const float2 (&o)[4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(o[e].x, o[e].y);
+    w[e] = *reinterpret_cast<const uint32_t *>(&x);
+  }
+  *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float sum8(const float2 (&x)[4]) {
+  const float2 s = __fadd2_rn(__fadd2_rn(x[0], x[1]), __fadd2_rn(x[2], x[3]));
+  return s.x + s.y;
+}
+__device__ __forceinline__ float dot8(const float2 (&x)[4], const float2 (&y)[4]) {
+  const float2 s = __ffma2_rn(x[0], y[0], __ffma2_rn(x[1], y[1], __ffma2_rn(x[2], y[2], __fmul2_rn(x[3], y[3]))));
+  return s.x + s.y;
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + __expf(-x)); }
-
-template <typename T, int D, int kRowsAhead>
-__global__ void __launch_bounds__(kMaxThreads)
-    group_norm_kernel(const __grid_constant__ NormProblem p, const __grid_constant__ Cut cut) {
-  const Place<D> me(cut, p.H);
-  const long tokens = (long)p.B * p.N, stride = (long)gridDim.x * cut.rows, HD = (long)p.H * D;
-  float w[8], b[8];
+// x - mean over the head, scaled to unit variance: the mean first, then the squared deviations (one
+// pass with the mean of the squares would cancel for rows far from zero).
+template <int D>
+__device__ __forceinline__ float normalize(float2 (&x)[4], float eps) {
+  const float mean = group_sum<D>(sum8(x)) * (1.f / D);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) w[e] = 1.f, b[e] = 0.f;
+  for (int e = 0; e < 4; ++e) x[e] = __fadd2_rn(x[e], both(-mean));
+  const float rstd = rsqrtf(group_sum<D>(dot8(x, x)) * (1.f / D) + eps);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x[e] = __fmul2_rn(x[e], both(rstd));
+  return rstd;
+}
+
+// 1 / (1 + e^-x): e^-x overflows to inf below -88, where the quotient is 0 as it should be.
+__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+
+// Quotients by N of numbers below 2^31 (round-up multiplier; add and shift).
+struct Divider {
+  uint32_t n, mul, shift;
+  __device__ uint32_t of(uint32_t x) const { return (__umulhi(x, mul) + x) >> shift; }
+};
+Divider make_divider(uint32_t n) {
+  Divider d{n, 0, 0};
+  while ((1ull << d.shift) < n) ++d.shift;
+  d.mul = (uint32_t)(((1ull << 32) * ((1ull << d.shift) - n)) / n + 1);
+  return d;
+}
+
+template <typename T, int D, bool kGate, int kRowsAhead>
+__global__ void __launch_bounds__(kMaxThreads)
+    group_norm_kernel(const __grid_constant__ NormProblem p, const __grid_constant__ Cut cut,
+                      const __grid_constant__ Divider by_n) {
+  const Place<D> me(cut, p.H);
+  const uint32_t tokens = (uint32_t)((long)p.B * p.N);
+  const long stride = (long)gridDim.x * cut.rows, HD = (long)p.H * D;
   const long col = (long)me.h * D + me.c;
-  if (me.live && p.weight) ld8(p.weight + col, w);
-  if (me.live && p.bias) ld8(p.bias + col, b);
+  float2 w[4], b[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) w[e] = both(1.f), b[e] = both(0.f);
+  if (me.live && p.weight) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = reinterpret_cast<const float2 *>(p.weight + col)[e];
+  }
+  if (me.live && p.bias) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) b[e] = reinterpret_cast<const float2 *>(p.bias + col)[e];
+  }
   // every lane of a warp runs the same number of turns: the shuffles need all of them
   for (long r0 = (long)blockIdx.x * cut.rows; r0 < tokens; r0 += kRowsAhead * stride) {
-    float x[kRowsAhead][8], g[kRowsAhead][8];
-    bool in[kRowsAhead];
+    Raw<T> x[kRowsAhead], g[kRowsAhead];
 #pragma unroll
     for (int u = 0; u < kRowsAhead; ++u) {
       const long r = r0 + u * stride + me.row;
-      in[u] = me.live && r < tokens;
-      if (in[u]) {
-        const long bi = r / p.N, n = r - bi * p.N;
-        ld8((const T *)p.x + ((bi * p.H + me.h) * p.N + n) * D + me.c, x[u]);
-        if (p.gate) ld8((const T *)p.gate + r * HD + col, g[u]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[u][e] = 0.f;
+      x[u].zero();
+      if (me.live && r < tokens) {
+        const uint32_t bi = by_n.of((uint32_t)r), n = (uint32_t)r - bi * by_n.n;
+        x[u].load((const T *)p.x + (((long)bi * p.H + me.h) * p.N + n) * D + me.c);
+        if (kGate) g[u].load((const T *)p.gate + r * HD + col);
       }
     }
 #pragma unroll
     for (int u = 0; u < kRowsAhead; ++u) {
-      float rstd;
-      normalize<D>(x[u], p.eps, rstd);
-      if (!in[u]) continue;
+      float2 y[4], t[4];
+      x[u].get(y);
+      normalize<D>(y, p.eps);
+      const long r = r0 + u * stride + me.row;
+      if (!(me.live && r < tokens)) continue;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float y = fmaf(x[u][e], w[e], b[e]);
-        if (p.gate) y *= g[u][e] * sigmoid(g[u][e]);
-        x[u][e] = y;
+      for (int e = 0; e < 4; ++e) y[e] = __ffma2_rn(y[e], w[e], b[e]);
+      if (kGate) {
+        g[u].get(t);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          y[e] = __fmul2_rn(y[e], __fmul2_rn(t[e], make_float2(sigmoid(t[e].x), sigmoid(t[e].y))));
       }
-      st8((T *)p.y + (r0 + u * stride + me.row) * HD + col, x[u]);
+      put8((T *)p.y + r * HD + col, y);
     }
   }
 }
 
-template <typename T, int D, int kRowsAhead>
-__global__ void __launch_bounds__(kMaxThreads)
-    group_norm_grad_kernel(const __grid_constant__ NormGradProblem q, const __grid_constant__ Cut cut) {
+template <typename T, int D, bool kGate, int kRowsAhead>
+__global__ void __launch_bounds__(kMaxThreads, 2)
+    group_norm_grad_kernel(const __grid_constant__ NormGradProblem q, const __grid_constant__ Cut cut,
+                           const __grid_constant__ Divider by_n) {
   __shared__ float sums[kMaxThreads][16 + 1];
   const NormProblem &p = q.p;
   const Place<D> me(cut, p.H);
-  const long tokens = (long)p.B * p.N, stride = (long)gridDim.x * cut.rows, HD = (long)p.H * D;
-  float w[8], b[8], dw[8], db[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) w[e] = 1.f, b[e] = dw[e] = db[e] = 0.f;
+  const uint32_t tokens = (uint32_t)((long)p.B * p.N);
+  const long stride = (long)gridDim.x * cut.rows, HD = (long)p.H * D;
   const long col = (long)me.h * D + me.c;
-  if (me.live && p.weight) ld8(p.weight + col, w);
-  if (me.live && p.bias) ld8(p.bias + col, b);
+  float2 w[4], b[4], dw[4], db[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) w[e] = both(1.f), b[e] = dw[e] = db[e] = both(0.f);
+  if (me.live && p.weight) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = reinterpret_cast<const float2 *>(p.weight + col)[e];
+  }
+  if (me.live && p.bias) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) b[e] = reinterpret_cast<const float2 *>(p.bias + col)[e];
+  }
   for (long r0 = (long)blockIdx.x * cut.rows; r0 < tokens; r0 += kRowsAhead * stride) {
-    float x[kRowsAhead][8], g[kRowsAhead][8], dy[kRowsAhead][8];
-    long at[kRowsAhead];
-    bool in[kRowsAhead];
+    Raw<T> x[kRowsAhead], g[kRowsAhead], dy[kRowsAhead];
 #pragma unroll
     for (int u = 0; u < kRowsAhead; ++u) {
       const long r = r0 + u * stride + me.row;
-      in[u] = me.live && r < tokens;
-      at[u] = 0;
-      if (in[u]) {
-        const long bi = r / p.N, n = r - bi * p.N;
-        at[u] = ((bi * p.H + me.h) * p.N + n) * D + me.c;
-        ld8((const T *)p.x + at[u], x[u]);
-        ld8((const T *)q.dy + r * HD + col, dy[u]);
-        if (p.gate) ld8((const T *)p.gate + r * HD + col, g[u]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[u][e] = dy[u][e] = g[u][e] = 0.f;
+      x[u].zero(), dy[u].zero(), g[u].zero();
+      if (me.live && r < tokens) {
+        const uint32_t bi = by_n.of((uint32_t)r), n = (uint32_t)r - bi * by_n.n;
+        x[u].load((const T *)p.x + (((long)bi * p.H + me.h) * p.N + n) * D + me.c);
+        dy[u].load((const T *)q.dy + r * HD + col);
+        if (kGate) g[u].load((const T *)p.gate + r * HD + col);
       }
     }
 #pragma unroll
     for (int u = 0; u < kRowsAhead; ++u) {
-      float rstd, o[8];
-      normalize<D>(x[u], p.eps, rstd);
-      float su = 0.f, suh = 0.f;
+      const long r = r0 + u * stride + me.row;
+      const bool in = me.live && r < tokens;
+      float2 h[4], t[4];
+      x[u].get(h);
+      dy[u].get(t);
+      const float rstd = normalize<D>(h, p.eps);
+      if (kGate) {
+        float2 gg[4], o[4];
+        g[u].get(gg);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float t = dy[u][e];
-        if (p.gate) {
-          const float gg = g[u][e], sg = sigmoid(gg);
-          o[e] = t * fmaf(x[u][e], w[e], b[e]) * sg * fmaf(gg, 1.f - sg, 1.f);
-          t *= gg * sg;
+        for (int e = 0; e < 4; ++e) {
+          const float2 sg = make_float2(sigmoid(gg[e].x), sigmoid(gg[e].y));
+          const float2 silu = __fmul2_rn(gg[e], sg);
+          // silu' = sigmoid + silu (1 - sigmoid)
+          const float2 ds = __ffma2_rn(__fmul2_rn(silu, both(-1.f)), sg, __fadd2_rn(sg, silu));
+          o[e] = __fmul2_rn(__fmul2_rn(t[e], __ffma2_rn(h[e], w[e], b[e])), ds);
+          t[e] = __fmul2_rn(t[e], silu);
         }
-        dw[e] = fmaf(t, x[u][e], dw[e]);
-        db[e] += t;
-        t *= w[e];
-        dy[u][e] = t;
-        su += t;
-        suh = fmaf(t, x[u][e], suh);
+        if (in) put8((T *)q.dgate + r * HD + col, o);
       }
-      if (p.gate && in[u]) st8((T *)q.dgate + (r0 + u * stride + me.row) * HD + col, o);
-      su = group_sum<D>(su) * (1.f / D);
-      suh = group_sum<D>(suh) * (1.f / D);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = rstd * (dy[u][e] - su - x[u][e] * suh);
-      if (in[u]) st8((T *)q.dx + at[u], o);
+      for (int e = 0; e < 4; ++e) {
+        dw[e] = __ffma2_rn(t[e], h[e], dw[e]);
+        db[e] = __fadd2_rn(db[e], t[e]);
+        t[e] = __fmul2_rn(t[e], w[e]);
+      }
+      const float su = group_sum<D>(sum8(t)) * (-1.f / D), suh = group_sum<D>(dot8(t, h)) * (-1.f / D);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) t[e] = __fmul2_rn(__fadd2_rn(__ffma2_rn(h[e], both(suh), t[e]), both(su)), both(rstd));
+      if (in) {
+        const uint32_t bi = by_n.of((uint32_t)r), n = (uint32_t)r - bi * by_n.n;
+        put8((T *)q.dx + (((long)bi * p.H + me.h) * p.N + n) * D + me.c, t);
+      }
     }
   }
   if (!q.ws) return;
   // the block's column sums over its token rows, rows added in order
 #pragma unroll
-  for (int e = 0; e < 8; ++e) sums[threadIdx.x][e] = dw[e], sums[threadIdx.x][8 + e] = db[e];
+  for (int e = 0; e < 4; ++e) {
+    sums[threadIdx.x][2 * e] = dw[e].x, sums[threadIdx.x][2 * e + 1] = dw[e].y;
+    sums[threadIdx.x][8 + 2 * e] = db[e].x, sums[threadIdx.x][9 + 2 * e] = db[e].y;
+  }
   __syncthreads();
   if (me.live && me.row == 0) {
     const int per_row = cut.heads * (D / 8);
+    float o[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[e] = sums[threadIdx.x][e];
     for (int r = 1; r < cut.rows; ++r)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        dw[e] += sums[threadIdx.x + r * per_row][e];
-        db[e] += sums[threadIdx.x + r * per_row][8 + e];
-      }
+      for (int e = 0; e < 16; ++e) o[e] += sums[threadIdx.x + r * per_row][e];
     float *dst = q.ws + (long)blockIdx.x * 2 * HD + col;
-    st8(dst, dw);
-    st8(dst + HD, db);
+#pragma unroll
+    for (int e = 0; e < 16; e += 4) st4(dst + (e >> 3) * HD + (e & 7), o[e], o[e + 1], o[e + 2], o[e + 3]);
   }
 }
 
-// Column sums of the blocks' sums [blocks][2][HD], a warp per column pair set: thread = column.
+// Column sums of the blocks' sums [blocks][2][HD]: 32 columns a block, four warps over the rows.
 __global__ void __launch_bounds__(128) norm_columns_kernel(const float *ws, int blocks, long HD, float *dw, float *db) {
   __shared__ float part[4][32];
   const long col = (long)blockIdx.x * 32 + (threadIdx.x & 31);
@@ -250,14 +310,18 @@ int token_blocks(const Cut &c, long tokens, int per_sm, int ahead) {
   return (int)std::max(1L, std::min<long>(turns, std::max(1, sms * per_sm / c.slabs)));
 }
 
-constexpr int kAheadFwd = 4, kAheadGrad = 2, kPerSmGrad = 4;
+constexpr int kAheadFwd = 4, kAheadGrad = 2, kPerSmGrad = 2;
 
 template <typename T, int D>
 cudaError_t launch_fwd(const NormProblem &p) {
   const Cut c = make_cut(p.H, D);
   LaunchTimer timer(kKGroupNorm, p.stream);
   const dim3 grid((unsigned)token_blocks(c, (long)p.B * p.N, 1 << 20, kAheadFwd), (unsigned)c.slabs);
-  group_norm_kernel<T, D, kAheadFwd><<<grid, c.threads, 0, p.stream>>>(p, c);
+  const Divider by_n = make_divider((uint32_t)p.N);
+  if (p.gate)
+    group_norm_kernel<T, D, true, kAheadFwd><<<grid, c.threads, 0, p.stream>>>(p, c, by_n);
+  else
+    group_norm_kernel<T, D, false, kAheadFwd><<<grid, c.threads, 0, p.stream>>>(p, c, by_n);
   const cudaError_t e = cudaGetLastError();
   timer.done(e);
   if (e == cudaSuccess) count_launch();
@@ -272,7 +336,12 @@ cudaError_t launch_grad(const NormGradProblem &q) {
   cudaError_t e;
   {
     LaunchTimer timer(kKGroupNormBackward, p.stream);
-    group_norm_grad_kernel<T, D, kAheadGrad><<<dim3((unsigned)blocks, (unsigned)c.slabs), c.threads, 0, p.stream>>>(q, c);
+    const Divider by_n = make_divider((uint32_t)p.N);
+    const dim3 grid((unsigned)blocks, (unsigned)c.slabs);
+    if (p.gate)
+      group_norm_grad_kernel<T, D, true, kAheadGrad><<<grid, c.threads, 0, p.stream>>>(q, c, by_n);
+    else
+      group_norm_grad_kernel<T, D, false, kAheadGrad><<<grid, c.threads, 0, p.stream>>>(q, c, by_n);
     e = cudaGetLastError();
     timer.done(e);
     if (e != cudaSuccess) return e;
