@@ -43,7 +43,7 @@ la_status gated(const void *q, const void *k, const void *v, const float *g, con
   if (st != LA_OK) return st;
   if ((long)B * H == 0) return LA_OK;
   if (!S || (N > 0 && (!q || !k || !v || !g || !out))) return LA_ERR_INVALID_VALUE;
-  if (!aligned({q, k, v, out, S, ws}, 16) || !aligned({g, lengths}, 4)) return LA_ERR_MISALIGNED;
+  if (!aligned({q, k, v, out, S}, 16) || !aligned({ws}, 256) || !aligned({g, lengths}, 4)) return LA_ERR_MISALIGNED;
   GatedProblem p{q, k, v, g, lengths, from_state ? S : nullptr, out, S, B, H, N, dk, dv, dt, ws, (cudaStream_t)stream};
   if (N == 0) {
     if (from_state) return LA_OK;
@@ -87,7 +87,7 @@ la_status la_gated_backward(const void *q, const void *k, const void *v, const f
   if (st != LA_OK) return st;
   if ((long)B * H == 0) return LA_OK;
   if (N > 0 && (!q || !k || !v || !g || !dout || !dq || !dk || !dv || !dg)) return LA_ERR_INVALID_VALUE;
-  if (!aligned({q, k, v, dout, S0, dS, dq, dk, dv, dS0, workspace}, 16) || !aligned({g, dg, lengths}, 4))
+  if (!aligned({q, k, v, dout, S0, dS, dq, dk, dv, dS0}, 16) || !aligned({workspace}, 256) || !aligned({g, dg, lengths}, 4))
     return LA_ERR_MISALIGNED;
   cudaStream_t s = (cudaStream_t)stream;
   if ((st = api_device()) != LA_OK) return st;

@@ -19,7 +19,11 @@
 // HBM bounds it at 14 D bytes a token of inputs and results plus 8 D of states (D = 128: 8.1 us a
 // chunk at an SM's share); the tensor work is 13 products of 128 x 128 x D.
 //
-// Warps: 0 TMA, 1 MMA and TMEM owner, 2 running sums and dg, 3-6 <S, R>, 7-14 everything elementwise.
+// Two chunks overlap: the score warps weigh a chunk's products while the row warps still write the
+// previous chunk's results; the score columns are free for it as soon as dV is read.
+//
+// Warps: 0 TMA, 1 MMA and TMEM owner, 2 running sums and dg, 3-6 <S, R>, 7-14 scores, 15-22 rows
+// (scales, dot products, results).
 // Every wait is bounded (tc_ptx.cuh).
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -33,11 +37,10 @@ namespace la {
 namespace {
 using namespace gtc;
 
-constexpr int kThreads = 480;
-constexpr int kWarpGate = 2, kWarpDot = 3, kWarpEl = 7;
-constexpr int kElThreads = 256;
-constexpr uint32_t kBarEl = 1;
-constexpr int kRing = 3;
+constexpr int kThreads = 736;
+constexpr int kWarpGate = 2, kWarpDot = 3, kWarpScore = 7, kWarpRow = 15;
+constexpr uint32_t kBarScore = 1;
+constexpr int kRing = 2;
 
 template <int D>
 struct Lay {
@@ -48,13 +51,12 @@ struct Lay {
   static constexpr uint32_t dO = K + kTile;
   static constexpr uint32_t V = dO + kTile;
   static constexpr uint32_t Ring = V + kTile;
-  // W D [keys][queries] bf16: in V's place once V's products are done, if it fits there
-  static constexpr uint32_t WD = D == 128 ? V : Ring + kRing * kState;
-  static constexpr uint32_t Gate = Ring + kRing * kState + (D == 128 ? 0 : 2 * kBlk);  // hi 128, lo 128
-  static constexpr uint32_t Buf = Gate + 2 * kC * 4;                                   // 320 floats
-  static constexpr uint32_t Red = Buf + 320 * 4;                                       // 4 floats
+  static constexpr uint32_t WD = Ring + kRing * kState;  // W D [keys][queries] bf16
+  static constexpr uint32_t Gate = WD + 2 * kBlk;        // hi 128, lo 128
+  static constexpr uint32_t Buf = Gate + 2 * kC * 4;     // 320 floats
+  static constexpr uint32_t Red = Buf + 320 * 4;         // 4 floats
   static constexpr uint32_t Bars = Red + 16;
-  static constexpr int kNumBars = 2 + 2 * kRing + 13;
+  static constexpr int kNumBars = 3 + 2 * kRing + 15;
   static constexpr uint32_t Misc = Bars + kNumBars * 8;
   static constexpr uint32_t Bytes = Misc + 16;
 };
@@ -63,29 +65,33 @@ constexpr uint32_t kColP = 0, kColD = 128, kColQ = 256, kColK = 384;  // dV in D
 
 struct Params {
   CUtensorMap tq, tk, tv, td;  // boxes of 64 x 128
+  CUtensorMap ts, tr;          // tiles of S and R: [blocks][D][64], boxes of one part
   const float *g;
   const int *lengths;
   const uint8_t *s_tiles, *r_tiles;
   __nv_bfloat16 *dq, *dk, *dv;
   float *dg;
+  float *mail;  // [CTAs][3][128] what each token adds to dg
   long N, n, items;
   int H;
+  bool wide;  // dq, dk, dv are 32-byte aligned
 };
 
 // Partial row sums of key rows [32 q, 32 q + 32) over queries i >= 32 q, packed.
 __device__ __forceinline__ int part_at(int q, int i) { return q * 128 - 16 * q * (q - 1) + i - 32 * q; }
 
-// Sum over the warp's lanes of x[c], returned by lane c.
-__device__ __forceinline__ float column_sums(float (&x)[32], int lane) {
+// Sum over the warp's lanes of x[c], returned by lanes c and c + 16.
+__device__ __forceinline__ float column_sums(uint32_t (&x)[16], int lane) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
+  for (int o = 8; o > 0; o >>= 1)
 #pragma unroll
     for (int k = 0; k < o; ++k) {
       const bool up = lane & o;
-      const float give = up ? x[k] : x[k + o], keep = up ? x[k + o] : x[k];
-      x[k] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+      const uint32_t give = up ? x[k] : x[k + o], keep = up ? x[k + o] : x[k];
+      x[k] = __float_as_uint(__uint_as_float(keep) + __uint_as_float(__shfl_xor_sync(0xffffffffu, give, o)));
     }
-  return x[0];
+  const float s = __uint_as_float(x[0]);
+  return s + __shfl_xor_sync(0xffffffffu, s, 16);
 }
 
 // Dot of 32 fp32 values (raw bits) with 32 bf16 values of a swizzled row.
@@ -125,10 +131,11 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
     return;
   }
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::Bars);
-  uint64_t *full_kq = bars, *full_vd = bars + 1, *ring_full = bars + 2, *ring_free = ring_full + kRing,
+  uint64_t *full_kq = bars, *full_v = bars + 1, *full_d = bars + 2, *ring_full = bars + 3, *ring_free = ring_full + kRing,
            *b0 = ring_free + kRing, *tok_free = b0, *gate_full = b0 + 1, *e_full = b0 + 2, *el_done = b0 + 3,
            *q_in = b0 + 4, *k_in = b0 + 5, *v_in = b0 + 6, *x_ready = b0 + 7, *out_full = b0 + 8, *out_free = b0 + 9,
-           *dg_in = b0 + 10, *dot_full = b0 + 11, *dot_free = b0 + 12;
+           *dg_in = b0 + 10, *dot_full = b0 + 11, *dot_free = b0 + 12,
+           *v_free = b0 + 13, *d_free = b0 + 14;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::Misc);
   volatile uint32_t *abort_word = reinterpret_cast<volatile uint32_t *>(sm + L::Misc + 4);
   uint64_t *drain = reinterpret_cast<uint64_t *>(sm + L::Misc + 8);
@@ -139,7 +146,9 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
 
   if (threadIdx.x == 0) {
     mbar_init(full_kq, 1);
-    mbar_init(full_vd, 1);
+    mbar_init(full_v, 1);
+    mbar_init(full_d, 1);
+    mbar_init(v_free, 1);
     for (int s = 0; s < kRing; ++s) {
       mbar_init(&ring_full[s], 1);
       mbar_init(&ring_free[s], 1);
@@ -147,14 +156,15 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
     mbar_init(tok_free, 1);
     mbar_init(gate_full, 32);
     mbar_init(e_full, 1);
-    mbar_init(el_done, kElThreads);
+    mbar_init(el_done, 256);
     mbar_init(q_in, 1);
     mbar_init(k_in, 1);
     mbar_init(v_in, 1);
-    mbar_init(x_ready, kElThreads);
+    mbar_init(x_ready, 256);
     mbar_init(out_full, 1);
-    mbar_init(out_free, kElThreads);
-    mbar_init(dg_in, 128);
+    mbar_init(out_free, 256);
+    mbar_init(d_free, 256);
+    mbar_init(dg_in, 256 + 128);
     mbar_init(dot_full, 4);
     mbar_init(dot_free, 32);
     mbar_init(drain, 1);
@@ -185,13 +195,14 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
   if (warp == 0) {
     if (lane == 0) {
       int it = 0, ring = 0;
-      bool kq = false, vd = false, ok = true;
-      auto piece = [&](const uint8_t *src) {
+      int kq = 0, vd = 0;  // tiles issued
+      bool ok = true;
+      auto piece = [&](const CUtensorMap *map, long x, int part) {
         const int s = ring % kRing;
         if (ring >= kRing) ok = ok && mbar_wait(&ring_free[s], (ring / kRing - 1) & 1, abort_word, status);
         if (!ok) return;
         mbar_arrive_expect_tx(&ring_full[s], kState);
-        bulk_load(sm + L::Ring + s * kState, src, kState, &ring_full[s]);
+        tma_load_3d(sm + L::Ring + s * kState, map, &ring_full[s], 0, 0, (int)(2 * x + part) * (D / 64));
         ++ring;
       };
       auto tile = [&](uint32_t at, const CUtensorMap *map, uint64_t *bar, const Item &w) {
@@ -200,25 +211,27 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
       for (long x = blockIdx.x; x < p.items && ok; x += gridDim.x) {
         const Item w = item(x);
         if (w.tv == 0) continue;
-        const uint8_t *S = p.s_tiles + x * (size_t)(2 * kState), *R = p.r_tiles + x * (size_t)(2 * kState);
-        piece(S);
-        piece(S + kState);
-        piece(R);
-        if (ok && it > 0) ok = mbar_wait(tok_free, (it - 1) & 1, abort_word, status);
+        piece(&p.ts, x, 0);
+        piece(&p.ts, x, 1);
+        if (ok && it > 0) ok = mbar_wait(v_free, (it - 1) & 1, abort_word, status);
         if (!ok) break;
-        kq = vd = true;
+        mbar_arrive_expect_tx(full_v, L::kTile);
+        tile(L::V, &p.tv, full_v, w);
+        vd = it + 1;
+        if (it > 0) ok = mbar_wait(tok_free, (it - 1) & 1, abort_word, status);
+        if (!ok) break;
         mbar_arrive_expect_tx(full_kq, 2 * L::kTile);
         tile(L::K, &p.tk, full_kq, w);
         tile(L::Q, &p.tq, full_kq, w);
-        mbar_arrive_expect_tx(full_vd, 2 * L::kTile);
-        tile(L::V, &p.tv, full_vd, w);
-        tile(L::dO, &p.td, full_vd, w);
-        ++it;
-        piece(R + kState);
+        mbar_arrive_expect_tx(full_d, L::kTile);
+        tile(L::dO, &p.td, full_d, w);
+        kq = ++it;
+        piece(&p.tr, x, 0);
+        piece(&p.tr, x, 1);
       }
       for (int r = max(0, ring - kRing); r < ring; ++r) wait_drain(&ring_full[r % kRing], (r / kRing) & 1, status);
-      if (kq) wait_drain(full_kq, (it - 1) & 1, status);
-      if (vd) wait_drain(full_vd, (it - 1) & 1, status);
+      if (kq) wait_drain(full_kq, (kq - 1) & 1, status), wait_drain(full_d, (kq - 1) & 1, status);
+      if (vd) wait_drain(full_v, (vd - 1) & 1, status);
     }
   } else if (warp == 1) {
     if (lane == 0) {
@@ -234,15 +247,19 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
         const uint32_t ph = it & 1;
         auto wait_ring = [&]() { return mbar_wait(&ring_full[ring % kRing], (ring / kRing) & 1, abort_word, status); };
         if (!mbar_wait(gate_full, ph, abort_word, status)) break;
-        if (it > 0 && !mbar_wait(out_free, ph ^ 1, abort_word, status)) break;
         if (!mbar_wait(full_kq, ph, abort_word, status)) break;
+        // the columns of P: the previous W P is read by the previous dV's product, in issue order
         tc_fence_after();
 #pragma unroll 4
         for (int ks = 0; ks < kDs; ++ks) mma_bf16(tP, kdesc(sK, ks), kdesc(sQ, ks), iE, ks > 0);
-        if (!mbar_wait(full_vd, ph, abort_word, status)) break;
+        if (!mbar_wait(full_v, ph, abort_word, status) || !mbar_wait(full_d, ph, abort_word, status)) break;
+        if (it > 0 && !mbar_wait(d_free, ph ^ 1, abort_word, status)) break;
+        tc_fence_after();
 #pragma unroll 4
         for (int ks = 0; ks < kDs; ++ks) mma_bf16(tD, kdesc(sV, ks), kdesc(sO, ks), iE, ks > 0);
         mma_commit(e_full);
+        if (it > 0 && !mbar_wait(out_free, ph ^ 1, abort_word, status)) break;
+        tc_fence_after();
         // dQ = dO S^T, both parts of S
         bool ok = true;
         for (int part = 0; part < 2 && ok; ++part) {
@@ -269,6 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
         for (int ks = 0; ks < kDs; ++ks) mma_bf16(tK, kdesc(sV, ks), kdesc(r_lo, ks, D * 128), iKK, 1);
         mma_commit(&ring_free[ring % kRing]);
         ++ring;
+        mma_commit(v_free);
         mma_commit(k_in);
         // dV = K R, over D^T once that is read
         if (!mbar_wait(el_done, ph, abort_word, status)) break;
@@ -296,11 +314,14 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
   } else if (warp == kWarpGate) {
     // ---- running sums for the next chunk, dg of the current one ----
     int it = 0;
-    auto gates = [&](const Item &w) -> bool {
-      scan_gates(p.g + w.bh * p.N + w.t0, w.tv, lane, hi, lo);
+    auto fetch = [&](const Item &w) { return load_gates(p.g + w.bh * p.N + w.t0, w.tv, lane); };
+    auto gates = [&](const Item &w, float4 g) -> bool {
+      scan_gates(g, lane, hi, lo);
       if (p.lengths && w.tv < kC) {
         // padding tokens are contracted over: clear whatever they hold
-        if (!warp_wait(full_kq, it & 1, abort_word) || !warp_wait(full_vd, it & 1, abort_word)) return false;
+        if (!warp_wait(full_kq, it & 1, abort_word) || !warp_wait(full_v, it & 1, abort_word) ||
+            !warp_wait(full_d, it & 1, abort_word))
+          return false;
         for (int e = w.tv * (D / 8) + lane; e < kC * (D / 8); e += 32) {
           const int row = e / (D / 8), ch = e % (D / 8);
           const uint32_t off = (ch >> 3) * kBlk + sw128_offset(row, (ch & 7) * 8);
@@ -321,42 +342,52 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
       return x;
     };
     long x = next(blockIdx.x);
-    bool ok = x < p.items && gates(item(x));
+    bool ok = x < p.items;
+    if (ok) ok = gates(item(x), fetch(item(x)));
     while (ok && x < p.items) {
       const Item w = item(x);
       const float total = exp2f(hi[kC - 1] + lo[kC - 1]);
+      x = next(x + gridDim.x);
+      Item w2 = w;
+      float4 g2 = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (x < p.items) w2 = item(x), g2 = fetch(w2);
       if (!warp_wait(dg_in, it & 1, abort_word) || !warp_wait(dot_full, it & 1, abort_word)) break;
-      const float4 e4 = *reinterpret_cast<const float4 *>(buf + 4 * lane);
-      const float4 r4 = *reinterpret_cast<const float4 *>(buf + kC + 4 * lane);
-      const double over = (double)total * ((red[0] + red[1]) + (red[2] + red[3]));
+      const float *mail = p.mail + (long)blockIdx.x * 3 * kC + 4 * lane;
+      const float4 s4 = __ldcg(reinterpret_cast<const float4 *>(mail)), l4 = __ldcg(reinterpret_cast<const float4 *>(mail + kC));
+      const float4 r4 = __ldcg(reinterpret_cast<const float4 *>(mail + 2 * kC));
+      const float4 e4 = make_float4(s4.x + l4.x, s4.y + l4.y, s4.z + l4.z, s4.w + l4.w);
+      const float over = total * ((red[0] + red[1]) + (red[2] + red[3]));
       __syncwarp();
       mbar_arrive(dot_free);
+      ++it;
+      if (x < p.items) ok = gates(w2, g2);  // the next chunk waits for these, nothing waits for dg
       // suffix sums of what queries at or behind t add, prefix sums of what keys before t add
-      double e[4] = {e4.x, e4.y, e4.z, e4.w}, r[4] = {r4.x, r4.y, r4.z, r4.w};
+      const float e[4] = {e4.x, e4.y, e4.z, e4.w}, r[4] = {r4.x, r4.y, r4.z, r4.w};
+      Sum2 es{0.f, 0.f}, rs{0.f, 0.f};
 #pragma unroll
-      for (int m = 2; m >= 0; --m) e[m] += e[m + 1];
-      double behind = e[0];
+      for (int m = 0; m < 4; ++m) es.add(e[m]), rs.add(r[m]);
+      Sum2 behind = warp_scan_others<true>(es, lane), before = warp_scan_others<false>(rs, lane);
+      float dgv[4];
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double y = __shfl_down_sync(0xffffffffu, behind, o);
-        if (lane + o < 32) behind += y;
+      for (int m = 3; m >= 0; --m) {
+        behind.add(e[m]);
+        Sum2 v = behind;
+        Sum2 b = before;
+#pragma unroll
+        for (int k = 0; k < m; ++k) b.add(r[k]);
+        v.add(b.s, b.e);
+        v.add(over);
+        dgv[m] = v.s + v.e;
       }
-      behind -= e[0];
-      const double mine = (r[0] + r[1]) + (r[2] + r[3]);
-      double before = warp_scan(mine, lane) - mine;
       float *dg = p.dg + w.bh * p.N + w.t0;
       const int rows = (int)min((long)kC, p.N - w.t0);
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
         const int t = 4 * lane + m;
-        if (t < rows) dg[t] = t < w.tv ? (float)(e[m] + behind + before + over) : 0.f;
-        before += r[m];
+        if (t < rows) dg[t] = t < w.tv ? dgv[m] : 0.f;
       }
-      ++it;
-      x = next(x + gridDim.x);
-      if (x < p.items) ok = gates(item(x));
     }
-  } else if (warp < kWarpEl) {
+  } else if (warp < kWarpScore) {
     // ---- <S, R> of the stored pairs ----
     int it = 0;
     for (long x = blockIdx.x; x < p.items; x += gridDim.x) {
@@ -375,139 +406,151 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
       }
       ++it;
     }
-  } else {
-    // ---- elementwise: weights, row scales, results ----
-    const int q = warp & 3, half = (warp - kWarpEl) >> 2, T = q * 32 + lane;
+  } else if (warp < kWarpRow) {
+    // ---- scores: key T (lane) against 64 queries ----
+    const int q = warp & 3, half = (warp - kWarpScore) >> 2, T = q * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16);
-    constexpr int kCols = D / 64;  // 32-column blocks of dQ, dK, dV per thread
+    float *mail = p.mail + (long)blockIdx.x * 3 * kC;
+    int it = 0;
+    for (long x = blockIdx.x; x < p.items; x += gridDim.x) {
+      if (item(x).tv == 0) continue;
+      const uint32_t ph = it & 1;
+      bool ok = mbar_wait(gate_full, ph, abort_word, status) && mbar_wait(e_full, ph, abort_word, status);
+      if (bar_or(kBarScore, 256, !ok)) break;  // also: the last chunk's partial sums are read
+      tc_fence_after();
+      // W P to tensor memory, W D to shared memory, and the sums of W P D by key and by query
+      const float hi_j = hi[T], lo_j = lo[T];
+      float2 col = make_float2(0.f, 0.f);
+#pragma unroll 1
+      for (int b = 0; b < 4; ++b) {
+        const int i0 = 64 * half + 16 * b;  // 16 queries: none of them, all, or those from the key on
+        const bool some = i0 + 15 >= 32 * q, cut = i0 < 32 * q + 32;
+        uint32_t o[8];
+        uint4 wd[2];
+        uint32_t *wdw = reinterpret_cast<uint32_t *>(wd);
+        if (!some) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = wdw[e] = 0u;
+        } else {
+          uint32_t pr[16], dr[16];
+          tmem_ld16x2(tl + kColP + i0, tl + kColD + i0, pr, dr);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float4 h = *reinterpret_cast<const float4 *>(hi + i0 + 4 * e), l = *reinterpret_cast<const float4 *>(lo + i0 + 4 * e);
+            float f[4];
+            decay4(h, l, hi_j, lo_j, 1.f, f);
+#pragma unroll
+            for (int k = 0; k < 4; k += 2) {
+              const int c = 4 * e + k;
+              const float2 pp = make_float2(__uint_as_float(pr[c]), __uint_as_float(pr[c + 1]));
+              float2 pw = __fmul2_rn(pp, make_float2(f[k], f[k + 1]));
+              float2 dw = __fmul2_rn(make_float2(__uint_as_float(dr[c]), __uint_as_float(dr[c + 1])), make_float2(f[k], f[k + 1]));
+              float2 m = __fmul2_rn(pp, dw);
+              if (cut) {  // queries before the key: nothing; its own: no part in dg
+                const int i = i0 + c;
+                pw = make_float2(i >= T ? pw.x : 0.f, i + 1 >= T ? pw.y : 0.f);
+                dw = make_float2(i >= T ? dw.x : 0.f, i + 1 >= T ? dw.y : 0.f);
+                m = make_float2(i > T ? m.x : 0.f, i + 1 > T ? m.y : 0.f);
+              }
+              col = __fadd2_rn(col, m);
+              o[c / 2] = pack_bf16(pw.x, pw.y);
+              wdw[c / 2] = pack_bf16(dw.x, dw.y);
+              pr[c] = __float_as_uint(m.x), pr[c + 1] = __float_as_uint(m.y);
+            }
+          }
+          const float s = column_sums(pr, lane);
+          if (lane < 16) buf[part_at(q, i0 + lane)] = s;
+        }
+        tmem_st8_nowait(tl + kColP + 64 * half + 8 * b, o);  // over columns this warp alone reads, and has read
+        uint8_t *W = sm + L::WD + half * kBlk;
+        *reinterpret_cast<uint4 *>(W + sw128_offset(T, 16 * b)) = wd[0];
+        *reinterpret_cast<uint4 *>(W + sw128_offset(T, 16 * b + 8)) = wd[1];
+      }
+      tmem_wait_st();
+      fence_async_smem();
+      tc_fence_before();
+      mbar_arrive(el_done);
+      // -(sum over later queries) + (sum over earlier keys), the two halves' column sums first
+      if (bar_or(kBarScore, 256, false)) break;
+      float ends = -(col.x + col.y);
+      float row = 0.f;
+      if (half == 0)
+        for (int k = 0; k <= q; ++k) row += buf[part_at(k, T)];
+      named_bar(kBarScore, 256);
+      if (half == 1) buf[T] = ends;
+      named_bar(kBarScore, 256);
+      if (half == 0) {
+        __stcg(mail + T, row + ends + buf[T]);
+        mbar_arrive(dg_in);
+      }
+      ++it;
+    }
+  } else {
+    // ---- rows: scale the first products, their dot products, results ----
+    // half 0: dQ (and dV's first half of columns), half 1: dK (and the second)
+    const int q = warp & 3, half = (warp - kWarpRow) >> 2, T = q * 32 + lane;
+    const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16), tX = tl + (half ? kColK : kColQ);
+    const uint8_t *X = sm + (half ? L::K : L::Q);
+    float *mail = p.mail + (long)blockIdx.x * 3 * kC + (1 + half) * kC;
+    __nv_bfloat16 *dx = half ? p.dk : p.dq;
     int it = 0;
     for (long x = blockIdx.x; x < p.items; x += gridDim.x) {
       const Item w = item(x);
       const int rows = (int)min((long)kC, p.N - w.t0);
-      const long at = (w.bh * p.N + w.t0 + T) * D + half * (D / 2);
-      auto put = [&](__nv_bfloat16 *dst, int cb, const uint4 (&v)[4], bool in) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          reinterpret_cast<uint4 *>(dst + at + cb * 32)[e] = in ? v[e] : make_uint4(0u, 0u, 0u, 0u);
-      };
-      if (w.tv == 0) {  // padding only
+      const long at = (w.bh * p.N + w.t0 + T) * D;
+      if (w.tv == 0) {  // padding only: zero gradients
         const uint4 z[4] = {};
-        if (T < rows)
-          for (int cb = 0; cb < kCols; ++cb) put(p.dq, cb, z, false), put(p.dk, cb, z, false), put(p.dv, cb, z, false);
-        if (half == 0 && T < rows) p.dg[w.bh * p.N + w.t0 + T] = 0.f;
+        if (T < rows) {
+          for (int cb = 0; cb < D / 32; ++cb) store_row64(dx + at + cb * 32, z, p.wide);
+          for (int cb = 0; cb < D / 64; ++cb) store_row64(p.dv + at + half * (D / 2) + cb * 32, z, p.wide);
+          if (half == 0) p.dg[w.bh * p.N + w.t0 + T] = 0.f;
+        }
         continue;
       }
       const uint32_t ph = it & 1;
-      bool ok = mbar_wait(gate_full, ph, abort_word, status) && mbar_wait(e_full, ph, abort_word, status);
-      if (bar_or(kBarEl, kElThreads, !ok)) break;
+      if (!warp_wait(gate_full, ph, abort_word)) break;
+      const float ew = exp2f((hi[kC - 1] - hi[T]) + (lo[kC - 1] - lo[T])), f = half ? ew : exp2f(hi[T] + lo[T]);
+      if (!warp_wait(half ? k_in : q_in, ph, abort_word)) break;
       tc_fence_after();
-      // key T (lane) against queries i: W P to tensor memory, W D to shared memory, and W P D's sums
-      const float hi_j = hi[T], lo_j = lo[T];
-      float col = 0.f;
-      uint32_t wd[2][16];
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int ib = 2 * half + b;
-        uint32_t o[16];
-        if (ib < q) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = wd[b][e] = 0u;
-        } else {
-          uint32_t pr[32], dr[32];
-          tmem_ld32x2(tl + kColP + ib * 32, tl + kColD + ib * 32, pr, dr);
-          float m[32];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int i0 = ib * 32 + 4 * e;
-            const float4 h = *reinterpret_cast<const float4 *>(hi + i0), l = *reinterpret_cast<const float4 *>(lo + i0);
-            const float y[4] = {(h.x - hi_j) + (l.x - lo_j), (h.y - hi_j) + (l.y - lo_j), (h.z - hi_j) + (l.z - lo_j),
-                                (h.w - hi_j) + (l.w - lo_j)};
-            float pw[4], dw[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int i = i0 + k;
-              const float f = ex2_approx(y[k]), pp = __uint_as_float(pr[4 * e + k]);
-              pw[k] = i >= T ? pp * f : 0.f;
-              dw[k] = i >= T ? __uint_as_float(dr[4 * e + k]) * f : 0.f;
-              m[4 * e + k] = i > T ? pp * dw[k] : 0.f;
-              col += m[4 * e + k];
-            }
-            o[2 * e] = pack_bf16(pw[0], pw[1]);
-            o[2 * e + 1] = pack_bf16(pw[2], pw[3]);
-            wd[b][2 * e] = pack_bf16(dw[0], dw[1]);
-            wd[b][2 * e + 1] = pack_bf16(dw[2], dw[3]);
-          }
-          buf[part_at(q, ib * 32 + lane)] = column_sums(m, lane);
-        }
-        tmem_st16(tl + kColP + 64 * half + 16 * b, o);  // over columns this warp alone reads
-      }
-      tc_fence_before();
-      mbar_arrive(el_done);
-      ok = mbar_wait(k_in, ph, abort_word, status) && mbar_wait(q_in, ph, abort_word, status);
-      if (bar_or(kBarEl, kElThreads, !ok)) break;  // and the partial sums are complete
-      tc_fence_after();
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          *reinterpret_cast<uint4 *>(sm + L::WD + half * kBlk + sw128_offset(T, b * 32 + 8 * e)) =
-              make_uint4(wd[b][4 * e], wd[b][4 * e + 1], wd[b][4 * e + 2], wd[b][4 * e + 3]);
-      float ends = -col, rgt = 0.f;  // what this token adds as a query (dg_t, t <= T) and as a key (t > T)
-      if (half == 0)
-        for (int k = 0; k <= q; ++k) ends += buf[part_at(k, T)];
-      const float ec = exp2f(hi_j + lo_j), ew = exp2f((hi[kC - 1] - hi_j) + (lo[kC - 1] - lo_j));
-#pragma unroll
-      for (int cb = 0; cb < kCols; ++cb) {
-        const int c0 = half * (D / 2) + cb * 32;
+      float dot = 0.f;
+#pragma unroll 1
+      for (int cb = 0; cb < D / 32; ++cb) {
         uint32_t r[32];
-        tmem_ld32(tl + kColQ + c0, r);
-        scale32(r, ec);
-        ends += dot_row32(r, sm + L::Q + (c0 >> 6) * kBlk, T, c0 & 63);
-        tmem_st32(tl + kColQ + c0, r);
-        tmem_ld32(tl + kColK + c0, r);
-        scale32(r, ew);
-        rgt += dot_row32(r, sm + L::K + (c0 >> 6) * kBlk, T, c0 & 63);
-        tmem_st32(tl + kColK + c0, r);
+        tmem_ld32(tX + cb * 32, r);
+        scale32(r, f);
+        tmem_st32(tX + cb * 32, r);
+        dot += dot_row32(r, X + (cb >> 1) * kBlk, T, (cb & 1) * 32);
       }
-      ok = mbar_wait(v_in, ph, abort_word, status);
-      if (bar_or(kBarEl, kElThreads, !ok)) break;  // and the partial sums are read
+      __stcg(mail + T, dot);
+      mbar_arrive(dg_in);
+      if (!warp_wait(v_in, ph, abort_word)) break;
       tc_fence_after();
 #pragma unroll
-      for (int cb = 0; cb < kCols; ++cb) {
+      for (int cb = 0; cb < D / 64; ++cb) {
         uint32_t r[32];
         tmem_ld32(tl + kColD + half * (D / 2) + cb * 32, r);
         scale32(r, ew);
         tmem_st32(tl + kColD + half * (D / 2) + cb * 32, r);
       }
-      fence_async_smem();
       tc_fence_before();
       mbar_arrive(x_ready);
-      if (half == 1) buf[T] = ends, buf[kC + T] = rgt;
-      named_bar(kBarEl, kElThreads);
-      if (half == 0) {
-        buf[T] += ends;
-        buf[kC + T] += rgt;
-        mbar_arrive(dg_in);
-      }
-      ok = mbar_wait(out_full, ph, abort_word, status);
-      if (bar_or(kBarEl, kElThreads, !ok)) break;
+      if (!warp_wait(out_full, ph, abort_word)) break;
       tc_fence_after();
-      const bool in = T < w.tv;
-#pragma unroll
-      for (int cb = 0; cb < kCols; ++cb) {
-        const uint32_t c0 = half * (D / 2) + cb * 32;
+      // padding rows (T >= tv) are zero whatever the states hold
+      auto put = [&](uint32_t col, __nv_bfloat16 *dst) {
         uint32_t r[32];
         uint4 v[4];
-        tmem_ld32(tl + kColQ + c0, r);
+        tmem_ld32(col, r);
         to_bf16x32(r, v);
-        if (T < rows) put(p.dq, cb, v, in);
-        tmem_ld32(tl + kColK + c0, r);
-        to_bf16x32(r, v);
-        if (T < rows) put(p.dk, cb, v, in);
-        tmem_ld32(tl + kColD + c0, r);
-        to_bf16x32(r, v);
-        if (T < rows) put(p.dv, cb, v, in);
-      }
+        if (T >= w.tv) v[0] = v[1] = v[2] = v[3] = make_uint4(0u, 0u, 0u, 0u);
+        if (T < rows) store_row64(dst + at, v, p.wide);
+      };
+#pragma unroll 1
+      for (int cb = 0; cb < D / 64; ++cb) put(tl + kColD + half * (D / 2) + cb * 32, p.dv + half * (D / 2) + cb * 32);
+      tc_fence_before();
+      mbar_arrive(d_free);
+#pragma unroll 1
+      for (int cb = 0; cb < D / 32; ++cb) put(tX + cb * 32, dx + cb * 32);
       tc_fence_before();
       mbar_arrive(out_free);
       ++it;
@@ -537,6 +580,19 @@ Plan make_plan(long BH, long N, int D) {
   return t;
 }
 
+// The state pass's tiles as [blocks][D][64] bf16, one box a part (hi or lo).
+bool tile_map(CUtensorMap *m, const void *base, long chunks, int D) {
+  auto fn = tensor_map_encoder();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {64, (cuuint64_t)D, (cuuint64_t)(2 * chunks * (D / 64))};
+  cuuint64_t strides[2] = {128, (cuuint64_t)D * 128};
+  cuuint32_t box[3] = {64, (cuuint32_t)D, (cuuint32_t)(D / 64)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D>
 cudaError_t launch_chunks(const Params &cp, cudaStream_t stream) {
   cudaError_t e = ensure_smem_optin((const void *)gated_grad_tc_kernel<D>, (int)Lay<D>::Bytes);
@@ -559,7 +615,8 @@ cudaError_t read_and_clear_gated_grad_status(unsigned int *value) {
 size_t gated_tc_grad_workspace(long BH, long N, int D) {
   const Plan t = make_plan(BH, N, D);
   const size_t tiles = 2 * (size_t)BH * t.n * gated_tile_bytes(D);
-  return tiles + (t.segs > 1 ? sizeof(float) * (size_t)BH * t.segs * (2 * (size_t)D * D + 1) : 0);
+  const size_t mail = sizeof(float) * 3 * kC * std::max(1, device_info(-1).sm_count);
+  return tiles + mail + (t.segs > 1 ? sizeof(float) * (size_t)BH * t.segs * (2 * (size_t)D * D + 1) : 0);
 }
 
 cudaError_t launch_gated_grad_tc(const GatedGradProblem &b) {
@@ -567,7 +624,8 @@ cudaError_t launch_gated_grad_tc(const GatedGradProblem &b) {
   const int D = p.dk;
   const long BH = p.BH();
   const Plan t = make_plan(BH, p.N, D);
-  uint8_t *ws = (uint8_t *)p.ws;
+  const size_t mail = sizeof(float) * 3 * kC * std::max(1, device_info(-1).sm_count);
+  uint8_t *ws = (uint8_t *)p.ws + mail;
   const size_t tiles = (size_t)BH * t.n * gated_tile_bytes(D);
   GatedStateParams sp;
   memset(&sp, 0, sizeof sp);
@@ -598,10 +656,13 @@ cudaError_t launch_gated_grad_tc(const GatedGradProblem &b) {
   Params cp;
   memset(&cp, 0, sizeof cp);
   if (!gated_map(&cp.tq, p.q, BH, p.N, D, kC) || !gated_map(&cp.tk, p.k, BH, p.N, D, kC) ||
-      !gated_map(&cp.tv, p.v, BH, p.N, D, kC) || !gated_map(&cp.td, b.dout, BH, p.N, D, kC))
+      !gated_map(&cp.tv, p.v, BH, p.N, D, kC) || !gated_map(&cp.td, b.dout, BH, p.N, D, kC) ||
+      !tile_map(&cp.ts, sp.tiles[0], BH * t.n, D) || !tile_map(&cp.tr, sp.tiles[1], BH * t.n, D))
     return cudaErrorInvalidValue;
   cp.g = p.g, cp.lengths = p.lengths, cp.s_tiles = sp.tiles[0], cp.r_tiles = sp.tiles[1];
   cp.dq = (__nv_bfloat16 *)b.dq, cp.dk = (__nv_bfloat16 *)b.dk, cp.dv = (__nv_bfloat16 *)b.dv, cp.dg = b.dg;
+  cp.mail = (float *)p.ws;
+  cp.wide = (((uintptr_t)b.dq | (uintptr_t)b.dk | (uintptr_t)b.dv) & 31) == 0;
   cp.N = p.N, cp.n = t.n, cp.items = BH * t.n, cp.H = p.H;
   return D == 64 ? launch_chunks<64>(cp, p.stream) : launch_chunks<128>(cp, p.stream);
 }

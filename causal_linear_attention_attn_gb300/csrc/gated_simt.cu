@@ -51,10 +51,17 @@ struct Args {
   long N, n;
 };
 
-// Decays of the chunk's tokens (lane t: token t; tokens past the end decay by 1).
-__device__ __forceinline__ double chunk_scan(const Args &a, long bh, long t0, int tv, int lane) {
-  const double x = lane < tv ? log2_decay(a.g[bh * a.N + t0 + lane]) : 0.0;
-  return warp_scan(x, lane);
+// Running sum of the log2 decays up to token `lane` of the chunk (tokens past the end decay by 1).
+__device__ __forceinline__ Cum chunk_scan(const Args &a, long bh, long t0, int tv, int lane) {
+  const float g = lane < tv ? a.g[bh * a.N + t0 + lane] : 0.f;
+  const bool nan = __ballot_sync(0xffffffffu, isnan(g)) & (0xffffffffu >> (31 - lane));
+  return split_cum(warp_scan(fixed_log2_decay(g), lane), nan);
+}
+__device__ __forceinline__ Cum last_lane(Cum c) {
+  return Cum{__shfl_sync(0xffffffffu, c.hi, 31), __shfl_sync(0xffffffffu, c.lo, 31)};
+}
+__device__ __forceinline__ float decay_between(Cum from, Cum to) {
+  return exp2f((to.hi - from.hi) + (to.lo - from.lo));
 }
 
 template <typename Tin>
@@ -81,10 +88,9 @@ __global__ void __launch_bounds__(kThreads) gated_sums_kernel(const __grid_const
   if (t0 >= len) return;  // the scan stops before this chunk
   const int tv = (int)min((long)kT, len - t0);
   if (tid < 32) {
-    const double c = chunk_scan(a, bh, t0, tv, tid);
-    const double T = __shfl_sync(0xffffffffu, c, 31);
-    w[tid] = exp2f((float)(rev ? c : T - c));
-    if (tid == 0 && !rev) a.tot[bh * a.n + ch] = (float)T;
+    const Cum c = chunk_scan(a, bh, t0, tv, tid), T = last_lane(c);
+    w[tid] = rev ? exp2f(c.hi + c.lo) : decay_between(c, T);
+    if (tid == 0 && !rev) a.tot[bh * a.n + ch] = T.hi + T.lo;
   }
   const long row = bh * a.N + t0;
   load_rows(A, dk, (const Tin *)(rev ? a.q : a.k) + row * dk, dk, tv);
@@ -206,7 +212,7 @@ __global__ void __launch_bounds__(kThreads) gated_out_kernel(const __grid_consta
   if (t0 >= len) return;
   const int tv = (int)min((long)kT, len - t0);
   if (tid < 32) {
-    const Cum c = split_cum(chunk_scan(a, bh, t0, tv, tid));
+    const Cum c = chunk_scan(a, bh, t0, tv, tid);
     hi[tid] = c.hi;
     lo[tid] = c.lo;
   }
@@ -268,13 +274,11 @@ __global__ void __launch_bounds__(kThreads) gated_grad_kernel(const __grid_const
   }
   float total = 0.f;
   if (tid < 32) {
-    const double c = chunk_scan(a, bh, t0, tv, tid);
-    const double T = __shfl_sync(0xffffffffu, c, 31);
-    const Cum u = split_cum(c);
-    hi[tid] = u.hi;
-    lo[tid] = u.lo;
-    ew[tid] = exp2f((float)(T - c));
-    total = exp2f((float)T);
+    const Cum c = chunk_scan(a, bh, t0, tv, tid), T = last_lane(c);
+    hi[tid] = c.hi;
+    lo[tid] = c.lo;
+    ew[tid] = decay_between(c, T);
+    total = exp2f(T.hi + T.lo);
   }
   load_rows(Q, lk, (const Tin *)a.q + row * dk, dk, tv);
   load_rows(K, lk, (const Tin *)a.k + row * dk, dk, tv);
@@ -386,21 +390,24 @@ __global__ void __launch_bounds__(kThreads) gated_grad_kernel(const __grid_const
   }
   __syncthreads();
   if (tid < 32) {
-    double ends = 0.0, rgt = 0.0;  // what token `lane` adds to every dg_t with t <= lane, and with t > lane
-    for (int j = 0; j < kT; ++j) ends += (double)M[lane * (kT + 1) + j] - (double)M[j * (kT + 1) + lane];
+    // what token `lane` adds to every dg_t with t <= lane, and with t > lane
+    Sum2 ends{0.f, 0.f}, rgt{0.f, 0.f};
+    for (int j = 0; j < kT; ++j) {
+      ends.add(M[lane * (kT + 1) + j]);
+      ends.add(-M[j * (kT + 1) + lane]);
+    }
     for (int x = 0; x < kq; ++x) {
-      ends += left[lane * 33 + x];
-      rgt += right[lane * 33 + x];
+      ends.add(left[lane * 33 + x]);
+      rgt.add(right[lane * 33 + x]);
     }
     float over = 0.f;
     for (int x = 0; x < kThreads / 32; ++x) over += red[x];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double y = __shfl_down_sync(0xffffffffu, ends, o);
-      if (lane + o < 32) ends += y;
-    }
-    const double upto = warp_scan(rgt, lane) - rgt;
-    if (lane < rows) dg[lane] = lane < tv ? (float)(ends + upto + (double)total * over) : 0.f;
+    Sum2 all = warp_scan_others<true>(ends, lane);
+    const Sum2 upto = warp_scan_others<false>(rgt, lane);
+    all.add(ends.s, ends.e);
+    all.add(upto.s, upto.e);
+    all.add(total * over);
+    if (lane < rows) dg[lane] = lane < tv ? all.s + all.e : 0.f;
   }
 }
 

@@ -246,17 +246,14 @@ __global__ void __launch_bounds__(kThreads, 1) gated_state_tc_kernel(const __gri
       if (tiles) {
         join();
         if (main_row) {
-          uint8_t *t = tiles + (bh * p.n + chunk(i)) * (size_t)(D * D * 4) + (col0 >> 6) * (D * 128);
+          uint8_t *t = tiles + (bh * p.n + chunk(i)) * (size_t)(D * D * 4) + (col0 >> 6) * (D * 128) + row * 128 + (col0 & 63) * 2;
 #pragma unroll
           for (int b = 0; b < kB; ++b) {
-            uint4 h[4], l[4];
-            split_bf16x32(r[b], h, l);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t off = sw128_offset(row, (col0 & 63) + b * 32 + e * 8);
-              *reinterpret_cast<uint4 *>(t + off) = h[e];
-              *reinterpret_cast<uint4 *>(t + D * D * 2 + off) = l[e];
-            }
+            uint4 v[4];
+            to_bf16x32(r[b], v);
+            store_row64(t + b * 64, v, true);
+            rest_bf16x32(r[b], v);
+            store_row64(t + D * D * 2 + b * 64, v, true);
           }
         }
       }
@@ -284,16 +281,22 @@ __global__ void __launch_bounds__(kThreads, 1) gated_state_tc_kernel(const __gri
       }
     }
   } else {
-    double total = 0.0;
+    Sum2 total{0.f, 0.f};
+    const float *g = p.g + bh * p.N;
+    float4 cur = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (run > 0) cur = load_gates(g + chunk(0) * kC, valid(0), lane);
     for (int i = 0; i < run; ++i) {
+      float4 nxt = cur;
+      if (i + 1 < run) nxt = load_gates(g + chunk(i + 1) * kC, valid(i + 1), lane);
       if (i >= 2 && !warp_wait(&gate_free[i & 1], ((i >> 1) - 1) & 1, abort_word)) break;
       float *hi = gate + (i & 1) * 2 * kC;
-      scan_gates(p.g + bh * p.N + chunk(i) * kC, valid(i), lane, hi, hi + kC);
+      scan_gates(cur, lane, hi, hi + kC);
       __syncwarp();
-      total += (double)hi[kC - 1] + (double)hi[2 * kC - 1];
+      total.add(hi[kC - 1], hi[2 * kC - 1]);
       mbar_arrive(&gate_full[i & 1]);
+      cur = nxt;
     }
-    if (p.seg_tot && fin && dir == 0 && lane == 0) p.seg_tot[bh * p.segs + seg] = (float)total;
+    if (p.seg_tot && fin && dir == 0 && lane == 0) p.seg_tot[bh * p.segs + seg] = total.s + total.e;
   }
 
   tc_fence_before();

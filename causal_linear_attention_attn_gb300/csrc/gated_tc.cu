@@ -46,7 +46,7 @@ struct Lay {
   static constexpr uint32_t Sum = Sb + D * D * 2;  // D = 64: low rows of the state [64][65] fp32
   static constexpr uint32_t Gate = Sum + (D == 64 ? 64 * 65 * 4 : 0);
   static constexpr uint32_t Bars = Gate + 2 * 2 * kC * 4;
-  static constexpr int kNumBars = 20;
+  static constexpr int kNumBars = 22;
   static constexpr uint32_t Misc = Bars + kNumBars * 8;
   static constexpr uint32_t Bytes = Misc + 16;
 };
@@ -62,6 +62,7 @@ struct Params {
   float *S;
   long N;
   int H, segs, seg_chunks, init_segs, init_step;
+  bool wide;  // out is 32-byte aligned
 };
 
 template <int D>
@@ -73,9 +74,9 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
     return;
   }
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::Bars);
-  uint64_t *full_k = bars, *full_v = bars + 2, *kv_free = bars + 4, *gate_full = bars + 6, *gate_free = bars + 8,
+  uint64_t *full_k = bars, *full_v = bars + 2, *k_free = bars + 4, *gate_full = bars + 6, *gate_free = bars + 8,
            *full_q = bars + 10, *q_free = bars + 11, *p_full = bars + 12, *k_ready = bars + 13, *pp_ready = bars + 14,
-           *sb_ready = bars + 15, *s_full = bars + 16, *o_full = bars + 17, *o_free = bars + 18, *drain = bars + 19;
+           *sb_ready = bars + 15, *s_full = bars + 16, *o_full = bars + 17, *o_free = bars + 18, *drain = bars + 19, *v_free = bars + 20;  // v_free: [2]
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::Misc);
   volatile uint32_t *abort_word = reinterpret_cast<volatile uint32_t *>(sm + L::Misc + 4);
   unsigned int *status = &g_gated_status;
@@ -94,7 +95,8 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
     for (int b = 0; b < 2; ++b) {
       mbar_init(&full_k[b], 1);
       mbar_init(&full_v[b], 1);
-      mbar_init(&kv_free[b], 1);
+      mbar_init(&k_free[b], 1);
+      mbar_init(&v_free[b], 1);
       mbar_init(&gate_full[b], 32);
       mbar_init(&gate_free[b], 640);
     }
@@ -126,21 +128,21 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
         mbar_arrive_expect_tx(bar, L::kTile);
         for (int b = 0; b < D / 64; ++b) tma_load_3d(sm + at + b * kBlk, map, bar, 64 * b, tok, (int)bh);
       };
-      int k_issued = 0, q_issued = 0;
+      int k_issued = 0, q_issued = 0, v_issued = 0;
       for (int c = 0; c < nc; ++c) {
         const int s = c & 1, tok = (int)((c_lo + c) * kC);
-        if (c >= 2 && !mbar_wait(&kv_free[s], ((c >> 1) - 1) & 1, abort_word, status)) break;
+        if (c >= 2 && !mbar_wait(&k_free[s], ((c >> 1) - 1) & 1, abort_word, status)) break;
         load(L::K + s * L::kTile, &p.tk, &full_k[s], tok);
-        load(L::V + s * L::kTile, &p.tv, &full_v[s], tok);
         k_issued = c + 1;
         if (c >= 1 && !mbar_wait(q_free, (c - 1) & 1, abort_word, status)) break;
         load(L::Q, &p.tq, full_q, tok);
         q_issued = c + 1;
+        if (c >= 2 && !mbar_wait(&v_free[s], ((c >> 1) - 1) & 1, abort_word, status)) break;
+        load(L::V + s * L::kTile, &p.tv, &full_v[s], tok);
+        v_issued = c + 1;
       }
-      for (int c = max(0, k_issued - 2); c < k_issued; ++c) {
-        wait_drain(&full_k[c & 1], (c >> 1) & 1, status);
-        wait_drain(&full_v[c & 1], (c >> 1) & 1, status);
-      }
+      for (int c = max(0, k_issued - 2); c < k_issued; ++c) wait_drain(&full_k[c & 1], (c >> 1) & 1, status);
+      for (int c = max(0, v_issued - 2); c < v_issued; ++c) wait_drain(&full_v[c & 1], (c >> 1) & 1, status);
       if (q_issued) wait_drain(full_q, (q_issued - 1) & 1, status);
     }
   } else if (warp == 1) {
@@ -179,12 +181,13 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
           }
         }
         mma_commit(s_full);
+        mma_commit(&k_free[s]);
         if (!mbar_wait(pp_ready, c & 1, abort_word, status)) break;
         tc_fence_after();
 #pragma unroll 4
         for (int ks = 0; ks < 8; ++ks)  // keys [16 ks, ..): columns 8 ks of the first or the second half
           mma_bf16_ts(tA, tP + (ks < 4 ? 8 * ks : 32 + 8 * ks), mndesc(v, ks), iO, ks > 0);
-        mma_commit(&kv_free[s]);
+        mma_commit(&v_free[s]);
         mma_commit(o_full);
       }
       mma_commit(drain);
@@ -367,31 +370,39 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
       const bool in = i < valid(c);
       __nv_bfloat16 *dst = p.out + (bh * p.N + (c_lo + c) * kC + i) * D;
 #pragma unroll 1
-      for (int cb = 0; cb < D / 16; ++cb) {
-        uint32_t x[16], y[16];
-        tmem_ld16x2(tl + kColI + cb * 16, tl + kColA + cb * 16, x, y);
-        if (cb == D / 16 - 1) {
+      for (int cb = 0; cb < D / 32; ++cb) {
+        uint4 o[4];
+        uint32_t *ow = reinterpret_cast<uint32_t *>(o);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t x[16], y[16];
+          tmem_ld16x2(tl + kColI + cb * 32 + 16 * h, tl + kColA + cb * 32 + 16 * h, x, y);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float2 z = __ffma2_rn(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), make_float2(f, f),
+                                        make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])));
+            ow[8 * h + e] = pack_bf16(z.x, z.y);
+          }
+        }
+        if (cb == D / 32 - 1) {
           tc_fence_before();
           mbar_arrive(o_free);
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float2 z = __ffma2_rn(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), make_float2(f, f),
-                                      make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])));
-          x[e] = pack_bf16(z.x, z.y);
-        }
-        if (in) {
-          reinterpret_cast<uint4 *>(dst + cb * 16)[0] = make_uint4(x[0], x[1], x[2], x[3]);
-          reinterpret_cast<uint4 *>(dst + cb * 16)[1] = make_uint4(x[4], x[5], x[6], x[7]);
-        }
+        if (in) store_row64(dst + cb * 32, o, p.wide);
       }
     }
   } else {
+    const float *g = p.g + bh * p.N + c_lo * kC;
+    float4 cur = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (nc > 0) cur = load_gates(g, valid(0), lane);
     for (int c = 0; c < nc; ++c) {
+      float4 nxt = cur;
+      if (c + 1 < nc) nxt = load_gates(g + (c + 1) * kC, valid(c + 1), lane);
       if (c >= 2 && !warp_wait(&gate_free[c & 1], ((c >> 1) - 1) & 1, abort_word)) break;
       float *hi = gate + (c & 1) * 2 * kC;
-      scan_gates(p.g + bh * p.N + (c_lo + c) * kC, valid(c), lane, hi, hi + kC);
+      scan_gates(cur, lane, hi, hi + kC);
       mbar_arrive(&gate_full[c & 1]);
+      cur = nxt;
     }
   }
 
@@ -471,6 +482,7 @@ cudaError_t launch_gated_tc(const GatedProblem &p) {
   mp.g = p.g, mp.lengths = p.lengths, mp.out = (__nv_bfloat16 *)p.out, mp.S = p.S, mp.N = p.N, mp.H = p.H;
   mp.segs = (int)t.G, mp.seg_chunks = (int)t.seg_chunks, mp.init_segs = 1, mp.init_step = 0;
   mp.init = p.S0;
+  mp.wide = ((uintptr_t)p.out & 31) == 0;
   cudaError_t e = cudaSuccess;
   if (t.split()) {
     float *sums = (float *)p.ws, *tot = sums + (size_t)BH * t.init_segs() * D * D;

@@ -38,17 +38,28 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, ok);
 }
 
-// Running sums of a chunk's log2 decays (one warp, four tokens a lane; tokens from tv on decay by 1).
-__device__ __forceinline__ void scan_gates(const float *g, int tv, int lane, float *hi, float *lo) {
-  double x[4];
+// A chunk's log decays, four consecutive tokens a lane (tokens from tv on decay by 1).
+__device__ __forceinline__ float4 load_gates(const float *g, int tv, int lane) {
+  float x[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) x[e] = 4 * lane + e < tv ? log2_decay(g[4 * lane + e]) : 0.0;
+  for (int e = 0; e < 4; ++e) x[e] = 4 * lane + e < tv ? g[4 * lane + e] : 0.f;
+  return make_float4(x[0], x[1], x[2], x[3]);
+}
+// Their inclusive running sums in base 2 (one warp).
+__device__ __forceinline__ void scan_gates(float4 g, int lane, float *hi, float *lo) {
+  const float v[4] = {g.x, g.y, g.z, g.w};
+  long long x[4];
+  bool nan[4];
 #pragma unroll
-  for (int e = 1; e < 4; ++e) x[e] += x[e - 1];
-  const double before = warp_scan(x[3], lane) - x[3];
+  for (int e = 0; e < 4; ++e) {
+    x[e] = fixed_log2_decay(v[e]) + (e ? x[e - 1] : 0);
+    nan[e] = isnan(v[e]) || (e && nan[e - 1]);
+  }
+  const long long before = warp_scan(x[3], lane) - x[3];
+  const bool nan_before = __ballot_sync(0xffffffffu, nan[3]) & ((1u << lane) - 1);
   Cum c[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) c[e] = split_cum(before + x[e]);
+  for (int e = 0; e < 4; ++e) c[e] = split_cum(before + x[e], nan[e] || nan_before);
   *reinterpret_cast<float4 *>(hi + 4 * lane) = make_float4(c[0].hi, c[1].hi, c[2].hi, c[3].hi);
   *reinterpret_cast<float4 *>(lo + 4 * lane) = make_float4(c[0].lo, c[1].lo, c[2].lo, c[3].lo);
 }
@@ -75,6 +86,12 @@ __device__ __forceinline__ void tmem_st16_nowait(uint32_t taddr, const uint32_t 
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+
+__device__ __forceinline__ void tmem_st8_nowait(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 // f = 2^{sign (c_t - c)} for the running sums c_t = h + l of four tokens and c = hi + lo.
@@ -109,6 +126,18 @@ __device__ __forceinline__ void to_bf16x32(const uint32_t (&r)[32], uint4 (&o)[4
     o[q] = make_uint4(pack_bf16(v[8 * q], v[8 * q + 1]), pack_bf16(v[8 * q + 2], v[8 * q + 3]),
                       pack_bf16(v[8 * q + 4], v[8 * q + 5]), pack_bf16(v[8 * q + 6], v[8 * q + 7]));
 }
+// What bf16 leaves of them, as bf16: bf16(x - bf16(x)).
+__device__ __forceinline__ void rest_bf16x32(const uint32_t (&r)[32], uint4 (&o)[4]) {
+  const float *v = reinterpret_cast<const float *>(r);
+  uint32_t *l = reinterpret_cast<uint32_t *>(o);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const uint32_t h = pack_bf16(v[2 * e], v[2 * e + 1]);
+    const float2 d = __ffma2_rn(make_float2(__uint_as_float(h << 16), __uint_as_float(h & 0xffff0000u)),
+                                make_float2(-1.f, -1.f), make_float2(v[2 * e], v[2 * e + 1]));
+    l[e] = pack_bf16(d.x, d.y);
+  }
+}
 // The same as a pair: hi = bf16(x), lo = bf16(x - hi).
 __device__ __forceinline__ void split_bf16x32(const uint32_t (&r)[32], uint4 (&hi)[4], uint4 (&lo)[4]) {
   const float *v = reinterpret_cast<const float *>(r);
@@ -131,12 +160,27 @@ __device__ __forceinline__ void scale32(uint32_t (&r)[32], float f) {
   }
 }
 
-// Contiguous copy of `bytes` (a multiple of 16) into shared memory, counted on an mbarrier.
-__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
+// A lane's row of 32 bf16 into a [rows x 128 bytes] block of shared memory, 128-byte swizzled.
+__device__ __forceinline__ void stage_row32(uint8_t *blk, int row, int half, const uint4 (&v)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4 *>(blk + sw128_offset(row, half * 32 + 8 * e)) = v[e];
+}
+
+// 64 bytes of a lane's own row.  Every lane is in another row, so an instruction touches 32 lines;
+// 32-byte stores (whole sectors) halve their number.  (Measured against staging the rows in shared
+// memory for bulk copies: the proxy fence, the copy and the wait for it cost each warp 2000 cycles.)
+__device__ __forceinline__ void store_row64(void *p, const uint4 (&v)[4], bool wide) {
+  if (wide) {
+#pragma unroll
+    for (int e = 0; e < 4; e += 2)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(reinterpret_cast<uint4 *>(p) + e),
+                   "r"(v[e].x), "r"(v[e].y), "r"(v[e].z), "r"(v[e].w), "r"(v[e + 1].x), "r"(v[e + 1].y), "r"(v[e + 1].z),
+                   "r"(v[e + 1].w)
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) reinterpret_cast<uint4 *>(p)[e] = v[e];
+  }
 }
 
 }  // namespace gtc
@@ -147,8 +191,8 @@ bool gated_map(CUtensorMap *m, const void *base, long BH, long N, int D, uint32_
 // The state pass (gated_state_tc.cu).  For each of `dirs` directions (0: forward, K and V, from the
 // first chunk; 1: backward, Q and dout, from the last) and each segment of seg_chunks chunks of
 // each head, starting from init: X = 2^{c_T} X + sum_t w_t a_t b_t^T per chunk, w_t = 2^{c_T - c_t}
-// (forward) or 2^{c_t} (backward).  tiles: X before each chunk as a bf16 pair in the shared-memory
-// image of the MMAs that read it (gated_tile_bytes a chunk, hi then lo); fin: X behind the segment.
+// (forward) or 2^{c_t} (backward).  tiles: X before each chunk as a bf16 pair (gated_tile_bytes a
+// chunk: hi then lo, each in blocks of 64 columns, [D][64] row-major); fin: X behind the segment.
 struct GatedStateParams {
   CUtensorMap ta[2], tb[2];  // boxes of 64 x 128
   const float *g;

@@ -339,11 +339,11 @@ LA_API la_status la_retention_decode_step(const void *q, const void *k, const vo
  * hold; out is left as it was there and S is the state after the last token
  * that does.  Values outside [0, N] are taken as the nearer bound.
  *
- * workspace: at least la_gated_workspace(..., 0) bytes of device memory, free
- * for other use when the call's work on `stream` is done; calls that may run
+ * workspace: at least la_gated_workspace(..., 0) bytes of device memory,
+ * 256-byte aligned, free for other use when the call's work on `stream` is done; calls that may run
  * at the same time (two streams, two graphs) need one each.  Nothing is
  * allocated.  d_k, d_v in {32, 64, 128}; dt LA_F32 or LA_BF16; LA_ERR_MISALIGNED
- * for g or lengths off 4 bytes or another pointer off 16; LA_ERR_INVALID_VALUE
+ * for g or lengths off 4 bytes, the workspace off 256 or another pointer off 16; LA_ERR_INVALID_VALUE
  * for a workspace that is NULL or too small; other errors as la_causal.
  * N == 0 zeroes S.
  */
