@@ -234,80 +234,84 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
       if (vd) wait_drain(full_v, (vd - 1) & 1, status);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t iE = idesc_bf16_f32(128, 128, 0, 0), iKK = idesc_bf16_f32(128, D, 0, 0),
-                         iKM = idesc_bf16_f32(128, D, 0, 1), iMM = idesc_bf16_f32(128, D, 1, 1);
-      constexpr int kDs = D / 16;
-      const uint32_t tP = tmem + kColP, tD = tmem + kColD, tQ = tmem + kColQ, tK = tmem + kColK;
-      const uint32_t sQ = smem_u32(sm + L::Q), sK = smem_u32(sm + L::K), sV = smem_u32(sm + L::V),
-                     sO = smem_u32(sm + L::dO), sW = smem_u32(sm + L::WD), sR = smem_u32(sm + L::Ring);
-      int it = 0, ring = 0;
-      for (long x = blockIdx.x; x < p.items; x += gridDim.x) {
-        if (item(x).tv == 0) continue;
-        const uint32_t ph = it & 1;
-        auto wait_ring = [&]() { return mbar_wait(&ring_full[ring % kRing], (ring / kRing) & 1, abort_word, status); };
-        if (!mbar_wait(gate_full, ph, abort_word, status)) break;
-        if (!mbar_wait(full_kq, ph, abort_word, status)) break;
-        // the columns of P: the previous W P is read by the previous dV's product, in issue order
-        tc_fence_after();
-#pragma unroll 4
-        for (int ks = 0; ks < kDs; ++ks) mma_bf16(tP, kdesc(sK, ks), kdesc(sQ, ks), iE, ks > 0);
-        if (!mbar_wait(full_v, ph, abort_word, status) || !mbar_wait(full_d, ph, abort_word, status)) break;
-        if (it > 0 && !mbar_wait(d_free, ph ^ 1, abort_word, status)) break;
-        tc_fence_after();
-#pragma unroll 4
-        for (int ks = 0; ks < kDs; ++ks) mma_bf16(tD, kdesc(sV, ks), kdesc(sO, ks), iE, ks > 0);
+    constexpr uint32_t iE = idesc_bf16_f32(128, 128, 0, 0), iKK = idesc_bf16_f32(128, D, 0, 0),
+                       iKM = idesc_bf16_f32(128, D, 0, 1), iMM = idesc_bf16_f32(128, D, 1, 1);
+    constexpr int kDs = D / 16;
+    constexpr uint32_t kSBlk = D * 128;  // a 64-column block of S or R
+    const bool leader = elect_one();
+    const uint32_t tP = tmem + kColP, tD = tmem + kColD, tQ = tmem + kColQ, tK = tmem + kColK;
+    const uint32_t sQ = smem_u32(sm + L::Q), sK = smem_u32(sm + L::K), sV = smem_u32(sm + L::V),
+                   sO = smem_u32(sm + L::dO), sW = smem_u32(sm + L::WD), sR = smem_u32(sm + L::Ring);
+    int it = 0;
+    for (long x = blockIdx.x; x < p.items; x += gridDim.x) {
+      if (item(x).tv == 0) continue;
+      const uint32_t ph = it & 1;
+      // the chunk's pieces S hi, S lo, R hi, R lo take the ring's two places in turn
+      static_assert(kRing == 2, "places by parity");
+      if (!warp_wait(gate_full, ph, abort_word)) break;
+      if (!warp_wait(full_kq, ph, abort_word)) break;
+      // the columns of P: the previous W P is read by the previous dV's product, in issue order
+      tc_fence_after();
+      if (leader) product<kDs, kK, kK>(tP, kbase(sK), kbase(sQ), iE, false);
+      __syncwarp();
+      if (!warp_wait(full_v, ph, abort_word) || !warp_wait(full_d, ph, abort_word)) break;
+      if (it > 0 && !warp_wait(d_free, ph ^ 1, abort_word)) break;
+      tc_fence_after();
+      if (leader) {
+        product<kDs, kK, kK>(tD, kbase(sV), kbase(sO), iE, false);
         mma_commit(e_full);
-        if (it > 0 && !mbar_wait(out_free, ph ^ 1, abort_word, status)) break;
-        tc_fence_after();
-        // dQ = dO S^T, both parts of S
-        bool ok = true;
-        for (int part = 0; part < 2 && ok; ++part) {
-          ok = wait_ring();
-          if (!ok) break;
-          const uint32_t st = sR + (ring % kRing) * kState;
-#pragma unroll 4
-          for (int ks = 0; ks < kDs; ++ks) mma_bf16(tQ, kdesc(sO, ks), kdesc(st, ks, D * 128), iKK, part | (ks > 0));
-          mma_commit(&ring_free[ring % kRing]);
-          ++ring;
-        }
-        if (!ok) break;
+      }
+      __syncwarp();
+      if (it > 0 && !warp_wait(out_free, ph ^ 1, abort_word)) break;
+      // dQ = dO S^T, both parts of S
+      if (!warp_wait(&ring_full[0], 0, abort_word)) break;
+      tc_fence_after();
+      if (leader) {
+        product<kDs, kK, kK, kBlk, kSBlk>(tQ, kbase(sO), kbase(sR), iKK, false);
+        mma_commit(&ring_free[0]);
+      }
+      __syncwarp();
+      if (!warp_wait(&ring_full[1], 0, abort_word)) break;
+      if (leader) {
+        product<kDs, kK, kK, kBlk, kSBlk>(tQ, kbase(sO), kbase(sR + kState), iKK, true);
+        mma_commit(&ring_free[1]);
         mma_commit(q_in);
-        // dK = V R^T; R's high part stays for dV
-        if (!wait_ring()) break;
-        const uint32_t r_hi = sR + (ring % kRing) * kState;
-        uint64_t *r_hi_free = &ring_free[ring % kRing];
-        ++ring;
-#pragma unroll 4
-        for (int ks = 0; ks < kDs; ++ks) mma_bf16(tK, kdesc(sV, ks), kdesc(r_hi, ks, D * 128), iKK, ks > 0);
-        if (!wait_ring()) break;
-        const uint32_t r_lo = sR + (ring % kRing) * kState;
-#pragma unroll 4
-        for (int ks = 0; ks < kDs; ++ks) mma_bf16(tK, kdesc(sV, ks), kdesc(r_lo, ks, D * 128), iKK, 1);
-        mma_commit(&ring_free[ring % kRing]);
-        ++ring;
+      }
+      __syncwarp();
+      // dK = V R^T; R's high part stays for dV
+      if (!warp_wait(&ring_full[0], 1, abort_word)) break;
+      if (leader) product<kDs, kK, kK, kBlk, kSBlk>(tK, kbase(sV), kbase(sR), iKK, false);
+      __syncwarp();
+      if (!warp_wait(&ring_full[1], 1, abort_word)) break;
+      if (leader) {
+        product<kDs, kK, kK, kBlk, kSBlk>(tK, kbase(sV), kbase(sR + kState), iKK, true);
+        mma_commit(&ring_free[1]);
         mma_commit(v_free);
         mma_commit(k_in);
-        // dV = K R, over D^T once that is read
-        if (!mbar_wait(el_done, ph, abort_word, status)) break;
-        tc_fence_after();
-#pragma unroll 4
-        for (int ks = 0; ks < kDs; ++ks) mma_bf16(tD, kdesc(sK, ks), mndesc(r_hi, ks, D * 128), iKM, ks > 0);
-        mma_commit(r_hi_free);
+      }
+      __syncwarp();
+      // dV = K R, over D^T once that is read
+      if (!warp_wait(el_done, ph, abort_word)) break;
+      tc_fence_after();
+      if (leader) {
+        product<kDs, kK, kMN, kBlk, kSBlk>(tD, kbase(sK), mnbase(sR, kSBlk), iKM, false);
+        mma_commit(&ring_free[0]);
         mma_commit(v_in);
-        if (!mbar_wait(x_ready, ph, abort_word, status)) break;
-        tc_fence_after();
-#pragma unroll 4
-        for (int ks = 0; ks < 8; ++ks)  // queries [16 ks, ..): columns 8 ks of the first or the second half
-          mma_bf16_ts(tD, tP + (ks < 4 ? 8 * ks : 32 + 8 * ks), mndesc(sO, ks), iKM, 1);
-#pragma unroll 4
-        for (int ks = 0; ks < 8; ++ks) mma_bf16(tK, kdesc(sW, ks), mndesc(sQ, ks), iKM, 1);
-#pragma unroll 4
-        for (int ks = 0; ks < 8; ++ks) mma_bf16(tQ, mndesc(sW, ks), mndesc(sK, ks), iMM, 1);
+      }
+      __syncwarp();
+      if (!warp_wait(x_ready, ph, abort_word)) break;
+      tc_fence_after();
+      if (leader) {
+        product_ts<kMN>(tD, tP, mnbase(sO), iKM, true);
+        product<8, kK, kMN>(tK, kbase(sW), mnbase(sQ), iKM, true);
+        product<8, kMN, kMN>(tQ, mnbase(sW), mnbase(sK), iMM, true);
         mma_commit(tok_free);
         mma_commit(out_full);
-        ++it;
       }
+      __syncwarp();
+      ++it;
+    }
+    if (leader) {
       mma_commit(drain);
       wait_drain(drain, 0, status);
     }

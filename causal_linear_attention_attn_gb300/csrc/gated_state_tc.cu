@@ -122,28 +122,29 @@ __global__ void __launch_bounds__(kThreads, 1) gated_state_tc_kernel(const __gri
       for (int i = max(0, issued - kStages); i < issued; ++i) wait_drain(&full[i % kStages], (i / kStages) & 1, status);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t iMM = idesc_bf16_f32(128, D, 1, 1);
-      const uint32_t sA = smem_u32(sm + L::A), sLo = smem_u32(sm + L::Lo), sB = smem_u32(sm + L::B);
-      for (int i = 0; i < run; ++i) {
-        const int s = i % kStages;
-        if (!mbar_wait(&done[s], (i / kStages) & 1, abort_word, status)) break;
-        if (!mbar_wait(x_ready, i & 1, abort_word, status)) break;
-        tc_fence_after();
-        const uint32_t a = sA + s * L::kTile, lo = sLo + (i & 1) * L::kTile, b = sB + s * L::kTile;
-#pragma unroll 4
-        for (int ks = 0; ks < 8; ++ks) {
-          if (D == 128) {
-            mma_bf16(tmem, mndesc(a, ks), mndesc(b, ks), iMM, 1);
-            mma_bf16(tmem, mndesc(lo, ks), mndesc(b, ks), iMM, 1);
-          } else {
-            mma_bf16(tmem, mndesc(a, ks, lo - a), mndesc(b, ks), iMM, 1);  // rows: hi, then lo
-          }
+    constexpr uint32_t iMM = idesc_bf16_f32(128, D, 1, 1);
+    const bool leader = elect_one();
+    const uint32_t sA = smem_u32(sm + L::A), sLo = smem_u32(sm + L::Lo), sB = smem_u32(sm + L::B);
+    for (int i = 0; i < run; ++i) {
+      const int s = i % kStages;
+      if (!warp_wait(&done[s], (i / kStages) & 1, abort_word)) break;
+      if (!warp_wait(x_ready, i & 1, abort_word)) break;
+      tc_fence_after();
+      const uint32_t a = sA + s * L::kTile, lo = sLo + (i & 1) * L::kTile, b = sB + s * L::kTile;
+      if (leader) {
+        if (D == 128) {
+          product<8, kMN, kMN>(tmem, mnbase(a), mnbase(b), iMM, true);
+          product<8, kMN, kMN>(tmem, mnbase(lo), mnbase(b), iMM, true);
+        } else {
+          product<8, kMN, kMN>(tmem, mnbase(a, lo - a), mnbase(b), iMM, true);  // rows: hi, then lo
         }
         mma_commit(&empty[s]);
         mma_commit(&lo_free[i & 1]);
         mma_commit(x_full);
       }
+      __syncwarp();
+    }
+    if (leader) {
       mma_commit(drain);
       wait_drain(drain, 0, status);
     }

@@ -146,50 +146,55 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
       if (q_issued) wait_drain(full_q, (q_issued - 1) & 1, status);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t iP = idesc_bf16_f32(128, 128, 0, 0), iO = idesc_bf16_f32(128, D, 0, 1),
-                         iS = idesc_bf16_f32(128, D, 1, 1);
-      constexpr int kDs = D / 16;
-      const uint32_t tS = tmem + kColS, tP = tmem + kColP, tI = tmem + kColI, tA = tmem + kColA;
-      const uint32_t sQ = smem_u32(sm + L::Q), sSb = smem_u32(sm + L::Sb), sKlo = smem_u32(sm + L::Klo);
-      for (int c = 0; c < nc; ++c) {
-        const int s = c & 1;
-        const uint32_t k = smem_u32(sm + L::K) + s * L::kTile, v = smem_u32(sm + L::V) + s * L::kTile;
-        if (!mbar_wait(full_q, c & 1, abort_word, status)) break;
-        if (!mbar_wait(&full_k[s], (c >> 1) & 1, abort_word, status)) break;
-        tc_fence_after();
-        // the scores' columns are free: the previous P' V reads them before, in issue order
-#pragma unroll 4
-        for (int ks = 0; ks < kDs; ++ks) mma_bf16(tP, kdesc(sQ, ks), kdesc(k, ks), iP, ks > 0);
+    constexpr uint32_t iP = idesc_bf16_f32(128, 128, 0, 0), iO = idesc_bf16_f32(128, D, 0, 1), iS = idesc_bf16_f32(128, D, 1, 1);
+    constexpr int kDs = D / 16;
+    const bool leader = elect_one();
+    const uint32_t tS = tmem + kColS, tP = tmem + kColP, tI = tmem + kColI, tA = tmem + kColA;
+    const uint32_t sQ = smem_u32(sm + L::Q), sSb = smem_u32(sm + L::Sb), sKlo = smem_u32(sm + L::Klo);
+    for (int c = 0; c < nc; ++c) {
+      const int s = c & 1;
+      const uint32_t k = smem_u32(sm + L::K) + s * L::kTile, v = smem_u32(sm + L::V) + s * L::kTile;
+      if (!warp_wait(full_q, c & 1, abort_word)) break;
+      if (!warp_wait(&full_k[s], (c >> 1) & 1, abort_word)) break;
+      tc_fence_after();
+      // the scores' columns are free: the previous P' V reads them before, in issue order
+      if (leader) {
+        product<kDs, kK, kK>(tP, kbase(sQ), kbase(k), iP, false);
         mma_commit(p_full);
-        if (!mbar_wait(sb_ready, c & 1, abort_word, status)) break;
-        if (c > 0 && !mbar_wait(o_free, (c - 1) & 1, abort_word, status)) break;
-        tc_fence_after();
-#pragma unroll 4
-        for (int ks = 0; ks < kDs; ++ks) mma_bf16(tI, kdesc(sQ, ks), mndesc(sSb, ks), iO, ks > 0);
+      }
+      __syncwarp();
+      if (!warp_wait(sb_ready, c & 1, abort_word)) break;
+      if (c > 0 && !warp_wait(o_free, (c - 1) & 1, abort_word)) break;
+      tc_fence_after();
+      if (leader) {
+        product<kDs, kK, kMN>(tI, kbase(sQ), mnbase(sSb), iO, false);
         mma_commit(q_free);
-        if (!mbar_wait(k_ready, c & 1, abort_word, status)) break;
-        if (!mbar_wait(&full_v[s], (c >> 1) & 1, abort_word, status)) break;
-        tc_fence_after();
-#pragma unroll 4
-        for (int ks = 0; ks < 8; ++ks) {
-          if (D == 128) {
-            mma_bf16(tS, mndesc(k, ks), mndesc(v, ks), iS, 1);
-            mma_bf16(tS, mndesc(sKlo, ks), mndesc(v, ks), iS, 1);
-          } else {
-            mma_bf16(tS, mndesc(k, ks, sKlo - k), mndesc(v, ks), iS, 1);  // rows: hi, then lo
-          }
+      }
+      __syncwarp();
+      if (!warp_wait(k_ready, c & 1, abort_word)) break;
+      if (!warp_wait(&full_v[s], (c >> 1) & 1, abort_word)) break;
+      tc_fence_after();
+      if (leader) {
+        if (D == 128) {
+          product<8, kMN, kMN>(tS, mnbase(k), mnbase(v), iS, true);
+          product<8, kMN, kMN>(tS, mnbase(sKlo), mnbase(v), iS, true);
+        } else {
+          product<8, kMN, kMN>(tS, mnbase(k, sKlo - k), mnbase(v), iS, true);  // rows: hi, then lo
         }
         mma_commit(s_full);
         mma_commit(&k_free[s]);
-        if (!mbar_wait(pp_ready, c & 1, abort_word, status)) break;
-        tc_fence_after();
-#pragma unroll 4
-        for (int ks = 0; ks < 8; ++ks)  // keys [16 ks, ..): columns 8 ks of the first or the second half
-          mma_bf16_ts(tA, tP + (ks < 4 ? 8 * ks : 32 + 8 * ks), mndesc(v, ks), iO, ks > 0);
+      }
+      __syncwarp();
+      if (!warp_wait(pp_ready, c & 1, abort_word)) break;
+      tc_fence_after();
+      if (leader) {
+        product_ts<kMN>(tA, tP, mnbase(v), iO, false);
         mma_commit(&v_free[s]);
         mma_commit(o_full);
       }
+      __syncwarp();
+    }
+    if (leader) {
       mma_commit(drain);
       wait_drain(drain, 0, status);
     }
