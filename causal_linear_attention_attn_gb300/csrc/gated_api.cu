@@ -51,7 +51,8 @@ la_status gated(const void *q, const void *k, const void *v, const float *g, con
     return api_status(cudaMemsetAsync(S, 0, sizeof(float) * (size_t)p.BH() * dk * dv, p.stream));
   }
   if ((st = api_device()) != LA_OK) return st;
-  if (!ws || ws_bytes < workspace(B, H, N, dk, dv, dt, false)) return LA_ERR_INVALID_VALUE;
+  const size_t need = workspace(B, H, N, dk, dv, dt, false);
+  if (ws_bytes < need || (need && !ws)) return LA_ERR_INVALID_VALUE;
   return api_status(gated_tc_supported(dk, dv, dt) ? launch_gated_tc(p) : launch_gated_simt(p));
 }
 

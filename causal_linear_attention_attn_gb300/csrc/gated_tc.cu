@@ -472,7 +472,7 @@ cudaError_t read_and_clear_gated_status(unsigned int *value) {
 
 size_t gated_tc_prefill_workspace(long BH, long N, int D) {
   const Plan t = make_plan(BH, N, D);
-  return t.split() ? sizeof(float) * (size_t)BH * t.init_segs() * ((size_t)D * D + 1) : 16;
+  return t.split() ? sizeof(float) * (size_t)BH * t.init_segs() * ((size_t)D * D + 1) : 0;
 }
 
 cudaError_t launch_gated_tc(const GatedProblem &p) {

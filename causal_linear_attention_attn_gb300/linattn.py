@@ -10,6 +10,7 @@ the library has not been built (``__graft_entry__.build()``).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -310,47 +311,41 @@ def la_causal_backward(q, k, v, dout, S0=None, z0=None, dS=None, dz=None, need_s
     return (dq, dkk, dvv, dS0, dz0) if need_state_grad else (dq, dkk, dvv)
 
 
-class _On:
-    """The device and stream a call runs on: the tensors' device, and the given stream or that device's
-    current one.  Outputs and workspaces are allocated inside, so that they belong to that stream."""
+def _on(device, stream):
+    """(stream handle, context to leave) of a call on `device`: the given stream, or that device's current one.
 
-    def __init__(self, device, stream):
-        if stream is None:
-            self.stream = torch.cuda.current_stream(device)
-        elif isinstance(stream, torch.cuda.Stream):
-            self.stream = stream
-        elif int(stream) == 0:
-            self.stream = torch.cuda.default_stream(device)
-        else:
-            self.stream = torch.cuda.ExternalStream(int(stream), device=device)
-        if self.stream.device != device:
-            raise ValueError(f"the stream belongs to {self.stream.device}, the tensors to {device}")
-        # entering the stream also makes its device current; not needed for a call on the current pair
-        self._ctx = None
-        if stream is not None or torch.cuda.current_device() != device.index:
-            self._ctx = torch.cuda.stream(self.stream)
+    Outputs and workspaces are allocated between this and :func:`_off`, so that they belong to that stream.
+    Entering a context is needed only for another stream or device than the current ones.
+    """
+    if stream is None:
+        if device.index == torch._C._cuda_getDevice():
+            return torch._C._cuda_getCurrentRawStream(device.index), None
+        stream = torch.cuda.current_stream(device)
+    elif not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else torch.cuda.default_stream(device)
+    if stream.device != device:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to {device}")
+    ctx = torch.cuda.stream(stream)
+    ctx.__enter__()  # makes the stream's device current too
+    return stream.cuda_stream, ctx
 
-    def __enter__(self):
-        if self._ctx is not None:
-            self._ctx.__enter__()
-        return self.stream.cuda_stream
 
-    def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
+def _off(ctx):
+    if ctx is not None:
+        ctx.__exit__(None, None, None)
 
 
 def _need(name, t, shape, dtype, device):
-    """t itself, after checking that it is a contiguous CUDA tensor of that shape, dtype and device."""
+    """t itself, after checking that it is a contiguous tensor of that shape, dtype and (CUDA) device."""
+    if isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous():
+        return t
     if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
-    return t
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _opt(name, t, shape, dtype, device):
@@ -361,30 +356,52 @@ def _out(name, t, shape, dtype, device):
     return torch.empty(shape, dtype=dtype, device=device) if t is None else _need(name, t, shape, dtype, device)
 
 
+def _first(name, t, nd):
+    """The device of a call, from its first tensor."""
+    if not isinstance(t, torch.Tensor) or t.dim() != nd:
+        raise ValueError(f"{name} must be a {nd}-d tensor")
+    if not t.is_cuda:
+        _dt(t)
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    return t.device
+
+
 def _gated_inputs(q, k, v, g, nd):
-    """(lead, d_k, d_v, dtype code) of gated inputs whose leading dims are [B, H, N] (nd = 4) or [B, H] (nd = 3)."""
-    if not isinstance(q, torch.Tensor) or q.dim() != nd or not isinstance(v, torch.Tensor) or v.dim() != nd:
-        raise ValueError(f"q and v must be {nd}-d tensors")
-    dt, lead, dev = _dt(q), tuple(q.shape[:-1]), q.device
-    dk, dv = q.shape[-1], v.shape[-1]
-    _need("q", q, (*lead, dk), q.dtype, dev)
-    _need("k", k, (*lead, dk), q.dtype, dev)
-    _need("v", v, (*lead, dv), q.dtype, dev)
+    """(device, lead, d_k, d_v, dtype code) of gated inputs whose leading dims are [B, H, N] (nd = 4) or [B, H] (nd = 3)."""
+    dev = _first("q", q, nd)
+    _first("v", v, nd)
+    dt, dtype, shape = _dt(q), q.dtype, q.shape
+    lead, dk, dv = shape[:-1], shape[-1], v.shape[-1]
+    _need("q", q, shape, dtype, dev)
+    _need("k", k, shape, dtype, dev)
+    _need("v", v, (*lead, dv), dtype, dev)
     _need("g", g, lead, torch.float32, dev)
-    return lead, dk, dv, dt
+    return dev, lead, dk, dv, dt
+
+
+@functools.lru_cache(maxsize=1024)
+def _gated_workspace(device, B, H, N, dk, dv, dt, backward):
+    with torch.cuda.device(device):
+        return lib.la_gated_workspace(B, H, N, dk, dv, dt, backward)
+
+
+def _workspace(need, device):
+    return torch.empty(need, dtype=torch.uint8, device=device) if need else None
 
 
 def _gated_call(fn, q, k, v, g, lengths, out, S, stream):
-    (B, H, N), dk, dv, dt = _gated_inputs(q, k, v, g, 4)
-    dev = q.device
+    dev, (B, H, N), dk, dv, dt = _gated_inputs(q, k, v, g, 4)
     _opt("lengths", lengths, (B,), torch.int32, dev)
-    with _On(dev, stream) as s:
+    s, ctx = _on(dev, stream)
+    try:
         out = _out("out", out, (B, H, N, dv), q.dtype, dev)
         S = _out("S", S, (B, H, dk, dv), torch.float32, dev)
-        need = lib.la_gated_workspace(B, H, N, dk, dv, dt, 0)
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        need = _gated_workspace(dev.index, B, H, N, dk, dv, dt, 0)
+        ws = _workspace(need, dev)
         rc = getattr(lib, fn)(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(lengths), _ptr(out), _ptr(S), B, H, N, dk, dv, dt,
                               _ptr(ws), need, s)
+    finally:
+        _off(ctx)
     if rc != 0:
         raise LinAttnError(fn, rc)
     return out, S
@@ -411,20 +428,22 @@ def la_gated_backward(q, k, v, g, dout, S0=None, dS=None, lengths=None, need_sta
     """Gradients of la_gated (la_gated_with_state when S0 is given) for the upstream gradient ``dout`` of its output
     (q's dtype) and, optionally, ``dS`` of its final state.  Returns (dq, dk, dv, dg), plus dS0 when
     ``need_state_grad``; dq, dk, dv in q's dtype, dg and dS0 float32."""
-    (B, H, N), dk, dv, dt = _gated_inputs(q, k, v, g, 4)
-    dev = q.device
+    dev, (B, H, N), dk, dv, dt = _gated_inputs(q, k, v, g, 4)
     _need("dout", dout, (B, H, N, dv), q.dtype, dev)
     _opt("lengths", lengths, (B,), torch.int32, dev)
     _opt("S0", S0, (B, H, dk, dv), torch.float32, dev)
     _opt("dS", dS, (B, H, dk, dv), torch.float32, dev)
-    with _On(dev, stream) as s:
+    s, ctx = _on(dev, stream)
+    try:
         dq, dkk, dvv, dg = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v), torch.empty_like(g)
         dS0 = torch.empty(B, H, dk, dv, dtype=torch.float32, device=dev) if need_state_grad else None
-        need = lib.la_gated_workspace(B, H, N, dk, dv, dt, 1)
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        need = _gated_workspace(dev.index, B, H, N, dk, dv, dt, 1)
+        ws = _workspace(need, dev)
         rc = lib.la_gated_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(lengths), _ptr(dout), _ptr(S0), _ptr(dS),
                                    _ptr(dq), _ptr(dkk), _ptr(dvv), _ptr(dg), _ptr(dS0), B, H, N, dk, dv, dt, _ptr(ws),
                                    need, s)
+    finally:
+        _off(ctx)
     if rc != 0:
         raise LinAttnError("la_gated_backward", rc)
     return (dq, dkk, dvv, dg, dS0) if need_state_grad else (dq, dkk, dvv, dg)
@@ -437,8 +456,7 @@ def la_gated_decode_step(q, k, v, g, S, slots=None, out=None, stream=None):
     row b on S[b]).  A negative slot marks an unused row (out zero).  A slot out of range or repeated in the batch
     is skipped too, and the next device_status() is 1.
     """
-    (B, H), dk, dv, dt = _gated_inputs(q, k, v, g, 3)
-    dev = q.device
+    dev, (B, H), dk, dv, dt = _gated_inputs(q, k, v, g, 3)
     if not isinstance(S, torch.Tensor) or S.dim() != 4:
         raise ValueError("S must be a [n_slots, H, d_k, d_v] tensor")
     n_slots = S.shape[0]
@@ -446,25 +464,27 @@ def la_gated_decode_step(q, k, v, g, S, slots=None, out=None, stream=None):
     _opt("slots", slots, (B,), torch.int32, dev)
     if slots is None and n_slots < B:
         raise ValueError(f"S holds {n_slots} states for {B} rows")
-    with _On(dev, stream) as s:
+    s, ctx = _on(dev, stream)
+    try:
         out = _out("out", out, (B, H, dv), q.dtype, dev)
         rc = lib.la_gated_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S), _ptr(slots), _ptr(out), B, H, n_slots,
                                       dk, dv, dt, s)
+    finally:
+        _off(ctx)
     if rc != 0:
         raise LinAttnError("la_gated_decode_step", rc)
     return out
 
 
 def _norm_inputs(x, gate, weight, bias):
-    if not isinstance(x, torch.Tensor) or x.dim() != 4:
-        raise ValueError("x must be a 4-d tensor")
+    dev = _first("x", x, 4)
     B, H, N, d = x.shape
-    _need("x", x, (B, H, N, d), x.dtype, x.device)
     dt = _dt(x)
-    _opt("gate", gate, (B, N, H * d), x.dtype, x.device)
-    _opt("weight", weight, (H * d,), torch.float32, x.device)
-    _opt("bias", bias, (H * d,), torch.float32, x.device)
-    return B, H, N, d, dt
+    _need("x", x, x.shape, x.dtype, dev)
+    _opt("gate", gate, (B, N, H * d), x.dtype, dev)
+    _opt("weight", weight, (H * d,), torch.float32, dev)
+    _opt("bias", bias, (H * d,), torch.float32, dev)
+    return dev, B, H, N, d, dt
 
 
 def la_group_norm(x, gate=None, weight=None, bias=None, eps: float = 1e-5, out=None, stream=None):
@@ -472,26 +492,38 @@ def la_group_norm(x, gate=None, weight=None, bias=None, eps: float = 1e-5, out=N
 
     gate [B, N, H*d] (x's dtype); weight, bias [H*d] float32; each may be None.
     """
-    B, H, N, d, dt = _norm_inputs(x, gate, weight, bias)
-    with _On(x.device, stream) as s:
-        out = _out("out", out, (B, N, H * d), x.dtype, x.device)
+    dev, B, H, N, d, dt = _norm_inputs(x, gate, weight, bias)
+    s, ctx = _on(dev, stream)
+    try:
+        out = _out("out", out, (B, N, H * d), x.dtype, dev)
         rc = lib.la_group_norm(_ptr(x), _ptr(gate), _ptr(weight), _ptr(bias), _ptr(out), B, H, N, d, float(eps), dt, s)
+    finally:
+        _off(ctx)
     if rc != 0:
         raise LinAttnError("la_group_norm", rc)
     return out
 
 
+@functools.lru_cache(maxsize=1024)
+def _norm_workspace(device, B, H, N, d):
+    with torch.cuda.device(device):
+        return lib.la_group_norm_workspace(B, H, N, d)
+
+
 def la_group_norm_backward(x, dy, gate=None, weight=None, bias=None, eps: float = 1e-5, stream=None):
     """Gradients of la_group_norm for dy [B, N, H*d]: (dx, dgate, dweight, dbias), None for an argument not given."""
-    B, H, N, d, dt = _norm_inputs(x, gate, weight, bias)
-    _need("dy", dy, (B, N, H * d), x.dtype, x.device)
-    with _On(x.device, stream) as s:
+    dev, B, H, N, d, dt = _norm_inputs(x, gate, weight, bias)
+    _need("dy", dy, (B, N, H * d), x.dtype, dev)
+    s, ctx = _on(dev, stream)
+    try:
         dx = torch.empty_like(x)
         dgate, dw, db = (None if t is None else torch.empty_like(t) for t in (gate, weight, bias))
-        need = 0 if dw is None and db is None else lib.la_group_norm_workspace(B, H, N, d)
-        ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+        need = 0 if dw is None and db is None else _norm_workspace(dev.index, B, H, N, d)
+        ws = _workspace(need, dev)
         rc = lib.la_group_norm_backward(_ptr(x), _ptr(dy), _ptr(gate), _ptr(weight), _ptr(bias), _ptr(dx), _ptr(dgate),
                                         _ptr(dw), _ptr(db), B, H, N, d, float(eps), dt, _ptr(ws), need, s)
+    finally:
+        _off(ctx)
     if rc != 0:
         raise LinAttnError("la_group_norm_backward", rc)
     return dx, dgate, dw, db

@@ -344,7 +344,7 @@ LA_API la_status la_retention_decode_step(const void *q, const void *k, const vo
  * at the same time (two streams, two graphs) need one each.  Nothing is
  * allocated.  d_k, d_v in {32, 64, 128}; dt LA_F32 or LA_BF16; LA_ERR_MISALIGNED
  * for g or lengths off 4 bytes, the workspace off 256 or another pointer off 16; LA_ERR_INVALID_VALUE
- * for a workspace that is NULL or too small; other errors as la_causal.
+ * for a workspace that is too small (NULL where 0 bytes are needed is fine); other errors as la_causal.
  * N == 0 zeroes S.
  */
 LA_API la_status la_gated(const void *q, const void *k, const void *v, const float *g, const int *lengths,
