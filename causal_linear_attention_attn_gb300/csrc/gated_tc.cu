@@ -17,8 +17,8 @@
 // HBM bounds it (8 D bytes per token in and out, 40 flops a byte at D = 128): a chunk's loads take
 // about 5000 cycles of an SM's share, its longest chain (P, weights, P' V) about 2800.
 //
-// Warps: 0 TMA, 1 MMA and TMEM owner, 2-9 weights of the scores, 10-13 weighted keys, 14-17 state
-// (bf16 copy, decay), 18-21 outputs, 22 running sums.  Every wait is bounded (tc_ptx.cuh).
+// Warps: 0 TMA, 1 MMA and TMEM owner, 2 running sums, 4-11 weights of the scores, 12-15 weighted keys,
+// 16-19 state (bf16 copy, decay), 20-23 outputs.  Every wait is bounded (tc_ptx.cuh).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -31,22 +31,27 @@ namespace la {
 namespace {
 using namespace gtc;
 
-constexpr int kThreads = 736;
-constexpr int kWarpK = 10, kWarpS = 14, kWarpO = 18, kWarpGate = 22;
+constexpr int kThreads = 768;
+constexpr int kWarpGate = 2, kWarpP = 4, kWarpK = 12, kWarpS = 16, kWarpO = 20;
 constexpr uint32_t kBarS = 1;
+// Registers a thread: the launch gives every warpgroup 80; the state and the outputs, which pass
+// through in blocks of 64 columns, take what the others leave.
+constexpr int kRegs = 80, kRegs0 = 56, kRegsK = 72, kRegsSO = 96;
+static_assert(kRegs0 + 2 * kRegs + kRegsK + 2 * kRegsSO <= 6 * kRegs, "warpgroups' shares within the launch's");
 
 template <int D>
 struct Lay {
   static constexpr uint32_t kTile = D / 64 * kBlk;  // 128 tokens
   static constexpr uint32_t Q = 0;
   static constexpr uint32_t K = Q + kTile;
-  static constexpr uint32_t Klo = K + 2 * kTile;
-  static constexpr uint32_t V = Klo + kTile;
+  static constexpr uint32_t Khi = K + kTile;
+  static constexpr uint32_t Klo = Khi + kTile;
+  static constexpr uint32_t V = Klo + kTile;  // 2 stages
   static constexpr uint32_t Sb = V + 2 * kTile;
   static constexpr uint32_t Sum = Sb + D * D * 2;  // D = 64: low rows of the state [64][65] fp32
   static constexpr uint32_t Gate = Sum + (D == 64 ? 64 * 65 * 4 : 0);
   static constexpr uint32_t Bars = Gate + 2 * 2 * kC * 4;
-  static constexpr int kNumBars = 22;
+  static constexpr int kNumBars = 19;
   static constexpr uint32_t Misc = Bars + kNumBars * 8;
   static constexpr uint32_t Bytes = Misc + 16;
 };
@@ -74,11 +79,12 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
     return;
   }
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::Bars);
-  uint64_t *full_k = bars, *full_v = bars + 2, *k_free = bars + 4, *gate_full = bars + 6, *gate_free = bars + 8,
-           *full_q = bars + 10, *q_free = bars + 11, *p_full = bars + 12, *k_ready = bars + 13, *pp_ready = bars + 14,
-           *sb_ready = bars + 15, *s_full = bars + 16, *o_full = bars + 17, *o_free = bars + 18, *drain = bars + 19, *v_free = bars + 20;  // v_free: [2]
+  uint64_t *full_v = bars, *v_free = bars + 2, *gate_full = bars + 4, *gate_free = bars + 6, *full_q = bars + 8,
+           *q_free = bars + 9, *full_k = bars + 10, *k_free = bars + 11, *p_full = bars + 12, *k_ready = bars + 13,
+           *pp_ready = bars + 14, *sb_ready = bars + 15, *s_full = bars + 16, *o_full = bars + 17, *o_free = bars + 18;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::Misc);
   volatile uint32_t *abort_word = reinterpret_cast<volatile uint32_t *>(sm + L::Misc + 4);
+  uint64_t *drain = reinterpret_cast<uint64_t *>(sm + L::Misc + 8);
   unsigned int *status = &g_gated_status;
   float *gate = reinterpret_cast<float *>(sm + L::Gate);  // [2][hi 128, lo 128]
 
@@ -93,13 +99,13 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
 
   if (threadIdx.x == 0) {
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&full_k[b], 1);
       mbar_init(&full_v[b], 1);
-      mbar_init(&k_free[b], 1);
       mbar_init(&v_free[b], 1);
       mbar_init(&gate_full[b], 32);
       mbar_init(&gate_free[b], 640);
     }
+    mbar_init(full_k, 1);
+    mbar_init(k_free, 1 + 128);  // the scores' product and the weighted keys' warps
     mbar_init(full_q, 1);
     mbar_init(q_free, 1);
     mbar_init(p_full, 1);
@@ -119,8 +125,9 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 0) {
-    if (lane == 0) {
+  if (warp < 4) {
+    reg_dec<kRegs0>();
+    if (warp == 0 && lane == 0) {
       prefetch_tmap(&p.tq);
       prefetch_tmap(&p.tk);
       prefetch_tmap(&p.tv);
@@ -131,76 +138,92 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
       int k_issued = 0, q_issued = 0, v_issued = 0;
       for (int c = 0; c < nc; ++c) {
         const int s = c & 1, tok = (int)((c_lo + c) * kC);
-        if (c >= 2 && !mbar_wait(&k_free[s], ((c >> 1) - 1) & 1, abort_word, status)) break;
-        load(L::K + s * L::kTile, &p.tk, &full_k[s], tok);
+        if (c >= 1 && !mbar_wait(k_free, (c - 1) & 1, abort_word, status)) break;
+        load(L::K, &p.tk, full_k, tok);
         k_issued = c + 1;
-        if (c >= 1 && !mbar_wait(q_free, (c - 1) & 1, abort_word, status)) break;
-        load(L::Q, &p.tq, full_q, tok);
-        q_issued = c + 1;
         if (c >= 2 && !mbar_wait(&v_free[s], ((c >> 1) - 1) & 1, abort_word, status)) break;
         load(L::V + s * L::kTile, &p.tv, &full_v[s], tok);
         v_issued = c + 1;
+        if (c >= 1 && !mbar_wait(q_free, (c - 1) & 1, abort_word, status)) break;
+        load(L::Q, &p.tq, full_q, tok);
+        q_issued = c + 1;
       }
-      for (int c = max(0, k_issued - 2); c < k_issued; ++c) wait_drain(&full_k[c & 1], (c >> 1) & 1, status);
       for (int c = max(0, v_issued - 2); c < v_issued; ++c) wait_drain(&full_v[c & 1], (c >> 1) & 1, status);
+      if (k_issued) wait_drain(full_k, (k_issued - 1) & 1, status);
       if (q_issued) wait_drain(full_q, (q_issued - 1) & 1, status);
-    }
-  } else if (warp == 1) {
-    constexpr uint32_t iP = idesc_bf16_f32(128, 128, 0, 0), iO = idesc_bf16_f32(128, D, 0, 1), iS = idesc_bf16_f32(128, D, 1, 1);
-    constexpr int kDs = D / 16;
-    const bool leader = elect_one();
-    const uint32_t tS = tmem + kColS, tP = tmem + kColP, tI = tmem + kColI, tA = tmem + kColA;
-    const uint32_t sQ = smem_u32(sm + L::Q), sSb = smem_u32(sm + L::Sb), sKlo = smem_u32(sm + L::Klo);
-    for (int c = 0; c < nc; ++c) {
-      const int s = c & 1;
-      const uint32_t k = smem_u32(sm + L::K) + s * L::kTile, v = smem_u32(sm + L::V) + s * L::kTile;
-      if (!warp_wait(full_q, c & 1, abort_word)) break;
-      if (!warp_wait(&full_k[s], (c >> 1) & 1, abort_word)) break;
-      tc_fence_after();
-      // the scores' columns are free: the previous P' V reads them before, in issue order
-      if (leader) {
-        product<kDs, kK, kK>(tP, kbase(sQ), kbase(k), iP, false);
-        mma_commit(p_full);
-      }
-      __syncwarp();
-      if (!warp_wait(sb_ready, c & 1, abort_word)) break;
-      if (c > 0 && !warp_wait(o_free, (c - 1) & 1, abort_word)) break;
-      tc_fence_after();
-      if (leader) {
-        product<kDs, kK, kMN>(tI, kbase(sQ), mnbase(sSb), iO, false);
-        mma_commit(q_free);
-      }
-      __syncwarp();
-      if (!warp_wait(k_ready, c & 1, abort_word)) break;
-      if (!warp_wait(&full_v[s], (c >> 1) & 1, abort_word)) break;
-      tc_fence_after();
-      if (leader) {
-        if (D == 128) {
-          product<8, kMN, kMN>(tS, mnbase(k), mnbase(v), iS, true);
-          product<8, kMN, kMN>(tS, mnbase(sKlo), mnbase(v), iS, true);
-        } else {
-          product<8, kMN, kMN>(tS, mnbase(k, sKlo - k), mnbase(v), iS, true);  // rows: hi, then lo
+    } else if (warp == 1) {
+      constexpr uint32_t iP = idesc_bf16_f32(128, 128, 0, 0), iO = idesc_bf16_f32(128, D, 0, 1), iS = idesc_bf16_f32(128, D, 1, 1);
+      constexpr int kDs = D / 16;
+      const bool leader = elect_one();
+      const uint32_t tS = tmem + kColS, tP = tmem + kColP, tI = tmem + kColI, tA = tmem + kColA;
+      const uint32_t sQ = smem_u32(sm + L::Q), sK = smem_u32(sm + L::K), sSb = smem_u32(sm + L::Sb),
+                     sKhi = smem_u32(sm + L::Khi), sKlo = smem_u32(sm + L::Klo);
+      for (int c = 0; c < nc; ++c) {
+        const int s = c & 1;
+        const uint32_t v = smem_u32(sm + L::V) + s * L::kTile;
+        if (!warp_wait(full_q, c & 1, abort_word)) break;
+        if (!warp_wait(full_k, c & 1, abort_word)) break;
+        tc_fence_after();
+        // the scores' columns are free: the previous P' V reads them before, in issue order
+        if (leader) {
+          product<kDs, kK, kK>(tP, kbase(sQ), kbase(sK), iP, false);
+          mma_commit(p_full);
+          mma_commit(k_free);
         }
-        mma_commit(s_full);
-        mma_commit(&k_free[s]);
+        __syncwarp();
+        // The update before the read: the read waits for the last outputs to be read out, the update
+        // only for the state's warps (the read takes the state from their copy).
+        if (!warp_wait(k_ready, c & 1, abort_word)) break;
+        if (!warp_wait(sb_ready, c & 1, abort_word)) break;
+        if (!warp_wait(&full_v[s], (c >> 1) & 1, abort_word)) break;
+        tc_fence_after();
+        if (leader) {
+          if (D == 128) {
+            product<8, kMN, kMN>(tS, mnbase(sKhi), mnbase(v), iS, true);
+            product<8, kMN, kMN>(tS, mnbase(sKlo), mnbase(v), iS, true);
+          } else {
+            product<8, kMN, kMN>(tS, mnbase(sKhi, L::kTile), mnbase(v), iS, true);  // rows: hi, then lo
+          }
+          mma_commit(s_full);
+        }
+        __syncwarp();
+        if (c > 0 && !warp_wait(o_free, (c - 1) & 1, abort_word)) break;
+        tc_fence_after();
+        if (leader) {
+          product<kDs, kK, kMN>(tI, kbase(sQ), mnbase(sSb), iO, false);
+          mma_commit(q_free);
+        }
+        __syncwarp();
+        if (!warp_wait(pp_ready, c & 1, abort_word)) break;
+        tc_fence_after();
+        if (leader) {
+          product_ts<kMN>(tA, tP, mnbase(v), iO, false);
+          mma_commit(&v_free[s]);
+          mma_commit(o_full);
+        }
+        __syncwarp();
       }
-      __syncwarp();
-      if (!warp_wait(pp_ready, c & 1, abort_word)) break;
-      tc_fence_after();
       if (leader) {
-        product_ts<kMN>(tA, tP, mnbase(v), iO, false);
-        mma_commit(&v_free[s]);
-        mma_commit(o_full);
+        mma_commit(drain);
+        wait_drain(drain, 0, status);
       }
-      __syncwarp();
-    }
-    if (leader) {
-      mma_commit(drain);
-      wait_drain(drain, 0, status);
+    } else if (warp == kWarpGate) {
+      const float *g = p.g + bh * p.N + c_lo * kC;
+      float4 cur = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (nc > 0) cur = load_gates(g, valid(0), lane);
+      for (int c = 0; c < nc; ++c) {
+        float4 nxt = cur;
+        if (c + 1 < nc) nxt = load_gates(g + (c + 1) * kC, valid(c + 1), lane);
+        if (c >= 2 && !warp_wait(&gate_free[c & 1], ((c >> 1) - 1) & 1, abort_word)) break;
+        float *hi = gate + (c & 1) * 2 * kC;
+        scan_gates(cur, lane, hi, hi + kC);
+        mbar_arrive(&gate_full[c & 1]);
+        cur = nxt;
+      }
     }
   } else if (warp < kWarpK) {
     // ---- weights of the scores: row i of this thread, keys [64 half, 64 half + 64) ----
-    const int q = warp & 3, i = q * 32 + lane, half = (warp - 2) >> 2;
+    const int q = warp & 3, i = q * 32 + lane, half = (warp - kWarpP) >> 2;
     const uint32_t tP = tmem + ((uint32_t)(q * 32) << 16) + kColP + 64 * half;
     for (int c = 0; c < nc; ++c) {
       if (!warp_wait(&gate_full[c & 1], (c >> 1) & 1, abort_word)) break;
@@ -242,7 +265,8 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
       mbar_arrive(&gate_free[c & 1]);
     }
   } else if (warp < kWarpS) {
-    // ---- weighted keys as a pair: hi in place once Q K^T has read them, lo beside them ----
+    // ---- weighted keys as a pair, in tiles of their own: the last update has read them ----
+    reg_dec<kRegsK>();
     const int r = threadIdx.x - kWarpK * 32;
     for (int c = 0; c < nc; ++c) {
       const int s = c & 1;
@@ -251,18 +275,19 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
       const float w = exp2f((hi[kC - 1] - hi[r]) + (lo[kC - 1] - lo[r]));
       const int tv = valid(c);
       mbar_arrive(&gate_free[c & 1]);
-      if (!warp_wait(&full_k[s], (c >> 1) & 1, abort_word)) break;
-      if (!warp_wait(p_full, c & 1, abort_word)) break;
-      if (c > 0 && !warp_wait(s_full, (c - 1) & 1, abort_word)) break;  // the last low parts are read
-      uint8_t *K = sm + L::K + s * L::kTile, *Klo = sm + L::Klo;
+      if (!warp_wait(full_k, c & 1, abort_word)) break;
+      if (c > 0 && !warp_wait(s_full, (c - 1) & 1, abort_word)) break;
+      const uint8_t *K = sm + L::K;
+      uint8_t *Khi = sm + L::Khi, *Klo = sm + L::Klo;
 #pragma unroll 4
       for (int e = 0; e < D / 8; ++e) {
         const uint32_t off = (e >> 3) * kBlk + sw128_offset(r, (e & 7) * 8);
         uint4 h = make_uint4(0u, 0u, 0u, 0u), l = h;
         if (r < tv) split8p(*reinterpret_cast<const uint4 *>(K + off), w, h, l);
-        *reinterpret_cast<uint4 *>(K + off) = h;
+        *reinterpret_cast<uint4 *>(Khi + off) = h;
         *reinterpret_cast<uint4 *>(Klo + off) = l;
       }
+      mbar_arrive(k_free);
       if (tv < kC) {  // padding tokens: a zero weight does not clear a NaN of the values
         if (!warp_wait(&full_v[s], (c >> 1) & 1, abort_word)) break;
         uint8_t *V = sm + L::V + s * L::kTile;
@@ -275,39 +300,42 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
     }
   } else if (warp < kWarpO) {
     // ---- state: bf16 copy for the queries, then decayed in place for the update ----
+    reg_inc<kRegsSO>();
     const int q = warp & 3, T = q * 32 + lane;
     const int row = D == 64 ? T & 63 : T;
     const bool main_row = D == 128 || q < 2;  // D = 64: lanes from 64 on hold the low keys' part
     const uint32_t tS = tmem + ((uint32_t)(q * 32) << 16) + kColS;
     float *sum = reinterpret_cast<float *>(sm + L::Sum);
-    uint32_t r[32];
+    uint32_t r[2][32];
     const long dd = (long)D * D;
     const float *init = p.init ? p.init + (bh * p.init_segs + (long)seg * p.init_step) * dd + (long)row * D : nullptr;
     auto load_init = [&](int cb) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (init && main_row) x = reinterpret_cast<const float4 *>(init + cb * 32)[e];
-        r[4 * e] = __float_as_uint(x.x), r[4 * e + 1] = __float_as_uint(x.y);
-        r[4 * e + 2] = __float_as_uint(x.z), r[4 * e + 3] = __float_as_uint(x.w);
-      }
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (init && main_row) x = reinterpret_cast<const float4 *>(init + cb * 64 + b * 32)[e];
+          r[b][4 * e] = __float_as_uint(x.x), r[b][4 * e + 1] = __float_as_uint(x.y);
+          r[b][4 * e + 2] = __float_as_uint(x.z), r[b][4 * e + 3] = __float_as_uint(x.w);
+        }
     };
-    auto join = [&]() {  // D = 64: the two parts of 32 columns meet in the rows of the first two warps
+    auto join = [&]() {  // D = 64: the two parts meet in the rows of the first two warps
       if (D == 128) return;
       if (!main_row)
 #pragma unroll
-        for (int e = 0; e < 32; ++e) sum[row * 65 + e] = __uint_as_float(r[e]);
+        for (int e = 0; e < 64; ++e) sum[row * 65 + e] = __uint_as_float(r[e >> 5][e & 31]);
       named_bar(kBarS, 128);
       if (main_row)
 #pragma unroll
-        for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) + sum[row * 65 + e]);
-      named_bar(kBarS, 128);
+        for (int e = 0; e < 64; ++e)
+          r[e >> 5][e & 31] = __float_as_uint(__uint_as_float(r[e >> 5][e & 31]) + sum[row * 65 + e]);
     };
     bool ok = true;
     for (int c = 0; c < nc; ++c) {
       bool w = mbar_wait(&gate_full[c & 1], (c >> 1) & 1, abort_word, status);
       if (w && c > 0) w = mbar_wait(s_full, (c - 1) & 1, abort_word, status);
-      if (bar_or(kBarS, 128, !w)) {
+      if (bar_or(kBarS, 128, !w)) {  // D = 64: also, the last joined rows are read
         ok = false;
         break;
       }
@@ -316,26 +344,37 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
       const float f = exp2f(hi[kC - 1] + hi[2 * kC - 1]);
       mbar_arrive(&gate_free[c & 1]);
 #pragma unroll 1
-      for (int cb = 0; cb < D / 32; ++cb) {
+      for (int cb = 0; cb < D / 64; ++cb) {
         if (c == 0)
           load_init(cb);
         else
-          tmem_ld32(tS + cb * 32, r);
-        uint32_t y[32];
+          tmem_ld32x2(tS + cb * 64, tS + cb * 64 + 32, r[0], r[1]);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) y[e] = r[e];
-        scale32(y, f);
-        tmem_st32(tS + cb * 32, y);
+        for (int h = 0; h < 4; ++h) {
+          uint32_t y[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(r[h >> 1][16 * (h & 1) + e]) * f);
+          tmem_st16_nowait(tS + cb * 64 + 16 * h, y);
+        }
+        if (cb == 0 && c > 0) {  // the last read of the copy is done
+          const bool qw = mbar_wait(q_free, (c - 1) & 1, abort_word, status);
+          if (bar_or(kBarS, 128, !qw)) {
+            ok = false;
+            break;
+          }
+        }
         join();
         if (main_row) {
-          uint4 h[4];
-          to_bf16x32(r, h);
-          uint8_t *Sb = sm + L::Sb + (cb >> 1) * kBlk;
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            *reinterpret_cast<uint4 *>(Sb + sw128_offset(row, (cb & 1) * 32 + 8 * e)) = h[e];
+          for (int b = 0; b < 2; ++b) {
+            uint4 h[4];
+            to_bf16x32(r[b], h);
+            stage_row32(sm + L::Sb + cb * kBlk, row, b, h);
+          }
         }
       }
+      if (!ok) break;
+      tmem_wait_st();
       fence_async_smem();
       tc_fence_before();
       mbar_arrive(sb_ready);
@@ -346,23 +385,24 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
         tc_fence_after();
         float *dst = p.S + bh * dd + (long)row * D;
 #pragma unroll 1
-        for (int cb = 0; cb < D / 32; ++cb) {
+        for (int cb = 0; cb < D / 64; ++cb) {
           if (nc == 0)
             load_init(cb);
           else
-            tmem_ld32(tS + cb * 32, r);
+            tmem_ld32x2(tS + cb * 64, tS + cb * 64 + 32, r[0], r[1]);
           join();
           if (main_row)
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              reinterpret_cast<float4 *>(dst + cb * 32)[e] =
-                  make_float4(__uint_as_float(r[4 * e]), __uint_as_float(r[4 * e + 1]), __uint_as_float(r[4 * e + 2]),
-                              __uint_as_float(r[4 * e + 3]));
+            for (int e = 0; e < 16; ++e)
+              reinterpret_cast<float4 *>(dst + cb * 64)[e] =
+                  make_float4(__uint_as_float(r[e >> 3][4 * (e & 7)]), __uint_as_float(r[e >> 3][4 * (e & 7) + 1]),
+                              __uint_as_float(r[e >> 3][4 * (e & 7) + 2]), __uint_as_float(r[e >> 3][4 * (e & 7) + 3]));
         }
       }
     }
-  } else if (warp < kWarpGate) {
+  } else {
     // ---- outputs: row i, 2^{c_i} (Q S) + P' V ----
+    reg_inc<kRegsSO>();
     const int q = warp & 3, i = q * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16);
     for (int c = 0; c < nc; ++c) {
@@ -376,38 +416,22 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
       __nv_bfloat16 *dst = p.out + (bh * p.N + (c_lo + c) * kC + i) * D;
 #pragma unroll 1
       for (int cb = 0; cb < D / 32; ++cb) {
+        uint32_t x[32], y[32];
         uint4 o[4];
-        uint32_t *ow = reinterpret_cast<uint32_t *>(o);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t x[16], y[16];
-          tmem_ld16x2(tl + kColI + cb * 32 + 16 * h, tl + kColA + cb * 32 + 16 * h, x, y);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float2 z = __ffma2_rn(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), make_float2(f, f),
-                                        make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])));
-            ow[8 * h + e] = pack_bf16(z.x, z.y);
-          }
-        }
+        tmem_ld32x2(tl + kColI + cb * 32, tl + kColA + cb * 32, x, y);
         if (cb == D / 32 - 1) {
           tc_fence_before();
           mbar_arrive(o_free);
         }
+        uint32_t *ow = reinterpret_cast<uint32_t *>(o);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float2 z = __ffma2_rn(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), make_float2(f, f),
+                                      make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])));
+          ow[e] = pack_bf16(z.x, z.y);
+        }
         if (in) store_row64(dst + cb * 32, o, p.wide);
       }
-    }
-  } else {
-    const float *g = p.g + bh * p.N + c_lo * kC;
-    float4 cur = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (nc > 0) cur = load_gates(g, valid(0), lane);
-    for (int c = 0; c < nc; ++c) {
-      float4 nxt = cur;
-      if (c + 1 < nc) nxt = load_gates(g + (c + 1) * kC, valid(c + 1), lane);
-      if (c >= 2 && !warp_wait(&gate_free[c & 1], ((c >> 1) - 1) & 1, abort_word)) break;
-      float *hi = gate + (c & 1) * 2 * kC;
-      scan_gates(cur, lane, hi, hi + kC);
-      mbar_arrive(&gate_full[c & 1]);
-      cur = nxt;
     }
   }
 
@@ -450,6 +474,12 @@ template <int D>
 cudaError_t launch_main(const Params &mp, long BH, cudaStream_t stream) {
   cudaError_t e = ensure_smem_optin((const void *)gated_tc_kernel<D>, (int)Lay<D>::Bytes);
   if (e != cudaSuccess) return e;
+  // the warpgroups' register shares add up to the launch's: with fewer they would wait forever
+  static const int regs = [] {
+    cudaFuncAttributes a;
+    return cudaFuncGetAttributes(&a, gated_tc_kernel<D>) == cudaSuccess ? a.numRegs : 0;
+  }();
+  if (regs != kRegs) return cudaErrorInvalidConfiguration;
   LaunchTimer timer(kKGated, stream);
   gated_tc_kernel<D><<<(unsigned)(BH * mp.segs), kThreads, Lay<D>::Bytes, stream>>>(mp);
   e = cudaGetLastError();

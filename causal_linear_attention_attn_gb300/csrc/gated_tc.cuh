@@ -58,6 +58,16 @@ __device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint64_t b, u
     mma_bf16_ts(d, a + (ks < 4 ? 8 * ks : 32 + 8 * ks), b + op_step<kB, kBlk>(ks), idesc, (ks > 0 || add) ? 1u : 0u);
 }
 
+// Registers of a warpgroup (four warps, aligned).
+template <int kN>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kN));
+}
+template <int kN>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kN));
+}
+
 // All lanes wait; false for the whole warp if any lane's wait gave up.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile uint32_t *abort_word) {
   const bool ok = mbar_wait(bar, parity, abort_word, &g_gated_status);
