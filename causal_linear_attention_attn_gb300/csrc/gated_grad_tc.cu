@@ -56,7 +56,7 @@ struct Lay {
   static constexpr uint32_t Buf = Gate + 2 * kC * 4;     // 320 floats
   static constexpr uint32_t Red = Buf + 320 * 4;         // 4 floats
   static constexpr uint32_t Bars = Red + 16;
-  static constexpr int kNumBars = 3 + 2 * kRing + 15;
+  static constexpr int kNumBars = 3 + 2 * kRing + 16;
   static constexpr uint32_t Misc = Bars + kNumBars * 8;
   static constexpr uint32_t Bytes = Misc + 16;
 };
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
            *b0 = ring_free + kRing, *tok_free = b0, *gate_full = b0 + 1, *e_full = b0 + 2, *el_done = b0 + 3,
            *q_in = b0 + 4, *k_in = b0 + 5, *v_in = b0 + 6, *x_ready = b0 + 7, *out_full = b0 + 8, *out_free = b0 + 9,
            *dg_in = b0 + 10, *dot_full = b0 + 11, *dot_free = b0 + 12,
-           *v_free = b0 + 13, *d_free = b0 + 14;
+           *v_free = b0 + 13, *d_free = b0 + 14, *dv_full = b0 + 15;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::Misc);
   volatile uint32_t *abort_word = reinterpret_cast<volatile uint32_t *>(sm + L::Misc + 4);
   uint64_t *drain = reinterpret_cast<uint64_t *>(sm + L::Misc + 8);
@@ -164,6 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
     mbar_init(out_full, 1);
     mbar_init(out_free, 256);
     mbar_init(d_free, 256);
+    mbar_init(dv_full, 1);
     mbar_init(dg_in, 256 + 128);
     mbar_init(dot_full, 4);
     mbar_init(dot_free, 32);
@@ -248,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
       const uint32_t ph = it & 1;
       // the chunk's pieces S hi, S lo, R hi, R lo take the ring's two places in turn
       static_assert(kRing == 2, "places by parity");
-      if (!warp_wait(gate_full, ph, abort_word)) break;
+      if (p.lengths && !warp_wait(gate_full, ph, abort_word)) break;  // padding tokens are cleared
       if (!warp_wait(full_kq, ph, abort_word)) break;
       // the columns of P: the previous W P is read by the previous dV's product, in issue order
       tc_fence_after();
@@ -303,6 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
       tc_fence_after();
       if (leader) {
         product_ts<kMN>(tD, tP, mnbase(sO), iKM, true);
+        mma_commit(dv_full);  // dV first: the next chunk's D^T waits for its columns
         product<8, kK, kMN>(tK, kbase(sW), mnbase(sQ), iKM, true);
         product<8, kMN, kMN>(tQ, mnbase(sW), mnbase(sK), iMM, true);
         mma_commit(tok_free);
@@ -538,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
       }
       tc_fence_before();
       mbar_arrive(x_ready);
-      if (!warp_wait(out_full, ph, abort_word)) break;
+      if (!warp_wait(dv_full, ph, abort_word)) break;
       tc_fence_after();
       // padding rows (T >= tv) are zero whatever the states hold
       auto put = [&](uint32_t col, __nv_bfloat16 *dst) {
@@ -553,6 +555,8 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
       for (int cb = 0; cb < D / 64; ++cb) put(tl + kColD + half * (D / 2) + cb * 32, p.dv + half * (D / 2) + cb * 32);
       tc_fence_before();
       mbar_arrive(d_free);
+      if (!warp_wait(out_full, ph, abort_word)) break;
+      tc_fence_after();
 #pragma unroll 1
       for (int cb = 0; cb < D / 32; ++cb) put(tX + cb * 32, dx + cb * 32);
       tc_fence_before();

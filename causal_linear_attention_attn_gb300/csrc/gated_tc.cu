@@ -147,6 +147,11 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
         if (c >= 1 && !mbar_wait(q_free, (c - 1) & 1, abort_word, status)) break;
         load(L::Q, &p.tq, full_q, tok);
         q_issued = c + 1;
+        if (c + 1 < nc)  // (values have a second stage)
+          for (int b = 0; b < D / 64; ++b) {
+            tma_prefetch_3d(&p.tk, 64 * b, tok + kC, (int)bh);
+            tma_prefetch_3d(&p.tq, 64 * b, tok + kC, (int)bh);
+          }
       }
       for (int c = max(0, v_issued - 2); c < v_issued; ++c) wait_drain(&full_v[c & 1], (c >> 1) & 1, status);
       if (k_issued) wait_drain(full_k, (k_issued - 1) & 1, status);

@@ -58,6 +58,15 @@ __device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint64_t b, u
     mma_bf16_ts(d, a + (ks < 4 ? 8 * ks : 32 + 8 * ks), b + op_step<kB, kBlk>(ks), idesc, (ks > 0 || add) ? 1u : 0u);
 }
 
+// A tile into L2 ahead of its load: shared memory has no room for a second stage of everything, and a
+// load that starts when its place frees up then waits for L2 and not for DRAM.
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+
 // Registers of a warpgroup (four warps, aligned).
 template <int kN>
 __device__ __forceinline__ void reg_inc() {
