@@ -20,12 +20,13 @@
 //   + sum_{j < t} 2^{c_T - c_j} k_j^T R v_j              i behind it
 //   + 2^{c_T} <S, R>                                     both outside.
 //
-// Three launches: each chunk's own sum of k v^T (and q do^T), one CTA a chunk; a scan over a
-// head's chunks, one thread for four elements of the state; each chunk's outputs, one CTA a chunk.
-// The states between the launches cost 4 dk dv / T bytes per token each way; in exchange a single
-// long sequence fills the device, where one CTA per head would leave it idle.
-// fp32 fma rate and latency bound it: at 2 x 4 x 333 tokens (64 x 32) the gradient's three
-// launches are shorter than their launch latency.
+// Three phases of one cooperative launch (small calls, which are most of this path's, are bound by
+// launches): each chunk's own sum of k v^T (and q do^T); a scan over a head's chunks, one thread for
+// four elements of the state; each chunk's outputs or gradients.  The states between the phases cost
+// 4 dk dv / T bytes per token each way; in exchange a single long sequence fills the device, where
+// one CTA per head would leave it idle.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 
 #include "gated.cuh"
@@ -77,12 +78,10 @@ __device__ __forceinline__ void load_rows(float *dst, int ld, const Tin *src, in
 
 // Chunk sums: blockIdx.z 0: sum_t 2^{c_T - c_t} k_t v_t^T; 1: sum_t 2^{c_t} q_t do_t^T.
 template <typename Tin>
-__global__ void __launch_bounds__(kThreads) gated_sums_kernel(const __grid_constant__ Args a) {
-  extern __shared__ float sm[];
+__device__ __forceinline__ void chunk_sums(const Args &a, float *sm, long item, bool rev) {
   const int dk = a.dk, dv = a.dv;
   float *A = sm, *B = A + kT * dk, *w = B + kT * dv;
-  const long bh = blockIdx.x / a.n, ch = blockIdx.x - bh * a.n, t0 = ch * kT;
-  const bool rev = blockIdx.z == 1;
+  const long bh = item / a.n, ch = item - bh * a.n, t0 = ch * kT;
   const int tid = threadIdx.x;
   const long len = row_length(a.lengths, bh / a.H, a.N);
   if (t0 >= len) return;  // the scan stops before this chunk
@@ -116,14 +115,11 @@ __global__ void __launch_bounds__(kThreads) gated_sums_kernel(const __grid_const
   }
 }
 
-// Scan over a head's chunks.  blockIdx.z 0: chunk sums -> state before each chunk, final state to S;
-// 1: sums -> gradient of the state behind each chunk, initial state's gradient to dS0.
-__global__ void __launch_bounds__(128) gated_scan_kernel(const __grid_constant__ Args a) {
-  const long dd = (long)a.dk * a.dv, parts = (dd / 4 + 127) / 128;
-  const long bh = blockIdx.x / parts;
-  const bool rev = blockIdx.z == 1;
-  const long e = ((blockIdx.x - bh * parts) * 128 + threadIdx.x) * 4;
-  if (e >= dd) return;
+// Scan over a head's chunks, elements [e, e + 4) of head bh's state.  Forward: chunk sums -> state
+// before each chunk, final state to S; rev: sums -> gradient of the state behind each chunk, initial
+// state's gradient to dS0.
+__device__ __forceinline__ void chunk_scan_states(const Args &a, long bh, long e, bool rev) {
+  const long dd = (long)a.dk * a.dv;
   const long len = row_length(a.lengths, bh / a.H, a.N);
   const int n = (int)((len + kT - 1) / kT);
   const float *first = rev ? a.dS : a.S0;
@@ -201,12 +197,11 @@ __device__ __forceinline__ void rows_times_t(float (&acc)[4][4], const float *A,
 }
 
 template <typename Tin>
-__global__ void __launch_bounds__(kThreads) gated_out_kernel(const __grid_constant__ Args a) {
-  extern __shared__ float sm[];
+__device__ __forceinline__ void chunk_out(const Args &a, float *sm, long item) {
   const int dk = a.dk, dv = a.dv, lk = dk + 4;
   float *Q = sm, *K = Q + kT * lk, *V = K + kT * lk, *P = V + kT * dv;
   float *hi = P + kT * (kT + 1), *lo = hi + kT;
-  const long bh = blockIdx.x / a.n, ch = blockIdx.x - bh * a.n, t0 = ch * kT;
+  const long bh = item / a.n, ch = item - bh * a.n, t0 = ch * kT;
   const int tid = threadIdx.x;
   const long len = row_length(a.lengths, bh / a.H, a.N);
   if (t0 >= len) return;
@@ -250,14 +245,13 @@ __global__ void __launch_bounds__(kThreads) gated_out_kernel(const __grid_consta
 }
 
 template <typename Tin>
-__global__ void __launch_bounds__(kThreads) gated_grad_kernel(const __grid_constant__ Args a) {
-  extern __shared__ float sm[];
+__device__ __forceinline__ void chunk_grad(const Args &a, float *sm, long item) {
   const int dk = a.dk, dv = a.dv, lk = dk + 4, lv = dv + 4;
   float *Q = sm, *K = Q + kT * lk, *V = K + kT * lk, *dO = V + kT * lv;
   float *P = dO + kT * lv, *D = P + kT * (kT + 1), *M = D + kT * (kT + 1);
   float *hi = M + kT * (kT + 1), *lo = hi + kT, *ew = lo + kT;
   float *left = ew + kT, *right = left + kT * 33, *red = right + kT * 33;  // [kT][33] partial dots, [8] warp sums
-  const long bh = blockIdx.x / a.n, ch = blockIdx.x - bh * a.n, t0 = ch * kT;
+  const long bh = item / a.n, ch = item - bh * a.n, t0 = ch * kT;
   const int tid = threadIdx.x, lane = tid & 31;
   const long len = row_length(a.lengths, bh / a.H, a.N);
   const int rows = (int)min((long)kT, a.N - t0);
@@ -411,41 +405,52 @@ __global__ void __launch_bounds__(kThreads) gated_grad_kernel(const __grid_const
   }
 }
 
+template <typename Tin, bool kGrad>
+__global__ void __launch_bounds__(kThreads) gated_simt_kernel(const __grid_constant__ Args a, long BH) {
+  extern __shared__ float sm[];
+  const cooperative_groups::grid_group grid = cooperative_groups::this_grid();
+  const long items = BH * a.n;
+  for (long x = blockIdx.x; x < items * (kGrad ? 2 : 1); x += gridDim.x) {
+    chunk_sums<Tin>(a, sm, x % items, x >= items);
+    __syncthreads();  // shared memory is free for the next chunk
+  }
+  grid.sync();
+  const long quads = (long)a.dk * a.dv / 4, all = BH * quads;
+  for (long x = (long)blockIdx.x * kThreads + threadIdx.x; x < all * (kGrad ? 2 : 1); x += (long)gridDim.x * kThreads) {
+    const long y = x % all;
+    chunk_scan_states(a, y / quads, (y % quads) * 4, x >= all);
+  }
+  grid.sync();
+  for (long x = blockIdx.x; x < items; x += gridDim.x) {
+    if (kGrad)
+      chunk_grad<Tin>(a, sm, x);
+    else
+      chunk_out<Tin>(a, sm, x);
+    __syncthreads();
+  }
+}
+
 size_t state_floats(long BH, long N, int dk, int dv) { return (size_t)BH * ((N + kT - 1) / kT) * dk * dv; }
 
-template <typename Tin>
-cudaError_t launch_t(const Args &a, long BH, bool grad, cudaStream_t stream) {
+template <typename Tin, bool kGrad>
+cudaError_t launch_t(Args a, long BH, cudaStream_t stream) {
   const int dk = a.dk, dv = a.dv;
   const size_t sm_sums = sizeof(float) * (kT * (dk + dv) + kT);
   const size_t sm_out = sizeof(float) * (2 * kT * (dk + 4) + kT * dv + kT * (kT + 1) + 2 * kT);
   const size_t sm_grad = sizeof(float) * (2 * kT * (dk + 4) + 2 * kT * (dv + 4) + 3 * kT * (kT + 1) + 3 * kT + 2 * kT * 33 + 8);
-  const void *last = grad ? (const void *)gated_grad_kernel<Tin> : (const void *)gated_out_kernel<Tin>;
-  cudaError_t e = ensure_smem_optin(last, (int)(grad ? sm_grad : sm_out));
+  const size_t smem = std::max(sm_sums, kGrad ? sm_grad : sm_out);
+  const void *fn = (const void *)gated_simt_kernel<Tin, kGrad>;
+  cudaError_t e = ensure_smem_optin(fn, (int)smem);
   if (e != cudaSuccess) return e;
-  if (a.n * BH > 0x7fffffffL || BH * 32 > 0x7fffffffL) return cudaErrorInvalidValue;
-  const dim3 chunks((unsigned)(a.n * BH)), both((unsigned)(a.n * BH), 1, grad ? 2 : 1);
-  {
-    LaunchTimer timer(kKGatedState, stream);
-    gated_sums_kernel<Tin><<<both, kThreads, sm_sums, stream>>>(a);
-    e = cudaGetLastError();
-    timer.done(e);
-    if (e != cudaSuccess) return e;
-    count_launch();
-  }
-  {
-    LaunchTimer timer(kKGatedState, stream);
-    gated_scan_kernel<<<dim3((unsigned)(BH * ((dk * dv / 4 + 127) / 128)), 1, grad ? 2 : 1), 128, 0, stream>>>(a);
-    e = cudaGetLastError();
-    timer.done(e);
-    if (e != cudaSuccess) return e;
-    count_launch();
-  }
-  LaunchTimer timer(grad ? kKGatedBackward : kKGated, stream);
-  if (grad)
-    gated_grad_kernel<Tin><<<chunks, kThreads, sm_grad, stream>>>(a);
-  else
-    gated_out_kernel<Tin><<<chunks, kThreads, sm_out, stream>>>(a);
-  e = cudaGetLastError();
+  int per_sm = 0;
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, kThreads, smem);
+  if (e != cudaSuccess) return e;
+  const long room = (long)std::max(1, per_sm) * std::max(1, device_info(-1).sm_count);
+  // enough blocks for the chunks and for the scan, all of them resident
+  const long want = std::max(BH * a.n * (kGrad ? 2 : 1), BH * dk * dv / 4 * (kGrad ? 2 : 1) / kThreads);
+  LaunchTimer timer(kGrad ? kKGatedBackward : kKGated, stream);
+  void *args[] = {&a, &BH};
+  e = cudaLaunchCooperativeKernel(fn, dim3((unsigned)std::max(1L, std::min(room, want))), dim3(kThreads), args, smem, stream);
   timer.done(e);
   if (e == cudaSuccess) count_launch();
   return e;
@@ -470,16 +475,16 @@ size_t gated_simt_workspace(long BH, long N, int dk, int dv, bool grad) {
 
 cudaError_t launch_gated_simt(const GatedProblem &p) {
   const Args a = make_args(p, false);
-  return p.dt == LA_F32 ? launch_t<float>(a, p.BH(), false, p.stream)
-                        : launch_t<__nv_bfloat16>(a, p.BH(), false, p.stream);
+  return p.dt == LA_F32 ? launch_t<float, false>(a, p.BH(), p.stream)
+                        : launch_t<__nv_bfloat16, false>(a, p.BH(), p.stream);
 }
 
 cudaError_t launch_gated_grad_simt(const GatedGradProblem &b) {
   Args a = make_args(b.p, true);
   a.dout = b.dout, a.dS = b.dS, a.dq = b.dq, a.dk_ = b.dk, a.dv_ = b.dv, a.dg = b.dg, a.dS0 = b.dS0;
   a.S = nullptr;
-  return b.p.dt == LA_F32 ? launch_t<float>(a, b.p.BH(), true, b.p.stream)
-                          : launch_t<__nv_bfloat16>(a, b.p.BH(), true, b.p.stream);
+  return b.p.dt == LA_F32 ? launch_t<float, true>(a, b.p.BH(), b.p.stream)
+                          : launch_t<__nv_bfloat16, true>(a, b.p.BH(), b.p.stream);
 }
 
 }  // namespace la

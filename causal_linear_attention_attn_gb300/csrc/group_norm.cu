@@ -17,8 +17,10 @@
 // of a block cover up to 2048 channels of one token or the same channels of several tokens.  So
 // channels-last rows move in runs of up to 4 KB, and every thread keeps its channels while the block
 // walks over tokens: the column sums dw, db stay in registers until the block's end.  Each block
-// writes its column sums once and a second kernel adds them in a fixed order (no atomics, so the
-// gradient is the same from run to run).
+// writes its column sums once and, behind a grid barrier (a cooperative launch: the blocks are resident
+// anyway), they are added in a fixed order: no atomics, so the gradient is the same from run to run.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 
 #include "gated.cuh"
@@ -38,7 +40,7 @@ __device__ __forceinline__ float group_sum(float x) {
 }
 
 // How a launch cuts [B * N tokens][H * d channels]: a block covers `heads` heads of `rows` tokens at
-// a time (blockIdx.y: which heads) and walks over tokens with stride gridDim.x * rows.
+// a time (a slab of heads), a few such groups of consecutive tokens in flight.
 struct Cut {
   int heads, rows, threads, slabs;
 };
@@ -56,11 +58,11 @@ template <int D>
 struct Place {  // what a thread owns
   int h, c, row;
   bool live;
-  __device__ Place(const Cut &cut, int H) {
+  __device__ Place(const Cut &cut, int H, int slab) {
     constexpr int kLanes = D / 8;
     const int grp = threadIdx.x / kLanes;
     row = grp / cut.heads;
-    h = blockIdx.y * cut.heads + grp % cut.heads;
+    h = slab * cut.heads + grp % cut.heads;
     c = (threadIdx.x % kLanes) * 8;
     live = row < cut.rows && h < H;
   }
@@ -139,12 +141,12 @@ Divider make_divider(uint32_t n) {
 }
 
 template <typename T, int D, bool kGate, int kRowsAhead>
-__global__ void __launch_bounds__(kMaxThreads)
+__global__ void __launch_bounds__(kMaxThreads, 3)
     group_norm_kernel(const __grid_constant__ NormProblem p, const __grid_constant__ Cut cut,
                       const __grid_constant__ Divider by_n) {
-  const Place<D> me(cut, p.H);
   const uint32_t tokens = (uint32_t)((long)p.B * p.N);
-  const long stride = (long)gridDim.x * cut.rows, HD = (long)p.H * D;
+  const long HD = (long)p.H * D;
+  const Place<D> me(cut, p.H, blockIdx.y);
   const long col = (long)me.h * D + me.c;
   float2 w[4], b[4];
 #pragma unroll
@@ -158,11 +160,11 @@ __global__ void __launch_bounds__(kMaxThreads)
     for (int e = 0; e < 4; ++e) b[e] = reinterpret_cast<const float2 *>(p.bias + col)[e];
   }
   // every lane of a warp runs the same number of turns: the shuffles need all of them
-  for (long r0 = (long)blockIdx.x * cut.rows; r0 < tokens; r0 += kRowsAhead * stride) {
+  for (long r0 = (long)blockIdx.x * cut.rows * kRowsAhead; r0 < tokens; r0 += (long)gridDim.x * cut.rows * kRowsAhead) {
     Raw<T> x[kRowsAhead], g[kRowsAhead];
 #pragma unroll
     for (int u = 0; u < kRowsAhead; ++u) {
-      const long r = r0 + u * stride + me.row;
+      const long r = r0 + u * cut.rows + me.row;
       x[u].zero();
       if (me.live && r < tokens) {
         const uint32_t bi = by_n.of((uint32_t)r), n = (uint32_t)r - bi * by_n.n;
@@ -175,7 +177,7 @@ __global__ void __launch_bounds__(kMaxThreads)
       float2 y[4], t[4];
       x[u].get(y);
       normalize<D>(y, p.eps);
-      const long r = r0 + u * stride + me.row;
+      const long r = r0 + u * cut.rows + me.row;
       if (!(me.live && r < tokens)) continue;
 #pragma unroll
       for (int e = 0; e < 4; ++e) y[e] = __ffma2_rn(y[e], w[e], b[e]);
@@ -196,109 +198,114 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
                            const __grid_constant__ Divider by_n) {
   __shared__ float sums[kMaxThreads][16 + 1];
   const NormProblem &p = q.p;
-  const Place<D> me(cut, p.H);
   const uint32_t tokens = (uint32_t)((long)p.B * p.N);
-  const long stride = (long)gridDim.x * cut.rows, HD = (long)p.H * D;
-  const long col = (long)me.h * D + me.c;
-  float2 w[4], b[4], dw[4], db[4];
+  const long HD = (long)p.H * D;
+  for (int slab = blockIdx.y; slab < cut.slabs; slab += gridDim.y) {
+    const Place<D> me(cut, p.H, slab);
+    const long col = (long)me.h * D + me.c;
+    float2 w[4], b[4], dw[4], db[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) w[e] = both(1.f), b[e] = dw[e] = db[e] = both(0.f);
-  if (me.live && p.weight) {
+    for (int e = 0; e < 4; ++e) w[e] = both(1.f), b[e] = dw[e] = db[e] = both(0.f);
+    if (me.live && p.weight) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) w[e] = reinterpret_cast<const float2 *>(p.weight + col)[e];
-  }
-  if (me.live && p.bias) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) b[e] = reinterpret_cast<const float2 *>(p.bias + col)[e];
-  }
-  for (long r0 = (long)blockIdx.x * cut.rows; r0 < tokens; r0 += kRowsAhead * stride) {
-    Raw<T> x[kRowsAhead], g[kRowsAhead], dy[kRowsAhead];
-#pragma unroll
-    for (int u = 0; u < kRowsAhead; ++u) {
-      const long r = r0 + u * stride + me.row;
-      x[u].zero(), dy[u].zero(), g[u].zero();
-      if (me.live && r < tokens) {
-        const uint32_t bi = by_n.of((uint32_t)r), n = (uint32_t)r - bi * by_n.n;
-        x[u].load((const T *)p.x + (((long)bi * p.H + me.h) * p.N + n) * D + me.c);
-        dy[u].load((const T *)q.dy + r * HD + col);
-        if (kGate) g[u].load((const T *)p.gate + r * HD + col);
-      }
+      for (int e = 0; e < 4; ++e) w[e] = reinterpret_cast<const float2 *>(p.weight + col)[e];
     }
+    if (me.live && p.bias) {
 #pragma unroll
-    for (int u = 0; u < kRowsAhead; ++u) {
-      const long r = r0 + u * stride + me.row;
-      const bool in = me.live && r < tokens;
-      float2 h[4], t[4];
-      x[u].get(h);
-      dy[u].get(t);
-      const float rstd = normalize<D>(h, p.eps);
-      if (kGate) {
-        float2 gg[4], o[4];
-        g[u].get(gg);
+      for (int e = 0; e < 4; ++e) b[e] = reinterpret_cast<const float2 *>(p.bias + col)[e];
+    }
+    for (long r0 = (long)blockIdx.x * cut.rows * kRowsAhead; r0 < tokens; r0 += (long)gridDim.x * cut.rows * kRowsAhead) {
+      Raw<T> x[kRowsAhead], g[kRowsAhead], dy[kRowsAhead];
+#pragma unroll
+      for (int u = 0; u < kRowsAhead; ++u) {
+        const long r = r0 + u * cut.rows + me.row;
+        x[u].zero(), dy[u].zero(), g[u].zero();
+        if (me.live && r < tokens) {
+          const uint32_t bi = by_n.of((uint32_t)r), n = (uint32_t)r - bi * by_n.n;
+          x[u].load((const T *)p.x + (((long)bi * p.H + me.h) * p.N + n) * D + me.c);
+          dy[u].load((const T *)q.dy + r * HD + col);
+          if (kGate) g[u].load((const T *)p.gate + r * HD + col);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kRowsAhead; ++u) {
+        const long r = r0 + u * cut.rows + me.row;
+        const bool in = me.live && r < tokens;
+        float2 h[4], t[4];
+        x[u].get(h);
+        dy[u].get(t);
+        const float rstd = normalize<D>(h, p.eps);
+        if (kGate) {
+          float2 gg[4], o[4];
+          g[u].get(gg);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 sg = make_float2(sigmoid(gg[e].x), sigmoid(gg[e].y));
+            const float2 silu = __fmul2_rn(gg[e], sg);
+            // silu' = sigmoid + silu (1 - sigmoid)
+            const float2 ds = __ffma2_rn(__fmul2_rn(silu, both(-1.f)), sg, __fadd2_rn(sg, silu));
+            o[e] = __fmul2_rn(__fmul2_rn(t[e], __ffma2_rn(h[e], w[e], b[e])), ds);
+            t[e] = __fmul2_rn(t[e], silu);
+          }
+          if (in) put8((T *)q.dgate + r * HD + col, o);
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float2 sg = make_float2(sigmoid(gg[e].x), sigmoid(gg[e].y));
-          const float2 silu = __fmul2_rn(gg[e], sg);
-          // silu' = sigmoid + silu (1 - sigmoid)
-          const float2 ds = __ffma2_rn(__fmul2_rn(silu, both(-1.f)), sg, __fadd2_rn(sg, silu));
-          o[e] = __fmul2_rn(__fmul2_rn(t[e], __ffma2_rn(h[e], w[e], b[e])), ds);
-          t[e] = __fmul2_rn(t[e], silu);
+          dw[e] = __ffma2_rn(t[e], h[e], dw[e]);
+          db[e] = __fadd2_rn(db[e], t[e]);
+          t[e] = __fmul2_rn(t[e], w[e]);
         }
-        if (in) put8((T *)q.dgate + r * HD + col, o);
-      }
+        const float su = group_sum<D>(sum8(t)) * (-1.f / D), suh = group_sum<D>(dot8(t, h)) * (-1.f / D);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        dw[e] = __ffma2_rn(t[e], h[e], dw[e]);
-        db[e] = __fadd2_rn(db[e], t[e]);
-        t[e] = __fmul2_rn(t[e], w[e]);
-      }
-      const float su = group_sum<D>(sum8(t)) * (-1.f / D), suh = group_sum<D>(dot8(t, h)) * (-1.f / D);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) t[e] = __fmul2_rn(__fadd2_rn(__ffma2_rn(h[e], both(suh), t[e]), both(su)), both(rstd));
-      if (in) {
-        const uint32_t bi = by_n.of((uint32_t)r), n = (uint32_t)r - bi * by_n.n;
-        put8((T *)q.dx + (((long)bi * p.H + me.h) * p.N + n) * D + me.c, t);
+        for (int e = 0; e < 4; ++e) t[e] = __fmul2_rn(__fadd2_rn(__ffma2_rn(h[e], both(suh), t[e]), both(su)), both(rstd));
+        if (in) {
+          const uint32_t bi = by_n.of((uint32_t)r), n = (uint32_t)r - bi * by_n.n;
+          put8((T *)q.dx + (((long)bi * p.H + me.h) * p.N + n) * D + me.c, t);
+        }
       }
     }
+    if (!q.ws) continue;
+    // the block's column sums over its token rows, rows added in order
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      sums[threadIdx.x][2 * e] = dw[e].x, sums[threadIdx.x][2 * e + 1] = dw[e].y;
+      sums[threadIdx.x][8 + 2 * e] = db[e].x, sums[threadIdx.x][9 + 2 * e] = db[e].y;
+    }
+    __syncthreads();
+    if (me.live && me.row == 0) {
+      const int per_row = cut.heads * (D / 8);
+      float o[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[e] = sums[threadIdx.x][e];
+      for (int r = 1; r < cut.rows; ++r)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] += sums[threadIdx.x + r * per_row][e];
+      float *dst = q.ws + (long)blockIdx.x * 2 * HD + col;
+#pragma unroll
+      for (int e = 0; e < 16; e += 4) st4(dst + (e >> 3) * HD + (e & 7), o[e], o[e + 1], o[e + 2], o[e + 3]);
+    }
+    __syncthreads();  // the sums' place is free for the next slab
   }
   if (!q.ws) return;
-  // the block's column sums over its token rows, rows added in order
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    sums[threadIdx.x][2 * e] = dw[e].x, sums[threadIdx.x][2 * e + 1] = dw[e].y;
-    sums[threadIdx.x][8 + 2 * e] = db[e].x, sums[threadIdx.x][9 + 2 * e] = db[e].y;
-  }
-  __syncthreads();
-  if (me.live && me.row == 0) {
-    const int per_row = cut.heads * (D / 8);
-    float o[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) o[e] = sums[threadIdx.x][e];
-    for (int r = 1; r < cut.rows; ++r)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) o[e] += sums[threadIdx.x + r * per_row][e];
-    float *dst = q.ws + (long)blockIdx.x * 2 * HD + col;
-#pragma unroll
-    for (int e = 0; e < 16; e += 4) st4(dst + (e >> 3) * HD + (e & 7), o[e], o[e + 1], o[e + 2], o[e + 3]);
-  }
-}
-
-// Column sums of the blocks' sums [blocks][2][HD]: 32 columns a block, four warps over the rows.
-__global__ void __launch_bounds__(128) norm_columns_kernel(const float *ws, int blocks, long HD, float *dw, float *db) {
-  __shared__ float part[4][32];
-  const long col = (long)blockIdx.x * 32 + (threadIdx.x & 31);
-  const int grp = threadIdx.x >> 5;
-  float s = 0.f;
-  if (col < 2 * HD)
-    for (int i = grp; i < blocks; i += 4) s += ws[(long)i * 2 * HD + col];
-  part[grp][threadIdx.x & 31] = s;
-  __syncthreads();
-  if (grp == 0 && col < 2 * HD) {
-    s = (part[0][threadIdx.x] + part[1][threadIdx.x]) + (part[2][threadIdx.x] + part[3][threadIdx.x]);
-    if (col < HD) {
-      if (dw) dw[col] = s;
-    } else if (db) {
-      db[col - HD] = s;
+  cooperative_groups::this_grid().sync();
+  // 32 columns a turn, a warp for every eighth row of blocks
+  const int warps = blockDim.x / 32, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long flat = (long)blockIdx.y * gridDim.x + blockIdx.x, all = (long)gridDim.x * gridDim.y;
+  for (long c0 = flat * 32; c0 < 2 * HD; c0 += all * 32) {
+    const long c = c0 + lane;
+    float s = 0.f;
+    if (c < 2 * HD)
+      for (int i = warp; i < (int)gridDim.x; i += warps) s += __ldcg(q.ws + (long)i * 2 * HD + c);
+    __syncthreads();
+    (&sums[0][0])[threadIdx.x] = s;
+    __syncthreads();
+    if (warp == 0 && c < 2 * HD) {
+      for (int w2 = 1; w2 < warps; ++w2) s += (&sums[0][0])[w2 * 32 + lane];
+      if (c < HD) {
+        if (q.dweight) q.dweight[c] = s;
+      } else if (q.dbias) {
+        q.dbias[c - HD] = s;
+      }
     }
   }
 }
@@ -310,7 +317,7 @@ int token_blocks(const Cut &c, long tokens, int per_sm, int ahead) {
   return (int)std::max(1L, std::min<long>(turns, std::max(1, sms * per_sm / c.slabs)));
 }
 
-constexpr int kAheadFwd = 4, kAheadGrad = 2, kPerSmGrad = 2;
+constexpr int kAheadFwd = 4, kAheadGrad = 3, kPerSmGrad = 2;
 
 template <typename T, int D>
 cudaError_t launch_fwd(const NormProblem &p) {
@@ -332,26 +339,19 @@ template <typename T, int D>
 cudaError_t launch_grad(const NormGradProblem &q) {
   const NormProblem &p = q.p;
   const Cut c = make_cut(p.H, D);
-  const int blocks = token_blocks(c, (long)p.B * p.N, kPerSmGrad, kAheadGrad);
-  cudaError_t e;
-  {
-    LaunchTimer timer(kKGroupNormBackward, p.stream);
-    const Divider by_n = make_divider((uint32_t)p.N);
-    const dim3 grid((unsigned)blocks, (unsigned)c.slabs);
-    if (p.gate)
-      group_norm_grad_kernel<T, D, true, kAheadGrad><<<grid, c.threads, 0, p.stream>>>(q, c, by_n);
-    else
-      group_norm_grad_kernel<T, D, false, kAheadGrad><<<grid, c.threads, 0, p.stream>>>(q, c, by_n);
-    e = cudaGetLastError();
-    timer.done(e);
-    if (e != cudaSuccess) return e;
-    count_launch();
-  }
-  if (!q.ws) return e;
-  const long HD = (long)p.H * D;
+  const Divider by_n = make_divider((uint32_t)p.N);
+  const int sms = std::max(1, device_info(-1).sm_count);
+  const dim3 grid((unsigned)token_blocks(c, (long)p.B * p.N, kPerSmGrad, kAheadGrad),
+                  (unsigned)std::min(c.slabs, sms * kPerSmGrad));
+  const void *fn = p.gate ? (const void *)group_norm_grad_kernel<T, D, true, kAheadGrad>
+                          : (const void *)group_norm_grad_kernel<T, D, false, kAheadGrad>;
   LaunchTimer timer(kKGroupNormBackward, p.stream);
-  norm_columns_kernel<<<(unsigned)((2 * HD + 31) / 32), 128, 0, p.stream>>>(q.ws, blocks, HD, q.dweight, q.dbias);
-  e = cudaGetLastError();
+  void *args[] = {const_cast<NormGradProblem *>(&q), const_cast<Cut *>(&c), const_cast<Divider *>(&by_n)};
+  cudaError_t e;
+  if (q.ws)  // column sums: a grid barrier; all blocks are resident (kPerSmGrad an SM)
+    e = cudaLaunchCooperativeKernel(fn, grid, dim3(c.threads), args, 0, p.stream);
+  else
+    e = cudaLaunchKernel(fn, grid, dim3(c.threads), args, 0, p.stream);
   timer.done(e);
   if (e == cudaSuccess) count_launch();
   return e;

@@ -337,7 +337,7 @@ def _off(ctx):
 
 def _need(name, t, shape, dtype, device):
     """t itself, after checking that it is a contiguous tensor of that shape, dtype and (CUDA) device."""
-    if isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous():
+    if isinstance(t, torch.Tensor) and t.get_device() == device.index and t.dtype is dtype and t.shape == shape and t.is_contiguous():
         return t
     if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor")

@@ -131,3 +131,10 @@ def quadratic64(q, k, v, g):
     low = torch.ones(q.shape[2], q.shape[2], dtype=torch.bool, device=q.device).tril()
     w = torch.where(low, c[..., :, None] - c[..., None, :], float("-inf")).exp()
     return (q @ k.transpose(-1, -2) * w) @ v
+
+
+def test_more_slabs_of_heads_than_blocks_fit(cuda_lib):
+    """H = 20000 heads of 32 channels are 313 slabs: the gradient's column sums wait at a grid barrier for resident blocks only."""
+    d, dy = inputs(1, 20000, 2, 32, BF16, 6)
+    close(cuda_lib.la_group_norm(**d), norm64(**d), BF16, "y")
+    check_grad(cuda_lib, d, dy, BF16)
