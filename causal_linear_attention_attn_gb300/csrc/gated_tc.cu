@@ -17,8 +17,8 @@
 // HBM bounds it (8 D bytes per token in and out, 40 flops a byte at D = 128): a chunk's loads take
 // about 5000 cycles of an SM's share, its longest chain (P, weights, P' V) about 2800.
 //
-// Warps: 0 TMA, 1 MMA and TMEM owner, 2 running sums, 4-11 weights of the scores, 12-15 weighted keys,
-// 16-19 state (bf16 copy, decay), 20-23 outputs.  Every wait is bounded (tc_ptx.cuh).
+// Warps: 0 TMA, 1 MMA and TMEM owner, 2 running sums, 4-11 weights of the scores, 12-19 weighted keys,
+// 20-23 state (bf16 copy, decay), 24-27 outputs.  Every wait is bounded (tc_ptx.cuh).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -31,13 +31,13 @@ namespace la {
 namespace {
 using namespace gtc;
 
-constexpr int kThreads = 768;
-constexpr int kWarpGate = 2, kWarpP = 4, kWarpK = 12, kWarpS = 16, kWarpO = 20;
+constexpr int kThreads = 896;
+constexpr int kWarpGate = 2, kWarpP = 4, kWarpK = 12, kWarpS = 20, kWarpO = 24;
 constexpr uint32_t kBarS = 1;
-// Registers a thread: the launch gives every warpgroup 80; the state and the outputs, which pass
-// through in blocks of 64 columns, take what the others leave.
-constexpr int kRegs = 80, kRegs0 = 56, kRegsK = 72, kRegsSO = 96;
-static_assert(kRegs0 + 2 * kRegs + kRegsK + 2 * kRegsSO <= 6 * kRegs, "warpgroups' shares within the launch's");
+// Registers a thread: the launch gives every warpgroup 72; the state and the outputs, which pass
+// through in blocks, take what the others leave.
+constexpr int kRegs = 72, kRegs0 = 48, kRegsK = 64, kRegsS = 96, kRegsO = 88;
+static_assert(kRegs0 + 2 * kRegs + 2 * kRegsK + kRegsS + kRegsO <= 7 * kRegs, "warpgroups' shares within the launch's");
 
 template <int D>
 struct Lay {
@@ -48,7 +48,7 @@ struct Lay {
   static constexpr uint32_t Klo = Khi + kTile;
   static constexpr uint32_t V = Klo + kTile;  // 2 stages
   static constexpr uint32_t Sb = V + 2 * kTile;
-  static constexpr uint32_t Sum = Sb + D * D * 2;  // D = 64: low rows of the state [64][65] fp32
+  static constexpr uint32_t Sum = Sb + 128 * D * 2;  // D = 64: low rows of the state [64][65] fp32
   static constexpr uint32_t Gate = Sum + (D == 64 ? 64 * 65 * 4 : 0);
   static constexpr uint32_t Bars = Gate + 2 * 2 * kC * 4;
   static constexpr int kNumBars = 19;
@@ -102,14 +102,14 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
       mbar_init(&full_v[b], 1);
       mbar_init(&v_free[b], 1);
       mbar_init(&gate_full[b], 32);
-      mbar_init(&gate_free[b], 640);
+      mbar_init(&gate_free[b], 768);
     }
     mbar_init(full_k, 1);
-    mbar_init(k_free, 1 + 128);  // the scores' product and the weighted keys' warps
+    mbar_init(k_free, 1 + 256);  // the scores' product and the weighted keys' warps
     mbar_init(full_q, 1);
     mbar_init(q_free, 1);
     mbar_init(p_full, 1);
-    mbar_init(k_ready, 128);
+    mbar_init(k_ready, 256);
     mbar_init(pp_ready, 256);
     mbar_init(sb_ready, 128);
     mbar_init(s_full, 1);
@@ -196,6 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
         tc_fence_after();
         if (leader) {
           product<kDs, kK, kMN>(tI, kbase(sQ), mnbase(sSb), iO, false);
+          if (D == 64) product<kDs, kK, kMN>(tI, kbase(sQ), mnbase(sSb + 64 * 128), iO, true);  // the low keys' part
           mma_commit(q_free);
         }
         __syncwarp();
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
   } else if (warp < kWarpS) {
     // ---- weighted keys as a pair, in tiles of their own: the last update has read them ----
     reg_dec<kRegsK>();
-    const int r = threadIdx.x - kWarpK * 32;
+    const int r = (threadIdx.x - kWarpK * 32) & 127, half = (threadIdx.x - kWarpK * 32) >> 7;
     for (int c = 0; c < nc; ++c) {
       const int s = c & 1;
       if (!warp_wait(&gate_full[c & 1], (c >> 1) & 1, abort_word)) break;
@@ -282,11 +283,14 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
       mbar_arrive(&gate_free[c & 1]);
       if (!warp_wait(full_k, c & 1, abort_word)) break;
       if (c > 0 && !warp_wait(s_full, (c - 1) & 1, abort_word)) break;
-      const uint8_t *K = sm + L::K;
-      uint8_t *Khi = sm + L::Khi, *Klo = sm + L::Klo;
+      // a thread's half of the row: one 64-feature block (D = 128) or half of the only one
+      const uint32_t blk = D == 128 ? half * kBlk : 0;
+      const int c0 = D == 128 ? 0 : half * 4;
+      const uint8_t *K = sm + L::K + blk;
+      uint8_t *Khi = sm + L::Khi + blk, *Klo = sm + L::Klo + blk;
 #pragma unroll 4
-      for (int e = 0; e < D / 8; ++e) {
-        const uint32_t off = (e >> 3) * kBlk + sw128_offset(r, (e & 7) * 8);
+      for (int e = 0; e < D / 16; ++e) {
+        const uint32_t off = sw128_offset(r, (c0 + e) * 8);
         uint4 h = make_uint4(0u, 0u, 0u, 0u), l = h;
         if (r < tv) split8p(*reinterpret_cast<const uint4 *>(K + off), w, h, l);
         *reinterpret_cast<uint4 *>(Khi + off) = h;
@@ -295,17 +299,17 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
       mbar_arrive(k_free);
       if (tv < kC) {  // padding tokens: a zero weight does not clear a NaN of the values
         if (!warp_wait(&full_v[s], (c >> 1) & 1, abort_word)) break;
-        uint8_t *V = sm + L::V + s * L::kTile;
+        uint8_t *V = sm + L::V + s * L::kTile + blk;
         if (r >= tv)
-          for (int e = 0; e < D / 8; ++e)
-            *reinterpret_cast<uint4 *>(V + (e >> 3) * kBlk + sw128_offset(r, (e & 7) * 8)) = make_uint4(0u, 0u, 0u, 0u);
+          for (int e = 0; e < D / 16; ++e)
+            *reinterpret_cast<uint4 *>(V + sw128_offset(r, (c0 + e) * 8)) = make_uint4(0u, 0u, 0u, 0u);
       }
       fence_async_smem();
       mbar_arrive(k_ready);
     }
   } else if (warp < kWarpO) {
     // ---- state: bf16 copy for the queries, then decayed in place for the update ----
-    reg_inc<kRegsSO>();
+    reg_inc<kRegsS>();
     const int q = warp & 3, T = q * 32 + lane;
     const int row = D == 64 ? T & 63 : T;
     const bool main_row = D == 128 || q < 2;  // D = 64: lanes from 64 on hold the low keys' part
@@ -340,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
     for (int c = 0; c < nc; ++c) {
       bool w = mbar_wait(&gate_full[c & 1], (c >> 1) & 1, abort_word, status);
       if (w && c > 0) w = mbar_wait(s_full, (c - 1) & 1, abort_word, status);
-      if (bar_or(kBarS, 128, !w)) {  // D = 64: also, the last joined rows are read
+      if (bar_or(kBarS, 128, !w)) {
         ok = false;
         break;
       }
@@ -368,14 +372,12 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
             break;
           }
         }
-        join();
-        if (main_row) {
+        // (D = 64: the low keys' part is the copy's rows from 64 on; the queries read both)
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            uint4 h[4];
-            to_bf16x32(r[b], h);
-            stage_row32(sm + L::Sb + cb * kBlk, row, b, h);
-          }
+        for (int b = 0; b < 2; ++b) {
+          uint4 h[4];
+          to_bf16x32(r[b], h);
+          stage_row32(sm + L::Sb + cb * kBlk, T, b, h);
         }
       }
       if (!ok) break;
@@ -407,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
     }
   } else {
     // ---- outputs: row i, 2^{c_i} (Q S) + P' V ----
-    reg_inc<kRegsSO>();
+    reg_inc<kRegsO>();
     const int q = warp & 3, i = q * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16);
     for (int c = 0; c < nc; ++c) {
@@ -421,19 +423,22 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
       __nv_bfloat16 *dst = p.out + (bh * p.N + (c_lo + c) * kC + i) * D;
 #pragma unroll 1
       for (int cb = 0; cb < D / 32; ++cb) {
-        uint32_t x[32], y[32];
         uint4 o[4];
-        tmem_ld32x2(tl + kColI + cb * 32, tl + kColA + cb * 32, x, y);
+        uint32_t *ow = reinterpret_cast<uint32_t *>(o);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t x[16], y[16];
+          tmem_ld16x2(tl + kColI + cb * 32 + 16 * h, tl + kColA + cb * 32 + 16 * h, x, y);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float2 z = __ffma2_rn(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), make_float2(f, f),
+                                        make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])));
+            ow[8 * h + e] = pack_bf16(z.x, z.y);
+          }
+        }
         if (cb == D / 32 - 1) {
           tc_fence_before();
           mbar_arrive(o_free);
-        }
-        uint32_t *ow = reinterpret_cast<uint32_t *>(o);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float2 z = __ffma2_rn(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), make_float2(f, f),
-                                      make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])));
-          ow[e] = pack_bf16(z.x, z.y);
         }
         if (in) store_row64(dst + cb * 32, o, p.wide);
       }
