@@ -606,12 +606,8 @@ cudaError_t launch_chunks(const Params &cp, cudaStream_t stream) {
   cudaError_t e = ensure_smem_optin((const void *)gated_grad_tc_kernel<D>, (int)Lay<D>::Bytes);
   if (e != cudaSuccess) return e;
   const long sms = std::max(1, device_info(-1).sm_count);
-  LaunchTimer timer(kKGatedBackward, stream);
-  gated_grad_tc_kernel<D><<<(unsigned)std::min(sms, cp.items), kThreads, Lay<D>::Bytes, stream>>>(cp);
-  e = cudaGetLastError();
-  timer.done(e);
-  if (e == cudaSuccess) count_launch();
-  return e;
+  return launch_gated_kernel(gated_grad_tc_kernel<D>, cp, dim3((unsigned)std::min(sms, cp.items)), kThreads, Lay<D>::Bytes, true,
+                             kKGatedBackward, stream);
 }
 
 }  // namespace
@@ -659,7 +655,7 @@ cudaError_t launch_gated_grad_tc(const GatedGradProblem &b) {
     sp.init[0] = p.S0, sp.init[1] = b.dS, sp.fin[1] = b.dS0;
   }
   sp.tiles[0] = ws, sp.tiles[1] = ws + tiles;
-  e = launch_gated_states(sp, D, BH, 2, false, p.stream);
+  e = launch_gated_states(sp, D, BH, 2, t.segs > 1, p.stream);
   if (e != cudaSuccess) return e;
   Params cp;
   memset(&cp, 0, sizeof cp);

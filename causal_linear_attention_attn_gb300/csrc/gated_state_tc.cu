@@ -9,6 +9,9 @@
 // A CTA owns one segment of one head and direction.  The chunks are a chain, state -> MMA -> state;
 // what is not on the chain (loads, weights, the bf16 pairs that are stored) runs beside it: the state
 // warps read the state, write it back decayed for the next MMA, and only then split and store it.
+// Where only a segment's sum is wanted (kSum: the pass before the prefill's segments), the weights run
+// to the segment's end instead of the chunk's, 2^{c_end - c_t}, from the last chunk to the first: then
+// nothing is decayed between chunks, there is no chain, and the state warps weigh every other chunk.
 // At D = 64 hi and lo make up the 128 rows of one MMA, [hi | lo]^T b, and meet when the state is read.
 // HBM bounds it: per token 4 D bytes in and, when tiles are written, 4 D bytes out per direction.
 //
@@ -46,7 +49,7 @@ struct Lay {
 };
 static_assert(Lay<128>::Bytes <= 232448, "shared memory budget");
 
-template <int D>
+template <int D, bool kSum>
 __global__ void __launch_bounds__(kThreads, 1) gated_state_tc_kernel(const __grid_constant__ GatedStateParams p) {
   using L = Lay<D>;
   constexpr int kStages = L::kStages;
@@ -75,8 +78,8 @@ __global__ void __launch_bounds__(kThreads, 1) gated_state_tc_kernel(const __gri
   uint8_t *tiles = p.tiles[dir];
   float *fin = p.fin[dir];
   // the last chunk is folded in only if the state behind it is wanted
-  const int run = fin ? nc : max(0, nc - 1);
-  auto chunk = [&](int i) -> long { return dir ? c_hi - 1 - i : c_lo + i; };
+  const int run = kSum || fin ? nc : max(0, nc - 1);
+  auto chunk = [&](int i) -> long { return (dir != 0) != kSum ? c_hi - 1 - i : c_lo + i; };
   auto valid = [&](int i) -> int { return (int)min((long)kC, len - chunk(i) * kC); };
 
   if (threadIdx.x == 0) {
@@ -88,7 +91,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_state_tc_kernel(const __gri
     for (int b = 0; b < 2; ++b) {
       mbar_init(&lo_free[b], 1);
       mbar_init(&gate_full[b], 32);
-      mbar_init(&gate_free[b], 512);
+      mbar_init(&gate_free[b], kSum ? 256 : 512);
     }
     mbar_init(x_ready, 256);
     mbar_init(x_full, 1);
@@ -128,19 +131,20 @@ __global__ void __launch_bounds__(kThreads, 1) gated_state_tc_kernel(const __gri
     for (int i = 0; i < run; ++i) {
       const int s = i % kStages;
       if (!warp_wait(&done[s], (i / kStages) & 1, abort_word)) break;
-      if (!warp_wait(x_ready, i & 1, abort_word)) break;
+      if (!kSum && !warp_wait(x_ready, i & 1, abort_word)) break;
+      const bool add = !kSum || i > 0;
       tc_fence_after();
       const uint32_t a = sA + s * L::kTile, lo = sLo + (i & 1) * L::kTile, b = sB + s * L::kTile;
       if (leader) {
         if (D == 128) {
-          product<8, kMN, kMN>(tmem, mnbase(a), mnbase(b), iMM, true);
+          product<8, kMN, kMN>(tmem, mnbase(a), mnbase(b), iMM, add);
           product<8, kMN, kMN>(tmem, mnbase(lo), mnbase(b), iMM, true);
         } else {
-          product<8, kMN, kMN>(tmem, mnbase(a, lo - a), mnbase(b), iMM, true);  // rows: hi, then lo
+          product<8, kMN, kMN>(tmem, mnbase(a, lo - a), mnbase(b), iMM, add);  // rows: hi, then lo
         }
         mma_commit(&empty[s]);
         mma_commit(&lo_free[i & 1]);
-        mma_commit(x_full);
+        if (!kSum || i + 1 == run) mma_commit(x_full);
       }
       __syncwarp();
     }
@@ -148,156 +152,179 @@ __global__ void __launch_bounds__(kThreads, 1) gated_state_tc_kernel(const __gri
       mma_commit(drain);
       wait_drain(drain, 0, status);
     }
-  } else if (warp < kWarpState) {
-    // weights: token r of the chunk, half of its features
-    const int r = (threadIdx.x - kWarpXform * 32) & 127, half = (threadIdx.x - kWarpXform * 32) >> 7;
-    constexpr int kChunks = D / 16;  // 16-byte chunks per thread
-    const int blk = D == 128 ? half * kBlk : 0, c0 = D == 128 ? 0 : half * 4;
-    for (int i = 0; i < run; ++i) {
-      const int s = i % kStages;
-      bool ok = mbar_wait(&gate_full[i & 1], (i >> 1) & 1, abort_word, status);
-      ok = ok && mbar_wait(&full[s], (i / kStages) & 1, abort_word, status);
-      if (ok && i >= 2) ok = mbar_wait(&lo_free[i & 1], ((i >> 1) - 1) & 1, abort_word, status);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      const float *hi = gate + (i & 1) * 2 * kC, *lo = hi + kC;
-      const bool in = r < valid(i);
-      const float w = dir ? exp2f(hi[r] + lo[r]) : exp2f((hi[kC - 1] - hi[r]) + (lo[kC - 1] - lo[r]));
-      mbar_arrive(&gate_free[i & 1]);
-      uint8_t *A = sm + L::A + s * L::kTile + blk, *Lo = sm + L::Lo + (i & 1) * L::kTile + blk;
-#pragma unroll 4
-      for (int e = 0; e < kChunks; ++e) {
-        const uint32_t off = sw128_offset(r, (c0 + e) * 8);
-        uint4 h = make_uint4(0u, 0u, 0u, 0u), l = h;
-        if (in) split8p(*reinterpret_cast<const uint4 *>(A + off), w, h, l);
-        *reinterpret_cast<uint4 *>(A + off) = h;
-        *reinterpret_cast<uint4 *>(Lo + off) = l;
-      }
-      if (!in) {  // padding tokens: a zero weight does not clear a NaN of the other operand
-        uint8_t *B = sm + L::B + s * L::kTile + blk;
-        for (int e = 0; e < kChunks; ++e)
-          *reinterpret_cast<uint4 *>(B + sw128_offset(r, (c0 + e) * 8)) = make_uint4(0u, 0u, 0u, 0u);
-      }
-      fence_async_smem();
-      mbar_arrive(&done[s]);
-    }
   } else if (warp < kWarpGate) {
-    const int q = warp & 3, T = q * 32 + lane;  // tensor-memory lane: a row of the state (D = 64: from 64 on, its low part)
-    const int col0 = ((warp - kWarpState) >> 2) * (D / 2);
-    constexpr int kB = D / 64;  // blocks of 32 columns
-    const uint32_t tx = tmem + ((uint32_t)(q * 32) << 16) + col0;
-    const int row = D == 64 ? T & 63 : T;
-    const bool main_row = D == 128 || q < 2;
-    float *sum = reinterpret_cast<float *>(sm + L::Sum);
-    uint32_t r[kB][32];
-    const long dd = (long)D * D;
-    const float *init = p.init[dir] ? p.init[dir] + (bh * p.segs + seg) * dd + (long)row * D + col0 : nullptr;
-#pragma unroll
-    for (int b = 0; b < kB; ++b) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (init && main_row) x = reinterpret_cast<const float4 *>(init + b * 32)[e];
-        r[b][4 * e] = __float_as_uint(x.x), r[b][4 * e + 1] = __float_as_uint(x.y);
-        r[b][4 * e + 2] = __float_as_uint(x.z), r[b][4 * e + 3] = __float_as_uint(x.w);
+    if (kSum || warp < kWarpState) {
+      // weights: token r of the chunk, half of its features
+      const int t = threadIdx.x - (warp < kWarpState ? kWarpXform : kWarpState) * 32, r = t & 127, half = t >> 7;
+      constexpr int kChunks = D / 16;  // 16-byte chunks per thread
+      const int blk = D == 128 ? half * kBlk : 0, c0 = D == 128 ? 0 : half * 4;
+      for (int i = kSum && warp >= kWarpState; i < run; i += kSum ? 2 : 1) {
+        const int s = i % kStages;
+        bool ok = mbar_wait(&gate_full[i & 1], (i >> 1) & 1, abort_word, status);
+        ok = ok && mbar_wait(&full[s], (i / kStages) & 1, abort_word, status);
+        if (ok && i >= 2) ok = mbar_wait(&lo_free[i & 1], ((i >> 1) - 1) & 1, abort_word, status);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        const float *hi = gate + (i & 1) * 2 * kC, *lo = hi + kC;
+        const bool in = r < valid(i);
+        const float w = kSum || dir ? exp2f(hi[r] + lo[r]) : exp2f((hi[kC - 1] - hi[r]) + (lo[kC - 1] - lo[r]));
+        mbar_arrive(&gate_free[i & 1]);
+        uint8_t *A = sm + L::A + s * L::kTile + blk, *Lo = sm + L::Lo + (i & 1) * L::kTile + blk;
+#pragma unroll 4
+        for (int e = 0; e < kChunks; ++e) {
+          const uint32_t off = sw128_offset(r, (c0 + e) * 8);
+          uint4 h = make_uint4(0u, 0u, 0u, 0u), l = h;
+          if (in) split8p(*reinterpret_cast<const uint4 *>(A + off), w, h, l);
+          *reinterpret_cast<uint4 *>(A + off) = h;
+          *reinterpret_cast<uint4 *>(Lo + off) = l;
+        }
+        if (!in) {  // padding tokens: a zero weight does not clear a NaN of the other operand
+          uint8_t *B = sm + L::B + s * L::kTile + blk;
+          for (int e = 0; e < kChunks; ++e)
+            *reinterpret_cast<uint4 *>(B + sw128_offset(r, (c0 + e) * 8)) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_async_smem();
+        mbar_arrive(&done[s]);
       }
     }
-    // D = 64: the two parts meet in the rows of the first two lane quarters
-    auto join = [&]() {
-      if (D == 128) return;
-      if (!main_row)
+    if (warp >= kWarpState) {
+      const int q = warp & 3, T = q * 32 + lane;  // tensor-memory lane: a row of the state (D = 64: from 64 on, its low part)
+      const int col0 = ((warp - kWarpState) >> 2) * (D / 2);
+      constexpr int kB = D / 64;  // blocks of 32 columns
+      const uint32_t tx = tmem + ((uint32_t)(q * 32) << 16) + col0;
+      const int row = D == 64 ? T & 63 : T;
+      const bool main_row = D == 128 || q < 2;
+      float *sum = reinterpret_cast<float *>(sm + L::Sum);
+      uint32_t r[kB][32];
+      const long dd = (long)D * D;
+      const float *init = !kSum && p.init[dir] ? p.init[dir] + (bh * p.segs + seg) * dd + (long)row * D + col0 : nullptr;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) sum[row * 65 + col0 + e] = __uint_as_float(r[0][e]);
-      named_bar(kBarState, 256);
-      if (main_row)
+      for (int b = 0; b < kB; ++b) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) r[0][e] = __float_as_uint(__uint_as_float(r[0][e]) + sum[row * 65 + col0 + e]);
-    };
-    bool ok = true;
-    for (int i = 0; i < nc && ok; ++i) {
-      bool w = i == 0 || mbar_wait(x_full, (i - 1) & 1, abort_word, status);
-      if (w && i < run) w = mbar_wait(&gate_full[i & 1], (i >> 1) & 1, abort_word, status);
-      if (bar_or(kBarState, 256, !w)) {  // D = 64: also, the last joined columns are read
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      if (i > 0) {
-        if constexpr (kB == 2)
-          tmem_ld32x2(tx, tx + 32, r[0], r[kB - 1]);
-        else
-          tmem_ld32(tx, r[0]);
-      }
-      if (i < run) {
-        const float *hi = gate + (i & 1) * 2 * kC;
-        const float f = exp2f(hi[kC - 1] + hi[2 * kC - 1]);
-        mbar_arrive(&gate_free[i & 1]);
-#pragma unroll
-        for (int b = 0; b < kB; ++b)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t y[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(r[b][16 * h + e]) * f);
-            tmem_st16_nowait(tx + 32 * b + 16 * h, y);
-          }
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(x_ready);
-      }
-      if (tiles) {
-        join();
-        if (main_row) {
-          uint8_t *t = tiles + (bh * p.n + chunk(i)) * (size_t)(D * D * 4) + (col0 >> 6) * (D * 128) + row * 128 + (col0 & 63) * 2;
-#pragma unroll
-          for (int b = 0; b < kB; ++b) {
-            uint4 v[4];
-            to_bf16x32(r[b], v);
-            store_row64(t + b * 64, v, true);
-            rest_bf16x32(r[b], v);
-            store_row64(t + D * D * 2 + b * 64, v, true);
-          }
+        for (int e = 0; e < 8; ++e) {
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (init && main_row) x = reinterpret_cast<const float4 *>(init + b * 32)[e];
+          r[b][4 * e] = __float_as_uint(x.x), r[b][4 * e + 1] = __float_as_uint(x.y);
+          r[b][4 * e + 2] = __float_as_uint(x.z), r[b][4 * e + 3] = __float_as_uint(x.w);
         }
       }
-    }
-    if (fin && ok) {
-      const bool w = run == 0 || mbar_wait(x_full, (run - 1) & 1, abort_word, status);
-      if (!bar_or(kBarState, 256, !w)) {
+      // D = 64: the two parts meet in the rows of the first two lane quarters
+      auto join = [&]() {
+        if (D == 128) return;
+        if (!main_row)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) sum[row * 65 + col0 + e] = __uint_as_float(r[0][e]);
+        named_bar(kBarState, 256);
+        if (main_row)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) r[0][e] = __float_as_uint(__uint_as_float(r[0][e]) + sum[row * 65 + col0 + e]);
+      };
+      bool ok = true;
+      for (int i = 0; !kSum && i < nc && ok; ++i) {
+        bool w = i == 0 || mbar_wait(x_full, (i - 1) & 1, abort_word, status);
+        if (w && i < run) w = mbar_wait(&gate_full[i & 1], (i >> 1) & 1, abort_word, status);
+        if (bar_or(kBarState, 256, !w)) {  // D = 64: also, the last joined columns are read
+          ok = false;
+          break;
+        }
         tc_fence_after();
-        if (run > 0) {
+        if (i > 0) {
           if constexpr (kB == 2)
             tmem_ld32x2(tx, tx + 32, r[0], r[kB - 1]);
           else
             tmem_ld32(tx, r[0]);
         }
-        join();
-        float *dst = fin + (bh * p.segs + seg) * dd + (long)row * D + col0;
-        if (main_row)
+        if (i < run) {
+          const float *hi = gate + (i & 1) * 2 * kC;
+          const float f = exp2f(hi[kC - 1] + hi[2 * kC - 1]);
+          mbar_arrive(&gate_free[i & 1]);
 #pragma unroll
           for (int b = 0; b < kB; ++b)
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              reinterpret_cast<float4 *>(dst + b * 32)[e] =
-                  make_float4(__uint_as_float(r[b][4 * e]), __uint_as_float(r[b][4 * e + 1]),
-                              __uint_as_float(r[b][4 * e + 2]), __uint_as_float(r[b][4 * e + 3]));
+            for (int h = 0; h < 2; ++h) {
+              uint32_t y[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(r[b][16 * h + e]) * f);
+              tmem_st16_nowait(tx + 32 * b + 16 * h, y);
+            }
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(x_ready);
+        }
+        if (tiles) {
+          join();
+          if (main_row) {
+            uint8_t *t = tiles + (bh * p.n + chunk(i)) * (size_t)(D * D * 4) + (col0 >> 6) * (D * 128) + row * 128 + (col0 & 63) * 2;
+#pragma unroll
+            for (int b = 0; b < kB; ++b) {
+              uint4 v[4];
+              to_bf16x32(r[b], v);
+              store_row64(t + b * 64, v, true);
+              rest_bf16x32(r[b], v);
+              store_row64(t + D * D * 2 + b * 64, v, true);
+            }
+          }
+        }
+      }
+      if (fin && ok) {
+        const bool w = run == 0 || mbar_wait(x_full, kSum ? 0 : (run - 1) & 1, abort_word, status);
+        if (!bar_or(kBarState, 256, !w)) {
+          tc_fence_after();
+          if (run > 0) {
+            if constexpr (kB == 2)
+              tmem_ld32x2(tx, tx + 32, r[0], r[kB - 1]);
+            else
+              tmem_ld32(tx, r[0]);
+          }
+          join();
+          float *dst = fin + (bh * p.segs + seg) * dd + (long)row * D + col0;
+          if (main_row)
+#pragma unroll
+            for (int b = 0; b < kB; ++b)
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                reinterpret_cast<float4 *>(dst + b * 32)[e] =
+                    make_float4(__uint_as_float(r[b][4 * e]), __uint_as_float(r[b][4 * e + 1]),
+                                __uint_as_float(r[b][4 * e + 2]), __uint_as_float(r[b][4 * e + 3]));
+        }
       }
     }
   } else {
-    Sum2 total{0.f, 0.f};
     const float *g = p.g + bh * p.N;
     float4 cur = make_float4(0.f, 0.f, 0.f, 0.f);
+    // kSum: decay of the chunks taken so far, which is what lies between this chunk and the segment's
+    // end; held at -2^15, far below where weights vanish
+    long long beyond = 0;
+    bool beyond_nan = false;
+    constexpr long long kFloor = -(1ll << 55);
     if (run > 0) cur = load_gates(g + chunk(0) * kC, valid(0), lane);
     for (int i = 0; i < run; ++i) {
       float4 nxt = cur;
       if (i + 1 < run) nxt = load_gates(g + chunk(i + 1) * kC, valid(i + 1), lane);
       if (i >= 2 && !warp_wait(&gate_free[i & 1], ((i >> 1) - 1) & 1, abort_word)) break;
       float *hi = gate + (i & 1) * 2 * kC;
-      scan_gates(cur, lane, hi, hi + kC);
-      __syncwarp();
-      total.add(hi[kC - 1], hi[2 * kC - 1]);
+      if constexpr (kSum) {
+        GateSums u(cur, lane);
+        const long long all = __shfl_sync(0xffffffffu, u.c[3], 31);
+        const bool all_nan = __shfl_sync(0xffffffffu, (int)u.nan[3], 31);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          u.c[e] = beyond + (dir ? u.c[e] : all - u.c[e]);
+          u.nan[e] = beyond_nan || (dir ? u.nan[e] : all_nan);
+        }
+        store_cums(u.c, u.nan, lane, hi, hi + kC);
+        beyond += all;
+        if (beyond < kFloor) beyond = kFloor;
+        beyond_nan = beyond_nan || all_nan;
+      } else {
+        scan_gates(cur, lane, hi, hi + kC);
+      }
       mbar_arrive(&gate_full[i & 1]);
       cur = nxt;
     }
-    if (p.seg_tot && fin && dir == 0 && lane == 0) p.seg_tot[bh * p.segs + seg] = total.s + total.e;
+    if (kSum && dir == 0 && lane == 0) {
+      const Cum t = split_cum(beyond, beyond_nan);
+      p.seg_tot[bh * p.segs + seg] = t.hi + t.lo;
+    }
   }
 
   tc_fence_before();
@@ -308,46 +335,51 @@ __global__ void __launch_bounds__(kThreads, 1) gated_state_tc_kernel(const __gri
   }
 }
 
-__global__ void __launch_bounds__(128) gated_seg_scan_kernel(const __grid_constant__ GatedSegScan a) {
+constexpr int kScanThreads = 256;
+
+__global__ void __launch_bounds__(kScanThreads) gated_seg_scan_kernel(const __grid_constant__ GatedSegScan a) {
+  if (threadIdx.x == 0) pdl_trigger();
   pdl_wait();
-  const int dir = blockIdx.z, parts = (a.dd / 4 + 127) / 128;
-  const long bh = blockIdx.x / parts;
-  const long e = ((blockIdx.x - bh * parts) * 128 + threadIdx.x) * 4L;
-  if (e >= a.dd) return;
+  const int dir = blockIdx.z, parts = a.dd / (4 * kScanThreads);
+  const int bh = blockIdx.x / parts;
+  const int e = ((blockIdx.x - bh * parts) * kScanThreads + threadIdx.x) * 4;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (a.first[dir]) s = *reinterpret_cast<const float4 *>(a.first[dir] + bh * a.dd + e);
-  for (int i = 0; i < a.segs; ++i) {
-    const int g = dir ? a.segs - 1 - i : i;
-    float4 *at = reinterpret_cast<float4 *>(a.sums[dir] + (bh * a.segs + g) * a.dd + e);
-    const bool has = !(a.skip_last && i == a.segs - 1);
-    const float4 x = has ? *at : make_float4(0.f, 0.f, 0.f, 0.f);
-    const float w = has ? exp2f(a.tot[bh * a.segs + g]) : 1.f;
-    *at = s;
-    s = make_float4(fmaf(w, s.x, x.x), fmaf(w, s.y, x.y), fmaf(w, s.z, x.z), fmaf(w, s.w, x.w));
+  if (a.first[dir]) s = *reinterpret_cast<const float4 *>(a.first[dir] + (long)bh * a.dd + e);
+  float *at = a.sums[dir] + (long)bh * a.segs * a.dd + e;
+  const float *tot = a.tot + (long)bh * a.segs;
+  constexpr int kAhead = 8;  // sums in flight per thread
+  for (int i0 = 0; i0 < a.segs; i0 += kAhead) {
+    float4 x[kAhead];
+    float w[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = i0 + u, g = dir ? a.segs - 1 - i : i;
+      const bool has = i < a.segs && !(a.skip_last && i == a.segs - 1);
+      x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      w[u] = 0.f;
+      if (has) {
+        x[u] = *reinterpret_cast<const float4 *>(at + (long)g * a.dd);
+        w[u] = tot[g];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = i0 + u, g = dir ? a.segs - 1 - i : i;
+      if (i >= a.segs) break;
+      *reinterpret_cast<float4 *>(at + (long)g * a.dd) = s;
+      const float f = exp2f(w[u]);
+      s = make_float4(fmaf(f, s.x, x[u].x), fmaf(f, s.y, x[u].y), fmaf(f, s.z, x[u].z), fmaf(f, s.w, x[u].w));
+    }
   }
-  if (a.last[dir]) *reinterpret_cast<float4 *>(a.last[dir] + bh * a.dd + e) = s;
+  if (a.last[dir]) *reinterpret_cast<float4 *>(a.last[dir] + (long)bh * a.dd + e) = s;
 }
 
-template <int D>
+template <int D, bool kSum>
 cudaError_t launch_t(const GatedStateParams &sp, long BH, int dirs, bool pdl, cudaStream_t stream) {
-  cudaError_t e = ensure_smem_optin((const void *)gated_state_tc_kernel<D>, (int)Lay<D>::Bytes);
+  cudaError_t e = ensure_smem_optin((const void *)gated_state_tc_kernel<D, kSum>, (int)Lay<D>::Bytes);
   if (e != cudaSuccess) return e;
-  LaunchTimer timer(kKGatedState, stream);
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)(BH * sp.run_segs), (unsigned)dirs);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Lay<D>::Bytes;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = pdl ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, gated_state_tc_kernel<D>, sp);
-  if (e == cudaSuccess) e = cudaGetLastError();
-  timer.done(e);
-  if (e == cudaSuccess) count_launch();
-  return e;
+  return launch_gated_kernel(gated_state_tc_kernel<D, kSum>, sp, dim3((unsigned)(BH * sp.run_segs), (unsigned)dirs), kThreads,
+                             Lay<D>::Bytes, pdl, kKGatedState, stream);
 }
 
 }  // namespace
@@ -365,7 +397,11 @@ bool gated_map(CUtensorMap *m, const void *base, long BH, long N, int D, uint32_
 }
 
 cudaError_t launch_gated_states(const GatedStateParams &sp, int D, long BH, int dirs, bool pdl, cudaStream_t stream) {
-  return D == 64 ? launch_t<64>(sp, BH, dirs, pdl, stream) : launch_t<128>(sp, BH, dirs, pdl, stream);
+  if (!sp.tiles[0]) {
+    if (!sp.fin[0] || (dirs == 2 && !sp.fin[1]) || !sp.seg_tot) return cudaErrorInvalidValue;
+    return D == 64 ? launch_t<64, true>(sp, BH, dirs, pdl, stream) : launch_t<128, true>(sp, BH, dirs, pdl, stream);
+  }
+  return D == 64 ? launch_t<64, false>(sp, BH, dirs, pdl, stream) : launch_t<128, false>(sp, BH, dirs, pdl, stream);
 }
 
 cudaError_t read_and_clear_gated_state_status(unsigned int *value) {
@@ -373,12 +409,8 @@ cudaError_t read_and_clear_gated_state_status(unsigned int *value) {
 }
 
 cudaError_t launch_gated_seg_scan(const GatedSegScan &a, long BH, int dirs, cudaStream_t stream) {
-  LaunchTimer timer(kKGatedState, stream);
-  gated_seg_scan_kernel<<<dim3((unsigned)(BH * ((a.dd / 4 + 127) / 128)), 1, (unsigned)dirs), 128, 0, stream>>>(a);
-  const cudaError_t e = cudaGetLastError();
-  timer.done(e);
-  if (e == cudaSuccess) count_launch();
-  return e;
+  return launch_gated_kernel(gated_seg_scan_kernel, a, dim3((unsigned)(BH * (a.dd / (4 * kScanThreads))), 1, (unsigned)dirs), kScanThreads, 0,
+                             true, kKGatedState, stream);
 }
 
 }  // namespace la

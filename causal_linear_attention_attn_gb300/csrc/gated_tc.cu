@@ -124,6 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  pdl_wait();  // the states before the segments are the previous kernels'
 
   if (warp < 4) {
     reg_dec<kRegs0>();
@@ -468,11 +469,15 @@ Plan make_plan(long BH, long N, int D) {
   // its keys and values
   t.G = std::max(1L, std::min(sms / std::max(1L, BH), t.n / 4));
   t.seg_chunks = (t.n + t.G - 1) / t.G;
-  // the state pass's CTAs: cut its segments finer while one wave of SMs holds them
+  // the state pass's CTAs, one an SM: parts a segment for the fewest turns of an SM, a CTA's start and
+  // end counted as two chunks
   t.step = 1;
   if (t.G > 1) {
-    const long per = BH * (t.G - 1);
-    while (per * t.step * 2 <= sms && t.seg_chunks / (t.step * 2) >= 2) t.step *= 2;
+    long best = -1;
+    for (long step = 1; step <= 8 && step <= t.seg_chunks; ++step) {
+      const long cost = (BH * (t.G - 1) * step + sms - 1) / sms * ((t.seg_chunks + step - 1) / step + 2);
+      if (best < 0 || cost < best) best = cost, t.step = step;
+    }
     t.seg_chunks = (t.seg_chunks + t.step - 1) / t.step * t.step;
     t.G = (t.n + t.seg_chunks - 1) / t.seg_chunks;
     if (t.G == 1) t.step = 1;
@@ -490,12 +495,8 @@ cudaError_t launch_main(const Params &mp, long BH, cudaStream_t stream) {
     return cudaFuncGetAttributes(&a, gated_tc_kernel<D>) == cudaSuccess ? a.numRegs : 0;
   }();
   if (regs != kRegs) return cudaErrorInvalidConfiguration;
-  LaunchTimer timer(kKGated, stream);
-  gated_tc_kernel<D><<<(unsigned)(BH * mp.segs), kThreads, Lay<D>::Bytes, stream>>>(mp);
-  e = cudaGetLastError();
-  timer.done(e);
-  if (e == cudaSuccess) count_launch();
-  return e;
+  return launch_gated_kernel(gated_tc_kernel<D>, mp, dim3((unsigned)(BH * mp.segs)), kThreads, Lay<D>::Bytes, mp.segs > 1, kKGated,
+                             stream);
 }
 
 }  // namespace

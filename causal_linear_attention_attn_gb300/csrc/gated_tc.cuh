@@ -91,22 +91,32 @@ __device__ __forceinline__ float4 load_gates(const float *g, int tv, int lane) {
   return make_float4(x[0], x[1], x[2], x[3]);
 }
 // Their inclusive running sums in base 2 (one warp).
-__device__ __forceinline__ void scan_gates(float4 g, int lane, float *hi, float *lo) {
-  const float v[4] = {g.x, g.y, g.z, g.w};
-  long long x[4];
+struct GateSums {
+  long long c[4];  // fixed point
   bool nan[4];
+  __device__ __forceinline__ GateSums(float4 g, int lane) {
+    const float v[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    x[e] = fixed_log2_decay(v[e]) + (e ? x[e - 1] : 0);
-    nan[e] = isnan(v[e]) || (e && nan[e - 1]);
+    for (int e = 0; e < 4; ++e) {
+      c[e] = fixed_log2_decay(v[e]) + (e ? c[e - 1] : 0);
+      nan[e] = isnan(v[e]) || (e && nan[e - 1]);
+    }
+    const long long before = warp_scan(c[3], lane) - c[3];
+    const bool nan_before = __ballot_sync(0xffffffffu, nan[3]) & ((1u << lane) - 1);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c[e] += before, nan[e] = nan[e] || nan_before;
   }
-  const long long before = warp_scan(x[3], lane) - x[3];
-  const bool nan_before = __ballot_sync(0xffffffffu, nan[3]) & ((1u << lane) - 1);
-  Cum c[4];
+};
+__device__ __forceinline__ void store_cums(const long long (&c)[4], const bool (&nan)[4], int lane, float *hi, float *lo) {
+  Cum u[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) c[e] = split_cum(before + x[e], nan[e] || nan_before);
-  *reinterpret_cast<float4 *>(hi + 4 * lane) = make_float4(c[0].hi, c[1].hi, c[2].hi, c[3].hi);
-  *reinterpret_cast<float4 *>(lo + 4 * lane) = make_float4(c[0].lo, c[1].lo, c[2].lo, c[3].lo);
+  for (int e = 0; e < 4; ++e) u[e] = split_cum(c[e], nan[e]);
+  *reinterpret_cast<float4 *>(hi + 4 * lane) = make_float4(u[0].hi, u[1].hi, u[2].hi, u[3].hi);
+  *reinterpret_cast<float4 *>(lo + 4 * lane) = make_float4(u[0].lo, u[1].lo, u[2].lo, u[3].lo);
+}
+__device__ __forceinline__ void scan_gates(float4 g, int lane, float *hi, float *lo) {
+  const GateSums s(g, lane);
+  store_cums(s.c, s.nan, lane, hi, lo);
 }
 
 // Two loads of 16 columns with a single wait.
@@ -230,6 +240,30 @@ __device__ __forceinline__ void store_row64(void *p, const uint4 (&v)[4], bool w
 
 }  // namespace gtc
 
+// One launch; pdl: it may start while the previous kernel of the stream, one of this family, still
+// runs (that kernel lets it in after its tensor-memory allocation, and it waits for that kernel's
+// results before it reads any).
+template <typename P>
+cudaError_t launch_gated_kernel(void (*fn)(P), const P &p, dim3 grid, int threads, uint32_t smem, bool pdl, int kernel_id,
+                                cudaStream_t stream) {
+  LaunchTimer timer(kernel_id, stream);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, fn, p);
+  if (e == cudaSuccess) e = cudaGetLastError();
+  timer.done(e);
+  if (e == cudaSuccess) count_launch();
+  return e;
+}
+
 // [BH][N][D] bf16 as a 3-D tensor with boxes of 64 features x `rows` tokens, 128-byte swizzle.
 bool gated_map(CUtensorMap *m, const void *base, long BH, long N, int D, uint32_t rows);
 
@@ -238,6 +272,7 @@ bool gated_map(CUtensorMap *m, const void *base, long BH, long N, int D, uint32_
 // each head, starting from init: X = 2^{c_T} X + sum_t w_t a_t b_t^T per chunk, w_t = 2^{c_T - c_t}
 // (forward) or 2^{c_t} (backward).  tiles: X before each chunk as a bf16 pair (gated_tile_bytes a
 // chunk: hi then lo, each in blocks of 64 columns, [D][64] row-major); fin: X behind the segment.
+// Without tiles only the segments' own sums are wanted (init is not read, fin is given).
 struct GatedStateParams {
   CUtensorMap ta[2], tb[2];  // boxes of 64 x 128
   const float *g;
