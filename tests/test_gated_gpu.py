@@ -295,3 +295,124 @@ def test_many_heads(cuda_lib):
     within(S[at], refS, absS, F32, "S")
     dq = cuda_lib.la_gated_backward(d["q"], d["k"], d["v"], d["g"], d["dout"])[0]
     within(dq[at], backward64(**part)[0], backward64(**absolute(part))[0], F32, "dq")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_segments_cut_by_lengths(cuda_lib, d):
+    """Few heads: several segments each, of which rows fill all, one and a half, or a part of the first."""
+    N = 2600 if d == 128 else 4100
+    lengths = torch.tensor([N, 130, N // 2 + 77], dtype=torch.int32, device="cuda")
+    x = make(3, 1, N, d, d, BF16, seed=91, state=True, resets=0.002)
+    check_forward(cuda_lib, x, lengths)
+    check_backward(cuda_lib, x, lengths)
+
+
+def test_long_decays_and_segments(cuda_lib):
+    """Decays of 2^-12 a token: the state before a segment carries thousands of tokens."""
+    x = make(1, 2, 3000, 64, 64, BF16, seed=92, scale=2.0**-11)
+    check_forward(cuda_lib, x)
+    check_backward(cuda_lib, x)
+
+
+@pytest.mark.parametrize("dt,dk,dv", CASES)
+def test_offset_storage(cuda_lib, dt, dk, dv):
+    """Tensors that start 16 but not 32 bytes, and decays that start 4 bytes, into their storage."""
+    d = make(2, 2, 161, dk, dv, dt, seed=93, state=True)
+
+    def shifted(t, by):
+        if t is None:
+            return None
+        s = torch.empty(t.numel() + by, dtype=t.dtype, device=t.device)
+        s[by:] = t.reshape(-1)
+        return s[by:].view(t.shape)
+
+    by = 16 // torch.empty((), dtype=dt).element_size()
+    e = {n: shifted(t, by if n in ("q", "k", "v", "dout") else 1 if n == "g" else 4) for n, t in d.items()}
+    out = shifted(torch.zeros_like(d["v"]), by)
+    S = shifted(d["S0"], 4)
+    cuda_lib.la_gated_with_state(e["q"], e["k"], e["v"], e["g"], S, out=out)
+    o2, S2 = call(cuda_lib, d)
+    assert torch.equal(out, o2) and torch.equal(S, S2)
+    grad = lambda x: cuda_lib.la_gated_backward(  # noqa: E731
+        x["q"], x["k"], x["v"], x["g"], x["dout"], S0=x["S0"], dS=x["dS"], need_state_grad=True)
+    assert all(torch.equal(a, b) for a, b in zip(grad(e), grad(d)))
+    with pytest.raises(cuda_lib.LinAttnError, match="MISALIGNED"):
+        cuda_lib.la_gated(shifted(d["q"], 1), d["k"], d["v"], d["g"])
+
+
+def test_gradient_written_to_unaligned_and_in_place_buffers(cuda_lib):
+    """Through the C ABI: dq, dk, dv 16 bytes into their storage, and dS0 written over dS."""
+    L = cuda_lib
+    d = make(2, 2, 300, 128, 128, BF16, seed=94, state=True)
+    want = L.la_gated_backward(d["q"], d["k"], d["v"], d["g"], d["dout"], S0=d["S0"], dS=d["dS"], need_state_grad=True)
+    bufs = [torch.full((d["q"].numel() + 8,), NAN, dtype=BF16, device="cuda")[8:] for _ in range(3)]
+    dg, dS = torch.empty_like(d["g"]), d["dS"].clone()
+    need = L.lib.la_gated_workspace(2, 2, 300, 128, 128, 1, 1)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    p = L._ptr
+    rc = L.lib.la_gated_backward(p(d["q"]), p(d["k"]), p(d["v"]), p(d["g"]), None, p(d["dout"]), p(d["S0"]), p(dS),
+                                 *map(p, bufs), p(dg), p(dS), 2, 2, 300, 128, 128, 1, p(ws), need,
+                                 torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    for b, w in zip(bufs, want):
+        assert torch.equal(b.view(w.shape), w)
+    assert torch.equal(dg, want[3]) and torch.equal(dS, want[4])
+    # a workspace that is too small is refused before anything runs
+    assert L.lib.la_gated_backward(p(d["q"]), p(d["k"]), p(d["v"]), p(d["g"]), None, p(d["dout"]), None, None, *map(p, bufs),
+                                   p(dg), None, 2, 2, 300, 128, 128, 1, p(ws), need - 1, None) == 1
+
+
+def test_many_heads_on_the_tensor_cores(cuda_lib):
+    d = make(70000, 1, 3, 64, 64, BF16, seed=71)
+    out, S = cuda_lib.la_gated(d["q"], d["k"], d["v"], d["g"])
+    at = [0, 1, 65534, 65535, 65536, 69999]
+    part = {n: None if t is None else t[at] for n, t in d.items()}
+    ref, refS, _ = forward64(**part)
+    abso, absS, _ = forward64(**absolute(part))
+    within(out[at], ref, abso, BF16, "out", pair=True, steps=2)
+    within(S[at], refS, absS, BF16, "S", pair=True)
+    dv = cuda_lib.la_gated_backward(d["q"], d["k"], d["v"], d["g"], d["dout"])[2]
+    within(dv[at], backward64(**part)[2], backward64(**absolute(part))[2], BF16, "dv", pair=True, steps=2)
+
+
+@pytest.mark.parametrize("dt,dk,dv", CASES)
+def test_nan_decay_reaches_only_what_follows(cuda_lib, dt, dk, dv):
+    d = make(1, 2, 200, dk, dv, dt, seed=95)
+    d["g"][0, 1, 90] = NAN
+    out, S = call(cuda_lib, d)
+    assert torch.isfinite(out[0, 0]).all() and torch.isfinite(S[0, 0]).all()
+    assert torch.isfinite(out[0, 1, :90]).all() and out[0, 1, 90:].isnan().all() and S[0, 1].isnan().all()
+
+
+@pytest.mark.parametrize("dt,dk,dv", CASES)
+def test_captured_on_two_streams_at_once(cuda_lib, dt, dk, dv):
+    """Prefill, gradient, step and norm captured twice, both graphs in flight, against eager calls."""
+    L = cuda_lib
+    sets = [make(2, 3, 500, dk, dv, dt, seed=96 + i, state=True) for i in range(2)]
+    gates = [torch.randn(2, 500, 3 * dv, device="cuda").to(dt) for _ in range(2)]
+    w, b = torch.randn(3 * dv, device="cuda"), torch.randn(3 * dv, device="cuda")
+
+    def run(d, gate):
+        out, S = L.la_gated(d["q"], d["k"], d["v"], d["g"])
+        y = L.la_group_norm(out, gate, w, b)
+        dn = L.la_group_norm_backward(out, y, gate, w, b)
+        gr = L.la_gated_backward(d["q"], d["k"], d["v"], d["g"], dn[0], dS=d["dS"], need_state_grad=True)
+        o = L.la_gated_decode_step(*(d[n][:, :, 0].contiguous() for n in ("q", "k", "v", "g")), S)
+        return [out, S, y, *dn, *gr, o]
+
+    want = [run(d, g) for d, g in zip(sets, gates)]
+    torch.cuda.synchronize()
+    graphs = []
+    for d, g in zip(sets, gates):
+        G = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(G):
+            r = run(d, g)
+        graphs.append((G, r, torch.cuda.Stream()))
+    for _ in range(5):
+        for G, _, s in graphs:
+            with torch.cuda.stream(s):
+                G.replay()
+    torch.cuda.synchronize()
+    for (_, r, _), x in zip(graphs, want):
+        assert all(torch.equal(a, c) for a, c in zip(r, x))
+    assert L.device_status() == 0
