@@ -60,6 +60,7 @@ constexpr uint32_t kColS = 0, kColP = 128, kColI = 256, kColA = 384;  // state, 
 
 struct Params {
   CUtensorMap tq, tk, tv;  // boxes of 64 x 128
+  CUtensorMap to;          // boxes of 64 x 32
   const float *g;
   const int *lengths;
   const float *init;  // state before each segment: [BH][init_segs][D][D], segment s at s * init_step; null: zero
@@ -100,7 +101,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
   if (threadIdx.x == 0) {
     for (int b = 0; b < 2; ++b) {
       mbar_init(&full_v[b], 1);
-      mbar_init(&v_free[b], 1);
+      mbar_init(&v_free[b], 4);  // the outputs' warps, when their rows have left it
       mbar_init(&gate_full[b], 32);
       mbar_init(&gate_free[b], 768);
     }
@@ -205,7 +206,6 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
         tc_fence_after();
         if (leader) {
           product_ts<kMN>(tA, tP, mnbase(v), iO, false);
-          mma_commit(&v_free[s]);
           mma_commit(o_full);
         }
         __syncwarp();
@@ -420,8 +420,14 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
       mbar_arrive(&gate_free[c & 1]);
       if (!warp_wait(o_full, c & 1, abort_word)) break;
       tc_fence_after();
-      const bool in = i < valid(c);
-      __nv_bfloat16 *dst = p.out + (bh * p.N + (c_lo + c) * kC + i) * D;
+      // The rows leave through the chunk's values, which are read by now: 32 rows of 64 columns a copy.
+      // (Stored from registers, a row a lane, they took 30 of the pass's 125 us at 4 x 16 x 8192.)  A
+      // chunk cut by its row's length, not by N where the copy is clipped, stores its rows itself.
+      const int tv = valid(c), s = c & 1;
+      const long t0 = (c_lo + c) * kC;
+      const bool whole = tv == (int)min((long)kC, p.N - t0);
+      uint8_t *stage = sm + L::V + s * L::kTile + q * 4096;
+      __nv_bfloat16 *dst = p.out + (bh * p.N + t0 + i) * D;
 #pragma unroll 1
       for (int cb = 0; cb < D / 32; ++cb) {
         uint4 o[4];
@@ -441,9 +447,25 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
           tc_fence_before();
           mbar_arrive(o_free);
         }
-        if (in) store_row64(dst + cb * 32, o, p.wide);
+        if (whole)
+          stage_row32(stage + (cb >> 1) * kBlk, lane, cb & 1, o);
+        else if (i < tv)
+          store_row64(dst + cb * 32, o, p.wide);
+        if (whole && (cb & 1)) {
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0 && q * 32 < tv) {
+            tma_store_3d(&p.to, stage + (cb >> 1) * kBlk, (cb >> 1) * 64, (int)(t0 + q * 32), (int)bh);
+            bulk_commit();
+          }
+        }
+      }
+      if (lane == 0) {
+        bulk_wait_read();
+        mbar_arrive(&v_free[s]);
       }
     }
+    if (lane == 0) bulk_wait_all();
   }
 
   tc_fence_before();
@@ -523,7 +545,7 @@ cudaError_t launch_gated_tc(const GatedProblem &p) {
   Params mp;
   memset(&mp, 0, sizeof mp);
   if (!gated_map(&mp.tq, p.q, BH, p.N, D, kC) || !gated_map(&mp.tk, p.k, BH, p.N, D, kC) ||
-      !gated_map(&mp.tv, p.v, BH, p.N, D, kC))
+      !gated_map(&mp.tv, p.v, BH, p.N, D, kC) || !gated_map(&mp.to, p.out, BH, p.N, D, 32))
     return cudaErrorInvalidValue;
   mp.g = p.g, mp.lengths = p.lengths, mp.out = (__nv_bfloat16 *)p.out, mp.S = p.S, mp.N = p.N, mp.H = p.H;
   mp.segs = (int)t.G, mp.seg_chunks = (int)t.seg_chunks, mp.init_segs = 1, mp.init_step = 0;
