@@ -51,12 +51,12 @@ struct Lay {
   static constexpr uint32_t dO = K + kTile;
   static constexpr uint32_t V = dO + kTile;
   static constexpr uint32_t Ring = V + kTile;
-  static constexpr uint32_t WD = Ring + kRing * kState;  // W D [keys][queries] bf16
+  static constexpr uint32_t WD = Ring + kRing * kState;  // W D [keys][queries] bf16; then results on their way out
   static constexpr uint32_t Gate = WD + 2 * kBlk;        // hi 128, lo 128
   static constexpr uint32_t Buf = Gate + 2 * kC * 4;     // 320 floats
   static constexpr uint32_t Red = Buf + 320 * 4;         // 4 floats
   static constexpr uint32_t Bars = Red + 16;
-  static constexpr int kNumBars = 3 + 2 * kRing + 16;
+  static constexpr int kNumBars = 3 + 2 * kRing + 15;
   static constexpr uint32_t Misc = Bars + kNumBars * 8;
   static constexpr uint32_t Bytes = Misc + 16;
 };
@@ -65,7 +65,8 @@ constexpr uint32_t kColP = 0, kColD = 128, kColQ = 256, kColK = 384;  // dV in D
 
 struct Params {
   CUtensorMap tq, tk, tv, td;  // boxes of 64 x 128
-  CUtensorMap ts, tr;          // tiles of S and R: [blocks][D][64], boxes of one part
+  CUtensorMap ts, tr;          // tiles of S and R, boxes of one part
+  CUtensorMap oq, ok, ov;      // dq, dk, dv: boxes of 64 x 32
   const float *g;
   const int *lengths;
   const uint8_t *s_tiles, *r_tiles;
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
            *b0 = ring_free + kRing, *tok_free = b0, *gate_full = b0 + 1, *e_full = b0 + 2, *el_done = b0 + 3,
            *q_in = b0 + 4, *k_in = b0 + 5, *v_in = b0 + 6, *x_ready = b0 + 7, *out_full = b0 + 8, *out_free = b0 + 9,
            *dg_in = b0 + 10, *dot_full = b0 + 11, *dot_free = b0 + 12,
-           *v_free = b0 + 13, *d_free = b0 + 14, *dv_full = b0 + 15;
+           *v_free = b0 + 13, *d_free = b0 + 14;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::Misc);
   volatile uint32_t *abort_word = reinterpret_cast<volatile uint32_t *>(sm + L::Misc + 4);
   uint64_t *drain = reinterpret_cast<uint64_t *>(sm + L::Misc + 8);
@@ -164,7 +165,6 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
     mbar_init(out_full, 1);
     mbar_init(out_free, 256);
     mbar_init(d_free, 256);
-    mbar_init(dv_full, 1);
     mbar_init(dg_in, 256 + 128);
     mbar_init(dot_full, 4);
     mbar_init(dot_free, 32);
@@ -304,7 +304,6 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
       tc_fence_after();
       if (leader) {
         product_ts<kMN>(tD, tP, mnbase(sO), iKM, true);
-        mma_commit(dv_full);  // dV first: the next chunk's D^T waits for its columns
         product<8, kK, kMN>(tK, kbase(sW), mnbase(sQ), iKM, true);
         product<8, kMN, kMN>(tQ, mnbase(sW), mnbase(sK), iMM, true);
         mma_commit(tok_free);
@@ -422,6 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
       if (item(x).tv == 0) continue;
       const uint32_t ph = it & 1;
       bool ok = mbar_wait(gate_full, ph, abort_word, status) && mbar_wait(e_full, ph, abort_word, status);
+      ok = ok && (it == 0 || mbar_wait(out_free, ph ^ 1, abort_word, status));  // W D's place is free
       if (bar_or(kBarScore, 256, !ok)) break;  // also: the last chunk's partial sums are read
       tc_fence_after();
       // W P to tensor memory, W D to shared memory, and the sums of W P D by key and by query
@@ -540,29 +540,44 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
       }
       tc_fence_before();
       mbar_arrive(x_ready);
-      if (!warp_wait(dv_full, ph, abort_word)) break;
-      tc_fence_after();
-      // padding rows (T >= tv) are zero whatever the states hold
-      auto put = [&](uint32_t col, __nv_bfloat16 *dst) {
-        uint32_t r[32];
-        uint4 v[4];
-        tmem_ld32(col, r);
-        to_bf16x32(r, v);
-        if (T >= w.tv) v[0] = v[1] = v[2] = v[3] = make_uint4(0u, 0u, 0u, 0u);
-        if (T < rows) store_row64(dst + at, v, p.wide);
+      // Results leave through W D's place, which its products have left: 32 rows of 64 columns a copy
+      // and warp (half 0: dV's first block and dQ; half 1: its second and dK).  Rows past N are clipped,
+      // padding rows (T >= tv) are zero whatever the states hold.
+      uint8_t *stage = sm + L::WD + (half * 4 + q) * 4096;
+      auto put = [&](uint32_t col, const CUtensorMap *map, int c0) {
+        if (lane == 0) bulk_wait_read();
+        __syncwarp();
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          uint32_t r[32];
+          uint4 v[4];
+          tmem_ld32(col + 32 * b, r);
+          to_bf16x32(r, v);
+          if (T >= w.tv) v[0] = v[1] = v[2] = v[3] = make_uint4(0u, 0u, 0u, 0u);
+          stage_row32(stage, lane, b, v);
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0 && q * 32 < rows) {
+          tma_store_3d(map, stage, c0, (int)w.t0 + q * 32, (int)w.bh);
+          bulk_commit();
+        }
       };
-#pragma unroll 1
-      for (int cb = 0; cb < D / 64; ++cb) put(tl + kColD + half * (D / 2) + cb * 32, p.dv + half * (D / 2) + cb * 32);
-      tc_fence_before();
-      mbar_arrive(d_free);
+      // (the place is W D's until every product that reads it is done)
       if (!warp_wait(out_full, ph, abort_word)) break;
       tc_fence_after();
+      if (D == 128 || half == 0) put(tl + kColD + half * 64, &p.ov, half * 64);
+      tc_fence_before();
+      mbar_arrive(d_free);
 #pragma unroll 1
-      for (int cb = 0; cb < D / 32; ++cb) put(tX + cb * 32, dx + cb * 32);
+      for (int cb = 0; cb < D / 64; ++cb) put(tX + cb * 64, half ? &p.ok : &p.oq, cb * 64);
+      if (lane == 0) bulk_wait_read();
+      __syncwarp();
       tc_fence_before();
       mbar_arrive(out_free);
       ++it;
     }
+    if (lane == 0) bulk_wait_all();
   }
 
   tc_fence_before();
@@ -586,19 +601,6 @@ Plan make_plan(long BH, long N, int D) {
   t.seg_chunks = (t.n + t.segs - 1) / t.segs;
   t.segs = (t.n + t.seg_chunks - 1) / t.seg_chunks;
   return t;
-}
-
-// The state pass's tiles as [blocks][D][64] bf16, one box a part (hi or lo).
-bool tile_map(CUtensorMap *m, const void *base, long chunks, int D) {
-  auto fn = tensor_map_encoder();
-  if (!fn) return false;
-  cuuint64_t dims[3] = {64, (cuuint64_t)D, (cuuint64_t)(2 * chunks * (D / 64))};
-  cuuint64_t strides[2] = {128, (cuuint64_t)D * 128};
-  cuuint32_t box[3] = {64, (cuuint32_t)D, (cuuint32_t)(D / 64)};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int D>
@@ -655,13 +657,17 @@ cudaError_t launch_gated_grad_tc(const GatedGradProblem &b) {
     sp.init[0] = p.S0, sp.init[1] = b.dS, sp.fin[1] = b.dS0;
   }
   sp.tiles[0] = ws, sp.tiles[1] = ws + tiles;
+  if (!gated_tile_map(&sp.to[0], sp.tiles[0], BH * t.n, D, 32, 1) || !gated_tile_map(&sp.to[1], sp.tiles[1], BH * t.n, D, 32, 1))
+    return cudaErrorInvalidValue;
   e = launch_gated_states(sp, D, BH, 2, t.segs > 1, p.stream);
   if (e != cudaSuccess) return e;
   Params cp;
   memset(&cp, 0, sizeof cp);
   if (!gated_map(&cp.tq, p.q, BH, p.N, D, kC) || !gated_map(&cp.tk, p.k, BH, p.N, D, kC) ||
       !gated_map(&cp.tv, p.v, BH, p.N, D, kC) || !gated_map(&cp.td, b.dout, BH, p.N, D, kC) ||
-      !tile_map(&cp.ts, sp.tiles[0], BH * t.n, D) || !tile_map(&cp.tr, sp.tiles[1], BH * t.n, D))
+      !gated_tile_map(&cp.ts, ws, BH * t.n, D, D, D / 64) || !gated_tile_map(&cp.tr, ws + tiles, BH * t.n, D, D, D / 64) ||
+      !gated_map(&cp.oq, b.dq, BH, p.N, D, 32) || !gated_map(&cp.ok, b.dk, BH, p.N, D, 32) ||
+      !gated_map(&cp.ov, b.dv, BH, p.N, D, 32))
     return cudaErrorInvalidValue;
   cp.g = p.g, cp.lengths = p.lengths, cp.s_tiles = sp.tiles[0], cp.r_tiles = sp.tiles[1];
   cp.dq = (__nv_bfloat16 *)b.dq, cp.dk = (__nv_bfloat16 *)b.dk, cp.dv = (__nv_bfloat16 *)b.dv, cp.dg = b.dg;

@@ -33,26 +33,29 @@ constexpr int kThreads = 608;
 constexpr int kWarpXform = 2, kWarpState = 10, kWarpGate = 18;
 constexpr uint32_t kBarState = 1;
 
-template <int D>
+template <int D, bool kSum>
 struct Lay {
   static constexpr int kStages = D == 128 ? 2 : 4;
-  static constexpr uint32_t kTile = D / 64 * kBlk;  // 128 tokens
+  static constexpr int kLo = D == 128 && !kSum ? 1 : 2;  // buffers of low parts
+  static constexpr uint32_t kTile = D / 64 * kBlk;       // 128 tokens
   static constexpr uint32_t A = 0;
-  static constexpr uint32_t Lo = A + kStages * kTile;  // 2 buffers
-  static constexpr uint32_t B = Lo + 2 * kTile;
-  static constexpr uint32_t Sum = B + kStages * kTile;  // D = 64: low rows of the state [64][65] fp32
-  static constexpr uint32_t Gate = Sum + (D == 64 ? 64 * 65 * 4 : 0);  // [2][hi 128, lo 128]
+  static constexpr uint32_t Lo = A + kStages * kTile;
+  static constexpr uint32_t B = Lo + kLo * kTile;
+  // tiles on their way out: 32 rows of 64 columns, hi and lo, for each state warp (D = 64: each of two)
+  static constexpr uint32_t Stage = B + kStages * kTile;
+  static constexpr uint32_t Sum = Stage + (kSum ? 0 : (D == 128 ? 8 : 2) * 8192);  // D = 64: low rows of the state [64][65] fp32
+  static constexpr uint32_t Gate = Sum + (D == 64 ? 64 * 65 * 4 : 0);              // [2][hi 128, lo 128]
   static constexpr uint32_t Bars = Gate + 2 * 2 * kC * 4;
   static constexpr int kNumBars = 3 * kStages + 2 + 4 + 3;
   static constexpr uint32_t Misc = Bars + kNumBars * 8;
   static constexpr uint32_t Bytes = Misc + 16;
 };
-static_assert(Lay<128>::Bytes <= 232448, "shared memory budget");
+static_assert(Lay<128, true>::Bytes <= 232448 && Lay<128, false>::Bytes <= 232448, "shared memory budget");
 
 template <int D, bool kSum>
 __global__ void __launch_bounds__(kThreads, 1) gated_state_tc_kernel(const __grid_constant__ GatedStateParams p) {
-  using L = Lay<D>;
-  constexpr int kStages = L::kStages;
+  using L = Lay<D, kSum>;
+  constexpr int kStages = L::kStages, kLo = L::kLo;
   extern __shared__ __align__(1024) uint8_t sm[];
   if (smem_u32(sm) & 1023u) {
     if (threadIdx.x == 0) atomicOr(&g_gated_status, kAbortMisaligned);
@@ -75,7 +78,6 @@ __global__ void __launch_bounds__(kThreads, 1) gated_state_tc_kernel(const __gri
   const long nb = (len + kC - 1) / kC;  // the row's chunks
   const long c_lo = min(nb, (long)seg * p.seg_chunks), c_hi = min(nb, c_lo + p.seg_chunks);
   const int nc = (int)(c_hi - c_lo);
-  uint8_t *tiles = p.tiles[dir];
   float *fin = p.fin[dir];
   // the last chunk is folded in only if the state behind it is wanted
   const int run = kSum || fin ? nc : max(0, nc - 1);
@@ -134,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_state_tc_kernel(const __gri
       if (!kSum && !warp_wait(x_ready, i & 1, abort_word)) break;
       const bool add = !kSum || i > 0;
       tc_fence_after();
-      const uint32_t a = sA + s * L::kTile, lo = sLo + (i & 1) * L::kTile, b = sB + s * L::kTile;
+      const uint32_t a = sA + s * L::kTile, lo = sLo + i % kLo * L::kTile, b = sB + s * L::kTile;
       if (leader) {
         if (D == 128) {
           product<8, kMN, kMN>(tmem, mnbase(a), mnbase(b), iMM, add);
@@ -143,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_state_tc_kernel(const __gri
           product<8, kMN, kMN>(tmem, mnbase(a, lo - a), mnbase(b), iMM, add);  // rows: hi, then lo
         }
         mma_commit(&empty[s]);
-        mma_commit(&lo_free[i & 1]);
+        mma_commit(&lo_free[i % kLo]);
         if (!kSum || i + 1 == run) mma_commit(x_full);
       }
       __syncwarp();
@@ -162,13 +164,13 @@ __global__ void __launch_bounds__(kThreads, 1) gated_state_tc_kernel(const __gri
         const int s = i % kStages;
         bool ok = mbar_wait(&gate_full[i & 1], (i >> 1) & 1, abort_word, status);
         ok = ok && mbar_wait(&full[s], (i / kStages) & 1, abort_word, status);
-        if (ok && i >= 2) ok = mbar_wait(&lo_free[i & 1], ((i >> 1) - 1) & 1, abort_word, status);
+        if (ok && i >= kLo) ok = mbar_wait(&lo_free[i % kLo], (i / kLo - 1) & 1, abort_word, status);
         if (!__all_sync(0xffffffffu, ok)) break;
         const float *hi = gate + (i & 1) * 2 * kC, *lo = hi + kC;
         const bool in = r < valid(i);
         const float w = kSum || dir ? exp2f(hi[r] + lo[r]) : exp2f((hi[kC - 1] - hi[r]) + (lo[kC - 1] - lo[r]));
         mbar_arrive(&gate_free[i & 1]);
-        uint8_t *A = sm + L::A + s * L::kTile + blk, *Lo = sm + L::Lo + (i & 1) * L::kTile + blk;
+        uint8_t *A = sm + L::A + s * L::kTile + blk, *Lo = sm + L::Lo + i % kLo * L::kTile + blk;
 #pragma unroll 4
         for (int e = 0; e < kChunks; ++e) {
           const uint32_t off = sw128_offset(r, (c0 + e) * 8);
@@ -220,6 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_state_tc_kernel(const __gri
       };
       bool ok = true;
       for (int i = 0; !kSum && i < nc && ok; ++i) {
+        if (D == 64 && lane == 0) bulk_wait_read();
         bool w = i == 0 || mbar_wait(x_full, (i - 1) & 1, abort_word, status);
         if (w && i < run) w = mbar_wait(&gate_full[i & 1], (i >> 1) & 1, abort_word, status);
         if (bar_or(kBarState, 256, !w)) {  // D = 64: also, the last joined columns are read
@@ -250,21 +253,41 @@ __global__ void __launch_bounds__(kThreads, 1) gated_state_tc_kernel(const __gri
           tc_fence_before();
           mbar_arrive(x_ready);
         }
-        if (tiles) {
+        // the tile: 32 rows of 64 columns a copy, read out of shared memory by the next chunk
+        if constexpr (!kSum) {
+          const int z = (int)((bh * p.n + chunk(i)) * 2 * (D / 64)) + (col0 >> 6);
+          uint8_t *stage = sm + L::Stage + (D == 128 ? warp - kWarpState : q & 1) * 8192;
+          if (D == 128) {
+            if (lane == 0) bulk_wait_read();
+            __syncwarp();
+          }
           join();
           if (main_row) {
-            uint8_t *t = tiles + (bh * p.n + chunk(i)) * (size_t)(D * D * 4) + (col0 >> 6) * (D * 128) + row * 128 + (col0 & 63) * 2;
+#pragma unroll 1
+            for (int part = 0; part < 2; ++part)
 #pragma unroll
-            for (int b = 0; b < kB; ++b) {
-              uint4 v[4];
-              to_bf16x32(r[b], v);
-              store_row64(t + b * 64, v, true);
-              rest_bf16x32(r[b], v);
-              store_row64(t + D * D * 2 + b * 64, v, true);
-            }
+              for (int b = 0; b < kB; ++b) {
+                uint4 v[4];
+                if (part)
+                  rest_bf16x32(r[b], v);
+                else
+                  to_bf16x32(r[b], v);
+                stage_row32(stage + part * 4096, lane, D == 128 ? b : col0 >> 5, v);
+              }
+          }
+          fence_async_smem();
+          if (D == 128)
+            __syncwarp();
+          else
+            named_bar(kBarState, 256);
+          if (lane == 0 && main_row && col0 % 64 == 0) {
+            tma_store_3d(&p.to[dir], stage, 0, q * 32, z);
+            tma_store_3d(&p.to[dir], stage + 4096, 0, q * 32, z + D / 64);
+            bulk_commit();
           }
         }
       }
+      if (!kSum && lane == 0) bulk_wait_all();
       if (fin && ok) {
         const bool w = run == 0 || mbar_wait(x_full, kSum ? 0 : (run - 1) & 1, abort_word, status);
         if (!bar_or(kBarState, 256, !w)) {
@@ -376,10 +399,10 @@ __global__ void __launch_bounds__(kScanThreads) gated_seg_scan_kernel(const __gr
 
 template <int D, bool kSum>
 cudaError_t launch_t(const GatedStateParams &sp, long BH, int dirs, bool pdl, cudaStream_t stream) {
-  cudaError_t e = ensure_smem_optin((const void *)gated_state_tc_kernel<D, kSum>, (int)Lay<D>::Bytes);
+  cudaError_t e = ensure_smem_optin((const void *)gated_state_tc_kernel<D, kSum>, (int)Lay<D, kSum>::Bytes);
   if (e != cudaSuccess) return e;
   return launch_gated_kernel(gated_state_tc_kernel<D, kSum>, sp, dim3((unsigned)(BH * sp.run_segs), (unsigned)dirs), kThreads,
-                             Lay<D>::Bytes, pdl, kKGatedState, stream);
+                             Lay<D, kSum>::Bytes, pdl, kKGatedState, stream);
 }
 
 }  // namespace
@@ -390,6 +413,18 @@ bool gated_map(CUtensorMap *m, const void *base, long BH, long N, int D, uint32_
   cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)N, (cuuint64_t)BH};
   cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)N * D * 2};
   cuuint32_t box[3] = {64, rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool gated_tile_map(CUtensorMap *m, const void *base, long chunks, int D, uint32_t rows, uint32_t blocks) {
+  auto fn = tensor_map_encoder();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {64, (cuuint64_t)D, (cuuint64_t)(2 * chunks * (D / 64))};
+  cuuint64_t strides[2] = {128, (cuuint64_t)D * 128};
+  cuuint32_t box[3] = {64, rows, blocks};
   cuuint32_t estr[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

@@ -221,9 +221,9 @@ __device__ __forceinline__ void stage_row32(uint8_t *blk, int row, int half, con
   for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4 *>(blk + sw128_offset(row, half * 32 + 8 * e)) = v[e];
 }
 
-// 64 bytes of a lane's own row.  Every lane is in another row, so an instruction touches 32 lines;
-// 32-byte stores (whole sectors) halve their number.  (Measured against staging the rows in shared
-// memory for bulk copies: the proxy fence, the copy and the wait for it cost each warp 2000 cycles.)
+// 64 bytes of a lane's own row, for what is not worth a copy through shared memory: every lane is in
+// another row, an instruction touches 32 lines (20 bytes a cycle and SM; a bulk copy moves 27, beside
+// the warp's other work).
 __device__ __forceinline__ void store_row64(void *p, const uint4 (&v)[4], bool wide) {
   if (wide) {
 #pragma unroll
@@ -267,6 +267,9 @@ cudaError_t launch_gated_kernel(void (*fn)(P), const P &p, dim3 grid, int thread
 // [BH][N][D] bf16 as a 3-D tensor with boxes of 64 features x `rows` tokens, 128-byte swizzle.
 bool gated_map(CUtensorMap *m, const void *base, long BH, long N, int D, uint32_t rows);
 
+// The state pass's tiles as [blocks][D][64] bf16 with boxes of `rows` rows of `blocks` blocks.
+bool gated_tile_map(CUtensorMap *m, const void *base, long chunks, int D, uint32_t rows, uint32_t blocks);
+
 // The state pass (gated_state_tc.cu).  For each of `dirs` directions (0: forward, K and V, from the
 // first chunk; 1: backward, Q and dout, from the last) and each segment of seg_chunks chunks of
 // each head, starting from init: X = 2^{c_T} X + sum_t w_t a_t b_t^T per chunk, w_t = 2^{c_T - c_t}
@@ -275,6 +278,7 @@ bool gated_map(CUtensorMap *m, const void *base, long BH, long N, int D, uint32_
 // Without tiles only the segments' own sums are wanted (init is not read, fin is given).
 struct GatedStateParams {
   CUtensorMap ta[2], tb[2];  // boxes of 64 x 128
+  CUtensorMap to[2];         // of tiles, boxes of 32 rows
   const float *g;
   const int *lengths;
   long N, n;  // tokens and chunks per head
