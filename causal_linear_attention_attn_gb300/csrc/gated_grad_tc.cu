@@ -663,9 +663,8 @@ cudaError_t launch_gated_grad_tc(const GatedGradProblem &b) {
   if (e != cudaSuccess) return e;
   Params cp;
   memset(&cp, 0, sizeof cp);
-  if (!gated_map(&cp.tq, p.q, BH, p.N, D, kC) || !gated_map(&cp.tk, p.k, BH, p.N, D, kC) ||
-      !gated_map(&cp.tv, p.v, BH, p.N, D, kC) || !gated_map(&cp.td, b.dout, BH, p.N, D, kC) ||
-      !gated_tile_map(&cp.ts, ws, BH * t.n, D, D, D / 64) || !gated_tile_map(&cp.tr, ws + tiles, BH * t.n, D, D, D / 64) ||
+  cp.tk = sp.ta[0], cp.tv = sp.tb[0], cp.tq = sp.ta[1], cp.td = sp.tb[1];
+  if (!gated_tile_map(&cp.ts, ws, BH * t.n, D, D, D / 64) || !gated_tile_map(&cp.tr, ws + tiles, BH * t.n, D, D, D / 64) ||
       !gated_map(&cp.oq, b.dq, BH, p.N, D, 32) || !gated_map(&cp.ok, b.dk, BH, p.N, D, 32) ||
       !gated_map(&cp.ov, b.dv, BH, p.N, D, 32))
     return cudaErrorInvalidValue;

@@ -31,6 +31,7 @@
 
 #include "gated.cuh"
 #include "internal.h"
+#include "per_device.h"
 
 namespace la {
 namespace {
@@ -442,10 +443,16 @@ cudaError_t launch_t(Args a, long BH, cudaStream_t stream) {
   const void *fn = (const void *)gated_simt_kernel<Tin, kGrad>;
   cudaError_t e = ensure_smem_optin(fn, (int)smem);
   if (e != cudaSuccess) return e;
-  int per_sm = 0;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, kThreads, smem);
+  // blocks that fit on the device at once, looked up once per device and size
+  static PerDeviceCache<size_t, int> fits;
+  int dev = 0;
+  e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const long room = (long)std::max(1, per_sm) * std::max(1, device_info(-1).sm_count);
+  const long room = fits.get(dev, smem, [&] {
+    int per_sm = 0;
+    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, kThreads, smem);
+    return std::max(1, per_sm) * std::max(1, device_info(dev).sm_count);
+  });
   // enough blocks for the chunks and for the scan, all of them resident
   const long want = std::max(BH * a.n * (kGrad ? 2 : 1), BH * dk * dv / 4 * (kGrad ? 2 : 1) / kThreads);
   LaunchTimer timer(kGrad ? kKGatedBackward : kKGated, stream);

@@ -556,8 +556,7 @@ cudaError_t launch_gated_tc(const GatedProblem &p) {
     float *sums = (float *)p.ws, *tot = sums + (size_t)BH * t.init_segs() * D * D;
     GatedStateParams sp;
     memset(&sp, 0, sizeof sp);
-    if (!gated_map(&sp.ta[0], p.k, BH, p.N, D, kC) || !gated_map(&sp.tb[0], p.v, BH, p.N, D, kC))
-      return cudaErrorInvalidValue;
+    sp.ta[0] = mp.tk, sp.tb[0] = mp.tv;
     sp.g = p.g, sp.lengths = p.lengths, sp.N = p.N, sp.n = t.n, sp.H = p.H;
     sp.segs = (int)t.init_segs(), sp.run_segs = sp.segs - 1, sp.seg_chunks = (int)(t.seg_chunks / t.step);
     sp.fin[0] = sums, sp.seg_tot = tot;
