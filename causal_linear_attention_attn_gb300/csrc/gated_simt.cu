@@ -24,7 +24,9 @@
 // launches): each chunk's own sum of k v^T (and q do^T); a scan over a head's chunks, one thread for
 // four elements of the state; each chunk's outputs or gradients.  The states between the phases cost
 // 4 dk dv / T bytes per token each way; in exchange a single long sequence fills the device, where
-// one CTA per head would leave it idle.
+// one CTA per head would leave it idle.  Measured in fp32: 1 x 2 x 256 tokens at d = 32 in 12 us on
+// the device (launch latency and two grid barriers), the gradient at 2 x 4 x 333 tokens, 64 x 32, in
+// 35 us (latency of a chunk's loops: 88 blocks).
 #include <cooperative_groups.h>
 
 #include <algorithm>

@@ -14,6 +14,8 @@
 // nothing is decayed between chunks, there is no chain, and the state warps weigh every other chunk.
 // At D = 64 hi and lo make up the 128 rows of one MMA, [hi | lo]^T b, and meet when the state is read.
 // HBM bounds it: per token 4 D bytes in and, when tiles are written, 4 D bytes out per direction.
+// Measured at 4 x 16 x 8192, D = 128, both directions with tiles: 170 us (6.3 TB/s); with the tiles
+// stored from registers, a row a lane, 209 us.
 //
 // Warps: 0 TMA, 1 MMA and TMEM owner, 2-9 weights (hi in place, lo beside it), 10-17 state, 18
 // running sums of the decays.  Every wait is bounded (tc_ptx.cuh).

@@ -13,6 +13,10 @@
 // costs no pass of its own.  HBM bounds it: every tensor is read or written once (the gradient
 // recomputes the statistics instead of storing them).
 //
+// Measured in bf16 with gate and affine map, d = 128: 4 x 16 x 8192 tokens forward in 76 us (5.3 TB/s),
+// 4 x 16 x 4096 tokens of the gradient in 76 us (4.4 TB/s); more blocks an SM, fewer or more rows in
+// flight were each slower (80 to 140 us).
+//
 // A thread owns eight channels of one head; the d/8 threads of a head meet in shuffles; the threads
 // of a block cover up to 2048 channels of one token or the same channels of several tokens.  So
 // channels-last rows move in runs of up to 4 KB, and every thread keeps its channels while the block
