@@ -13,9 +13,10 @@
 // costs no pass of its own.  HBM bounds it: every tensor is read or written once (the gradient
 // recomputes the statistics instead of storing them).
 //
-// Measured in bf16 with gate and affine map, d = 128: 4 x 16 x 8192 tokens forward in 76 us (5.3 TB/s),
-// 4 x 16 x 4096 tokens of the gradient in 76 us (4.4 TB/s); more blocks an SM, fewer or more rows in
-// flight were each slower (80 to 140 us).
+// Two rows a thread are in flight, each loaded again as soon as its values are taken.  Measured in bf16
+// with gate and affine map, d = 128: 4 x 16 x 8192 tokens forward in 68 us (5.9 TB/s), 4 x 16 x 4096
+// tokens of the gradient in 73 us (4.6 TB/s); loads and use in turns took 77 and 78, other numbers of
+// rows and of blocks an SM 69 to 120 and 73 to 105, the affine map read again for each row 83.
 //
 // A thread owns eight channels of one head; the d/8 threads of a head meet in shuffles; the threads
 // of a block cover up to 2048 channels of one token or the same channels of several tokens.  So
@@ -34,6 +35,8 @@ namespace la {
 namespace {
 
 constexpr int kMaxThreads = 256;
+// rows in flight a thread, blocks an SM
+constexpr int kAheadFwd = 2, kPerSmFwd = 4, kAheadGrad = 2, kPerSmGrad = 2;
 
 // Sum over the aligned group of D / 8 lanes of one head.
 template <int D>
@@ -44,7 +47,7 @@ __device__ __forceinline__ float group_sum(float x) {
 }
 
 // How a launch cuts [B * N tokens][H * d channels]: a block covers `heads` heads of `rows` tokens at
-// a time (a slab of heads), a few such groups of consecutive tokens in flight.
+// a time (a slab of heads), two such groups of consecutive tokens in flight.
 struct Cut {
   int heads, rows, threads, slabs;
 };
@@ -145,7 +148,7 @@ Divider make_divider(uint32_t n) {
 }
 
 template <typename T, int D, bool kGate, int kRowsAhead>
-__global__ void __launch_bounds__(kMaxThreads, 3)
+__global__ void __launch_bounds__(kMaxThreads, kPerSmFwd)
     group_norm_kernel(const __grid_constant__ NormProblem p, const __grid_constant__ Cut cut,
                       const __grid_constant__ Divider by_n) {
   const uint32_t tokens = (uint32_t)((long)p.B * p.N);
@@ -163,30 +166,33 @@ __global__ void __launch_bounds__(kMaxThreads, 3)
 #pragma unroll
     for (int e = 0; e < 4; ++e) b[e] = reinterpret_cast<const float2 *>(p.bias + col)[e];
   }
-  // every lane of a warp runs the same number of turns: the shuffles need all of them
-  for (long r0 = (long)blockIdx.x * cut.rows * kRowsAhead; r0 < tokens; r0 += (long)gridDim.x * cut.rows * kRowsAhead) {
-    Raw<T> x[kRowsAhead], g[kRowsAhead];
-#pragma unroll
-    for (int u = 0; u < kRowsAhead; ++u) {
-      const long r = r0 + u * cut.rows + me.row;
-      x[u].zero();
-      if (me.live && r < tokens) {
-        const uint32_t bi = by_n.of((uint32_t)r), n = (uint32_t)r - bi * by_n.n;
-        x[u].load((const T *)p.x + (((long)bi * p.H + me.h) * p.N + n) * D + me.c);
-        if (kGate) g[u].load((const T *)p.gate + r * HD + col);
-      }
+  const long step = (long)gridDim.x * cut.rows * kRowsAhead;
+  Raw<T> x[kRowsAhead], g[kRowsAhead];
+  auto load = [&](int u, long r) {
+    x[u].zero();
+    if (me.live && r < tokens) {
+      const uint32_t bi = by_n.of((uint32_t)r), n = (uint32_t)r - bi * by_n.n;
+      x[u].load((const T *)p.x + (((long)bi * p.H + me.h) * p.N + n) * D + me.c);
+      if (kGate) g[u].load((const T *)p.gate + r * HD + col);
     }
+  };
+  long r0 = (long)blockIdx.x * cut.rows * kRowsAhead;
+#pragma unroll
+  for (int u = 0; u < kRowsAhead; ++u) load(u, r0 + u * cut.rows + me.row);
+  // every lane of a warp runs the same number of turns: the shuffles need all of them
+  for (; r0 < tokens; r0 += step) {
 #pragma unroll
     for (int u = 0; u < kRowsAhead; ++u) {
       float2 y[4], t[4];
       x[u].get(y);
-      normalize<D>(y, p.eps);
+      if (kGate) g[u].get(t);
       const long r = r0 + u * cut.rows + me.row;
+      load(u, r + step);
+      normalize<D>(y, p.eps);
       if (!(me.live && r < tokens)) continue;
 #pragma unroll
       for (int e = 0; e < 4; ++e) y[e] = __ffma2_rn(y[e], w[e], b[e]);
       if (kGate) {
-        g[u].get(t);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           y[e] = __fmul2_rn(y[e], __fmul2_rn(t[e], make_float2(sigmoid(t[e].x), sigmoid(t[e].y))));
@@ -197,7 +203,7 @@ __global__ void __launch_bounds__(kMaxThreads, 3)
 }
 
 template <typename T, int D, bool kGate, int kRowsAhead>
-__global__ void __launch_bounds__(kMaxThreads, 2)
+__global__ void __launch_bounds__(kMaxThreads, kPerSmGrad)
     group_norm_grad_kernel(const __grid_constant__ NormGradProblem q, const __grid_constant__ Cut cut,
                            const __grid_constant__ Divider by_n) {
   __shared__ float sums[kMaxThreads][16 + 1];
@@ -218,30 +224,33 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
 #pragma unroll
       for (int e = 0; e < 4; ++e) b[e] = reinterpret_cast<const float2 *>(p.bias + col)[e];
     }
-    for (long r0 = (long)blockIdx.x * cut.rows * kRowsAhead; r0 < tokens; r0 += (long)gridDim.x * cut.rows * kRowsAhead) {
-      Raw<T> x[kRowsAhead], g[kRowsAhead], dy[kRowsAhead];
-#pragma unroll
-      for (int u = 0; u < kRowsAhead; ++u) {
-        const long r = r0 + u * cut.rows + me.row;
-        x[u].zero(), dy[u].zero(), g[u].zero();
-        if (me.live && r < tokens) {
-          const uint32_t bi = by_n.of((uint32_t)r), n = (uint32_t)r - bi * by_n.n;
-          x[u].load((const T *)p.x + (((long)bi * p.H + me.h) * p.N + n) * D + me.c);
-          dy[u].load((const T *)q.dy + r * HD + col);
-          if (kGate) g[u].load((const T *)p.gate + r * HD + col);
-        }
+    const long step = (long)gridDim.x * cut.rows * kRowsAhead;
+    Raw<T> x[kRowsAhead], g[kRowsAhead], dy[kRowsAhead];
+    auto load = [&](int u, long r) {
+      x[u].zero(), dy[u].zero(), g[u].zero();
+      if (me.live && r < tokens) {
+        const uint32_t bi = by_n.of((uint32_t)r), n = (uint32_t)r - bi * by_n.n;
+        x[u].load((const T *)p.x + (((long)bi * p.H + me.h) * p.N + n) * D + me.c);
+        dy[u].load((const T *)q.dy + r * HD + col);
+        if (kGate) g[u].load((const T *)p.gate + r * HD + col);
       }
+    };
+    long r0 = (long)blockIdx.x * cut.rows * kRowsAhead;
+#pragma unroll
+    for (int u = 0; u < kRowsAhead; ++u) load(u, r0 + u * cut.rows + me.row);
+    for (; r0 < tokens; r0 += step) {
 #pragma unroll
       for (int u = 0; u < kRowsAhead; ++u) {
         const long r = r0 + u * cut.rows + me.row;
         const bool in = me.live && r < tokens;
-        float2 h[4], t[4];
+        float2 h[4], t[4], gg[4];
         x[u].get(h);
         dy[u].get(t);
+        if (kGate) g[u].get(gg);
+        load(u, r + step);
         const float rstd = normalize<D>(h, p.eps);
         if (kGate) {
-          float2 gg[4], o[4];
-          g[u].get(gg);
+          float2 o[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float2 sg = make_float2(sigmoid(gg[e].x), sigmoid(gg[e].y));
@@ -321,13 +330,11 @@ int token_blocks(const Cut &c, long tokens, int per_sm, int ahead) {
   return (int)std::max(1L, std::min<long>(turns, std::max(1, sms * per_sm / c.slabs)));
 }
 
-constexpr int kAheadFwd = 4, kAheadGrad = 3, kPerSmGrad = 2;
-
 template <typename T, int D>
 cudaError_t launch_fwd(const NormProblem &p) {
   const Cut c = make_cut(p.H, D);
   LaunchTimer timer(kKGroupNorm, p.stream);
-  const dim3 grid((unsigned)token_blocks(c, (long)p.B * p.N, 1 << 20, kAheadFwd), (unsigned)c.slabs);
+  const dim3 grid((unsigned)token_blocks(c, (long)p.B * p.N, kPerSmFwd, kAheadFwd), (unsigned)c.slabs);
   const Divider by_n = make_divider((uint32_t)p.N);
   if (p.gate)
     group_norm_kernel<T, D, true, kAheadFwd><<<grid, c.threads, 0, p.stream>>>(p, c, by_n);

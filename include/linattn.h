@@ -423,7 +423,8 @@ LA_API la_status la_group_norm(const void *x, const void *gate, const float *wei
  * Gradient of la_group_norm for dy ([B,N,H*d], dtype dt).  Written: dx
  * [B,H,N,d] and dgate [B,N,H*d] (given exactly when gate is) of dtype dt;
  * dweight, dbias [H*d] float32, each nullable, whether or not the forward had
- * weight and bias.  The column sums are added in a fixed order.  workspace:
+ * weight and bias.  No output may overlap an input.  The column sums are added in
+ * a fixed order.  workspace:
  * la_group_norm_workspace bytes when dweight or dbias is wanted (NULL
  * otherwise); calls that may run at the same time need one each.
  */
