@@ -80,7 +80,7 @@ __device__ __forceinline__ void load_rows(float *dst, int ld, const Tin *src, in
   }
 }
 
-// Chunk sums: blockIdx.z 0: sum_t 2^{c_T - c_t} k_t v_t^T; 1: sum_t 2^{c_t} q_t do_t^T.
+// Chunk sums: sum_t 2^{c_T - c_t} k_t v_t^T; rev: sum_t 2^{c_t} q_t do_t^T.
 template <typename Tin>
 __device__ __forceinline__ void chunk_sums(const Args &a, float *sm, long item, bool rev) {
   const int dk = a.dk, dv = a.dv;
