@@ -18,8 +18,14 @@
 // first products are scaled by row in tensor memory, then the second ones accumulate on top.
 // HBM bounds it at 14 D bytes a token of inputs and results plus 8 D of states (D = 128: 8.1 us a
 // chunk at an SM's share); the tensor work is 13 products of 128 x 128 x D.  Measured at 4 x 16 x 8192,
-// D = 128: 280 us (5.2 TB/s); without the score warps' work it takes as long, without the second
-// reading of the states for <S, R> (from L2) 34 us less.  At D = 64 a chunk's chain of steps bounds it.
+// D = 128: 255 us (5.7 TB/s); without the score warps' work it takes as long, without the second
+// reading of the states for <S, R> (from L2) 34 us less.  At D = 64 a chunk's chain of steps bounds it,
+// 16000 cycles; two chunks' tokens in shared memory and a place for results beside W D's, for which
+// there is room, took 3 % off and were not kept.
+//
+// Every warp runs its code once a chunk, out of a cold instruction cache (the first of a score warp's
+// four equal turns takes 4000 cycles, the others 1500): less code is faster.  32-bit quotients in place
+// of 64-bit ones took 269 to 258 us, turns of a loop unrolled by two 280.
 //
 // Two chunks overlap: the score warps weigh a chunk's products while the row warps still write the
 // previous chunk's results; the score columns are free for it as soon as dV is read.
@@ -75,7 +81,8 @@ struct Params {
   __nv_bfloat16 *dq, *dk, *dv;
   float *dg;
   float *mail;  // [CTAs][3][128] what each token adds to dg
-  long N, n, items;
+  long N;
+  uint32_t n, items;  // chunks a head, all chunks (below 2^31)
   int H;
   bool wide;  // dq, dk, dv are 32-byte aligned
 };
@@ -186,11 +193,13 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
     long bh, t0;
     int tv;
   };
-  auto item = [&](long x) -> Item {
+  // (32-bit quotients: every warp's code is run once a chunk, out of a cold instruction cache)
+  auto item = [&](uint32_t x) -> Item {
     Item r;
-    r.bh = x / p.n;
-    r.t0 = (x - r.bh * p.n) * kC;
-    const long len = row_length(p.lengths, r.bh / p.H, p.N);
+    const uint32_t bh = x / p.n;
+    r.bh = bh;
+    r.t0 = (long)(x - bh * p.n) * kC;
+    const long len = p.lengths ? row_length(p.lengths, bh / (uint32_t)p.H, p.N) : p.N;
     r.tv = (int)max(0L, min((long)kC, len - r.t0));
     return r;
   };
@@ -200,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
       int it = 0, ring = 0;
       int kq = 0, vd = 0;  // tiles issued
       bool ok = true;
-      auto piece = [&](const CUtensorMap *map, long x, int part) {
+      auto piece = [&](const CUtensorMap *map, uint32_t x, int part) {
         const int s = ring % kRing;
         if (ring >= kRing) ok = ok && mbar_wait(&ring_free[s], (ring / kRing - 1) & 1, abort_word, status);
         if (!ok) return;
@@ -211,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
       auto tile = [&](uint32_t at, const CUtensorMap *map, uint64_t *bar, const Item &w) {
         for (int b = 0; b < D / 64; ++b) tma_load_3d(sm + at + b * kBlk, map, bar, 64 * b, (int)w.t0, (int)w.bh);
       };
-      for (long x = blockIdx.x; x < p.items && ok; x += gridDim.x) {
+      for (uint32_t x = blockIdx.x; x < p.items && ok; x += gridDim.x) {
         const Item w = item(x);
         if (w.tv == 0) continue;
         piece(&p.ts, x, 0);
@@ -246,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
     const uint32_t sQ = smem_u32(sm + L::Q), sK = smem_u32(sm + L::K), sV = smem_u32(sm + L::V),
                    sO = smem_u32(sm + L::dO), sW = smem_u32(sm + L::WD), sR = smem_u32(sm + L::Ring);
     int it = 0;
-    for (long x = blockIdx.x; x < p.items; x += gridDim.x) {
+    for (uint32_t x = blockIdx.x; x < p.items; x += gridDim.x) {
       if (item(x).tv == 0) continue;
       const uint32_t ph = it & 1;
       // the chunk's pieces S hi, S lo, R hi, R lo take the ring's two places in turn
@@ -344,11 +353,11 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
       mbar_arrive(gate_full);
       return true;
     };
-    auto next = [&](long x) -> long {
+    auto next = [&](uint32_t x) -> uint32_t {
       while (x < p.items && item(x).tv == 0) x += gridDim.x;
       return x;
     };
-    long x = next(blockIdx.x);
+    uint32_t x = next(blockIdx.x);
     bool ok = x < p.items;
     if (ok) ok = gates(item(x), fetch(item(x)));
     while (ok && x < p.items) {
@@ -397,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
   } else if (warp < kWarpScore) {
     // ---- <S, R> of the stored pairs ----
     int it = 0;
-    for (long x = blockIdx.x; x < p.items; x += gridDim.x) {
+    for (uint32_t x = blockIdx.x; x < p.items; x += gridDim.x) {
       if (item(x).tv == 0) continue;
       const uint4 *S = reinterpret_cast<const uint4 *>(p.s_tiles + x * (size_t)(2 * kState));
       const uint4 *R = reinterpret_cast<const uint4 *>(p.r_tiles + x * (size_t)(2 * kState));
@@ -419,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
     const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16);
     float *mail = p.mail + (long)blockIdx.x * 3 * kC;
     int it = 0;
-    for (long x = blockIdx.x; x < p.items; x += gridDim.x) {
+    for (uint32_t x = blockIdx.x; x < p.items; x += gridDim.x) {
       if (item(x).tv == 0) continue;
       const uint32_t ph = it & 1;
       bool ok = mbar_wait(gate_full, ph, abort_word, status) && mbar_wait(e_full, ph, abort_word, status);
@@ -502,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
     float *mail = p.mail + (long)blockIdx.x * 3 * kC + (1 + half) * kC;
     __nv_bfloat16 *dx = half ? p.dk : p.dq;
     int it = 0;
-    for (long x = blockIdx.x; x < p.items; x += gridDim.x) {
+    for (uint32_t x = blockIdx.x; x < p.items; x += gridDim.x) {
       const Item w = item(x);
       const int rows = (int)min((long)kC, p.N - w.t0);
       const long at = (w.bh * p.N + w.t0 + T) * D;
@@ -568,11 +577,17 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
       // (the place is W D's until every product that reads it is done)
       if (!warp_wait(out_full, ph, abort_word)) break;
       tc_fence_after();
-      if (D == 128 || half == 0) put(tl + kColD + half * 64, &p.ov, half * 64);
-      tc_fence_before();
-      mbar_arrive(d_free);
+      // dV's block first: its columns are the next chunk's D
 #pragma unroll 1
-      for (int cb = 0; cb < D / 64; ++cb) put(tX + cb * 64, half ? &p.ok : &p.oq, cb * 64);
+      for (int cb = -1; cb < D / 64; ++cb) {
+        if (D == 128 || half == 0 || cb >= 0)
+          put(cb < 0 ? tl + kColD + half * 64 : tX + cb * 64, cb < 0 ? &p.ov : half ? &p.ok : &p.oq,
+              64 * (cb < 0 ? half : cb));
+        if (cb < 0) {
+          tc_fence_before();
+          mbar_arrive(d_free);
+        }
+      }
       if (lane == 0) bulk_wait_read();
       __syncwarp();
       tc_fence_before();
@@ -610,7 +625,7 @@ cudaError_t launch_chunks(const Params &cp, cudaStream_t stream) {
   cudaError_t e = ensure_smem_optin((const void *)gated_grad_tc_kernel<D>, (int)Lay<D>::Bytes);
   if (e != cudaSuccess) return e;
   const long sms = std::max(1, device_info(-1).sm_count);
-  return launch_gated_kernel(gated_grad_tc_kernel<D>, cp, dim3((unsigned)std::min(sms, cp.items)), kThreads, Lay<D>::Bytes, true,
+  return launch_gated_kernel(gated_grad_tc_kernel<D>, cp, dim3((unsigned)std::min(sms, (long)cp.items)), kThreads, Lay<D>::Bytes, true,
                              kKGatedBackward, stream);
 }
 
@@ -674,7 +689,7 @@ cudaError_t launch_gated_grad_tc(const GatedGradProblem &b) {
   cp.dq = (__nv_bfloat16 *)b.dq, cp.dk = (__nv_bfloat16 *)b.dk, cp.dv = (__nv_bfloat16 *)b.dv, cp.dg = b.dg;
   cp.mail = (float *)p.ws;
   cp.wide = (((uintptr_t)b.dq | (uintptr_t)b.dk | (uintptr_t)b.dv) & 31) == 0;
-  cp.N = p.N, cp.n = t.n, cp.items = BH * t.n, cp.H = p.H;
+  cp.N = p.N, cp.n = (uint32_t)t.n, cp.items = (uint32_t)(BH * t.n), cp.H = p.H;
   return D == 64 ? launch_chunks<64>(cp, p.stream) : launch_chunks<128>(cp, p.stream);
 }
 
