@@ -275,12 +275,15 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSmGrad)
           }
           if (in) put8((T *)q.dgate + r * HD + col, o);
         }
+        if (in) {  // (past the last token h is 0 / 0 when eps is 0)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          dw[e] = __ffma2_rn(t[e], h[e], dw[e]);
-          db[e] = __fadd2_rn(db[e], t[e]);
-          t[e] = __fmul2_rn(t[e], w[e]);
+          for (int e = 0; e < 4; ++e) {
+            dw[e] = __ffma2_rn(t[e], h[e], dw[e]);
+            db[e] = __fadd2_rn(db[e], t[e]);
+          }
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[e] = __fmul2_rn(t[e], w[e]);
         const float su = group_sum<D>(sum8(t)) * (-1.f / D), suh = group_sum<D>(dot8(t, h)) * (-1.f / D);
 #pragma unroll
         for (int e = 0; e < 4; ++e) t[e] = __fmul2_rn(__fadd2_rn(__ffma2_rn(h[e], both(suh), t[e]), both(su)), both(rstd));
