@@ -133,20 +133,27 @@ __device__ __forceinline__ float normalize(float2 (&x)[4], float eps) {
   return rstd;
 }
 
-// 1 / (1 + e^-x), two at a time: e^-x overflows to inf below -88, where the quotient is 0 as it should
-// be.  The approximate instructions are taken without their care for subnormal numbers (there 1 + e^-x
+// e^-x and 1 / (1 + e^-x), two at a time: e^-x overflows to inf below -88, where the quotient is 0 as it
+// should be.  The approximate instructions are taken without their care for subnormal numbers (there 1 + e^-x
 // is 1, and the quotient below 1e-38): issue slots, 70 % of them taken, bound the forward
 // beside HBM: 68 to 65 us.
-__device__ __forceinline__ float2 sigmoid2(float2 x) {
-  const float2 t = __fmul2_rn(x, both(-1.44269504f));  // -log2 e
-  float2 e;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
-  e = __fadd2_rn(e, both(1.f));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(e.x));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(e.y));
-  return e;
-}
+struct Sigmoid2 {
+  float2 e, s;
+  __device__ __forceinline__ explicit Sigmoid2(float2 x) {
+    const float2 t = __fmul2_rn(x, both(-1.44269504f));  // -log2 e
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+    const float2 d = __fadd2_rn(e, both(1.f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(d.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(d.y));
+  }
+  // 1 - s as e^-x s, which keeps its bits where s is near 1 (a gate of 1e4 multiplies what 1 - s would
+  // have lost); inf * 0 is NaN, of which the minimum takes the 1.
+  __device__ __forceinline__ float2 one_less() const {
+    const float2 o = __fmul2_rn(e, s);
+    return make_float2(fminf(o.x, 1.f), fminf(o.y, 1.f));
+  }
+};
 
 // Quotients by N of numbers below 2^31 (round-up multiplier; add and shift).
 struct Divider {
@@ -208,7 +215,7 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSmFwd)
       if (kGate) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          y[e] = __fmul2_rn(y[e], __fmul2_rn(t[e], sigmoid2(t[e])));
+          y[e] = __fmul2_rn(y[e], __fmul2_rn(t[e], Sigmoid2(t[e]).s));
       }
       put8((T *)p.y + r * HD + col, y);
     }
@@ -266,10 +273,9 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSmGrad)
           float2 o[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float2 sg = sigmoid2(gg[e]);
-            const float2 silu = __fmul2_rn(gg[e], sg);
-            // silu' = sigmoid + silu (1 - sigmoid)
-            const float2 ds = __ffma2_rn(__fmul2_rn(silu, both(-1.f)), sg, __fadd2_rn(sg, silu));
+            const Sigmoid2 sg(gg[e]);
+            const float2 silu = __fmul2_rn(gg[e], sg.s);
+            const float2 ds = __ffma2_rn(silu, sg.one_less(), sg.s);  // silu' = s + silu (1 - s)
             o[e] = __fmul2_rn(__fmul2_rn(t[e], __ffma2_rn(h[e], w[e], b[e])), ds);
             t[e] = __fmul2_rn(t[e], silu);
           }
