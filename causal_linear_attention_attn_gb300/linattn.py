@@ -394,6 +394,8 @@ def _gated_call(fn, q, k, v, g, lengths, out, S, stream):
     _opt("lengths", lengths, (B,), torch.int32, dev)
     s, ctx = _on(dev, stream)
     try:
+        if out is None and lengths is not None:  # the call does not write padding rows, the next layer may read them
+            out = torch.zeros((B, H, N, dv), dtype=q.dtype, device=dev)
         out = _out("out", out, (B, H, N, dv), q.dtype, dev)
         S = _out("S", S, (B, H, dk, dv), torch.float32, dev)
         need = _gated_workspace(dev.index, B, H, N, dk, dv, dt, 0)
@@ -411,7 +413,8 @@ def la_gated(q, k, v, g, lengths=None, out=None, S=None, stream=None):
     """Gated linear attention S_t = e^{g_t} S_{t-1} + k_t v_t^T, out_t = q_t^T S_t from the zero state.
 
     q, k [B, H, N, d_k], v [B, H, N, d_v] (float32 or bfloat16); g [B, H, N] float32 log decays (<= 0; -inf resets).
-    lengths [B] int32: tokens past a row's length take no part and their ``out`` rows are not written.
+    lengths [B] int32: tokens past a row's length take no part and their rows of a given ``out`` are not written (give
+    it finite rows there if la_group_norm and its gradient read them); without ``out`` they are zero.
     Returns (out in q's dtype, final state S float32).
     """
     return _gated_call("la_gated", q, k, v, g, lengths, out, S, stream)
@@ -511,7 +514,10 @@ def _norm_workspace(device, B, H, N, d):
 
 
 def la_group_norm_backward(x, dy, gate=None, weight=None, bias=None, eps: float = 1e-5, stream=None):
-    """Gradients of la_group_norm for dy [B, N, H*d]: (dx, dgate, dweight, dbias), None for an argument not given."""
+    """Gradients of la_group_norm for dy [B, N, H*d]: (dx, dgate, dweight, dbias), None for an argument not given.
+
+    Every row adds to dweight and dbias: padding rows need finite x and gate, and zeros in dy.
+    """
     dev, B, H, N, d, dt = _norm_inputs(x, gate, weight, bias)
     _need("dy", dy, (B, N, H * d), x.dtype, dev)
     s, ctx = _on(dev, stream)

@@ -424,7 +424,8 @@ LA_API la_status la_group_norm(const void *x, const void *gate, const float *wei
  * [B,H,N,d] and dgate [B,N,H*d] (given exactly when gate is) of dtype dt;
  * dweight, dbias [H*d] float32, each nullable, whether or not the forward had
  * weight and bias.  No output may overlap an input.  The column sums are added in
- * a fixed order.  workspace:
+ * a fixed order, over all rows: rows of padding tokens need finite x and gate and
+ * zeros in dy.  workspace:
  * la_group_norm_workspace bytes when dweight or dbias is wanted (NULL
  * otherwise); calls that may run at the same time need one each.
  */
