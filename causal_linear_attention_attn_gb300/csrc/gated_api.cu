@@ -31,7 +31,7 @@ la_status sizes(int B, int H, long N, int dk, int dv, la_dtype dt) {
 
 size_t workspace(int B, int H, long N, int dk, int dv, la_dtype dt, bool grad) {
   const long BH = (long)B * H;
-  if (gated_tc_supported(dk, dv, dt))
+  if (gated_tc_supported(dk, dv, dt, grad))
     return grad ? gated_tc_grad_workspace(BH, N, dk) : gated_tc_prefill_workspace(BH, N, dk);
   return gated_simt_workspace(BH, N, dk, dv, grad);
 }
@@ -53,7 +53,7 @@ la_status gated(const void *q, const void *k, const void *v, const float *g, con
   if ((st = api_device()) != LA_OK) return st;
   const size_t need = workspace(B, H, N, dk, dv, dt, false);
   if (ws_bytes < need || (need && !ws)) return LA_ERR_INVALID_VALUE;
-  return api_status(gated_tc_supported(dk, dv, dt) ? launch_gated_tc(p) : launch_gated_simt(p));
+  return api_status(gated_tc_supported(dk, dv, dt, false) ? launch_gated_tc(p) : launch_gated_simt(p));
 }
 
 }  // namespace
@@ -100,7 +100,7 @@ la_status la_gated_backward(const void *q, const void *k, const void *v, const f
   if (!workspace || workspace_bytes < la::workspace(B, H, N, d_k, d_v, dt, true)) return LA_ERR_INVALID_VALUE;
   GatedGradProblem b{{q, k, v, g, lengths, S0, nullptr, nullptr, B, H, N, d_k, d_v, dt, workspace, s},
                      dout, dS, dq, dk, dv, dg, dS0};
-  return api_status(gated_tc_supported(d_k, d_v, dt) ? launch_gated_grad_tc(b) : launch_gated_grad_simt(b));
+  return api_status(gated_tc_supported(d_k, d_v, dt, true) ? launch_gated_grad_tc(b) : launch_gated_grad_simt(b));
 }
 
 la_status la_gated_decode_step(const void *q, const void *k, const void *v, const float *g, float *S, const int *slots,

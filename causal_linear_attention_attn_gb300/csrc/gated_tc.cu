@@ -28,6 +28,7 @@
 #include <cstring>
 
 #include "gated_tc.cuh"
+#include "register_shares.h"
 
 namespace la {
 namespace {
@@ -513,22 +514,30 @@ template <int D>
 cudaError_t launch_main(const Params &mp, long BH, cudaStream_t stream) {
   cudaError_t e = ensure_smem_optin((const void *)gated_tc_kernel<D>, (int)Lay<D>::Bytes);
   if (e != cudaSuccess) return e;
-  // the warpgroups' register shares add up to the launch's: with fewer they would wait forever
-  static const int regs = [] {
-    cudaFuncAttributes a;
-    return cudaFuncGetAttributes(&a, gated_tc_kernel<D>) == cudaSuccess ? a.numRegs : 0;
-  }();
-  if (regs != kRegs) return cudaErrorInvalidConfiguration;
   return launch_gated_kernel(gated_tc_kernel<D>, mp, dim3((unsigned)(BH * mp.segs)), kThreads, Lay<D>::Bytes, mp.segs > 1, kKGated,
                              stream);
 }
 
+template <int D>
+bool shares_fit() {
+  static RegisterShares shares;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  return shares.fit(dev, kRegs, [] {
+    cudaFuncAttributes a;
+    if (cudaFuncGetAttributes(&a, gated_tc_kernel<D>) == cudaSuccess) return a.numRegs;
+    cudaGetLastError();
+    return -1;
+  });
+}
+
 }  // namespace
 
-bool gated_tc_supported(int dk, int dv, la_dtype dt) {
+bool gated_tc_supported(int dk, int dv, la_dtype dt, bool grad) {
   if (dt != LA_BF16 || dk != dv || (dk != 64 && dk != 128)) return false;
   const DeviceInfo di = device_info(-1);
-  return di.cc_major == 10 && di.cc_minor == 3 && tensor_map_encoder() != nullptr;
+  if (di.cc_major != 10 || di.cc_minor != 3 || tensor_map_encoder() == nullptr) return false;
+  return grad || (dk == 64 ? shares_fit<64>() : shares_fit<128>());  // the prefill alone splits its registers
 }
 
 cudaError_t read_and_clear_gated_status(unsigned int *value) {

@@ -157,8 +157,8 @@ size_t gated_simt_workspace(long BH, long N, int dk, int dv, bool grad);
 cudaError_t launch_gated_simt(const GatedProblem &p);
 cudaError_t launch_gated_grad_simt(const GatedGradProblem &b);
 
-// The same on the tensor cores (bf16, d_k = d_v in {64, 128}, sm_103).
-bool gated_tc_supported(int dk, int dv, la_dtype dt);
+// The same on the tensor cores (bf16, d_k = d_v in {64, 128}, sm_103): whether they take a prefill, or its gradient.
+bool gated_tc_supported(int dk, int dv, la_dtype dt, bool grad);
 size_t gated_tc_prefill_workspace(long BH, long N, int d);
 size_t gated_tc_grad_workspace(long BH, long N, int d);
 cudaError_t launch_gated_tc(const GatedProblem &p);
