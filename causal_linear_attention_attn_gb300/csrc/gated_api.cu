@@ -20,6 +20,11 @@ bool aligned(std::initializer_list<const void *> ptrs, uintptr_t to) {
   return true;
 }
 
+bool overlap(const void *a, const void *b, size_t bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && (x < y ? y - x : x - y) < bytes;
+}
+
 la_status sizes(int B, int H, long N, int dk, int dv, la_dtype dt) {
   if (B < 0 || H < 0 || N < 0 || dk <= 0 || dv <= 0) return LA_ERR_INVALID_VALUE;
   // every launch indexes chunks of a head in one 31-bit grid dimension
@@ -90,11 +95,13 @@ la_status la_gated_backward(const void *q, const void *k, const void *v, const f
   if (N > 0 && (!q || !k || !v || !g || !dout || !dq || !dk || !dv || !dg)) return LA_ERR_INVALID_VALUE;
   if (!aligned({q, k, v, dout, S0, dS, dq, dk, dv, dS0}, 16) || !aligned({workspace}, 256) || !aligned({g, dg, lengths}, 4))
     return LA_ERR_MISALIGNED;
+  const size_t bytes = sizeof(float) * (size_t)B * H * d_k * d_v;
+  // the state and its gradient are walked in opposite directions, neither waits for the other
+  if ((N > 0 && overlap(S0, dS0, bytes)) || (dS != dS0 && overlap(dS, dS0, bytes))) return LA_ERR_INVALID_VALUE;
   cudaStream_t s = (cudaStream_t)stream;
   if ((st = api_device()) != LA_OK) return st;
   if (N == 0) {  // the state passes through
-    if (!dS0) return LA_OK;
-    const size_t bytes = sizeof(float) * (size_t)B * H * d_k * d_v;
+    if (!dS0 || dS0 == dS) return LA_OK;
     return api_status(dS ? cudaMemcpyAsync(dS0, dS, bytes, cudaMemcpyDeviceToDevice, s) : cudaMemsetAsync(dS0, 0, bytes, s));
   }
   if (!workspace || workspace_bytes < la::workspace(B, H, N, d_k, d_v, dt, true)) return LA_ERR_INVALID_VALUE;

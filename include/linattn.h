@@ -377,9 +377,10 @@ LA_API size_t la_gated_workspace(int B, int H, int N, int d_k, int d_v, la_dtype
  * S0 (NULL = zero): the forward's initial state.  dS (NULL = zero): gradient
  * of its final state.  Written: dq, dk: [B,H,N,d_k], dv: [B,H,N,d_v], dtype
  * dt; dg: [B,H,N] float32; dS0 (nullable): [B,H,d_k,d_v] float32, gradient of
- * the initial state, which may be dS itself.  Rows t >= lengths[b] get zero
- * gradients.  Workspace, sizes and errors as la_gated, with
- * la_gated_workspace(..., 1).
+ * the initial state, which may be dS itself.  No output may overlap an input
+ * otherwise (LA_ERR_INVALID_VALUE for dS0 on S0 or on a part of dS).  Rows
+ * t >= lengths[b] get zero gradients.  Workspace, sizes and errors as la_gated,
+ * with la_gated_workspace(..., 1).
  */
 LA_API la_status la_gated_backward(const void *q, const void *k, const void *v, const float *g,
                                    const int *lengths, const void *dout, const float *S0, const float *dS,
