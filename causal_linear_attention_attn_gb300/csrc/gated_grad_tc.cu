@@ -11,7 +11,11 @@
 //          + sum_{j < t} k_j . [2^{c_T - c_j} R v_j] + 2^{c_T} <S, R>
 // dg is an fp32 result: its first term comes from the fp32 products before any rounding, the next
 // two from dQ's and dK's first products, which take S and R as pairs, the last from the stored pairs.
-// No term is a difference of larger ones, and no error is carried from chunk to chunk.  dQ, dK and dV
+// The first term adds only pairs on both sides of t, in blocks of 32 tokens: pairs of earlier keys and
+// later queries by block, t's own block's keys and queries by row and column sums, and inside the block by
+// each key's sums over the queries from t on.  (Row sums less column sums, summed from the end, would cancel all
+// pairs behind t: a strong decay's gradient is small beside them, and a reset's is 0.)  So no term is a
+// difference of larger ones, and no error is carried from chunk to chunk.  dQ, dK and dV
 // are bf16: W D, W P and dV's R are rounded to bf16 once.
 //
 // Tensor memory holds P^T and D^T, dQ and dK; W P overwrites P^T and dV takes D^T's columns.  The
@@ -80,14 +84,15 @@ struct Params {
   const uint8_t *s_tiles, *r_tiles;
   __nv_bfloat16 *dq, *dk, *dv;
   float *dg;
-  float *mail;  // [CTAs][3][128] what each token adds to dg
+  float *mail;  // [CTAs][3][128] a token's dg inside the chunk; what it adds to those up to it, and behind it
   long N;
   uint32_t n, items;  // chunks a head, all chunks (below 2^31)
   int H;
   bool wide;  // dq, dk, dv are 32-byte aligned
 };
 
-// Partial row sums of key rows [32 q, 32 q + 32) over queries i >= 32 q, packed.
+// Place of what the keys [32 q, 32 q + 32) add to query i > 32 q + 31, packed.  The first 32 places of
+// each q hold, by key, what the other half of the queries adds.
 __device__ __forceinline__ int part_at(int q, int i) { return q * 128 - 16 * q * (q - 1) + i - 32 * q; }
 
 // Sum over the warp's lanes of x[c], returned by lanes c and c + 16.
@@ -371,14 +376,13 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
       const float *mail = p.mail + (long)blockIdx.x * 3 * kC + 4 * lane;
       const float4 s4 = __ldcg(reinterpret_cast<const float4 *>(mail)), l4 = __ldcg(reinterpret_cast<const float4 *>(mail + kC));
       const float4 r4 = __ldcg(reinterpret_cast<const float4 *>(mail + 2 * kC));
-      const float4 e4 = make_float4(s4.x + l4.x, s4.y + l4.y, s4.z + l4.z, s4.w + l4.w);
       const float over = total * ((red[0] + red[1]) + (red[2] + red[3]));
       __syncwarp();
       mbar_arrive(dot_free);
       ++it;
       if (x < p.items) ok = gates(w2, g2);  // the next chunk waits for these, nothing waits for dg
-      // suffix sums of what queries at or behind t add, prefix sums of what keys before t add
-      const float e[4] = {e4.x, e4.y, e4.z, e4.w}, r[4] = {r4.x, r4.y, r4.z, r4.w};
+      // suffix sums of what the state gives queries at or behind t, prefix sums of what keys before t give it
+      const float e[4] = {l4.x, l4.y, l4.z, l4.w}, r[4] = {r4.x, r4.y, r4.z, r4.w}, in[4] = {s4.x, s4.y, s4.z, s4.w};
       Sum2 es{0.f, 0.f}, rs{0.f, 0.f};
 #pragma unroll
       for (int m = 0; m < 4; ++m) es.add(e[m]), rs.add(r[m]);
@@ -393,6 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
         for (int k = 0; k < m; ++k) b.add(r[k]);
         v.add(b.s, b.e);
         v.add(over);
+        v.add(in[m]);
         dgv[m] = v.s + v.e;
       }
       float *dg = p.dg + w.bh * p.N + w.t0;
@@ -435,9 +440,10 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
       ok = ok && (it == 0 || mbar_wait(out_free, ph ^ 1, abort_word, status));  // W D's place is free
       if (bar_or(kBarScore, 256, !ok)) break;  // also: the last chunk's partial sums are read
       tc_fence_after();
-      // W P to tensor memory, W D to shared memory, and the sums of W P D by key and by query
+      // W P to tensor memory, W D to shared memory, and W P D's share of dg
       const float hi_j = hi[T], lo_j = lo[T];
-      float2 col = make_float2(0.f, 0.f);
+      float2 col = make_float2(0.f, 0.f);  // this key's sum over the queries of later blocks
+      float own = 0.f;                     // pairs of this block on both sides of token T
 #pragma unroll 1
       for (int b = 0; b < 4; ++b) {
         const int i0 = 64 * half + 16 * b;  // 16 queries: none of them, all, or those from the key on
@@ -469,14 +475,36 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
                 dw = make_float2(i >= T ? dw.x : 0.f, i + 1 >= T ? dw.y : 0.f);
                 m = make_float2(i > T ? m.x : 0.f, i + 1 > T ? m.y : 0.f);
               }
-              col = __fadd2_rn(col, m);
+              if (!cut) col = __fadd2_rn(col, m);
               o[c / 2] = pack_bf16(pw.x, pw.y);
               wdw[c / 2] = pack_bf16(dw.x, dw.y);
               pr[c] = __float_as_uint(m.x), pr[c + 1] = __float_as_uint(m.y);
             }
           }
+          const int sub = b & 1;  // which half of its block of 32
+          if (cut) {              // the keys' own block: for each token t of it, queries from t on of keys before t
+#pragma unroll
+            for (int c = 14; c >= 0; --c)
+              pr[c] = __float_as_uint(__uint_as_float(pr[c]) + __uint_as_float(pr[c + 1]));
+            if (sub) {  // and for the tokens of its first half, all of these queries
+              float pre = __shfl_up_sync(0xffffffffu, __uint_as_float(pr[0]), 1);
+              if (lane == 0) pre = 0.f;
+#pragma unroll
+              for (int k = 1; k < 16; k <<= 1) {
+                const float y = __shfl_up_sync(0xffffffffu, pre, k);
+                if (lane >= k) pre += y;
+              }
+              if (lane < 16) own = pre + own;
+            }
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+              if (lane >= 16 * sub + c) pr[c] = 0u;
+          }
           const float s = column_sums(pr, lane);
-          if (lane < 16) buf[part_at(q, i0 + lane)] = s;
+          if (cut)
+            own += lane >> 4 == sub ? s : 0.f;
+          else if (lane < 16)
+            buf[part_at(q, i0 + lane)] = s;
         }
         tmem_st8_nowait(tl + kColP + 64 * half + 8 * b, o);  // over columns this warp alone reads, and has read
         uint8_t *W = sm + L::WD + half * kBlk;
@@ -487,17 +515,27 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
       fence_async_smem();
       tc_fence_before();
       mbar_arrive(el_done);
-      // -(sum over later queries) + (sum over earlier keys), the two halves' column sums first
-      if (bar_or(kBarScore, 256, false)) break;
-      float ends = -(col.x + col.y);
-      float row = 0.f;
-      if (half == 0)
-        for (int k = 0; k <= q; ++k) row += buf[part_at(k, T)];
+      // token T's dg inside the chunk, by the half that has its block
+      const bool mine = half == q >> 1;
+      if (!mine) buf[part_at(q, T)] = col.x + col.y;
       named_bar(kBarScore, 256);
-      if (half == 1) buf[T] = ends;
-      named_bar(kBarScore, 256);
-      if (half == 0) {
-        __stcg(mail + T, row + ends + buf[T]);
+      if (mine) {
+        const float keys = (col.x + col.y) + buf[part_at(q, T)];
+        float row = 0.f, across = 0.f;  // of this query from earlier blocks; of later blocks' queries from earlier blocks' keys
+        for (int k = 0; k < q; ++k) {
+          row += buf[part_at(k, T)];
+          for (int i = T + 32; i < kC; i += 32) across += buf[part_at(k, i)];
+        }
+        // queries from T on, keys before T
+        float before = __shfl_up_sync(0xffffffffu, keys, 1);
+        if (lane == 0) before = 0.f;
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) {
+          const float r = __shfl_down_sync(0xffffffffu, row, k), u = __shfl_up_sync(0xffffffffu, before, k);
+          if (lane + k < 32) row += r;
+          if (lane >= k) before += u;
+        }
+        __stcg(mail + T, (own + warp_sum(across)) + (row + before));
         mbar_arrive(dg_in);
       }
       ++it;

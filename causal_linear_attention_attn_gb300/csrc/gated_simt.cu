@@ -316,9 +316,17 @@ __device__ __forceinline__ void chunk_grad(const Args &a, float *sm, long item, 
     const int i = e / kT, j = e % kT, x = i * kTp + j;
     const float w = j <= i ? exp2f((hi[i] - hi[j]) + (lo[i] - lo[j])) : 0.f;
     const float p = j <= i ? P[x] : 0.f, d = j <= i ? D[x] * w : 0.f;
-    M[i * (kT + 1) + j] = j < i ? p * d : 0.f;
     P[x] = p * w;
     D[x] = d;
+    // M[i][t]: the query's sum over the keys before t (a warp has a row)
+    float m = j < i ? p * d : 0.f;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float y = __shfl_up_sync(0xffffffffu, m, o);
+      if (j >= o) m += y;
+    }
+    M[i * (kT + 1) + j + 1] = m;
+    if (j == 0) M[i * (kT + 1)] = 0.f;
   }
   __syncthreads();
 
@@ -384,12 +392,13 @@ __device__ __forceinline__ void chunk_grad(const Args &a, float *sm, long item, 
   }
   __syncthreads();
   if (tid < 32) {
+    // pairs in the chunk on both sides of token `lane`: keys before it (summed above), queries from it on
+    // (row sums less column sums, added from the end, would cancel all pairs behind it)
+    float in = 0.f;
+#pragma unroll
+    for (int i = 0; i < kT; ++i) in += i >= lane ? M[i * (kT + 1) + lane] : 0.f;
     // what token `lane` adds to every dg_t with t <= lane, and with t > lane
     Sum2 ends{0.f, 0.f}, rgt{0.f, 0.f};
-    for (int j = 0; j < kT; ++j) {
-      ends.add(M[lane * (kT + 1) + j]);
-      ends.add(-M[j * (kT + 1) + lane]);
-    }
     for (int x = 0; x < kq; ++x) {
       ends.add(left[lane * 33 + x]);
       rgt.add(right[lane * 33 + x]);
@@ -401,6 +410,7 @@ __device__ __forceinline__ void chunk_grad(const Args &a, float *sm, long item, 
     all.add(ends.s, ends.e);
     all.add(upto.s, upto.e);
     all.add(total * over);
+    all.add(in);
     if (lane < rows) dg[lane] = lane < tv ? all.s + all.e : 0.f;
   }
 }
