@@ -5,29 +5,32 @@
 
 namespace la {
 
-// Running sums of log2 decays, in 64-bit fixed point with 40 fraction bits: a chunk full of resets
-// sums to 128 * 173, where fp32 resolves 2^-9 only, and the FP64 unit of this GPU is slow enough to
+// Running sums of log2 decays, in 64-bit fixed point with 40 fraction bits: a chunk full of strong decays
+// sums to 128 * 150, where fp32 resolves 2^-9 only, and the FP64 unit of this GPU is slow enough to
 // set the pace of a whole kernel (a warp's scan of 128 doubles took 8000 cycles, this one under 1000).
 //
-// e^g below e^-120 is zero in fp32, and so is every product of it with a state the recurrence could
-// hold; clamping there gives the same results and keeps differences of sums finite (a log decay of
-// -inf, i.e. a reset of the state, would give inf - inf).  Above e^120 it is inf in fp32 as well.
+// A decay that is zero in fp32 (e^-104 < 2^-150; a log decay of -inf among them) is a cut: the recurrence
+// reads nothing across it, whatever follows.  It counts as 2^-32768: decays above e^120 are taken as that
+// (inf in fp32 as well), so the 127 other tokens of a chunk grow by 2^21986 at most, and every weight across a
+// cut is zero.  The state, which may be inf or NaN, is dropped there and not multiplied by zero.
+// (The floats are chosen from, not the sums: choosing between those cost 3 of the prefill's 148 us.)
+__device__ __forceinline__ bool is_cut(float g) { return g < -104.f; }
 __device__ __forceinline__ long long fixed_log2_decay(float g) {
-  const float x = fminf(fmaxf(g, -120.f), 120.f);  // a NaN is dealt with apart (nan_before)
+  const float x = is_cut(g) ? -22713.f : fminf(g, 120.f);  // a NaN is dealt with apart (split_cum)
   const float l2e = 1.44269504f, l2e_lo = 1.92596303e-8f;  // log2(e) in two parts
   const float p = x * l2e, e = fmaf(x, l2e_lo, fmaf(x, l2e, -p));
   return __float2ll_rn(p * 1099511627776.f) + __float2ll_rn(e * 1099511627776.f);
 }
 
-// A sum as hi (a multiple of 1/64, exact in fp32) plus lo, so that (hi_i - hi_j) + (lo_i - lo_j) is
-// c_i - c_j to 2^-30.
+// A sum as hi (a multiple of 1/4, exact in fp32: 128 cuts are 2^22) plus lo, so that
+// (hi_i - hi_j) + (lo_i - lo_j) is c_i - c_j to 2^-27.
 struct Cum {
   float hi, lo;
 };
 __device__ __forceinline__ Cum split_cum(long long c, bool nan) {
-  const int h = (int)((c + (1ll << 33)) >> 34);
-  const int rem = (int)((c - ((long long)h << 34)) >> 3);
-  return Cum{nan ? __int_as_float(0x7fffffff) : (float)h * 0.015625f, (float)rem * 7.275957614183426e-12f};
+  const int h = (int)((c + (1ll << 37)) >> 38);
+  const int rem = (int)((c - ((long long)h << 38)) >> 7);
+  return Cum{nan ? __int_as_float(0x7fffffff) : (float)h * 0.25f, (float)rem * 1.1641532182693481e-10f};
 }
 
 __device__ __forceinline__ long long warp_scan(long long x, int lane) {

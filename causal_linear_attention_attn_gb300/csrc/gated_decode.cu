@@ -57,6 +57,10 @@ __global__ void __launch_bounds__(kThreads) gated_decode_kernel(const __grid_con
     if (tid < DV / 4) st4(out + 4 * tid, 0.f, 0.f, 0.f, 0.f);
     return;
   }
+  if (a == 0.f) {  // a cut: the state may be anything, a slot that was never written among others
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) s[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
   const float4 vq = reinterpret_cast<const float4 *>(vv)[cq];
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll

@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
       const float *mail = p.mail + (long)blockIdx.x * 3 * kC + 4 * lane;
       const float4 s4 = __ldcg(reinterpret_cast<const float4 *>(mail)), l4 = __ldcg(reinterpret_cast<const float4 *>(mail + kC));
       const float4 r4 = __ldcg(reinterpret_cast<const float4 *>(mail + 2 * kC));
-      const float over = total * ((red[0] + red[1]) + (red[2] + red[3]));
+      const float over = total == 0.f ? 0.f : total * ((red[0] + red[1]) + (red[2] + red[3]));
       __syncwarp();
       mbar_arrive(dot_free);
       ++it;

@@ -144,7 +144,7 @@ __device__ __forceinline__ void chunk_scan_states(const Args &a, long bh, long e
     for (int u = 0; u < kAhead; ++u)
       if (c0 + u < n) {
         *at = s;
-        s = fmaf(f[u], s, x[u]);
+        s = f[u] == 0.f ? x[u] : fmaf(f[u], s, x[u]);
         at += step;
       }
     tot += kAhead * dt;
@@ -176,9 +176,9 @@ __device__ __forceinline__ void tile_dots(float *X, const float *A, const float 
 __device__ __forceinline__ void fma4(float (&acc)[4], float u, float4 y) {
   acc[0] = fmaf(u, y.x, acc[0]), acc[1] = fmaf(u, y.y, acc[1]), acc[2] = fmaf(u, y.z, acc[2]), acc[3] = fmaf(u, y.w, acc[3]);
 }
-__device__ __forceinline__ void scale(float (&acc)[4], float f) {
+__device__ __forceinline__ void scale(float (&acc)[4], float f) {  // across a cut: nothing, not even a NaN
 #pragma unroll
-  for (int m = 0; m < 4; ++m) acc[m] *= f;
+  for (int m = 0; m < 4; ++m) acc[m] = f == 0.f ? 0.f : acc[m] * f;
 }
 
 // acc[r][m] += sum_x A[i + r][x] M[x][c + m], four x at a time (dx a multiple of 4).
@@ -409,7 +409,7 @@ __device__ __forceinline__ void chunk_grad(const Args &a, float *sm, long item, 
     const Sum2 upto = warp_scan_others<false>(rgt, lane);
     all.add(ends.s, ends.e);
     all.add(upto.s, upto.e);
-    all.add(total * over);
+    all.add(total == 0.f ? 0.f : total * over);
     all.add(in);
     if (lane < rows) dg[lane] = lane < tv ? all.s + all.e : 0.f;
   }
@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 2) gated_simt_kernel(const __grid_co
         const float *first = kGrad ? dS : S0;
         const float f = rows ? a.tot[bh] : 1.f;
         for (long e = threadIdx.x; e < dd; e += kThreads)
-          last[bh * dd + e] = fmaf(f, first ? first[e] : 0.f, rows ? sum[e] : 0.f);
+          last[bh * dd + e] = fmaf(f, first && f != 0.f ? first[e] : 0.f, rows ? sum[e] : 0.f);
       }
     }
     return;

@@ -242,15 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_state_tc_kernel(const __gri
           const float *hi = gate + (i & 1) * 2 * kC;
           const float f = exp2f(hi[kC - 1] + hi[2 * kC - 1]);
           mbar_arrive(&gate_free[i & 1]);
-#pragma unroll
-          for (int b = 0; b < kB; ++b)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t y[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(r[b][16 * h + e]) * f);
-              tmem_st16_nowait(tx + 32 * b + 16 * h, y);
-            }
+          tmem_st_scaled(tx, r, f);
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(x_ready);
@@ -317,10 +309,11 @@ __global__ void __launch_bounds__(kThreads, 1) gated_state_tc_kernel(const __gri
     const float *g = p.g + bh * p.N;
     float4 cur = make_float4(0.f, 0.f, 0.f, 0.f);
     // kSum: decay of the chunks taken so far, which is what lies between this chunk and the segment's
-    // end; held at -2^15, far below where weights vanish
+    // end.  Behind a cut, or below 2^-32768, nothing comes back: it stays at 2^-65536, whatever the chunks
+    // that follow.  Growth is held at 2^8192, inf as well, which a cut of a chunk's own still outweighs.
     long long beyond = 0;
-    bool beyond_nan = false;
-    constexpr long long kFloor = -(1ll << 55);
+    bool beyond_nan = false, gone = false;
+    constexpr long long kLeast = -(1ll << 55), kGone = -(1ll << 56), kMost = 1ll << 53;
     if (run > 0) cur = load_gates(g + chunk(0) * kC, valid(0), lane);
     for (int i = 0; i < run; ++i) {
       float4 nxt = cur;
@@ -334,12 +327,13 @@ __global__ void __launch_bounds__(kThreads, 1) gated_state_tc_kernel(const __gri
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           u.c[e] = beyond + (dir ? u.c[e] : all - u.c[e]);
-          u.nan[e] = beyond_nan || (dir ? u.nan[e] : all_nan);
+          u.nan[e] = !gone && (beyond_nan || (dir ? u.nan[e] : all_nan));
         }
         store_cums(u.c, u.nan, lane, hi, hi + kC);
+        beyond_nan = !gone && (beyond_nan || all_nan);
         beyond += all;
-        if (beyond < kFloor) beyond = kFloor;
-        beyond_nan = beyond_nan || all_nan;
+        gone = gone || __any_sync(0xffffffffu, u.cut) || beyond < kLeast;
+        beyond = gone ? kGone : min(beyond, kMost);
       } else {
         scan_gates(cur, lane, hi, hi + kC);
       }
@@ -393,6 +387,7 @@ __global__ void __launch_bounds__(kScanThreads) gated_seg_scan_kernel(const __gr
       if (i >= a.segs) break;
       *reinterpret_cast<float4 *>(at + (long)g * a.dd) = s;
       const float f = exp2f(w[u]);
+      if (f == 0.f) s = make_float4(0.f, 0.f, 0.f, 0.f);  // a cut: not even a NaN stays
       s = make_float4(fmaf(f, s.x, x[u].x), fmaf(f, s.y, x[u].y), fmaf(f, s.z, x[u].z), fmaf(f, s.w, x[u].w));
     }
   }

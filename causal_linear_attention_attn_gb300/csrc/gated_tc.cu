@@ -362,13 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
           load_init(cb);
         else
           tmem_ld32x2(tS + cb * 64, tS + cb * 64 + 32, r[0], r[1]);
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          uint32_t y[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(r[h >> 1][16 * (h & 1) + e]) * f);
-          tmem_st16_nowait(tS + cb * 64 + 16 * h, y);
-        }
+        tmem_st_scaled(tS + cb * 64, r, f);
         if (cb == 0 && c > 0) {  // the last read of the copy is done
           const bool qw = mbar_wait(q_free, (c - 1) & 1, abort_word, status);
           if (bar_or(kBarS, 128, !qw)) {
@@ -441,8 +435,8 @@ __global__ void __launch_bounds__(kThreads, 1) gated_tc_kernel(const __grid_cons
           tmem_ld16x2(tl + kColI + cb * 32 + 16 * h, tl + kColA + cb * 32 + 16 * h, x, y);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float2 z = __ffma2_rn(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), make_float2(f, f),
-                                        make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])));
+            const float2 z = add_scaled(make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])),
+                                        make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), f);
             ow[8 * h + e] = pack_bf16(z.x, z.y);
           }
         }

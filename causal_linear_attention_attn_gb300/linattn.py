@@ -456,8 +456,8 @@ def la_gated_decode_step(q, k, v, g, S, slots=None, out=None, stream=None):
     """One gated step; q, k [B, H, d_k], v [B, H, d_v], g [B, H]; returns out [B, H, d_v] in q's dtype.
 
     S [n_slots, H, d_k, d_v] is a pool of states: row b works in place on S[slots[b]] (slots [B] int32; without it,
-    row b on S[b]).  A negative slot marks an unused row (out zero).  A slot out of range or repeated in the batch
-    is skipped too, and the next device_status() is 1.
+    row b on S[b]).  g = -inf starts a state anew, whatever its slot held.  A negative slot marks an unused row (out
+    zero).  A slot out of range or repeated in the batch is skipped too, and the next device_status() is 1.
     """
     dev, (B, H), dk, dv, dt = _gated_inputs(q, k, v, g, 3)
     if not isinstance(S, torch.Tensor) or S.dim() != 4:

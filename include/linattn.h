@@ -331,9 +331,16 @@ LA_API la_status la_retention_decode_step(const void *q, const void *k, const vo
  *
  * q, k: [B,H,N,d_k]; v, out: [B,H,N,d_v], all of dtype dt (out too, unlike
  * the normalized forms: the next layer takes the inputs' type).  g:
- * [B,H,N] float32 DEVICE array of natural-log decays, meant to be <= 0; -inf
- * resets the state (nothing before the token is read at or after it), and a
- * positive value grows it.  S: [B,H,d_k,d_v] float32, OVERWRITTEN with the
+ * [B,H,N] float32 DEVICE array of natural-log decays, meant to be <= 0.  -inf,
+ * and everything below -104 (e^g is zero in float32), resets the state: nothing
+ * before the token is read at or after it, whatever the state held and however
+ * later decays grow it.  A positive value grows the state; where the growth of
+ * up to 128 tokens passes float32's range, or after a decay that is NaN, results
+ * may be inf or NaN until a reset in a later chunk.  Chunks are 128 tokens (32 off
+ * the tensor cores), and a masked product in one is a product with zero: q, k, v
+ * and dout have to be finite, an inf or NaN among them may reach every result of
+ * its chunk, those of earlier tokens and behind a reset included.
+ * S: [B,H,d_k,d_v] float32, OVERWRITTEN with the
  * final state.  lengths: [B] int32 DEVICE array or NULL (every row has N
  * tokens): tokens t >= lengths[b] of batch row b take no part, whatever they
  * hold; out is left as it was there and S is the state after the last token
@@ -394,7 +401,8 @@ LA_API la_status la_gated_backward(const void *q, const void *k, const void *v, 
  *     S = e^{g} S + k v^T;   out = q^T S,   S the state of row b's slot.
  * q, k: [B,H,d_k]; v, out: [B,H,d_v], dtype dt; g: [B,H] float32.  S:
  * [n_slots,H,d_k,d_v] float32, the slots of this batch read and written IN
- * PLACE, the others untouched.  slots: [B] int32 DEVICE array or NULL (row b
+ * PLACE, the others untouched.  A g below -104 (-inf) starts the state anew, also
+ * in a slot that was never written.  slots: [B] int32 DEVICE array or NULL (row b
  * uses slot b; n_slots >= B).  A negative slot marks an unused row: no state
  * is touched and its out is zero.  A slot >= n_slots, or one that an earlier
  * row of the batch has, is treated the same way and also makes the next
