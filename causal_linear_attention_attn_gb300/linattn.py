@@ -311,6 +311,13 @@ def la_causal_backward(q, k, v, dout, S0=None, z0=None, dS=None, dz=None, need_s
     return (dq, dkk, dvv, dS0, dz0) if need_state_grad else (dq, dkk, dvv)
 
 
+# The current device and a device's current stream without the public calls' wrappers (host time counts in small
+# calls); where torch does not have these, the public calls.
+_device_index = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _on(device, stream):
     """(stream handle, context to leave) of a call on `device`: the given stream, or that device's current one.
 
@@ -318,8 +325,8 @@ def _on(device, stream):
     Entering a context is needed only for another stream or device than the current ones.
     """
     if stream is None:
-        if device.index == torch._C._cuda_getDevice():
-            return torch._C._cuda_getCurrentRawStream(device.index), None
+        if device.index == _device_index():
+            return _stream_handle(device.index), None
         stream = torch.cuda.current_stream(device)
     elif not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else torch.cuda.default_stream(device)
