@@ -22,14 +22,11 @@
 // first products are scaled by row in tensor memory, then the second ones accumulate on top.
 // HBM bounds it at 14 D bytes a token of inputs and results plus 8 D of states (D = 128: 8.1 us a
 // chunk at an SM's share); the tensor work is 13 products of 128 x 128 x D.  Measured at 4 x 16 x 8192,
-// D = 128: 255 us (5.7 TB/s); without the score warps' work it takes as long, without the second
+// D = 128: 260 us (5.6 TB/s), of which dg's pairs by blocks take 4 and the test for cuts 2; before them, without
+// the score warps' work it took as long, without the second
 // reading of the states for <S, R> (from L2) 34 us less.  At D = 64 a chunk's chain of steps bounds it,
 // 16000 cycles; two chunks' tokens in shared memory and a place for results beside W D's, for which
 // there is room, took 3 % off and were not kept.
-//
-// Every warp runs its code once a chunk, out of a cold instruction cache (the first of a score warp's
-// four equal turns takes 4000 cycles, the others 1500): less code is faster.  32-bit quotients in place
-// of 64-bit ones took 269 to 258 us, turns of a loop unrolled by two 280.
 //
 // Two chunks overlap: the score warps weigh a chunk's products while the row warps still write the
 // previous chunk's results; the score columns are free for it as soon as dV is read.
@@ -68,7 +65,7 @@ struct Lay {
   static constexpr uint32_t Buf = Gate + 2 * kC * 4;     // 320 floats
   static constexpr uint32_t Red = Buf + 320 * 4;         // 4 floats
   static constexpr uint32_t Bars = Red + 16;
-  static constexpr int kNumBars = 3 + 2 * kRing + 15;
+  static constexpr int kNumBars = 3 + 2 * kRing + 16;
   static constexpr uint32_t Misc = Bars + kNumBars * 8;
   static constexpr uint32_t Bytes = Misc + 16;
 };
@@ -84,7 +81,7 @@ struct Params {
   const uint8_t *s_tiles, *r_tiles;
   __nv_bfloat16 *dq, *dk, *dv;
   float *dg;
-  float *mail;  // [CTAs][3][128] a token's dg inside the chunk; what it adds to those up to it, and behind it
+  float *mail;  // [CTAs][4][128] a token's dg inside the chunk, two chunks in turn; what it adds to those up to it, and behind it
   long N;
   uint32_t n, items;  // chunks a head, all chunks (below 2^31)
   int H;
@@ -150,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
            *b0 = ring_free + kRing, *tok_free = b0, *gate_full = b0 + 1, *e_full = b0 + 2, *el_done = b0 + 3,
            *q_in = b0 + 4, *k_in = b0 + 5, *v_in = b0 + 6, *x_ready = b0 + 7, *out_full = b0 + 8, *out_free = b0 + 9,
            *dg_in = b0 + 10, *dot_full = b0 + 11, *dot_free = b0 + 12,
-           *v_free = b0 + 13, *d_free = b0 + 14;
+           *v_free = b0 + 13, *d_free = b0 + 14, *in_full = b0 + 15;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::Misc);
   volatile uint32_t *abort_word = reinterpret_cast<volatile uint32_t *>(sm + L::Misc + 4);
   uint64_t *drain = reinterpret_cast<uint64_t *>(sm + L::Misc + 8);
@@ -179,7 +176,8 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
     mbar_init(out_full, 1);
     mbar_init(out_free, 256);
     mbar_init(d_free, 256);
-    mbar_init(dg_in, 256 + 128);
+    mbar_init(dg_in, 256 + 256);
+    mbar_init(in_full, 128);
     mbar_init(dot_full, 4);
     mbar_init(dot_free, 32);
     mbar_init(drain, 1);
@@ -373,14 +371,15 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
       float4 g2 = make_float4(0.f, 0.f, 0.f, 0.f);
       if (x < p.items) w2 = item(x), g2 = fetch(w2);
       if (!warp_wait(dg_in, it & 1, abort_word) || !warp_wait(dot_full, it & 1, abort_word)) break;
-      const float *mail = p.mail + (long)blockIdx.x * 3 * kC + 4 * lane;
-      const float4 s4 = __ldcg(reinterpret_cast<const float4 *>(mail)), l4 = __ldcg(reinterpret_cast<const float4 *>(mail + kC));
-      const float4 r4 = __ldcg(reinterpret_cast<const float4 *>(mail + 2 * kC));
+      const float *mail = p.mail + (long)blockIdx.x * 4 * kC + 4 * lane;
+      const float4 l4 = __ldcg(reinterpret_cast<const float4 *>(mail + 2 * kC)), r4 = __ldcg(reinterpret_cast<const float4 *>(mail + 3 * kC));
       const float over = total == 0.f ? 0.f : total * ((red[0] + red[1]) + (red[2] + red[3]));
       __syncwarp();
       mbar_arrive(dot_free);
       ++it;
       if (x < p.items) ok = gates(w2, g2);  // the next chunk waits for these, nothing waits for dg
+      if (!warp_wait(in_full, (it - 1) & 1, abort_word)) break;
+      const float4 s4 = __ldcg(reinterpret_cast<const float4 *>(mail + ((it - 1) & 1) * kC));
       // suffix sums of what the state gives queries at or behind t, prefix sums of what keys before t give it
       const float e[4] = {l4.x, l4.y, l4.z, l4.w}, r[4] = {r4.x, r4.y, r4.z, r4.w}, in[4] = {s4.x, s4.y, s4.z, s4.w};
       Sum2 es{0.f, 0.f}, rs{0.f, 0.f};
@@ -431,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
     // ---- scores: key T (lane) against 64 queries ----
     const int q = warp & 3, half = (warp - kWarpScore) >> 2, T = q * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16);
-    float *mail = p.mail + (long)blockIdx.x * 3 * kC;
+    float *mail = p.mail + (long)blockIdx.x * 4 * kC;
     int it = 0;
     for (uint32_t x = blockIdx.x; x < p.items; x += gridDim.x) {
       if (item(x).tv == 0) continue;
@@ -515,6 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
       fence_async_smem();
       tc_fence_before();
       mbar_arrive(el_done);
+      mbar_arrive(dg_in);  // the running sums are read; what follows has time until the next chunk's
       // token T's dg inside the chunk, by the half that has its block
       const bool mine = half == q >> 1;
       if (!mine) buf[part_at(q, T)] = col.x + col.y;
@@ -535,8 +535,8 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
           if (lane + k < 32) row += r;
           if (lane >= k) before += u;
         }
-        __stcg(mail + T, (own + warp_sum(across)) + (row + before));
-        mbar_arrive(dg_in);
+        __stcg(mail + ph * kC + T, (own + warp_sum(across)) + (row + before));
+        mbar_arrive(in_full);
       }
       ++it;
     }
@@ -546,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
     const int q = warp & 3, half = (warp - kWarpRow) >> 2, T = q * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16), tX = tl + (half ? kColK : kColQ);
     const uint8_t *X = sm + (half ? L::K : L::Q);
-    float *mail = p.mail + (long)blockIdx.x * 3 * kC + (1 + half) * kC;
+    float *mail = p.mail + (long)blockIdx.x * 4 * kC + (2 + half) * kC;
     __nv_bfloat16 *dx = half ? p.dk : p.dq;
     int it = 0;
     for (uint32_t x = blockIdx.x; x < p.items; x += gridDim.x) {
@@ -567,6 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
       const float ew = exp2f((hi[kC - 1] - hi[T]) + (lo[kC - 1] - lo[T])), f = half ? ew : exp2f(hi[T] + lo[T]);
       if (!warp_wait(half ? k_in : q_in, ph, abort_word)) break;
       tc_fence_after();
+      drop_cut_rows(tX, D, f);
       float dot = 0.f;
 #pragma unroll 1
       for (int cb = 0; cb < D / 32; ++cb) {
@@ -580,6 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
       mbar_arrive(dg_in);
       if (!warp_wait(v_in, ph, abort_word)) break;
       tc_fence_after();
+      drop_cut_rows(tl + kColD + half * (D / 2), D / 2, ew);
 #pragma unroll
       for (int cb = 0; cb < D / 64; ++cb) {
         uint32_t r[32];
@@ -676,7 +678,7 @@ cudaError_t read_and_clear_gated_grad_status(unsigned int *value) {
 size_t gated_tc_grad_workspace(long BH, long N, int D) {
   const Plan t = make_plan(BH, N, D);
   const size_t tiles = 2 * (size_t)BH * t.n * gated_tile_bytes(D);
-  const size_t mail = sizeof(float) * 3 * kC * std::max(1, device_info(-1).sm_count);
+  const size_t mail = sizeof(float) * 4 * kC * std::max(1, device_info(-1).sm_count);
   return tiles + mail + (t.segs > 1 ? sizeof(float) * (size_t)BH * t.segs * (2 * (size_t)D * D + 1) : 0);
 }
 
@@ -685,7 +687,7 @@ cudaError_t launch_gated_grad_tc(const GatedGradProblem &b) {
   const int D = p.dk;
   const long BH = p.BH();
   const Plan t = make_plan(BH, p.N, D);
-  const size_t mail = sizeof(float) * 3 * kC * std::max(1, device_info(-1).sm_count);
+  const size_t mail = sizeof(float) * 4 * kC * std::max(1, device_info(-1).sm_count);
   uint8_t *ws = (uint8_t *)p.ws + mail;
   const size_t tiles = (size_t)BH * t.n * gated_tile_bytes(D);
   GatedStateParams sp;
