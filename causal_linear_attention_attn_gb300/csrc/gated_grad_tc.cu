@@ -22,11 +22,14 @@
 // first products are scaled by row in tensor memory, then the second ones accumulate on top.
 // HBM bounds it at 14 D bytes a token of inputs and results plus 8 D of states (D = 128: 8.1 us a
 // chunk at an SM's share); the tensor work is 13 products of 128 x 128 x D.  Measured at 4 x 16 x 8192,
-// D = 128: 260 us (5.6 TB/s), of which dg's pairs by blocks take 4 and the test for cuts 2; before them, without
-// the score warps' work it took as long, without the second
-// reading of the states for <S, R> (from L2) 34 us less.  At D = 64 a chunk's chain of steps bounds it,
-// 16000 cycles; two chunks' tokens in shared memory and a place for results beside W D's, for which
-// there is room, took 3 % off and were not kept.
+// D = 128: 260 us (5.6 TB/s).  Of these dg's pairs by blocks take 4 and the test for cuts 2; before these two
+// it took as long without the score warps' work, and 34 us less without the second reading of the states for
+// <S, R> (from L2).  At D = 64 a chunk's chain of steps bounds it, 16000 cycles; two chunks' tokens in shared
+// memory and a place for results beside W D's, for which there is room, took 3 % off and were not kept.
+//
+// Every warp runs its code once a chunk, out of a cold instruction cache (the first of a score warp's
+// four equal turns takes 4000 cycles, the others 1500): less code is faster.  32-bit quotients in place
+// of 64-bit ones took 269 to 258 us, turns of a loop unrolled by two 280.
 //
 // Two chunks overlap: the score warps weigh a chunk's products while the row warps still write the
 // previous chunk's results; the score columns are free for it as soon as dV is read.
@@ -81,7 +84,7 @@ struct Params {
   const uint8_t *s_tiles, *r_tiles;
   __nv_bfloat16 *dq, *dk, *dv;
   float *dg;
-  float *mail;  // [CTAs][4][128] a token's dg inside the chunk, two chunks in turn; what it adds to those up to it, and behind it
+  float *mail;  // [CTAs][4][128] a token's dg inside the chunk (two chunks in turn), what it adds up to it, and behind it
   long N;
   uint32_t n, items;  // chunks a head, all chunks (below 2^31)
   int H;
@@ -650,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
 struct Plan {
   long n, segs, seg_chunks;
 };
-Plan make_plan(long BH, long N, int D) {
+Plan make_plan(long BH, long N) {
   const long slots = std::max(1, device_info(-1).sm_count), ctas = BH * 2;
   Plan t;
   t.n = (N + kC - 1) / kC;
@@ -676,7 +679,7 @@ cudaError_t read_and_clear_gated_grad_status(unsigned int *value) {
 }
 
 size_t gated_tc_grad_workspace(long BH, long N, int D) {
-  const Plan t = make_plan(BH, N, D);
+  const Plan t = make_plan(BH, N);
   const size_t tiles = 2 * (size_t)BH * t.n * gated_tile_bytes(D);
   const size_t mail = sizeof(float) * 4 * kC * std::max(1, device_info(-1).sm_count);
   return tiles + mail + (t.segs > 1 ? sizeof(float) * (size_t)BH * t.segs * (2 * (size_t)D * D + 1) : 0);
@@ -686,7 +689,7 @@ cudaError_t launch_gated_grad_tc(const GatedGradProblem &b) {
   const GatedProblem &p = b.p;
   const int D = p.dk;
   const long BH = p.BH();
-  const Plan t = make_plan(BH, p.N, D);
+  const Plan t = make_plan(BH, p.N);
   const size_t mail = sizeof(float) * 4 * kC * std::max(1, device_info(-1).sm_count);
   uint8_t *ws = (uint8_t *)p.ws + mail;
   const size_t tiles = (size_t)BH * t.n * gated_tile_bytes(D);

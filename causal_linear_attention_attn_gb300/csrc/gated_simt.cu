@@ -25,7 +25,7 @@
 // one thread for an element of the state; each chunk's outputs or gradients.  The states between the
 // phases cost 4 dk dv / T bytes per token each way; in exchange a single long sequence fills the
 // device, where one CTA per head would leave it idle.  Measured in fp32, whole calls: 2 x 4 x 4096
-// tokens at d = 64 in 69 us and the gradient in 170 us (shared-memory reads of the products),
+// tokens at d = 64 in 71 us and the gradient in 161 us (shared-memory reads of the products),
 // 1 x 1 x 16384 in 69 and 121 us (the scan's rounds of loads), 4 x 4 x 300 in 24 and 50 us (latency
 // of a chunk's loops).
 #include <cooperative_groups.h>
@@ -415,8 +415,8 @@ __device__ __forceinline__ void chunk_grad(const Args &a, float *sm, long item, 
   }
 }
 
-// Two blocks an SM: the gradient then spills 4 bytes, and takes 170 us at 2 x 4 x 4096, d = 64, where
-// one block and all its registers take 220.
+// Two blocks an SM, 128 registers a thread (the prefill spills 4 bytes): the gradient took 170 us at
+// 2 x 4 x 4096, d = 64, where one block and all its registers took 220.
 template <typename Tin, bool kGrad>
 __global__ void __launch_bounds__(kThreads, 2) gated_simt_kernel(const __grid_constant__ Args a, long BH) {
   extern __shared__ float sm[];

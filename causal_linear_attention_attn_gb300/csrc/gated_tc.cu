@@ -17,7 +17,7 @@
 // HBM is its floor (8 D bytes per token in and out, 40 flops a byte at D = 128); built, a chunk takes
 // about 5500 cycles, of which the one thread that issues its 40 MMAs is busy for most: they take 64
 // cycles each alone and about twice that beside 26 busy warps.  Measured at 4 x 16 x 8192, D = 128:
-// 101 us for this pass (5.3 TB/s of its bytes), 148 us with the state pass and scan before it.
+// 102 us for this pass (5.3 TB/s of its bytes), 149 us with the state pass and scan before it.
 //
 // Warps: 0 TMA, 1 MMA and TMEM owner, 2 running sums, 4-11 weights of the scores, 12-19 weighted keys,
 // 20-23 state (bf16 copy, decay), 24-27 outputs.  Every wait is bounded (tc_ptx.cuh).
@@ -480,7 +480,7 @@ struct Plan {
   long init_segs() const { return (G - 1) * step + 1; }
   bool split() const { return G > 1; }
 };
-Plan make_plan(long BH, long N, int D) {
+Plan make_plan(long BH, long N) {
   const long sms = std::max(1, device_info(-1).sm_count);
   Plan t;
   t.n = (N + kC - 1) / kC;
@@ -539,14 +539,14 @@ cudaError_t read_and_clear_gated_status(unsigned int *value) {
 }
 
 size_t gated_tc_prefill_workspace(long BH, long N, int D) {
-  const Plan t = make_plan(BH, N, D);
+  const Plan t = make_plan(BH, N);
   return t.split() ? sizeof(float) * (size_t)BH * t.init_segs() * ((size_t)D * D + 1) : 0;
 }
 
 cudaError_t launch_gated_tc(const GatedProblem &p) {
   const int D = p.dk;
   const long BH = p.BH();
-  const Plan t = make_plan(BH, p.N, D);
+  const Plan t = make_plan(BH, p.N);
   Params mp;
   memset(&mp, 0, sizeof mp);
   if (!gated_map(&mp.tq, p.q, BH, p.N, D, kC) || !gated_map(&mp.tk, p.k, BH, p.N, D, kC) ||

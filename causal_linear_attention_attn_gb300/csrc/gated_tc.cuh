@@ -234,7 +234,7 @@ __device__ __forceinline__ void scale32(uint32_t (&r)[32], float f) {
 }
 
 // Rows whose factor is zero, which is a cut, cleared: times zero an inf or a NaN would stay.  (A test in
-// scale32 costs the gradient 10 us of 254 where no row is cut, one for all of a row's columns nothing.)
+// scale32 cost the gradient's chunks 10 us of 254 where no row is cut, one for all of a row's columns 2.)
 __device__ __forceinline__ void drop_cut_rows(uint32_t taddr, int columns, float f) {
   if (!__any_sync(0xffffffffu, f == 0.f)) return;
 #pragma unroll 1
