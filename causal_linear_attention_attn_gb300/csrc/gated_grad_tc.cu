@@ -68,7 +68,7 @@ struct Lay {
   static constexpr uint32_t Buf = Gate + 2 * kC * 4;     // 320 floats
   static constexpr uint32_t Red = Buf + 320 * 4;         // 4 floats
   static constexpr uint32_t Bars = Red + 16;
-  static constexpr int kNumBars = 3 + 2 * kRing + 16;
+  static constexpr int kNumBars = 3 + 2 * kRing + 17;
   static constexpr uint32_t Misc = Bars + kNumBars * 8;
   static constexpr uint32_t Bytes = Misc + 16;
 };
@@ -180,7 +180,8 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
     mbar_init(out_free, 256);
     mbar_init(d_free, 256);
     mbar_init(dg_in, 256 + 256);
-    mbar_init(in_full, 128);
+    mbar_init(&in_full[0], 128);  // by parity: the gate warp may still have a chunk to wait for when the next is through
+    mbar_init(&in_full[1], 128);
     mbar_init(dot_full, 4);
     mbar_init(dot_free, 32);
     mbar_init(drain, 1);
@@ -381,8 +382,9 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
       mbar_arrive(dot_free);
       ++it;
       if (x < p.items) ok = gates(w2, g2);  // the next chunk waits for these, nothing waits for dg
-      if (!warp_wait(in_full, (it - 1) & 1, abort_word)) break;
-      const float4 s4 = __ldcg(reinterpret_cast<const float4 *>(mail + ((it - 1) & 1) * kC));
+      const int done = it - 1;
+      if (!warp_wait(&in_full[done & 1], (done >> 1) & 1, abort_word)) break;
+      const float4 s4 = __ldcg(reinterpret_cast<const float4 *>(mail + (done & 1) * kC));
       // suffix sums of what the state gives queries at or behind t, prefix sums of what keys before t give it
       const float e[4] = {l4.x, l4.y, l4.z, l4.w}, r[4] = {r4.x, r4.y, r4.z, r4.w}, in[4] = {s4.x, s4.y, s4.z, s4.w};
       Sum2 es{0.f, 0.f}, rs{0.f, 0.f};
@@ -539,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1) gated_grad_tc_kernel(const __grid
           if (lane >= k) before += u;
         }
         __stcg(mail + ph * kC + T, (own + warp_sum(across)) + (row + before));
-        mbar_arrive(in_full);
+        mbar_arrive(&in_full[ph]);
       }
       ++it;
     }
