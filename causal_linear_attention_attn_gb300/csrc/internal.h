@@ -206,6 +206,156 @@ cudaError_t launch_group_norm(const NormProblem &p);
 size_t norm_grad_workspace(int B, int H, long N, int d);
 cudaError_t launch_group_norm_grad(const NormGradProblem &b);
 
+// Short causal convolution (channels last; rows of x are ldx elements apart), its gradient and step.
+struct ConvProblem {
+  const void *x;
+  long ldx;
+  const float *weight, *bias;  // [D][K]; [D], nullable
+  const int *lengths;          // nullable
+  bool from_state;             // S holds the K - 1 inputs before the first
+  void *out, *S;
+  int B;
+  long N;
+  int D, K;
+  bool silu;
+  la_dtype dt;
+  cudaStream_t stream;
+};
+struct ConvGradProblem {
+  ConvProblem p;  // out and S unused
+  const void *dout, *S0, *dS;
+  void *dx;
+  float *dweight, *dbias;  // nullable
+  void *dS0;               // nullable
+  float *ws;               // short_conv_grad_workspace bytes when dweight or dbias is wanted
+};
+struct ConvStepProblem {
+  const void *x;
+  long ldx;
+  const float *weight, *bias;
+  void *S;
+  const int *slots;
+  void *out;
+  int B, D, K, n_slots;
+  bool silu;
+  la_dtype dt;
+  cudaStream_t stream;
+};
+cudaError_t launch_short_conv(const ConvProblem &p);
+size_t short_conv_grad_workspace(const ConvProblem &p);
+cudaError_t launch_short_conv_grad(const ConvGradProblem &b);
+cudaError_t launch_short_conv_step(const ConvStepProblem &p);
+cudaError_t read_and_clear_conv_step_status(unsigned int *value);
+
+// Selective scan: rows of x, delta (before its bias and softplus), z, Bm, Cm are ld* elements apart.
+struct ScanProblem {
+  const void *x, *delta, *z, *Bm, *Cm;  // z nullable
+  long ldx, ldt, ldz, ldb, ldc;
+  const float *A, *Dskip, *dt_bias;  // [D][ds]; [D], nullable
+  const int *lengths;                // nullable
+  const float *S0;                   // nullable; may be S
+  void *out;
+  float *S;
+  int B;
+  long N;
+  int D, ds;
+  bool softplus;
+  la_dtype dt;
+  void *ws;
+  cudaStream_t stream;
+};
+// How a call is cut along the tokens, and its workspace.
+struct ScanSplit {
+  int segs, launched;  // segments; of which a pass runs so many
+  long len;            // tokens of each, a multiple of every chunk
+  // [B][segs][D][ds] states in front of the segments ([B][segs][D] sums of delta); null: one segment.  The same for
+  // the state's gradient behind them.
+  float *starts, *total, *rev_starts, *rev_total;
+  int chunk;              // gradient: tokens between the kept states
+  long all_chunks;        // of them in N tokens
+  float *chunk_states;    // [B][all_chunks][D][ds]
+  float *bc, *columns;    // partial sums of dB and dC; of dA, dD, ddt_bias
+};
+struct ScanGradProblem {
+  ScanProblem p;  // out and S unused
+  const void *dout;
+  const float *dS;
+  void *dx, *ddt, *dB, *dC, *dz;  // dz null exactly when z is
+  float *dA, *dD, *dbias, *dS0;   // nullable
+};
+struct ScanStepProblem {
+  const void *x, *delta, *z, *Bm, *Cm;
+  long ldx, ldt, ldz, ldb, ldc;
+  const float *A, *Dskip, *dt_bias;
+  float *S;
+  const int *slots;
+  void *out;
+  int B, D, ds, n_slots;
+  bool softplus;
+  la_dtype dt;
+  cudaStream_t stream;
+};
+ScanSplit scan_split(const ScanProblem &p);
+size_t scan_workspace(const ScanProblem &p);
+cudaError_t launch_selective_scan(const ScanProblem &p);
+cudaError_t launch_scan_starts(const ScanProblem &p, const ScanSplit &s);
+cudaError_t launch_scan_reverse_starts(const ScanProblem &p, const ScanSplit &s, const float *dS);
+cudaError_t launch_scan_states(const ScanProblem &p, const ScanSplit &s);
+size_t scan_grad_workspace(const ScanProblem &p);
+cudaError_t launch_selective_scan_grad(const ScanGradProblem &b);
+cudaError_t launch_selective_step(const ScanStepProblem &p);
+cudaError_t read_and_clear_scan_step_status(unsigned int *value);
+
+// Sums over the rows of a table; its columns belong to up to three arrays, one behind the other.  Array i ends at
+// column part[i].end; with taps > 1 the table has it as [taps][n] and the array is [n][taps].
+struct ColumnSums {
+  const float *in;
+  long rows, cols;
+  struct {
+    float *out;  // nullable
+    long end;
+    int taps;
+  } part[3];
+};
+cudaError_t launch_column_sums(const ColumnSums &p, int kernel_id, cudaStream_t stream);
+
+// Beam selection (logits' rows are ld elements apart) and the reordering of pools of states.
+struct BeamProblem {
+  const void *logits;
+  long ld;
+  const float *scores;
+  const unsigned char *finished;  // nullable
+  float *out_scores;
+  int *parents, *tokens;
+  int G, W, k;
+  long V;
+  int eos;
+  la_dtype dt;
+  void *ws;
+  cudaStream_t stream;
+};
+struct BeamSplit {
+  int runs, run_chunks;
+  size_t bytes;
+  void *cands;
+  float *stats;
+};
+constexpr int kMaxPools = 64;
+struct ReorderProblem {
+  void *pool[kMaxPools];
+  long row_bytes[kMaxPools];
+  int pools;
+  bool first;  // of the calls that share the slots: writes new_slots
+  const int *slots, *parents;
+  int *new_slots;
+  int G, W, n_slots;
+  cudaStream_t stream;
+};
+BeamSplit beam_split(int G, int W, int k, long V, la_dtype dt);
+cudaError_t launch_beam_select(const BeamProblem &p);
+cudaError_t launch_beam_reorder(const ReorderProblem &p);
+cudaError_t read_and_clear_beam_status(unsigned int *value);
+
 // For the entry points: whether a current device exists, and the status of a CUDA result (whose
 // detail la_last_error_detail then gives).
 la_status api_device();
@@ -235,7 +385,16 @@ enum KernelId : int {
   kKGatedDecode = 16,
   kKGroupNorm = 17,
   kKGroupNormBackward = 18,
-  kKNumKernels = 19
+  kKShortConv = 19,
+  kKShortConvBackward = 20,
+  kKShortConvStep = 21,
+  kKSelectiveScan = 22,
+  kKSelectiveState = 23,
+  kKSelectiveBackward = 24,
+  kKSelectiveStep = 25,
+  kKBeamSelect = 26,
+  kKBeamReorder = 27,
+  kKNumKernels = 28
 };
 
 // While profiling is on (la_profile_enable), brackets one launch with a CUDA

@@ -215,6 +215,11 @@ la_status la_device_status(void *stream) {
   if (e == cudaSuccess) e = la::read_and_clear_gated_status(&vm);
   if (e == cudaSuccess) e = la::read_and_clear_gated_grad_status(&vd);
   if (e == cudaSuccess) e = la::read_and_clear_gated_step_status(&vs);
+  unsigned int vc = 0, vx = 0, vp = 0;
+  if (e == cudaSuccess) e = la::read_and_clear_conv_step_status(&vc);
+  if (e == cudaSuccess) e = la::read_and_clear_scan_step_status(&vx);
+  if (e == cudaSuccess) e = la::read_and_clear_beam_status(&vp);
+  vs |= vc | vx | vp;
   if (e != cudaSuccess) return la::from_cuda(e);
   v |= vg | vf | vb | vt | vm | vd;
   if (v & 1u) return LA_ERR_TIMEOUT;

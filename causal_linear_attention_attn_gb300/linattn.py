@@ -58,6 +58,33 @@ lib.la_group_norm_workspace.argtypes = [_i] * 4
 lib.la_group_norm_workspace.restype = _sz
 lib.la_group_norm_backward.argtypes = [_vp] * 9 + [_i] * 4 + [_f, _i, _vp, _sz, _vp]
 lib.la_group_norm_backward.restype = _i
+_l = ctypes.c_long
+_CONV_ARGS = [_vp, _l, _vp, _vp, _vp]
+for _name in ("la_short_conv", "la_short_conv_with_state"):
+    getattr(lib, _name).argtypes = _CONV_ARGS + [_vp, _vp] + [_i] * 6 + [_vp]
+    getattr(lib, _name).restype = _i
+lib.la_short_conv_workspace.argtypes = [_i] * 4
+lib.la_short_conv_workspace.restype = _sz
+lib.la_short_conv_backward.argtypes = _CONV_ARGS + [_vp] * 7 + [_i] * 6 + [_vp, _sz, _vp]
+lib.la_short_conv_backward.restype = _i
+lib.la_short_conv_step.argtypes = [_vp, _l] + [_vp] * 5 + [_i] * 6 + [_vp]
+lib.la_short_conv_step.restype = _i
+_SCAN_ARGS = [_vp, _l, _vp, _l, _vp, _vp, _l, _vp, _l, _vp, _vp, _l, _vp]
+for _name in ("la_selective_scan", "la_selective_scan_with_state"):
+    getattr(lib, _name).argtypes = _SCAN_ARGS + [_vp] * 3 + [_i] * 6 + [_vp, _sz, _vp]
+    getattr(lib, _name).restype = _i
+lib.la_selective_scan_workspace.argtypes = [_i] * 6
+lib.la_selective_scan_workspace.restype = _sz
+lib.la_selective_scan_backward.argtypes = _SCAN_ARGS + [_vp] * 13 + [_i] * 6 + [_vp, _sz, _vp]
+lib.la_selective_scan_backward.restype = _i
+lib.la_selective_scan_step.argtypes = _SCAN_ARGS + [_vp] * 3 + [_i] * 6 + [_vp]
+lib.la_selective_scan_step.restype = _i
+lib.la_beam_select.argtypes = [_vp, _l] + [_vp] * 5 + [_i] * 6 + [_vp, _sz, _vp]
+lib.la_beam_select.restype = _i
+lib.la_beam_select_workspace.argtypes = [_i] * 5
+lib.la_beam_select_workspace.restype = _sz
+lib.la_beam_reorder.argtypes = [ctypes.POINTER(_vp), ctypes.POINTER(_sz), _i, _vp, _vp, _vp, _i, _i, _i, _vp]
+lib.la_beam_reorder.restype = _i
 lib.la_decode_step.restype = _i
 lib.la_status_string.argtypes = [_i]
 lib.la_status_string.restype = ctypes.c_char_p
@@ -82,7 +109,9 @@ lib.la_profile_read.restype = _i
 KERNELS = {"causal_main": 0, "causal_state": 1, "exact_head": 2, "causal_simt": 3, "global_state": 4,
            "global_read": 5, "decode": 6, "retention_main": 7, "retention_state": 8, "retention_decode": 9,
            "backward": 10, "favor": 11, "global_fused": 12, "gated": 13, "gated_state": 14, "gated_backward": 15,
-           "gated_decode": 16, "group_norm": 17, "group_norm_backward": 18}
+           "gated_decode": 16, "group_norm": 17, "group_norm_backward": 18, "short_conv": 19, "short_conv_backward": 20,
+           "short_conv_step": 21, "selective_scan": 22, "selective_state": 23, "selective_backward": 24,
+           "selective_step": 25, "beam_select": 26, "beam_reorder": 27}
 
 
 class LinAttnError(RuntimeError):
@@ -540,6 +569,337 @@ def la_group_norm_backward(x, dy, gate=None, weight=None, bias=None, eps: float 
     if rc != 0:
         raise LinAttnError("la_group_norm_backward", rc)
     return dx, dgate, dw, db
+
+
+def _rows(name, t, shape, dtype, device):
+    """The distance of t's rows in elements, after checking its shape, dtype and device: rows of consecutive values at
+    one distance throughout (a contiguous tensor, or a part of the last dimension of one)."""
+    if isinstance(t, torch.Tensor) and t.get_device() == device.index and t.dtype is dtype and t.shape == shape:
+        if t.is_contiguous():
+            return shape[-1]
+        strides = [(n, d) for n, d in zip(shape[:-1], t.stride()[:-1]) if n > 1]
+        if not strides:
+            return shape[-1]
+        if t.stride(-1) == 1 and (len(strides) == 1 or strides[0][1] == strides[1][0] * strides[1][1]):
+            return strides[-1][1]
+        raise ValueError(f"{name} must be contiguous, or one part of the last dimension of a contiguous tensor")
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _first_rows(name, t, nd):
+    """The device of a call, from its first tensor, which may be a part of a wider one."""
+    if not isinstance(t, torch.Tensor) or t.dim() != nd:
+        raise ValueError(f"{name} must be a {nd}-d tensor")
+    _dt(t)
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _conv_inputs(x, weight, bias, nd):
+    dev = _first_rows("x", x, nd)
+    D = x.shape[-1]
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be a [D, K] tensor")
+    K = weight.shape[1]
+    ldx = _rows("x", x, x.shape, x.dtype, dev)
+    _need("weight", weight, (D, K), torch.float32, dev)
+    _opt("bias", bias, (D,), torch.float32, dev)
+    return dev, D, K, ldx, _dt(x)
+
+
+def _zero_padding(t, lengths, shape, dtype, device):
+    """An output to allocate, zero where the call does not write padding rows that the next layer may read."""
+    return torch.zeros(shape, dtype=dtype, device=device) if t is None and lengths is not None else t
+
+
+def _short_conv_call(fn, x, weight, S, bias, silu, lengths, out, stream):
+    dev, D, K, ldx, dt = _conv_inputs(x, weight, bias, 3)
+    B, N, _ = x.shape
+    _opt("lengths", lengths, (B,), torch.int32, dev)
+    s, ctx = _on(dev, stream)
+    try:
+        out = _out("out", _zero_padding(out, lengths, (B, N, D), x.dtype, dev), (B, N, D), x.dtype, dev)
+        S = _out("S", S, (B, max(K - 1, 0), D), x.dtype, dev)
+        rc = getattr(lib, fn)(_ptr(x), ldx, _ptr(weight), _ptr(bias), _ptr(lengths), _ptr(out), _ptr(S), B, N, D, K,
+                              int(silu), dt, s)
+    finally:
+        _off(ctx)
+    if rc != 0:
+        raise LinAttnError(fn, rc)
+    return out, S
+
+
+def la_short_conv(x, weight, bias=None, silu: bool = True, lengths=None, out=None, S=None, stream=None):
+    """Causal convolution along the tokens with a window of K = 2, 3 or 4 weights per channel, and SiLU.
+
+    x [B, N, D] (float32 or bfloat16, D a multiple of 8; a part of the last dimension of a wider tensor will do); weight
+    [D, K] (the last one is the current token's), bias [D], float32.  lengths [B] int32: tokens past a row's length take
+    no part and their rows of a given ``out`` are not written; without ``out`` they are zero.  Returns (out [B, N, D],
+    S [B, K-1, D] the last inputs), both in x's dtype.
+    """
+    return _short_conv_call("la_short_conv", x, weight, S, bias, silu, lengths, out, stream)
+
+
+def la_short_conv_with_state(x, weight, S, bias=None, silu: bool = True, lengths=None, out=None, stream=None):
+    """Short convolution continuing from the inputs in S, which is updated in place; returns (out, S)."""
+    if S is None:
+        raise ValueError("la_short_conv_with_state needs the inputs S before the first")
+    return _short_conv_call("la_short_conv_with_state", x, weight, S, bias, silu, lengths, out, stream)
+
+
+@functools.lru_cache(maxsize=1024)
+def _conv_workspace(device, B, N, D, K):
+    with torch.cuda.device(device):
+        return lib.la_short_conv_workspace(B, N, D, K)
+
+
+def la_short_conv_backward(x, weight, dout, bias=None, silu: bool = True, S0=None, dS=None, lengths=None,
+                           need_state_grad: bool = False, stream=None):
+    """Gradients of la_short_conv (la_short_conv_with_state when S0 is given) for ``dout`` [B, N, D] (x's dtype) and,
+    optionally, ``dS`` of the inputs it carries on.  Returns (dx, dweight, dbias), plus dS0 when ``need_state_grad``; dx
+    and dS0 in x's dtype, dweight and dbias float32, dbias None without bias."""
+    dev, D, K, ldx, dt = _conv_inputs(x, weight, bias, 3)
+    B, N, _ = x.shape
+    _need("dout", dout, (B, N, D), x.dtype, dev)
+    _opt("lengths", lengths, (B,), torch.int32, dev)
+    _opt("S0", S0, (B, max(K - 1, 0), D), x.dtype, dev)
+    _opt("dS", dS, (B, max(K - 1, 0), D), x.dtype, dev)
+    s, ctx = _on(dev, stream)
+    try:
+        dx, dw = torch.empty(B, N, D, dtype=x.dtype, device=dev), torch.empty_like(weight)
+        db = None if bias is None else torch.empty_like(bias)
+        dS0 = torch.empty(B, max(K - 1, 0), D, dtype=x.dtype, device=dev) if need_state_grad else None
+        need = _conv_workspace(dev.index, B, N, D, K)
+        ws = _workspace(need, dev)
+        rc = lib.la_short_conv_backward(_ptr(x), ldx, _ptr(weight), _ptr(bias), _ptr(lengths), _ptr(dout), _ptr(S0),
+                                        _ptr(dS), _ptr(dx), _ptr(dw), _ptr(db), _ptr(dS0), B, N, D, K, int(silu), dt,
+                                        _ptr(ws), need, s)
+    finally:
+        _off(ctx)
+    if rc != 0:
+        raise LinAttnError("la_short_conv_backward", rc)
+    return (dx, dw, db, dS0) if need_state_grad else (dx, dw, db)
+
+
+def _pool(S, B, slots, row, dtype, device):
+    if not isinstance(S, torch.Tensor) or S.dim() != 1 + len(row):
+        raise ValueError(f"S must be a [n_slots, {', '.join(map(str, row))}] tensor")
+    _need("S", S, (S.shape[0], *row), dtype, device)
+    _opt("slots", slots, (B,), torch.int32, device)
+    if slots is None and S.shape[0] < B:
+        raise ValueError(f"S holds {S.shape[0]} states for {B} rows")
+    return S.shape[0]
+
+
+def la_short_conv_step(x, weight, S, bias=None, silu: bool = True, slots=None, out=None, stream=None):
+    """One token of the short convolution; x [B, D]; returns out [B, D] in x's dtype.
+
+    S [n_slots, K-1, D] (x's dtype) is a pool of windows: row b works in place on S[slots[b]].  slots as in
+    la_gated_decode_step, unused, bad and repeated ones too.
+    """
+    dev, D, K, ldx, dt = _conv_inputs(x, weight, bias, 2)
+    B = x.shape[0]
+    n_slots = _pool(S, B, slots, (max(K - 1, 0), D), x.dtype, dev)
+    s, ctx = _on(dev, stream)
+    try:
+        out = _out("out", out, (B, D), x.dtype, dev)
+        rc = lib.la_short_conv_step(_ptr(x), ldx, _ptr(weight), _ptr(bias), _ptr(S), _ptr(slots), _ptr(out), B, n_slots, D,
+                                    K, int(silu), dt, s)
+    finally:
+        _off(ctx)
+    if rc != 0:
+        raise LinAttnError("la_short_conv_step", rc)
+    return out
+
+
+def _scan_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, nd):
+    """(device, lead, channels, d_state, dtype code, the arguments that every selective call begins with)."""
+    dev = _first_rows("x", x, nd)
+    if not isinstance(A, torch.Tensor) or A.dim() != 2:
+        raise ValueError("A must be a [D, d_state] tensor")
+    shape, dtype = x.shape, x.dtype
+    lead, C, ds = shape[:-1], shape[-1], A.shape[1]
+    ldx, ldt = _rows("x", x, shape, dtype, dev), _rows("dt", dt, shape, dtype, dev)
+    ldb, ldc = _rows("Bm", Bm, (*lead, ds), dtype, dev), _rows("Cm", Cm, (*lead, ds), dtype, dev)
+    ldz = 0 if z is None else _rows("z", z, shape, dtype, dev)
+    _need("A", A, (C, ds), torch.float32, dev)
+    _opt("D", D, (C,), torch.float32, dev)
+    _opt("dt_bias", dt_bias, (C,), torch.float32, dev)
+    args = (_ptr(x), ldx, _ptr(dt), ldt, _ptr(A), _ptr(Bm), ldb, _ptr(Cm), ldc, _ptr(D), _ptr(z), ldz, _ptr(dt_bias))
+    return dev, lead, C, ds, _dt(x), args
+
+
+@functools.lru_cache(maxsize=1024)
+def _scan_workspace(device, B, N, D, ds, dt, backward):
+    with torch.cuda.device(device):
+        return lib.la_selective_scan_workspace(B, N, D, ds, dt, backward)
+
+
+def _scan_call(fn, x, dt, A, Bm, Cm, S, D, z, dt_bias, softplus, lengths, out, stream):
+    dev, (B, N), C, ds, code, args = _scan_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, 3)
+    _opt("lengths", lengths, (B,), torch.int32, dev)
+    s, ctx = _on(dev, stream)
+    try:
+        out = _out("out", _zero_padding(out, lengths, (B, N, C), x.dtype, dev), (B, N, C), x.dtype, dev)
+        S = _out("S", S, (B, C, ds), torch.float32, dev)
+        need = _scan_workspace(dev.index, B, N, C, ds, code, 0)
+        ws = _workspace(need, dev)
+        rc = getattr(lib, fn)(*args, _ptr(lengths), _ptr(out), _ptr(S), B, N, C, ds, int(softplus), code, _ptr(ws), need, s)
+    finally:
+        _off(ctx)
+    if rc != 0:
+        raise LinAttnError(fn, rc)
+    return out, S
+
+
+def la_selective_scan(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, softplus: bool = True, lengths=None, out=None,
+                      S=None, stream=None):
+    """Selective state space scan from the zero state: with delta = softplus(dt + dt_bias), per channel
+
+        h_t = e^{delta A} h_{t-1} + (delta x_t) Bm_t,   out_t = (Cm_t . h_t + D x_t) silu(z_t).
+
+    x, dt, z [B, N, D], Bm, Cm [B, N, d_state] (float32 or bfloat16; parts of the last dimension of wider tensors will
+    do); A [D, d_state], D and dt_bias [D] float32.  D a multiple of 8, d_state 8, 16, 32 or 64.  lengths and padding rows
+    as in la_short_conv.  Returns (out in x's dtype, final state S [B, D, d_state] float32).
+    """
+    return _scan_call("la_selective_scan", x, dt, A, Bm, Cm, S, D, z, dt_bias, softplus, lengths, out, stream)
+
+
+def la_selective_scan_with_state(x, dt, A, Bm, Cm, S, D=None, z=None, dt_bias=None, softplus: bool = True, lengths=None,
+                                 out=None, stream=None):
+    """Selective scan continuing from S, which is updated in place; returns (out, S)."""
+    if S is None:
+        raise ValueError("la_selective_scan_with_state needs the initial state S")
+    return _scan_call("la_selective_scan_with_state", x, dt, A, Bm, Cm, S, D, z, dt_bias, softplus, lengths, out, stream)
+
+
+def la_selective_scan_backward(x, dt, A, Bm, Cm, dout, D=None, z=None, dt_bias=None, softplus: bool = True, S0=None,
+                               dS=None, lengths=None, need_state_grad: bool = False, stream=None):
+    """Gradients of la_selective_scan (la_selective_scan_with_state when S0 is given) for the upstream gradient ``dout``
+    of its output (x's dtype) and, optionally, ``dS`` of its final state.  Returns (dx, ddt, dA, dBm, dCm, dD, dz,
+    ddt_bias), plus dS0 when ``need_state_grad``; None for an argument not given.  Gradients of x, dt, Bm, Cm, z have x's
+    dtype, the others are float32."""
+    dev, (B, N), C, ds, code, args = _scan_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, 3)
+    _need("dout", dout, (B, N, C), x.dtype, dev)
+    _opt("lengths", lengths, (B,), torch.int32, dev)
+    _opt("S0", S0, (B, C, ds), torch.float32, dev)
+    _opt("dS", dS, (B, C, ds), torch.float32, dev)
+    s, ctx = _on(dev, stream)
+    try:
+        wide = lambda t: None if t is None else torch.empty(B, N, t.shape[-1], dtype=x.dtype, device=dev)  # noqa: E731
+        dx, ddt, dB, dC, dz = wide(x), wide(dt), wide(Bm), wide(Cm), wide(z)
+        dA, dD, dbias = torch.empty_like(A), *(None if t is None else torch.empty_like(t) for t in (D, dt_bias))
+        dS0 = torch.empty(B, C, ds, dtype=torch.float32, device=dev) if need_state_grad else None
+        need = _scan_workspace(dev.index, B, N, C, ds, code, 1)
+        ws = _workspace(need, dev)
+        rc = lib.la_selective_scan_backward(*args, _ptr(lengths), _ptr(dout), _ptr(S0), _ptr(dS), _ptr(dx), _ptr(ddt),
+                                            _ptr(dA), _ptr(dB), _ptr(dC), _ptr(dD), _ptr(dz), _ptr(dbias), _ptr(dS0), B, N,
+                                            C, ds, int(softplus), code, _ptr(ws), need, s)
+    finally:
+        _off(ctx)
+    if rc != 0:
+        raise LinAttnError("la_selective_scan_backward", rc)
+    r = (dx, ddt, dA, dB, dC, dD, dz, dbias)
+    return (*r, dS0) if need_state_grad else r
+
+
+def la_selective_scan_step(x, dt, A, Bm, Cm, S, D=None, z=None, dt_bias=None, softplus: bool = True, slots=None, out=None,
+                           stream=None):
+    """One token of the selective scan; x, dt, z [B, D], Bm, Cm [B, d_state]; returns out [B, D] in x's dtype.
+
+    S [n_slots, D, d_state] float32 is a pool of states: row b works in place on S[slots[b]].  slots as in
+    la_gated_decode_step, unused, bad and repeated ones too.
+    """
+    dev, (B,), C, ds, code, args = _scan_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, 2)
+    n_slots = _pool(S, B, slots, (C, ds), torch.float32, dev)
+    s, ctx = _on(dev, stream)
+    try:
+        out = _out("out", out, (B, C), x.dtype, dev)
+        rc = lib.la_selective_scan_step(*args, _ptr(S), _ptr(slots), _ptr(out), B, n_slots, C, ds, int(softplus), code, s)
+    finally:
+        _off(ctx)
+    if rc != 0:
+        raise LinAttnError("la_selective_scan_step", rc)
+    return out
+
+
+@functools.lru_cache(maxsize=1024)
+def _beam_workspace(device, G, W, k, V, dt):
+    with torch.cuda.device(device):
+        return lib.la_beam_select_workspace(G, W, k, V, dt)
+
+
+def la_beam_select(logits, scores, k=None, finished=None, eos: int = 0, stream=None):
+    """The k (default W) best continuations of each group's W beams by score + log_softmax(logits), best first.
+
+    logits [G, W, V] (float32 or bfloat16; a part of the last dimension of a wider tensor will do), scores [G, W] float32
+    accumulated log probabilities (-inf: an unused beam).  Compared in 64 bits; ties go to the lowest beam and token.
+    finished [G, W] bool: such a beam has one continuation, token ``eos``, and keeps its score.  Logits of -inf or NaN are
+    chosen only where nothing else is left.  W and k up to 64.  Returns (scores float32, parents int32, tokens int32),
+    each [G, k].
+    """
+    dev = _first_rows("logits", logits, 3)
+    G, W, V = logits.shape
+    k = W if k is None else int(k)
+    ld, dt = _rows("logits", logits, logits.shape, logits.dtype, dev), _dt(logits)
+    _need("scores", scores, (G, W), torch.float32, dev)
+    _opt("finished", finished, (G, W), torch.bool, dev)
+    s, ctx = _on(dev, stream)
+    try:
+        best = torch.empty(G, max(k, 0), dtype=torch.float32, device=dev)
+        parents, tokens = (torch.empty(G, max(k, 0), dtype=torch.int32, device=dev) for _ in range(2))
+        need = _beam_workspace(dev.index, G, W, k, V, dt)
+        ws = _workspace(need, dev)
+        rc = lib.la_beam_select(_ptr(logits), ld, _ptr(scores), _ptr(finished), _ptr(best), _ptr(parents), _ptr(tokens), G,
+                                W, k, V, int(eos), dt, _ptr(ws), need, s)
+    finally:
+        _off(ctx)
+    if rc != 0:
+        raise LinAttnError("la_beam_select", rc)
+    return best, parents, tokens
+
+
+def la_beam_reorder(pools, slots, parents, stream=None):
+    """Pools of states follow the beams that la_beam_select chose; returns the new slots [G, W].
+
+    pools: contiguous tensors [n_slots, ...] of any dtype (rows of a multiple of 16 bytes), changed in place; slots [G, W]
+    int32: each beam's row in every pool; parents [G, W] int32.  A beam's first child keeps its slot, the others get the
+    slots of the group's childless beams (lowest first) with a copy of their parent's rows; a negative parent gets one
+    without a copy.  A parent or slot out of range, and a slot that two beams have, are not copied to, and the next
+    device_status() is 1.
+    """
+    if isinstance(pools, torch.Tensor):
+        pools = [pools]
+    if not isinstance(slots, torch.Tensor) or slots.dim() != 2 or not slots.is_cuda:
+        raise ValueError("slots must be a contiguous 2-d CUDA tensor")
+    dev, (G, W) = slots.device, slots.shape
+    _need("slots", slots, (G, W), torch.int32, dev)
+    _need("parents", parents, (G, W), torch.int32, dev)
+    n = len(pools)
+    at, rows, n_slots = (_vp * max(n, 1))(), (_sz * max(n, 1))(), None
+    for i, p in enumerate(pools):
+        if not isinstance(p, torch.Tensor) or p.dim() < 1 or p.get_device() != dev.index or not p.is_contiguous():
+            raise ValueError(f"pools[{i}] must be a contiguous [n_slots, ...] tensor on {dev}")
+        if n_slots not in (None, p.shape[0]):
+            raise ValueError(f"pools[{i}] has {p.shape[0]} slots, pools[0] has {n_slots}")
+        n_slots = p.shape[0]
+        at[i], rows[i] = p.data_ptr() or None, p.nbytes // n_slots if n_slots else 0
+    s, ctx = _on(dev, stream)
+    try:
+        new = torch.empty_like(slots)
+        rc = lib.la_beam_reorder(at, rows, n, _ptr(slots), _ptr(parents), _ptr(new), G, W, n_slots or 0, s)
+    finally:
+        _off(ctx)
+    if rc != 0:
+        raise LinAttnError("la_beam_reorder", rc)
+    return new
 
 
 def device_status(stream=None) -> int:

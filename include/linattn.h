@@ -445,13 +445,165 @@ LA_API la_status la_group_norm_backward(const void *x, const void *dy, const voi
 LA_API size_t la_group_norm_workspace(int B, int H, int N, int d);
 
 /*
+ * Short causal convolution along the tokens, one window of K weights per
+ * channel, the layer in front of the selective scan:
+ *     u_t = bias + sum_{j<K} weight_j x_{t-K+1+j},   out_t = silu(u_t)
+ * (silu == 0: out_t = u_t), with x_t = 0 before the first token.  Channels
+ * last: x: [B,N,D] of dtype dt, whose token rows are ldx elements apart (D
+ * when contiguous, more for one part of a wider projection; batch rows N * ldx
+ * apart); out: [B,N,D], dtype dt.  weight: [D,K], bias: [D] (nullable), float32.
+ * S: [B,K-1,D], dtype dt, the last K - 1 inputs, written.  lengths (nullable,
+ * [B] int32, device): tokens t >= lengths[b] take no part and their rows of out
+ * are not written.  D a multiple of 8, K in {2, 3, 4}.
+ * la_short_conv_with_state starts from the window in S and updates it in
+ * place.  Sums in fp32.  Pointers 16-byte aligned (lengths 4), ldx >= D and a
+ * multiple of 16 bytes.  N == 0 leaves the carried window (zeros without one).
+ */
+LA_API la_status la_short_conv(const void *x, long ldx, const float *weight, const float *bias, const int *lengths,
+                               void *out, void *S, int B, int N, int D, int K, int silu, la_dtype dt, void *stream);
+LA_API la_status la_short_conv_with_state(const void *x, long ldx, const float *weight, const float *bias,
+                                          const int *lengths, void *out, void *S, int B, int N, int D, int K, int silu,
+                                          la_dtype dt, void *stream);
+
+/*
+ * Gradient of la_short_conv(_with_state): dout [B,N,D], dtype dt, contiguous;
+ * S0 (NULL = zero) the forward's window, dS (NULL = zero) the gradient of the
+ * one it left, both [B,K-1,D], dtype dt.  Written: dx [B,N,D] and dS0 (nullable;
+ * it may be neither S0 nor overlap dS) of dtype dt; dweight [D,K], dbias [D]
+ * float32, each nullable, added in a fixed order.  Rows t >= lengths[b] of dx are
+ * zero.  workspace: la_short_conv_workspace bytes, 256-byte aligned, when dweight
+ * or dbias is wanted (NULL otherwise); calls that may run at the same time need
+ * one each.
+ */
+LA_API la_status la_short_conv_backward(const void *x, long ldx, const float *weight, const float *bias,
+                                        const int *lengths, const void *dout, const void *S0, const void *dS, void *dx,
+                                        float *dweight, float *dbias, void *dS0, int B, int N, int D, int K, int silu,
+                                        la_dtype dt, void *workspace, size_t workspace_bytes, void *stream);
+LA_API size_t la_short_conv_workspace(int B, int N, int D, int K);
+
+/*
+ * One token of la_short_conv per batch row, on windows that live in a pool S
+ * [n_slots,K-1,D], dtype dt, read and written in place: row b works on
+ * S[slots[b]].  x: [B,D], rows ldx apart; out: [B,D].  slots as in
+ * la_gated_decode_step (unused, bad and repeated ones too).
+ */
+LA_API la_status la_short_conv_step(const void *x, long ldx, const float *weight, const float *bias, void *S,
+                                    const int *slots, void *out, int B, int n_slots, int D, int K, int silu, la_dtype dt,
+                                    void *stream);
+
+/*
+ * Selective state space scan, per channel with d_state components ("Linear
+ * Attention Math", "The kernel cousins: SSMs and RetNet", with steps and
+ * projections that depend on the token):
+ *     delta = softplus(dt + dt_bias)  (softplus == 0: dt + dt_bias)
+ *     h_t = e^{delta A} h_{t-1} + (delta x_t) B_t
+ *     out_t = (C_t . h_t + D x_t) silu(z_t)
+ * x, delta (dt above), z (nullable: no gate): [B,N,D]; Bm, Cm (B_t and C_t, shared by
+ * all channels): [B,N,d_state]; all of dtype dt, token rows ld* elements apart
+ * (parts of wider projections; batch rows N * ld* apart).  A: [D,d_state], Dskip
+ * (nullable: 0) and dt_bias (nullable: 0): [D], float32.  Written: out [B,N,D],
+ * dtype dt; S [B,D,d_state] float32, the final state.  lengths as in
+ * la_short_conv.  la_selective_scan_with_state starts from S and updates it in
+ * place.  Steps, states and sums in fp32.  D a multiple of 8, d_state in {8, 16,
+ * 32, 64}; pointers 16-byte aligned (lengths 4), every ld at least its row and a
+ * multiple of 16 bytes.  workspace: la_selective_scan_workspace(..., 0) bytes,
+ * 256-byte aligned (NULL if that is 0).  N == 0 leaves the carried state (zeros
+ * without one).
+ */
+LA_API la_status la_selective_scan(const void *x, long ldx, const void *delta, long ld_delta, const float *A,
+                                   const void *Bm, long ldb, const void *Cm, long ldc, const float *Dskip, const void *z,
+                                   long ldz, const float *dt_bias, const int *lengths, void *out, float *S, int B, int N,
+                                   int D, int d_state, int softplus, la_dtype dt, void *workspace,
+                                   size_t workspace_bytes, void *stream);
+LA_API la_status la_selective_scan_with_state(const void *x, long ldx, const void *delta, long ld_delta, const float *A,
+                                              const void *Bm, long ldb, const void *Cm, long ldc, const float *Dskip,
+                                              const void *z, long ldz, const float *dt_bias, const int *lengths,
+                                              void *out, float *S, int B, int N, int D, int d_state, int softplus,
+                                              la_dtype dt, void *workspace, size_t workspace_bytes, void *stream);
+LA_API size_t la_selective_scan_workspace(int B, int N, int D, int d_state, la_dtype dt, int backward);
+
+/*
+ * Gradient of la_selective_scan(_with_state): with dy = dout silu(z) and G_t the
+ * gradient of h_t,
+ *     G_t = C_t dy_t + e^{delta_{t+1} A} G_{t+1},  behind the last token G = dS,
+ *     dx = D dy + delta (G . B),  d delta = x (G . B) + (G e^{delta A} h_{t-1}) . A,
+ *     dB_t = sum over channels of G delta x,  dC_t = sum over channels of h dy.
+ * dout [B,N,D], dtype dt, contiguous; S0 (NULL = zero) the forward's initial state,
+ * dS (NULL = zero) the gradient of its final one.  Written, contiguous: dx, ddelta
+ * (of dt, before its bias) [B,N,D], dB, dC [B,N,d_state], dz [B,N,D] (given
+ * exactly when z is), dtype dt; dA [D,d_state], dDskip, ddt_bias [D], dS0
+ * [B,D,d_state] (which may be dS itself), float32, each nullable.  Rows t >=
+ * lengths[b] are zero.  All sums in a fixed order.  No output may overlap an input
+ * otherwise.  workspace: la_selective_scan_workspace(..., 1) bytes, 256-byte
+ * aligned; calls that may run at the same time need one each.
+ */
+LA_API la_status la_selective_scan_backward(const void *x, long ldx, const void *delta, long ld_delta, const float *A,
+                                            const void *Bm, long ldb, const void *Cm, long ldc, const float *Dskip,
+                                            const void *z, long ldz, const float *dt_bias, const int *lengths,
+                                            const void *dout, const float *S0, const float *dS, void *dx, void *ddelta,
+                                            float *dA, void *dB, void *dC, float *dDskip, void *dz, float *ddt_bias,
+                                            float *dS0, int B, int N, int D, int d_state, int softplus, la_dtype dt,
+                                            void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One token of la_selective_scan per batch row, on states that live in a pool S
+ * [n_slots,D,d_state] float32, read and written in place: row b works on
+ * S[slots[b]].  x, delta, z: [B,D]; Bm, Cm: [B,d_state]; rows ld* apart; out
+ * [B,D].  slots as in la_gated_decode_step (unused, bad and repeated ones too).
+ */
+LA_API la_status la_selective_scan_step(const void *x, long ldx, const void *delta, long ld_delta, const float *A,
+                                        const void *Bm, long ldb, const void *Cm, long ldc, const float *Dskip,
+                                        const void *z, long ldz, const float *dt_bias, float *S, const int *slots,
+                                        void *out, int B, int n_slots, int D, int d_state, int softplus, la_dtype dt,
+                                        void *stream);
+
+/*
+ * Beam search, selection: of each group's W beams with accumulated log
+ * probabilities `scores` ([G,W] float32, finite or -inf) and next-token logits
+ * ([G,W,V], dtype dt, rows ld elements apart), the k best continuations by
+ *     scores_w + logits_{w,v} - log sum_v' e^{logits_{w,v'}},
+ * best first, ties to the lowest w V + v.  Compared in 64 bits from the float32
+ * logits and scores (within a beam: by the logits).  Written, [G,k]: out_scores
+ * float32, parents (w) and tokens (v) int32.  finished (nullable, [G,W], one byte
+ * each): a finished beam has one continuation, token eos, and keeps its score.
+ * Everything else is -inf: a logit of -inf or NaN, all continuations of a beam
+ * whose score is -inf or NaN; where nothing else is left these are chosen too, with
+ * score -inf.  Infinite logits count as the largest finite number.  1 <= k <=
+ * min(64, W V), W <= 64, 0 <= eos < V, ld >= V.  logits 16-byte aligned, the other
+ * pointers 4 (finished 1).  workspace: la_beam_select_workspace bytes, 256-byte
+ * aligned; calls that may run at the same time need one each.
+ */
+LA_API la_status la_beam_select(const void *logits, long ld, const float *scores, const unsigned char *finished,
+                                float *out_scores, int *parents, int *tokens, int G, int W, int k, int V, int eos,
+                                la_dtype dt, void *workspace, size_t workspace_bytes, void *stream);
+LA_API size_t la_beam_select_workspace(int G, int W, int k, int V, la_dtype dt);
+
+/*
+ * Beam search, states: pools of states follow the beams that were chosen.
+ * slots [G,W] int32: the slot of each beam's state in every pool; parents [G,W]
+ * int32: the beam that each new beam continues.  The first child of a beam keeps
+ * its slot; the others get the slots of the group's childless beams, lowest beam
+ * first, and a copy of their parent's row there, in place, in each of n_pools
+ * pools (host arrays of device pointers [n_slots, row_bytes] and row sizes, a
+ * multiple of 16 bytes each; pools 16-byte aligned).  new_slots [G,W] int32,
+ * written, not overlapping slots.  A negative parent takes a childless beam's slot
+ * without a copy, and nothing is copied from or to a negative slot.  A parent >= W,
+ * a slot >= n_slots that a copy reads or writes, and a slot to be written that
+ * another beam of the call has too: no copy, and the next la_device_status returns
+ * LA_ERR_INVALID_VALUE.  W <= 64.  Allocates nothing.
+ */
+LA_API la_status la_beam_reorder(void *const *pools, const size_t *row_bytes, int n_pools, const int *slots,
+                                 const int *parents, int *new_slots, int G, int W, int n_slots, void *stream);
+
+/*
  * Synchronizes `stream`, then reads and clears the library's device status
  * word on the current device.  Returns LA_ERR_TIMEOUT if a bounded
  * device-side wait inside one of the library's kernels gave up since the
  * last check, LA_ERR_LAUNCH if a kernel refused to run on this device
  * configuration (its shared-memory base was not 1024-byte aligned); in both
  * cases that call's outputs are not valid.  LA_ERR_INVALID_VALUE if a
- * la_gated_decode_step skipped a row whose slot was out of range or repeated.
+ * la_gated_decode_step, la_short_conv_step or la_selective_scan_step skipped a
+ * row, or a la_beam_reorder a copy, whose slot was out of range or repeated.
  * LA_OK otherwise, or the error of the synchronization itself.
  */
 LA_API la_status la_device_status(void *stream);
@@ -526,7 +678,16 @@ typedef enum {
   LA_KERNEL_GATED_BACKWARD = 15,  /* its gradient */
   LA_KERNEL_GATED_DECODE = 16,    /* its recurrent step */
   LA_KERNEL_GROUP_NORM = 17,      /* gated group norm */
-  LA_KERNEL_GROUP_NORM_BACKWARD = 18 /* its gradient */
+  LA_KERNEL_GROUP_NORM_BACKWARD = 18, /* its gradient */
+  LA_KERNEL_SHORT_CONV = 19,          /* short causal convolution */
+  LA_KERNEL_SHORT_CONV_BACKWARD = 20, /* its gradient */
+  LA_KERNEL_SHORT_CONV_STEP = 21,     /* its step */
+  LA_KERNEL_SELECTIVE_SCAN = 22,      /* selective scan: outputs */
+  LA_KERNEL_SELECTIVE_STATE = 23,     /* its passes over states, forward and backward */
+  LA_KERNEL_SELECTIVE_BACKWARD = 24,  /* its gradient */
+  LA_KERNEL_SELECTIVE_STEP = 25,      /* its step */
+  LA_KERNEL_BEAM_SELECT = 26,         /* beam selection */
+  LA_KERNEL_BEAM_REORDER = 27         /* states following their beams */
 } la_kernel;
 
 /*
