@@ -25,24 +25,47 @@ namespace la {
 namespace {
 
 constexpr int kTok = 32;         // tokens a chunk
-constexpr int kCols = 32;        // channels a block
-constexpr int kRow = kCols + 8;  // floats between tokens of the sums' place: four tokens of eight channels meet no bank twice
+constexpr int kAround = 128;     // threads around the recurrence: (token, eight channels) in turns
+
+// Channels a block: as many as keep it within 400 threads.
+constexpr int scan_cols(int ds) { return ds == 64 ? 32 : 64; }
 
 enum Mode { kOutputs, kEnds, kStates, kReverseEnds };
+
+template <int DS, int kMode>
+struct Smem {
+  static constexpr int kCols = scan_cols(DS), kRow = kCols + 8;  // floats between tokens of the sums' place
+  float4 steps[kTok][kCols / 2];  // of two channels: delta, delta x (reverse: dy); at step_slot
+  float B[kTok][DS];          // (reverse: C)
+  float C[kMode == kOutputs ? kTok : 1][DS];
+  float sums[kMode == kOutputs ? kTok : 1][kRow];
+};
+
+// Where two channels' steps are: eight lanes that write four neighbours each meet no bank twice.
+__device__ __forceinline__ int step_slot(int pair) { return pair ^ (pair >> 3 & 3); }
+
+// Named barriers: chunk k's inputs are in place (k even, odd); its recurrence is through.
+template <int kThreads>
+__device__ __forceinline__ void bar_sync(int id) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kThreads) : "memory");
+}
+template <int kThreads>
+__device__ __forceinline__ void bar_arrive(int id) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(kThreads) : "memory");
+}
 
 // kOutputs: out, and the last segment's end state to S.  kEnds: each segment's end state from zero and sum of
 // delta.  kStates: the state in front of each chunk of s.chunk tokens.  kReverseEnds: the same as kEnds for the
 // recurrence of the state's gradient, from a segment's last token to its first: G <- a_t (G + C_t dy_t).
 template <typename T, int DS, int kMode>
-__global__ void __launch_bounds__(8 * DS) scan_kernel(const __grid_constant__ ScanProblem p, const __grid_constant__ ScanSplit s) {
-  constexpr int kThreads = 8 * DS, kLanes = DS / 4, kPerWarp = 32 / kLanes;
-  constexpr int kGroups = (kTok * 4 + kThreads - 1) / kThreads;  // (token, eight channels) a thread
+__global__ void __launch_bounds__(scan_cols(DS) * DS / 8 + kAround) scan_kernel(const __grid_constant__ ScanProblem p, const __grid_constant__ ScanSplit s) {
+  constexpr int kCols = Smem<DS, kMode>::kCols, kTurns = kTok * kCols / 8 / kAround;
+  constexpr int kScan = kCols * DS / 8, kThreads = kScan + kAround, kLanes = DS / 4, kPerWarp = 64 / kLanes;
   constexpr bool kRev = kMode == kReverseEnds;
-  __shared__ __align__(16) float2 steps[kTok][kCols];  // delta; delta x (reverse: dy)
-  __shared__ __align__(16) float sB[kTok][DS];         // (reverse: C)
-  __shared__ __align__(16) float sC[kMode == kOutputs ? kTok : 1][DS];
-  __shared__ __align__(16) float sums[kMode == kOutputs ? kTok : 1][kRow];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  extern __shared__ __align__(16) unsigned char raw_smem[];
+  Smem<DS, kMode> *m = reinterpret_cast<Smem<DS, kMode> *>(raw_smem);
+  __shared__ float part[kAround / 32][Smem<DS, kMode>::kCols];
+  const int tid = threadIdx.x, lane = tid & 31;
   const int nb = (p.D + kCols - 1) / kCols;
   const int cb = blockIdx.x % nb;
   const long rest = blockIdx.x / nb;
@@ -50,185 +73,227 @@ __global__ void __launch_bounds__(8 * DS) scan_kernel(const __grid_constant__ Sc
   const long b = rest / s.launched;
   const long n = row_length(p.lengths, b, p.N);
   const long begin = (long)seg * s.len, end = min(begin + s.len, n);
-  const long chunks = end > begin ? (end - begin + kTok - 1) / kTok : 0;
+  const int chunks = end > begin ? (int)((end - begin + kTok - 1) / kTok) : 0;
+  auto first_of = [&](int k) { return begin + (long)(kRev ? chunks - 1 - k : k) * kTok; };
 
-  // as (channel, components)
-  const int q = lane % kLanes, ch = warp * kPerWarp + lane / kLanes;
-  const int c = cb * kCols + ch;
-  const long at = (long)c * DS + 4 * q;  // in a state
-  const long state = (long)p.D * DS;
-  float2 A[2] = {both(0.f), both(0.f)}, h[2] = {both(0.f), both(0.f)};
-  if (c < p.D) {
-    const float4 a = *reinterpret_cast<const float4 *>(p.A + at);
-    A[0] = __fmul2_rn(make_float2(a.x, a.y), both(kLog2e)), A[1] = __fmul2_rn(make_float2(a.z, a.w), both(kLog2e));
-    const float *from = nullptr;
-    if (kMode == kOutputs || kMode == kStates) from = s.starts ? s.starts + (b * s.segs + seg) * state : p.S0 ? p.S0 + b * state : nullptr;
-    if (from) {
-      const float4 v = *reinterpret_cast<const float4 *>(from + at);
-      h[0] = make_float2(v.x, v.y), h[1] = make_float2(v.z, v.w);
+  if (tid >= kScan) {
+    // around the recurrence
+    const int at = tid - kScan, col = (at % (kCols / 8)) * 8, c8 = cb * kCols + col, row0 = at / (kCols / 8);
+    constexpr int kRows = kAround / (kCols / 8);  // tokens between a thread's turns
+    const bool live = c8 < p.D;
+    float2 bias[4], skip[4], total[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      bias[e] = live && p.dt_bias ? reinterpret_cast<const float2 *>(p.dt_bias + c8)[e] : both(0.f);
+      skip[e] = live && p.Dskip && kMode == kOutputs ? reinterpret_cast<const float2 *>(p.Dskip + c8)[e] : both(0.f);
+      total[e] = both(0.f);
     }
-  }
-
-  // as (token, eight channels): every group of a thread has the same channels
-  const int c8 = cb * kCols + (tid & 3) * 8;
-  const bool live = c8 < p.D;
-  float2 bias[4], skip[4], total[4];
+    const T *x = (const T *)p.x + b * p.N * p.ldx + c8, *dt = (const T *)p.delta + b * p.N * p.ldt + c8;
+    const T *z = p.z ? (const T *)p.z + b * p.N * p.ldz + c8 : nullptr;
+    T *out = (T *)p.out + b * p.N * p.D + c8;
+    constexpr bool kNeedZ = kMode == kOutputs || kRev;
+    // rows of B (and C), eight components a piece
+    constexpr int kPerRow = DS / 8, kOne = kTok * kPerRow, kPieces = kMode == kOutputs ? 2 * kOne : kOne;
+    constexpr int kEach = (kPieces + kAround - 1) / kAround;
+    const T *Bm = (const T *)(kRev ? p.Cm : p.Bm) + b * p.N * (kRev ? p.ldc : p.ldb), *Cm = (const T *)p.Cm + b * p.N * p.ldc;
+    Raw<T> rx[kTurns], rt[kTurns], rz[kTurns], rb[kEach], kx[kTurns], kz[kTurns];
+    auto load = [&](long t0) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    bias[e] = live && p.dt_bias ? reinterpret_cast<const float2 *>(p.dt_bias + c8)[e] : both(0.f);
-    skip[e] = live && p.Dskip && kMode == kOutputs ? reinterpret_cast<const float2 *>(p.Dskip + c8)[e] : both(0.f);
-    total[e] = both(0.f);
-  }
-  const T *x = (const T *)p.x + b * p.N * p.ldx + c8, *dt = (const T *)p.delta + b * p.N * p.ldt + c8;
-  const T *z = p.z ? (const T *)p.z + b * p.N * p.ldz + c8 : nullptr;
-  constexpr bool kNeedZ = kMode == kOutputs || kRev;
-  Raw<T> rx[kGroups], rt[kGroups], rz[kNeedZ ? kGroups : 1], rb, rc;
-  // rows of B (and C): eight components a thread, as many threads as kTok * DS / 8
-  constexpr int kPieces = kTok * DS / 8, kPerRow = DS / 8;
-  const bool with_c = kMode == kOutputs && tid >= kPieces;
-  const int piece = with_c ? tid - kPieces : tid, brow = piece / kPerRow, bcol = piece % kPerRow * 8;
-  const T *bc = with_c || kRev ? (const T *)p.Cm + b * p.N * p.ldc + bcol : (const T *)p.Bm + b * p.N * p.ldb + bcol;
-  const long ldbc = with_c || kRev ? p.ldc : p.ldb;
-  const bool has_bc = kMode == kOutputs ? tid < 2 * kPieces : tid < kPieces;
-  static_assert(2 * kPieces == kThreads, "a piece a thread");
-  auto load = [&](long t0) {
+      for (int u = 0; u < kTurns; ++u) {
+        const long t = t0 + row0 + u * kRows;
+        rx[u].zero(), rt[u].zero(), rz[u].zero();
+        if (live && t < end) {
+          rx[u].load(x + t * p.ldx), rt[u].load(dt + t * p.ldt);
+          if (kNeedZ && z) rz[u].load(z + t * p.ldz);
+        }
+      }
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      const int i = tid + g * kThreads;
-      const long t = t0 + (i >> 2);
-      rx[g].zero(), rt[g].zero();
-      if (kNeedZ) rz[g].zero();
-      if (i < kTok * 4 && live && t < end) {
-        rx[g].load(x + t * p.ldx);
-        rt[g].load(dt + t * p.ldt);
-        if (kNeedZ && z) rz[g].load(z + t * p.ldz);
+      for (int i = 0; i < kEach; ++i) {
+        const int k = at + i * kAround, which = k >= kOne, j = which ? k - kOne : k;
+        rb[i].zero();
+        if (k < kPieces && t0 + j / kPerRow < end)
+          rb[i].load((which ? Cm : Bm) + (t0 + j / kPerRow) * (which ? p.ldc : kRev ? p.ldc : p.ldb) + j % kPerRow * 8);
+      }
+    };
+    if (chunks) load(first_of(0));
+    for (int k = 0; k <= chunks; ++k) {
+      Raw<T> px[kTurns], pz[kTurns];  // of the chunk whose sums come next
+#pragma unroll
+      for (int u = 0; u < kTurns; ++u) px[u] = kx[u], pz[u] = kz[u];
+      if (k < chunks) {
+        Smem<DS, kMode> &to = m[k & 1];
+#pragma unroll
+        for (int u = 0; u < kTurns; ++u) {
+          const int row = row0 + u * kRows;
+          const bool in = first_of(k) + row < end;
+          float2 xv[4], tv[4], zv[4];
+          rx[u].get(xv), rt[u].get(tv);
+          if (kRev) rz[u].get(zv);
+          kx[u] = rx[u], kz[u] = rz[u];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float2 d = __fadd2_rn(tv[e], bias[e]);
+            if (p.softplus) d = softplus2(d);
+            if (!in) d = both(0.f);
+            if (kMode == kEnds || kRev) total[e] = __fadd2_rn(total[e], d);
+            float2 v = kRev ? xv[e] : __fmul2_rn(d, xv[e]);
+            if (kRev && z) v = __fmul2_rn(v, __fmul2_rn(zv[e], Sigmoid2(zv[e]).s));
+            if (!in) v = both(0.f);
+            to.steps[row][step_slot(col / 2 + e)] = make_float4(d.x, v.x, d.y, v.y);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          const int q = at + i * kAround, which = q >= kOne, j = which ? q - kOne : q;
+          float2 v[4];
+          rb[i].get(v);
+          if (q < kPieces) put8((which ? &to.C[0][0] : &to.B[0][0]) + j * 8, v);
+        }
+        if (k + 1 < chunks) load(first_of(k + 1));
+        bar_arrive<kThreads>(1 + (k & 1));
+      }
+      if (k > 0) {
+        bar_sync<kThreads>(3 + ((k - 1) & 1));
+        const Smem<DS, kMode> &from = m[(k - 1) & 1];
+#pragma unroll
+        for (int u = 0; u < kTurns; ++u) {
+          const int row = row0 + u * kRows;
+          const long t = first_of(k - 1) + row;
+          if (kMode == kOutputs && live && t < end) {
+            const float4 y0 = *reinterpret_cast<const float4 *>(&from.sums[row][col]);
+            const float4 y1 = *reinterpret_cast<const float4 *>(&from.sums[row][col + 4]);
+            float2 y[4] = {make_float2(y0.x, y0.y), make_float2(y0.z, y0.w), make_float2(y1.x, y1.y), make_float2(y1.z, y1.w)};
+            float2 xv[4], zv[4];
+            px[u].get(xv), pz[u].get(zv);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              y[e] = __ffma2_rn(skip[e], xv[e], y[e]);
+              if (z) y[e] = __fmul2_rn(y[e], __fmul2_rn(zv[e], Sigmoid2(zv[e]).s));
+            }
+            put8(out + t * p.D, y);
+          }
+        }
       }
     }
-    rb.zero();
-    if (has_bc && t0 + brow < end) rb.load(bc + (t0 + brow) * ldbc);
-  };
-  (void)rc;
-  auto first_of = [&](long k) { return begin + (kRev ? chunks - 1 - k : k) * kTok; };
-  if (chunks) load(first_of(0));
-  for (long k = 0; k < chunks; ++k) {
-    const long t0 = first_of(k);
-    Raw<T> kx[kMode == kOutputs ? kGroups : 1], kz[kMode == kOutputs ? kGroups : 1];
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      const int i = tid + g * kThreads;
-      if (i >= kTok * 4) break;
-      const long t = t0 + (i >> 2);
-      if (kMode == kOutputs) kx[g] = rx[g], kz[g] = rz[g];
-      float2 xv[4], tv[4], zv[4];
-      rx[g].get(xv), rt[g].get(tv);
-      if (kRev) rz[g].get(zv);
-      float4 *to = reinterpret_cast<float4 *>(&steps[i >> 2][(tid & 3) * 8]);
+    if (kMode == kEnds || kRev) {
+      // sums of delta: lanes 8 apart have the same channels, then the warps in order
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float2 d = __fadd2_rn(tv[e], bias[e]);
-        if (p.softplus) d = softplus2(d);
-        if (t >= end) d = both(0.f);
-        if (kMode == kEnds || kRev) total[e] = __fadd2_rn(total[e], d);
-        float2 u = kRev ? xv[e] : __fmul2_rn(d, xv[e]);
-        if (kRev && z) u = __fmul2_rn(u, __fmul2_rn(zv[e], Sigmoid2(zv[e]).s));
-        if (t >= end) u = both(0.f);
-        to[e] = make_float4(d.x, u.x, d.y, u.y);
+#pragma unroll
+        for (int o = kCols / 8; o < 32; o <<= 1) {
+          total[e].x += __shfl_xor_sync(0xffffffffu, total[e].x, o);
+          total[e].y += __shfl_xor_sync(0xffffffffu, total[e].y, o);
+        }
+        if (lane < kCols / 8) *reinterpret_cast<float2 *>(&part[at >> 5][col + 2 * e]) = total[e];
+      }
+      bar_sync<kAround>(5);
+      if (at < kCols && cb * kCols + at < p.D) {
+        float v = part[0][at];
+#pragma unroll
+        for (int w = 1; w < kAround / 32; ++w) v += part[w][at];
+        (kRev ? s.rev_total : s.total)[(b * s.segs + seg) * p.D + cb * kCols + at] = v;
       }
     }
-    if (has_bc) {
-      float2 v[4];
-      rb.get(v);
-      float *to = with_c ? &sC[kMode == kOutputs ? brow : 0][bcol] : &sB[brow][bcol];
-      put8(to, v);
-    }
-    if (k + 1 < chunks) load(first_of(k + 1));
-    if (kMode == kStates && c < p.D && (t0 - begin) % s.chunk == 0)
-      *reinterpret_cast<float4 *>(s.chunk_states + (b * s.all_chunks + t0 / s.chunk) * state + at) =
-          make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
-    __syncthreads();
-#pragma unroll 1
-    for (int i0 = 0; i0 < kTok; i0 += kLanes < 4 ? 4 : kLanes) {
-      constexpr int kStep = kLanes < 4 ? 4 : kLanes;
-      float y[kStep];
+    return;
+  }
+
+  // the recurrence
+  const int q = lane % kLanes, ch = (tid >> 5) * kPerWarp + lane / kLanes * 2;
+  const int c = cb * kCols + ch;  // and the next one; D is even
+  const int slot = step_slot(ch / 2);
+  const bool mine = c < p.D;
+  const long at = (long)c * DS + 4 * q;  // in a state
+  const long state = (long)p.D * DS;
+  float2 A[4], h[4];  // two channels of two pairs
+  auto get = [&](float2 (&v)[4], const float *from) {
 #pragma unroll
-      for (int j = 0; j < kStep; ++j) {
-        const int i = kRev ? kTok - 1 - (i0 + j) : i0 + j;
-        if (kMode == kStates && j % 8 == 0 && s.chunk < kTok && i > 0 && i % s.chunk == 0 && c < p.D && t0 + i < end)
-          *reinterpret_cast<float4 *>(s.chunk_states + (b * s.all_chunks + (t0 + i) / s.chunk) * state + at) =
-              make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
-        const float2 d = steps[i][ch];
-        const float4 bv = *reinterpret_cast<const float4 *>(&sB[i][4 * q]);
-        const float2 a0 = exp2_approx(__fmul2_rn(both(d.x), A[0])), a1 = exp2_approx(__fmul2_rn(both(d.x), A[1]));
-        const float2 u0 = __fmul2_rn(both(d.y), make_float2(bv.x, bv.y)), u1 = __fmul2_rn(both(d.y), make_float2(bv.z, bv.w));
-        if (kRev) {
-          h[0] = __fmul2_rn(a0, __fadd2_rn(h[0], u0)), h[1] = __fmul2_rn(a1, __fadd2_rn(h[1], u1));
-        } else {
-          h[0] = __ffma2_rn(a0, h[0], u0), h[1] = __ffma2_rn(a1, h[1], u1);
+    for (int i = 0; i < 2; ++i) {
+      const float4 f = *reinterpret_cast<const float4 *>(from + at + i * DS);
+      v[2 * i] = make_float2(f.x, f.y), v[2 * i + 1] = make_float2(f.z, f.w);
+    }
+  };
+  auto put = [&](float *to) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) st4(to + at + i * DS, h[2 * i].x, h[2 * i].y, h[2 * i + 1].x, h[2 * i + 1].y);
+  };
+#pragma unroll
+  for (int i = 0; i < 4; ++i) A[i] = h[i] = both(0.f);
+  if (mine) {
+    get(A, p.A);
+    const float *from = nullptr;
+    if (kMode == kOutputs || kMode == kStates) from = s.starts ? s.starts + (b * s.segs + seg) * state : p.S0 ? p.S0 + b * state : nullptr;
+    if (from) get(h, from);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) A[i] = __fmul2_rn(A[i], both(kLog2e));
+  for (int k = 0; k < chunks; ++k) {
+    Smem<DS, kMode> &in = m[k & 1];
+    const long t0 = first_of(k);
+    bar_sync<kThreads>(1 + (k & 1));
+    // two tokens' values ahead of their use: the compiler does not move loads across the stores of sums
+    struct Two {
+      float4 d[2], b[2], c[kMode == kOutputs ? 2 : 1];
+    };
+    auto token = [](int i) { return kRev ? kTok - 1 - i : i; };
+    auto fetch = [&](Two &v, int i0) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        v.d[j] = in.steps[token(i0 + j)][slot];
+        v.b[j] = *reinterpret_cast<const float4 *>(&in.B[token(i0 + j)][4 * q]);
+        if (kMode == kOutputs) v.c[j] = *reinterpret_cast<const float4 *>(&in.C[token(i0 + j)][4 * q]);
+      }
+    };
+    constexpr int kStep = kLanes < 4 ? 4 : kLanes;
+    Two now, then;
+    fetch(now, 0);
+#pragma unroll
+    for (int i0 = 0; i0 < kTok; i0 += kStep) {
+      float y[2 * kStep];  // of the first channel, of the second
+#pragma unroll
+      for (int f = 0; f < kStep; f += 2) {
+        if (i0 + f + 2 < kTok) fetch(then, i0 + f + 2);
+        float2 a[2][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) a[j][i] = exp2_approx(__fmul2_rn(both(i < 2 ? now.d[j].x : now.d[j].z), A[i]));
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if (kMode == kStates && (f + j) % 8 == 0) {
+            const int i = i0 + f + j;
+            if (i % s.chunk == 0 && mine && t0 + i < end) put(s.chunk_states + (b * s.all_chunks + (t0 + i) / s.chunk) * state);
+          }
+          const float2 bv[2] = {make_float2(now.b[j].x, now.b[j].y), make_float2(now.b[j].z, now.b[j].w)};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 u = both(i < 2 ? now.d[j].y : now.d[j].w);
+            h[i] = kRev ? __fmul2_rn(a[j][i], __ffma2_rn(u, bv[i & 1], h[i])) : __ffma2_rn(a[j][i], h[i], __fmul2_rn(u, bv[i & 1]));
+          }
+          if (kMode == kOutputs) {
+            const float2 cv[2] = {make_float2(now.c[j].x, now.c[j].y), make_float2(now.c[j].z, now.c[j].w)};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float2 yy = __ffma2_rn(h[2 * i + 1], cv[1], __fmul2_rn(h[2 * i], cv[0]));
+              y[i * kStep + f + j] = yy.x + yy.y;
+            }
+          }
         }
-        if (kMode == kOutputs) {
-          const float4 cv = *reinterpret_cast<const float4 *>(&sC[i][4 * q]);
-          const float2 yy = __ffma2_rn(h[1], make_float2(cv.z, cv.w), __fmul2_rn(h[0], make_float2(cv.x, cv.y)));
-          y[j] = yy.x + yy.y;
-        }
+        now = then;
       }
       if (kMode == kOutputs) {
-        spread_sum<kLanes, kStep, 1>(y, q);
-        if (kLanes >= 4) {
-          sums[i0 + q][ch] = y[0];
-        } else {
-          sums[i0 + q][ch] = y[0];
-          sums[i0 + 2 + q][ch] = y[1];
-        }
+        spread_sum<kLanes, 2 * kStep, 1>(y, q);
+        constexpr int kHave = kStep / kLanes;
+#pragma unroll
+        for (int v = 0; v < kHave; ++v)
+          *reinterpret_cast<float2 *>(&in.sums[i0 + v * kLanes + q][ch]) = make_float2(y[v], y[kHave + v]);
       }
     }
-    __syncthreads();
-    if (kMode == kOutputs) {
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        const int i = tid + g * kThreads;
-        const long t = t0 + (i >> 2);
-        if (i >= kTok * 4 || !live || t >= end) break;
-        const float4 y0 = *reinterpret_cast<const float4 *>(&sums[i >> 2][(tid & 3) * 8]);
-        const float4 y1 = *reinterpret_cast<const float4 *>(&sums[i >> 2][(tid & 3) * 8 + 4]);
-        float2 y[4] = {make_float2(y0.x, y0.y), make_float2(y0.z, y0.w), make_float2(y1.x, y1.y), make_float2(y1.z, y1.w)};
-        float2 xv[4], zv[4];
-        kx[g].get(xv), kz[g].get(zv);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          y[e] = __ffma2_rn(skip[e], xv[e], y[e]);
-          if (z) y[e] = __fmul2_rn(y[e], __fmul2_rn(zv[e], Sigmoid2(zv[e]).s));
-        }
-        put8((T *)p.out + (b * p.N + t) * p.D + c8, y);
-      }
-    }
+    bar_arrive<kThreads>(3 + (k & 1));
   }
-  const float4 hv = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
   if (kMode == kOutputs) {
-    if (seg == s.segs - 1 && c < p.D) *reinterpret_cast<float4 *>(p.S + b * state + at) = hv;
+    if (seg == s.segs - 1 && mine) put(p.S + b * state);
   } else if (kMode == kEnds || kRev) {
-    if (c < p.D) *reinterpret_cast<float4 *>((kRev ? s.rev_starts : s.starts) + (b * s.segs + seg) * state + at) = hv;
-    // sums of delta: the threads of the same eight channels in order
-    float *part = &steps[0][0].x;
-    static_assert(8 * kThreads <= 2 * kTok * kCols * (kThreads > 256 ? 2 : 1), "place for the sums");
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {  // neighbours in a warp first: lanes 4 apart have the same channels
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
-        total[e].x += __shfl_xor_sync(0xffffffffu, total[e].x, o);
-        total[e].y += __shfl_xor_sync(0xffffffffu, total[e].y, o);
-      }
-      if (lane < 4) {
-        part[warp * kCols + lane * 8 + 2 * e] = total[e].x;
-        part[warp * kCols + lane * 8 + 2 * e + 1] = total[e].y;
-      }
-    }
-    __syncthreads();
-    if (tid < kCols && cb * kCols + tid < p.D) {
-      float v = part[tid];
-#pragma unroll
-      for (int w = 1; w < kThreads / 32; ++w) v += part[w * kCols + tid];
-      (kRev ? s.rev_total : s.total)[(b * s.segs + seg) * p.D + cb * kCols + tid] = v;
-    }
+    if (mine) put((kRev ? s.rev_starts : s.starts) + (b * s.segs + seg) * state);
   }
 }
 
@@ -266,17 +331,18 @@ __global__ void __launch_bounds__(256) scan_join_kernel(const __grid_constant__ 
 template <typename T, int DS>
 cudaError_t launch_mode(const ScanProblem &p, ScanSplit s, int mode) {
   s.launched = mode == kEnds || mode == kReverseEnds ? s.segs - 1 : s.segs;
+  constexpr int kCols = scan_cols(DS);
   const long blocks = (long)p.B * s.launched * ((p.D + kCols - 1) / kCols);
+  const void *fn = mode == kOutputs ? (const void *)scan_kernel<T, DS, kOutputs>
+                   : mode == kEnds  ? (const void *)scan_kernel<T, DS, kEnds>
+                   : mode == kStates ? (const void *)scan_kernel<T, DS, kStates>
+                                     : (const void *)scan_kernel<T, DS, kReverseEnds>;
+  const int smem = 2 * (int)(mode == kOutputs ? sizeof(Smem<DS, kOutputs>) : sizeof(Smem<DS, kEnds>));
+  cudaError_t e = smem > 48 * 1024 ? ensure_smem_optin(fn, smem) : cudaSuccess;
+  if (e != cudaSuccess) return e;
   LaunchTimer timer(mode == kOutputs ? kKSelectiveScan : kKSelectiveState, p.stream);
-  if (mode == kOutputs)
-    scan_kernel<T, DS, kOutputs><<<(unsigned)blocks, 8 * DS, 0, p.stream>>>(p, s);
-  else if (mode == kEnds)
-    scan_kernel<T, DS, kEnds><<<(unsigned)blocks, 8 * DS, 0, p.stream>>>(p, s);
-  else if (mode == kStates)
-    scan_kernel<T, DS, kStates><<<(unsigned)blocks, 8 * DS, 0, p.stream>>>(p, s);
-  else
-    scan_kernel<T, DS, kReverseEnds><<<(unsigned)blocks, 8 * DS, 0, p.stream>>>(p, s);
-  const cudaError_t e = cudaGetLastError();
+  void *args[] = {const_cast<ScanProblem *>(&p), &s};
+  e = cudaLaunchKernel(fn, dim3((unsigned)blocks), dim3(kCols * DS / 8 + kAround), args, smem, p.stream);
   timer.done(e);
   if (e == cudaSuccess) count_launch();
   return e;
@@ -311,9 +377,10 @@ cudaError_t join(const ScanProblem &p, const ScanSplit &s, const float *from, bo
 ScanSplit scan_split(const ScanProblem &p) {
   ScanSplit s{};
   const long schedulers = 4L * std::max(1, device_info(-1).sm_count);
-  const long warps = (long)p.B * ((p.D + kCols - 1) / kCols) * (p.ds / 4);
+  const int cols = scan_cols(p.ds);
+  const long warps = (long)p.B * ((p.D + cols - 1) / cols) * (cols * p.ds / 256);  // of the recurrence
   long segs = 1;
-  if (warps < schedulers) segs = std::max(1L, std::min((2 * schedulers + warps - 1) / warps, p.N / 256));
+  if (warps < 3 * schedulers / 5) segs = std::max(1L, std::min((2 * schedulers + warps - 1) / warps, p.N / 256));
   s.len = (p.N + segs - 1) / segs;
   s.len = (s.len + kTok - 1) / kTok * kTok;
   s.segs = (int)std::max(1L, (p.N + s.len - 1) / s.len);

@@ -12,6 +12,7 @@
 //
 // Column sums dw, db leave each run once and are added in a fixed order by a second kernel.
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.h"
 #include "vec8.cuh"
@@ -22,8 +23,14 @@ __device__ unsigned int g_conv_step_status;
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kGradThreads = 128;
+constexpr int kV = 4;      // channels a thread of the passes over tokens
 constexpr int kAhead = 4;  // rows in flight a thread
+// Blocks an SM, and threads an SM that the tokens are cut for.  The forward wants many short runs (its registers leave
+// four blocks; 1024 threads an SM 52 us, 2048 47, 4096 42 at 4 x up to 8192 x 2048), the gradient one long run for
+// each thread that is resident (128 registers; 512 threads 96 us, 1024 104, 2048 123; three blocks of more
+// registers 122).
+constexpr int kPerSm = 4, kCutThreads = 4096, kCutThreadsGrad = 512;
 
 // V consecutive channels as loaded.
 template <typename T, int V>
@@ -111,10 +118,9 @@ struct Run {
 };
 
 template <typename T, int K>
-__global__ void __launch_bounds__(kThreads) short_conv_kernel(const __grid_constant__ ConvProblem p, int segs, int len) {
-  constexpr int V = 8;
-  const int groups = p.D / V;
-  const Run me(p, (long)blockIdx.x * kThreads + threadIdx.x, groups, segs, len);
+__global__ void __launch_bounds__(kThreads, kPerSm) short_conv_kernel(const __grid_constant__ ConvProblem p, int segs, int len) {
+  constexpr int V = kV;
+  const Run me(p, (long)blockIdx.x * kThreads + threadIdx.x, p.D / V, segs, len);
   if (!me.live || (me.t0 >= me.n && me.seg > 0)) return;
   const long c = (long)me.g * V;
   const T *x = (const T *)p.x + me.b * p.N * p.ldx + c;
@@ -145,65 +151,74 @@ __global__ void __launch_bounds__(kThreads) short_conv_kernel(const __grid_const
       r.store(S + i * p.D);
     }
   }
-  if (me.t0 >= me.t1) return;
+  const int count = (int)(me.t1 - me.t0);
+  if (count <= 0) return;
   float2 w[K][V / 2], bias[V / 2], v[K][V / 2];
   load_weights<K, V>(p.weight, p.bias, c, w, bias);
 #pragma unroll
   for (int i = 0; i < K - 1; ++i)
 #pragma unroll
     for (int e = 0; e < V / 2; ++e) v[i][e] = win[i].pair(e);
-  T *out = (T *)p.out + me.b * p.N * p.D + c;
+  T *out = (T *)p.out + (me.b * p.N + me.t0) * p.D + c;
+  x += me.t0 * p.ldx;
   Row<T, V> r[kAhead];
 #pragma unroll
   for (int u = 0; u < kAhead; ++u)
-    if (me.t0 + u < me.t1) r[u].load(x + (me.t0 + u) * p.ldx);
-  for (long t = me.t0; t < me.t1; t += kAhead) {
+    if (u < count) r[u].load(x + u * p.ldx);
+  for (int i0 = 0; i0 < count; i0 += kAhead) {
+    x += kAhead * p.ldx;
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      if (t + u >= me.t1) break;
+      if (i0 + u < count) {
 #pragma unroll
-      for (int e = 0; e < V / 2; ++e) v[K - 1][e] = r[u].pair(e);
-      if (t + u + kAhead < me.t1) r[u].load(x + (t + u + kAhead) * p.ldx);
-      Row<T, V> o;
+        for (int e = 0; e < V / 2; ++e) v[K - 1][e] = r[u].pair(e);
+        if (i0 + u + kAhead < count) r[u].load(x + u * p.ldx);
+        Row<T, V> o;
 #pragma unroll
-      for (int e = 0; e < V / 2; ++e) {
-        float2 a = bias[e];
+        for (int e = 0; e < V / 2; ++e) {
+          float2 a = bias[e];
 #pragma unroll
-        for (int j = 0; j < K; ++j) a = __ffma2_rn(w[j][e], v[j][e], a);
-        if (p.silu) a = __fmul2_rn(a, Sigmoid2(a).s);
-        o.set(e, a);
+          for (int j = 0; j < K; ++j) a = __ffma2_rn(w[j][e], v[j][e], a);
+          if (p.silu) a = __fmul2_rn(a, Sigmoid2(a).s);
+          o.set(e, a);
 #pragma unroll
-        for (int j = 0; j < K - 1; ++j) v[j][e] = v[j + 1][e];
+          for (int j = 0; j < K - 1; ++j) v[j][e] = v[j + 1][e];
+        }
+        o.store(out + (long)u * p.D);
       }
-      o.store(out + (t + u) * p.D);
     }
+    out += (long)kAhead * p.D;
   }
 }
 
 template <typename T, int K>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kGradThreads, kPerSm)
     short_conv_grad_kernel(const __grid_constant__ ConvGradProblem q, int segs, int len, float *sums) {
-  constexpr int V = 4;
+  constexpr int V = kV;
   const ConvProblem &p = q.p;
-  const int groups = p.D / V;
-  const Run me(p, (long)blockIdx.x * kThreads + threadIdx.x, groups, segs, len);
+  const Run me(p, (long)blockIdx.x * kGradThreads + threadIdx.x, p.D / V, segs, len);
   if (!me.live) return;
   const long c = (long)me.g * V;
   const T *x = (const T *)p.x + me.b * p.N * p.ldx + c;
-  const T *dy = (const T *)q.dout + me.b * p.N * p.D + c;
   T *dx = (T *)q.dx + me.b * p.N * p.D + c;
   const T *S0 = q.S0 ? (const T *)q.S0 + me.b * (K - 1) * p.D + c : nullptr;
   const T *dS = q.dS ? (const T *)q.dS + me.b * (K - 1) * p.D + c : nullptr;
   T *dS0 = q.dS0 ? (T *)q.dS0 + me.b * (K - 1) * p.D + c : nullptr;
-  float2 w[K][V / 2], bias[V / 2], v[K][V / 2], g[K][V / 2], dw[K][V / 2], db[V / 2];
-  load_weights<K, V>(p.weight, p.bias, c, w, bias);
+  float2 dw[K][V / 2], db[V / 2];
 #pragma unroll
   for (int e = 0; e < V / 2; ++e) {
     db[e] = both(0.f);
 #pragma unroll
-    for (int j = 0; j < K; ++j) dw[j][e] = g[j][e] = both(0.f);
+    for (int j = 0; j < K; ++j) dw[j][e] = both(0.f);
   }
-  if (me.t0 < me.t1 || (me.seg == 0 && dS0)) {
+  const int count = (int)max(me.t1 - me.t0, 0L);
+  if (count > 0 || (me.seg == 0 && dS0)) {
+    float2 w[K][V / 2], bias[V / 2], v[K][V / 2], g[K][V / 2];
+    load_weights<K, V>(p.weight, p.bias, c, w, bias);
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e)
+#pragma unroll
+      for (int j = 0; j < K; ++j) g[j][e] = both(0.f);
 #pragma unroll
     for (int i = 0; i < K - 1; ++i) {
       const long t = me.t0 - (K - 1) + i;
@@ -216,55 +231,73 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
       for (int e = 0; e < V / 2; ++e) v[i][e] = r.pair(e);
     }
+    // Step i takes token t0 + i and completes row t0 + i - (K - 1) of dx, which lacks no later g.  The rows in front
+    // of the first are the carried window's, and the K - 1 last steps only finish rows.
+    const int steps = count + K - 1, there = (int)min(me.n - me.t0, (long)steps);
+    const int carried = dS ? (int)min(me.n - me.t0, 0x3fffffffL) : 0x3fffffff;  // from that step on dS adds
+    const T *xi = x + me.t0 * p.ldx, *yi = (const T *)q.dout + (me.b * p.N + me.t0) * p.D + c;
+    T *o = dx + (me.t0 - (K - 1)) * p.D;
     Row<T, V> rx[kAhead], ry[kAhead];
-    auto load = [&](int u, long t) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
       rx[u].zero(), ry[u].zero();
-      if (t < me.n) rx[u].load(x + t * p.ldx), ry[u].load(dy + t * p.D);
-    };
-    // row t of dx is complete with g of token t + K - 1; rows in front of the first are the carried window's
-    const long end = max(me.t1, me.t0) + K - 1;
+      if (u < there) rx[u].load(xi + u * p.ldx), ry[u].load(yi + (long)u * p.D);
+    }
+    // one step; kInside: nothing about it is special
+    auto step = [&](auto inside, int i, int u) {
+      constexpr bool kInside = decltype(inside)::value;
+      float2 gg[V / 2];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) load(u, me.t0 + u);
-    for (long s0 = me.t0; s0 < end; s0 += kAhead) {
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const long s = s0 + u, t = s - (K - 1);
-        if (s >= end) break;
-        float2 dyv[V / 2];
-#pragma unroll
-        for (int e = 0; e < V / 2; ++e) v[K - 1][e] = rx[u].pair(e), dyv[e] = ry[u].pair(e);
-        load(u, s + kAhead < end ? s + kAhead : me.n);
-        const bool put = t >= me.t0 || (me.seg == 0 && (t >= 0 || dS0));
-        Row<T, V> o, ds;
-        ds.zero();
-        const long from_end = t - (me.n - (K - 1));  // the window that the call carries on gives its gradient
-        if (dS && put && from_end >= 0 && from_end < K - 1) ds.load(dS + from_end * p.D);
-#pragma unroll
-        for (int e = 0; e < V / 2; ++e) {
-          float2 gg = dyv[e];
-          if (p.silu) {
-            float2 a = bias[e];
-#pragma unroll
-            for (int j = 0; j < K; ++j) a = __ffma2_rn(w[j][e], v[j][e], a);
-            const Sigmoid2 sg(a);
-            gg = __fmul2_rn(gg, __ffma2_rn(__fmul2_rn(a, sg.s), sg.one_less(), sg.s));
-          }
-          if (s >= me.n) gg = both(0.f);  // nothing is there, and bias alone may not be finite
-          if (s < me.t1) {
-#pragma unroll
-            for (int j = 0; j < K; ++j) dw[j][e] = __ffma2_rn(gg, v[j][e], dw[j][e]);
-            db[e] = __fadd2_rn(db[e], gg);
-          }
-#pragma unroll
-          for (int j = 0; j < K - 1; ++j) g[j][e] = g[j + 1][e], v[j][e] = v[j + 1][e];
-          g[K - 1][e] = gg;
-          float2 d = ds.pair(e);
-#pragma unroll
-          for (int j = 0; j < K; ++j) d = __ffma2_rn(w[j][e], g[K - 1 - j][e], d);
-          o.set(e, d);
-        }
-        if (put) o.store(t >= 0 ? dx + t * p.D : dS0 + (t + K - 1) * p.D);
+      for (int e = 0; e < V / 2; ++e) v[K - 1][e] = rx[u].pair(e), gg[e] = ry[u].pair(e);
+      if (i + kAhead < there) {
+        rx[u].load(xi + u * p.ldx), ry[u].load(yi + (long)u * p.D);
+      } else if (!kInside) {
+        rx[u].zero(), ry[u].zero();
       }
+      Row<T, V> ds, to;
+      if (!kInside) {
+        ds.zero();
+        if (i >= carried && i - carried < K - 1) ds.load(dS + (long)(i - carried) * p.D);
+      }
+#pragma unroll
+      for (int e = 0; e < V / 2; ++e) {
+        if (p.silu) {
+          float2 a = bias[e];
+#pragma unroll
+          for (int j = 0; j < K; ++j) a = __ffma2_rn(w[j][e], v[j][e], a);
+          const Sigmoid2 sg(a);
+          gg[e] = __fmul2_rn(gg[e], __ffma2_rn(__fmul2_rn(a, sg.s), sg.one_less(), sg.s));
+        }
+        if (!kInside && i >= there) gg[e] = both(0.f);  // nothing is there, and bias alone may not be finite
+        if (kInside || i < count) {
+#pragma unroll
+          for (int j = 0; j < K; ++j) dw[j][e] = __ffma2_rn(gg[e], v[j][e], dw[j][e]);
+          db[e] = __fadd2_rn(db[e], gg[e]);
+        }
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) g[j][e] = g[j + 1][e], v[j][e] = v[j + 1][e];
+        g[K - 1][e] = gg[e];
+        float2 d = kInside ? both(0.f) : ds.pair(e);
+#pragma unroll
+        for (int j = 0; j < K; ++j) d = __ffma2_rn(w[j][e], g[K - 1 - j][e], d);
+        to.set(e, d);
+      }
+      if (kInside || i >= K - 1)
+        to.store(o + (long)u * p.D);
+      else if (me.seg == 0 && dS0)
+        to.store(dS0 + (long)i * p.D);
+    };
+    for (int i0 = 0; i0 < steps; i0 += kAhead) {
+      xi += kAhead * p.ldx, yi += (long)kAhead * p.D;
+      if (i0 >= K - 1 && i0 + kAhead <= min(count, carried)) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) step(std::true_type{}, i0 + u, u);
+      } else {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+          if (i0 + u < steps) step(std::false_type{}, i0 + u, u);
+      }
+      o += (long)kAhead * p.D;
     }
   }
   Row<T, V> none;
@@ -320,19 +353,18 @@ __global__ void __launch_bounds__(kThreads) short_conv_step_kernel(const __grid_
   o.store((T *)p.out + (long)b * p.D + c);
 }
 
-// Runs of tokens: enough threads to fill the SMs (1024 each), but at least kMinRun tokens a run, whose
-// K - 1 extra rows then cost at most a fifth more reads, from L2.
+// Runs of tokens: at least kMinRun, so that their K - 1 extra rows cost at most a fifth more reads, from L2.
 constexpr int kMinRun = 16;
-int run_length(const ConvProblem &p, int v) {
-  const long threads = (long)std::max(1, device_info(-1).sm_count) * 1024;
-  const long len = ((long)p.B * (p.D / v) * p.N + threads - 1) / threads;
+int run_length(const ConvProblem &p, int per_sm) {
+  const long threads = (long)std::max(1, device_info(-1).sm_count) * per_sm;
+  const long len = ((long)p.B * (p.D / kV) * p.N + threads - 1) / threads;
   return (int)std::max<long>(kMinRun, std::min<long>(len, p.N));
 }
 
 template <typename T, int K>
 cudaError_t launch_fwd(const ConvProblem &p) {
-  const int len = run_length(p, 8), segs = (int)((p.N + len - 1) / len);
-  const long units = (long)p.B * segs * (p.D / 8);
+  const int len = run_length(p, kCutThreads), segs = (int)((p.N + len - 1) / len);
+  const long units = (long)p.B * segs * (p.D / kV);
   LaunchTimer timer(kKShortConv, p.stream);
   short_conv_kernel<T, K><<<(unsigned)((units + kThreads - 1) / kThreads), kThreads, 0, p.stream>>>(p, segs, len);
   const cudaError_t e = cudaGetLastError();
@@ -344,12 +376,12 @@ cudaError_t launch_fwd(const ConvProblem &p) {
 template <typename T, int K>
 cudaError_t launch_grad(const ConvGradProblem &q) {
   const ConvProblem &p = q.p;
-  const int len = run_length(p, 4), segs = (int)((p.N + len - 1) / len);
-  const long units = (long)p.B * segs * (p.D / 4);
+  const int len = run_length(p, kCutThreadsGrad), segs = (int)((p.N + len - 1) / len);
+  const long units = (long)p.B * segs * (p.D / kV);
   const bool sums = q.dweight || q.dbias;
   LaunchTimer timer(kKShortConvBackward, p.stream);
   short_conv_grad_kernel<T, K>
-      <<<(unsigned)((units + kThreads - 1) / kThreads), kThreads, 0, p.stream>>>(q, segs, len, sums ? q.ws : nullptr);
+      <<<(unsigned)((units + kGradThreads - 1) / kGradThreads), kGradThreads, 0, p.stream>>>(q, segs, len, sums ? q.ws : nullptr);
   cudaError_t e = cudaGetLastError();
   timer.done(e);
   if (e != cudaSuccess) return e;
@@ -384,7 +416,7 @@ cudaError_t launch_short_conv(const ConvProblem &p) {
 }
 
 size_t short_conv_grad_workspace(const ConvProblem &p) {
-  const int len = run_length(p, 4);
+  const int len = run_length(p, kCutThreadsGrad);
   return sizeof(float) * (size_t)p.B * ((p.N + len - 1) / len) * (p.K + 1) * p.D;
 }
 
