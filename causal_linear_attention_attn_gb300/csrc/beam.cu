@@ -5,12 +5,13 @@
 // in 64 bits (near a border the rounding of 32 bits would choose), ties to the lowest w V + v.  Within a beam the
 // order is that of the logits, so the k best of each row are enough; HBM bounds it: the logits once.
 //
-// A block takes a run of one row in chunks of 8192 values held in registers, adds up its exponentials against a
-// running maximum, and keeps candidates for the k best: each thread's largest value of the chunk, sorted across the
-// warp's lanes, gives a value that at least k of the warp's values reach; the largest such bound of all warps and
-// chunks lets a few dozen of the 8192 through.  Those are ranked by counting (every candidate against every other), not
-// extracted one after another.  A second kernel, a block a group, joins the runs of a row and the rows of the
-// group the same way in 64 bits.
+// A block takes a run of one row in chunks of 4096 values, its warps an eighth of each, without waiting for one
+// another: a warp keeps 512 values in registers while the next ones are on their way, adds up their exponentials
+// against its running maximum, and keeps a list of candidates for its k best.  The bound that lets values into
+// the list is its k-th best so far; before there is one, the k-th largest of the lanes' largest values, sorted across
+// the lanes, is a value that at least k reach.  Lists are ranked by counting (every candidate against every other), not
+// extracted one after another.  A second kernel, a block a group, joins the runs of a row and the rows of the group the
+// same way in 64 bits.
 //
 // Reordering.  A beam's first child keeps the slot of its state in every pool; its other children get the
 // slots of the group's childless beams, with a copy.  So the states move no more than they must, in place:
@@ -18,7 +19,7 @@
 #include <algorithm>
 
 #include "internal.h"
-#include "vec8.cuh"
+#include "selective.cuh"
 
 namespace la {
 
@@ -27,20 +28,15 @@ __device__ unsigned int g_beam_status;
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kPer = 32;                  // values a thread and chunk
+constexpr int kPer = 16;                  // values a thread and chunk
 constexpr int kChunk = kThreads * kPer;   // values a chunk
-constexpr int kCap = 1024;                // candidates of a block
-constexpr int kCompact = 256;             // more than these are ranked before the next chunk
+constexpr int kCap = 256;                 // candidates of a warp
 constexpr int kMaxK = 64;
 
 // NaN counts as -inf, inf as the largest finite number: infinite logits share the probability.
 __device__ __forceinline__ float clean(float x) { return fminf(fmaxf(x, -INFINITY), 3.402823466e38f); }
 // e^(x - top), top finite
-__device__ __forceinline__ float exp_under(float x, float top) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"((x - top) * 1.44269504f));
-  return y;
-}
+__device__ __forceinline__ float exp_under(float x, float top) { return exp2_approx((x - top) * kLog2e); }
 // Clean floats in order as unsigned numbers, all above 0 (no value); -0 as 0: they are equal.
 __device__ __forceinline__ uint32_t ordered(float x) {
   const uint32_t u = __float_as_uint(x + 0.f);
@@ -75,21 +71,22 @@ template <typename T>
 struct Chunk {  // a thread's kPer values: groups of kVec neighbours (16 bytes), kThreads groups apart
   static constexpr int kVec = 16 / (int)sizeof(T), kVecs = kPer / kVec;
   uint4 a[kVecs];
-  // from place `at` behind base (aligned to 16 bytes): groups that begin before `row_end`, and nothing past `last`,
-  // the end of the logits.
-  __device__ __forceinline__ void load(const T *base, long at, const T *row_end, const T *last) {
+  // from place `at` of a row of n values.  Rows off 16-byte borders are loaded value by value, to the same lanes: equal
+  // rows have equal sums then, to the last bit, and their ties are ties.
+  __device__ __forceinline__ void load(const T *row, long at, long n) {
+    const T *p = row + at + threadIdx.x * kVec;
+    if ((reinterpret_cast<uintptr_t>(row) & 15) == 0 && at + kChunk <= n) {
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j) {
-      const T *p = base + at + ((long)j * kThreads + threadIdx.x) * kVec;
-      a[j] = make_uint4(0u, 0u, 0u, 0u);
-      if (p >= row_end) continue;
-      if (p + kVec <= last) {
-        a[j] = __ldcs(reinterpret_cast<const uint4 *>(p));
-      } else {
+      for (int j = 0; j < kVecs; ++j) a[j] = __ldcs(reinterpret_cast<const uint4 *>(p + j * kThreads * kVec));
+    } else {
+      const int left = (int)min(n - at, (long)kChunk) - (int)threadIdx.x * kVec;
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j) {
+        a[j] = make_uint4(0u, 0u, 0u, 0u);
         T *e = reinterpret_cast<T *>(&a[j]);
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
-          if (p + i < last) e[i] = p[i];
+          if (j * kThreads * kVec + i < left) e[i] = p[j * kThreads * kVec + i];
       }
     }
   }
@@ -103,27 +100,47 @@ struct Chunk {  // a thread's kPer values: groups of kVec neighbours (16 bytes),
 };
 
 struct RowSmem {
-  Cand list[kCap], best[kMaxK];
-  float bound[kWarps], top[kWarps], sum[kWarps];
-  float threshold;
-  int count;
+  Cand list[kWarps][kCap], best[kWarps][kMaxK];
+  float top[kWarps], sum[kWarps];
+  int count[kWarps], total;
+  uint32_t bound;  // what at least k of the block's values reach, in order; 0: nothing yet
 };
 
-// The k best of the list, in order, to best (key 0 behind the last); all threads.
-__device__ __forceinline__ void rank_list(RowSmem &m, int n, int k) {
-  if (threadIdx.x < kMaxK) m.best[threadIdx.x] = Cand{0u, 0u};
-  __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const Cand c = m.list[i];
+// The k best of a list of n, in order (key 0 behind the last); all of `threads` threads, of which this is number `at`.
+__device__ __forceinline__ void rank_list(const Cand *list, int n, int k, Cand *best, int at, int threads) {
+  for (int i = max(n, 0) + at; i < k; i += threads) best[i] = Cand{0u, 0u};
+  for (int i = at; i < n; i += threads) {
+    const Cand c = list[i];
     int r = 0;
-    for (int j = 0; j < n; ++j) r += before(m.list[j], c);
-    if (r < k) m.best[r] = c;
+    for (int j = 0; j < n; ++j) r += before(list[j], c);
+    if (r < k) best[r] = c;
   }
-  __syncthreads();
+}
+
+// Places of the block's candidates, the k best of each warp, among all of them: put(candidate, its place).
+template <typename Put>
+__device__ __forceinline__ void place_candidates(const RowSmem &m, int k, Put &&put) {
+  for (int i = threadIdx.x; i < kWarps * k; i += kThreads) {
+    const Cand c = m.best[i / k][i % k];
+    if (c.key == 0) continue;
+    int r = 0;  // its places in the warps' lists together
+    for (int w = 0; w < kWarps; ++w) {
+      int lower = 0, upper = k;  // the first of the list that it is not behind
+      while (lower < upper) {
+        const int mid = (lower + upper) / 2;
+        if (before(m.best[w][mid], c))
+          lower = mid + 1;
+        else
+          upper = mid;
+      }
+      r += lower;
+    }
+    if (r < k) put(c, r);
+  }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) beam_rows_kernel(const __grid_constant__ BeamProblem p, const __grid_constant__ BeamSplit s) {
+__global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const __grid_constant__ BeamProblem p, const __grid_constant__ BeamSplit s) {
   __shared__ RowSmem m;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long row = blockIdx.x / s.runs;
@@ -150,191 +167,217 @@ __global__ void __launch_bounds__(kThreads) beam_rows_kernel(const __grid_consta
     }
     return;
   }
-  const T *base = (const T *)p.logits + row * p.ld, *last = (const T *)p.logits + ((long)p.G * p.W - 1) * p.ld + p.V;
-  const int off = (int)((reinterpret_cast<uintptr_t>(base) & 15) / sizeof(T));
-  base -= off;
-  // places [off, off + V) behind base are the row's; this run's are whole chunks of them
-  const long first = (long)run * s.run_chunks * kChunk, end = min(first + (long)s.run_chunks * kChunk, (long)off + p.V);
-  const T *row_end = base + off + p.V;
-  if (tid == 0) m.count = 0, m.threshold = -INFINITY;
-  float top = -INFINITY, sum = 0.f;  // the warp's running maximum; this thread's sum against it
-  const int share = k > 32 ? 2 : 1, each = (k + share - 1) / share;  // a bound takes `each` values of `share` warps
-  // if fewer than k values are above -inf, then of those at -inf only the run's first 2 k can be needed
-  const long few = max(first, (long)off) + 2 * k;
-  Chunk<T> next;
-  if (first < end) next.load(base, first, row_end, last);
+  const T *logits = (const T *)p.logits + row * p.ld;
+  const long first = (long)run * s.run_chunks * kChunk, end = min(first + (long)s.run_chunks * kChunk, p.V);
+  Cand *list = m.list[warp], *best = m.best[warp];
+  int &count = m.count[warp];
+  if (lane == 0) count = 0;
+  if (tid == 0) m.bound = 0, m.total = 0;
   __syncthreads();
+  float top = -INFINITY, sum = 0.f;  // the warp's running maximum; this lane's sum against it
+  int n = 0;                         // candidates in the list
+  // if fewer than k values are above -inf, then of those at -inf only the run's first 2 k can be needed
+  const long few = first + 2 * k;
+  Chunk<T> next;
+  if (first < end) next.load(logits, first, end);
   for (long at = first; at < end; at += kChunk) {
     const Chunk<T> c = next;
-    if (at + kChunk < end) next.load(base, at + kChunk, row_end, last);
-    const int lo = (int)max(0L, off - at), hi = (int)min((long)kChunk, end - at);  // the row's places in this chunk
-    const bool whole = lo == 0 && hi == kChunk;
-    auto inside = [&](int i) { return whole || (c.place(i) >= lo && c.place(i) < hi); };
-    auto value = [&](int i) { return inside(i) ? c.value(i) : -INFINITY; };
-    float mine = -INFINITY;
+    if (at + kChunk < end) next.load(logits, at + kChunk, end);
+    const int size = (int)min((long)kChunk, end - at);
+    auto inside = [&](int i) { return c.place(i) < size; };
+    float v[kPer];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) mine = fmaxf(mine, value(i));
-    mine = clean(mine);
-    const float sorted = warp_sort(mine, lane);
-    const float new_top = fmaxf(top, __shfl_sync(0xffffffffu, sorted, 0));
+    for (int i = 0; i < kPer; ++i) v[i] = c.value(i);
+    if (size < kChunk) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (!inside(i)) v[i] = -INFINITY;
+    }
+    constexpr int kPart = 8;  // values a part, whose largest is kept
+    float most[kPer / kPart];
+#pragma unroll
+    for (int g = 0; g < kPer / kPart; ++g) {
+      most[g] = v[g * kPart];
+#pragma unroll
+      for (int i = 1; i < kPart; ++i) most[g] = fmaxf(most[g], v[g * kPart + i]);
+    }
+    float mine = most[0];
+#pragma unroll
+    for (int g = 1; g < kPer / kPart; ++g) mine = fmaxf(mine, most[g]);
+    bool odd = !(mine < INFINITY);  // an inf is there (a NaN shows in the sum)
+    const float new_top = fmaxf(top, unordered(__reduce_max_sync(0xffffffffu, ordered(clean(mine)))));
     if (new_top > -INFINITY) {
-      float part[4] = {0.f, 0.f, 0.f, 0.f};
+      float2 part[2] = {both(0.f), both(0.f)};
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) part[i & 3] += exp_under(value(i), new_top);
-      float all = (part[0] + part[1]) + (part[2] + part[3]);
-      if (!(all < INFINITY)) {  // a NaN or inf among them
+      for (int i = 0; i < kPer; i += 2) {
+        const float2 d = __fmul2_rn(__fadd2_rn(make_float2(v[i], v[i + 1]), both(-new_top)), both(kLog2e));
+        part[i >> 1 & 1] = __fadd2_rn(part[i >> 1 & 1], exp2_approx(d));
+      }
+      float all = (part[0].x + part[0].y) + (part[1].x + part[1].y);
+      odd |= !(all < INFINITY);
+      if (odd) {
         all = 0.f;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) all += exp_under(clean(value(i)), new_top);
+        for (int i = 0; i < kPer; ++i) v[i] = clean(v[i]), all += exp_under(v[i], new_top);
+#pragma unroll
+        for (int g = 0; g < kPer / kPart; ++g) most[g] = clean(most[g]);
       }
       sum = sum * exp_under(top, new_top) + all;
+    } else {  // all -inf or NaN
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) v[i] = -INFINITY;
+#pragma unroll
+      for (int g = 0; g < kPer / kPart; ++g) most[g] = -INFINITY;
     }
+    mine = clean(mine);
     top = new_top;
-    if (lane == each - 1) m.bound[warp] = sorted;
-    __syncthreads();
-    float b1 = -INFINITY, b2 = -INFINITY;  // the two largest of the warps' bounds
+    const uint32_t key = *(volatile uint32_t *)&m.bound;
+    float bound = key ? unordered(key) : -INFINITY;
+    if (bound == -INFINITY) {  // one from these values alone: at least k reach it
+      float x = mine;
+      if (k > 32) {  // two of each lane: its second largest
+        float largest = -INFINITY;
+        x = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float b = m.bound[w];
-      b2 = fmaxf(b2, fminf(b1, b)), b1 = fmaxf(b1, b);
+        for (int i = 0; i < kPer; ++i) x = fmaxf(x, fminf(largest, v[i])), largest = fmaxf(largest, v[i]);
+      }
+      bound = __shfl_sync(0xffffffffu, warp_sort(x, lane), (k > 32 ? (k + 1) / 2 : k) - 1);
     }
-    const float bound = fmaxf(m.threshold, share == 2 ? b2 : b1);
-    const int had = m.count;
-    __syncthreads();
-    if (mine >= bound) {
+    if (__any_sync(0xffffffffu, mine >= bound && (mine > -INFINITY || at < few))) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const float v = clean(value(i));
-        const long place = at + c.place(i);
-        if (v >= bound && inside(i) && (v > -INFINITY || place < few)) {
-          const int n = atomicAdd(&m.count, 1);
-          if (n < kCap) m.list[n] = Cand{ordered(v), (uint32_t)(place - off)};
+      for (int g = 0; g < kPer / kPart; ++g) {
+        if (!(most[g] >= bound)) continue;
+#pragma unroll
+        for (int j = 0; j < kPart; ++j) {
+          const int i = g * kPart + j;
+          if (v[i] >= bound && (v[i] > -INFINITY || (at + c.place(i) < few && inside(i)))) {
+            const int o = atomicAdd(&count, 1);
+            if (o < kCap) list[o] = Cand{ordered(v[i]), (uint32_t)at + c.place(i)};
+          }
         }
       }
-    }
-    __syncthreads();
-    int n = m.count;
-    bool ranked = false;
-    if (n > kCap) {
-      // too many equal values: the k best of what the list had and of this chunk, one after another
-      Cand prev{0xffffffffu, 0u};
-      n = 0;
-      for (; n < k; ++n) {
-        Cand best{0u, 0xffffffffu};
-        for (int i = tid; i < had; i += kThreads)
-          if (before(prev, m.list[i]) && before(m.list[i], best)) best = m.list[i];
+      __syncwarp();
+      const int had = n;
+      n = count;
+      bool ranked = false;
+      if (n > kCap) {
+        // too many equal values: the k best of what the list had and of these, one after another
+        Cand prev{0xffffffffu, 0u};
+        for (n = 0; n < k; ++n) {
+          Cand x{0u, 0xffffffffu};
+          for (int i = lane; i < had; i += 32)
+            if (before(prev, list[i]) && before(list[i], x)) x = list[i];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const Cand x{ordered(clean(value(i))), (uint32_t)(at + c.place(i) - off)};
-          if (inside(i) && before(prev, x) && before(x, best)) best = x;
+          for (int i = 0; i < kPer; ++i) {
+            const Cand y{ordered(v[i]), (uint32_t)at + c.place(i)};
+            if (inside(i) && before(prev, y) && before(y, x)) x = y;
+          }
+          prev.key = __reduce_max_sync(0xffffffffu, x.key);
+          prev.token = __reduce_min_sync(0xffffffffu, x.key == prev.key ? x.token : 0xffffffffu);
+          if (prev.key == 0) break;
+          if (lane == 0) best[n] = prev;
         }
-        const uint32_t key = __reduce_max_sync(0xffffffffu, best.key);
-        const uint32_t token = __reduce_min_sync(0xffffffffu, best.key == key ? best.token : 0xffffffffu);
-        if (lane == 0) m.list[had + warp] = Cand{key, token};  // had <= kCompact
-        __syncthreads();
-        prev = m.list[had];
-        for (int w = 1; w < kWarps; ++w)
-          if (before(m.list[had + w], prev)) prev = m.list[had + w];
-        if (tid == 0) m.best[n] = prev;
-        __syncthreads();
-        if (prev.key == 0) break;
+        ranked = true;
+      } else if (n >= k + 16) {
+        rank_list(list, n, k, best, lane, 32);
+        n = k;
+        ranked = true;
       }
-      ranked = true;
-    } else if (n > kCompact) {
-      rank_list(m, n, k);
-      n = min(n, k);
-      ranked = true;
+      if (ranked) {
+        __syncwarp();
+        for (int i = lane; i < n; i += 32) list[i] = best[i];
+        if (lane == 0) {
+          count = n;
+          if (n == k) atomicMax(&m.bound, best[k - 1].key);
+        }
+        __syncwarp();
+      }
     }
-    if (ranked && tid < n) m.list[tid] = m.best[tid];
-    __syncthreads();
-    if (tid == 0) {
-      m.count = n;
-      m.threshold = ranked && n == k ? fmaxf(bound, unordered(m.list[n - 1].key)) : bound;
+    if (at == first && at + kChunk < end) {  // the block's k-th best of the first chunk bounds the others
+      rank_list(list, n, k, best, lane, 32);
+      __syncthreads();
+      place_candidates(m, k, [&](const Cand &x, int r) {
+        if (r == k - 1) atomicMax(&m.bound, x.key);
+      });
+      __syncthreads();
     }
-    __syncthreads();
   }
-  rank_list(m, m.count, k);
-  if (tid < k) out[tid] = m.best[tid];
-  // the row's maximum and sum over the block
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // not before: its blocks would take the others' places
+  rank_list(list, n, k, best, lane, 32);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) m.top[warp] = top, m.sum[warp] = sum;
+  if (lane == 0) m.top[warp] = top, m.sum[warp] = sum, atomicAdd(&m.total, min(n, k));
   __syncthreads();
-  if (tid == 0) {
-    float t = m.top[0], z = 0.f;
-    for (int w = 1; w < kWarps; ++w) t = fmaxf(t, m.top[w]);
-    for (int w = 0; w < kWarps; ++w)
-      if (m.top[w] > -INFINITY) z += m.sum[w] * exp_under(m.top[w], t);
-    stat[0] = t, stat[1] = z;
+  if (warp == 0) {
+    const float t0 = lane < kWarps ? m.top[lane] : -INFINITY;
+    const float t = unordered(__reduce_max_sync(0xffffffffu, ordered(t0)));
+    float z = t0 > -INFINITY ? m.sum[lane] * exp_under(t0, t) : 0.f;
+#pragma unroll
+    for (int o = kWarps / 2; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    if (lane == 0) stat[0] = t, stat[1] = z;
   }
+  place_candidates(m, k, [&](const Cand &x, int r) { out[r] = x; });
+  if (tid < k && tid >= m.total) out[tid] = Cand{0u, 0u};  // fewer than k values in the run
 }
 
+// A continuation: its score in order as an unsigned number (0: none), its beam and token.
 struct Scored {
-  double score;
-  long flat;  // w V + v, or -1: none
+  unsigned long long key;
+  uint32_t beam, token;
 };
 __device__ __forceinline__ bool before(const Scored &a, const Scored &b) {
-  if (a.flat < 0 || b.flat < 0) return b.flat < 0 && a.flat >= 0;
-  return a.score > b.score || (a.score == b.score && a.flat < b.flat);
+  return a.key > b.key ||
+         (a.key == b.key && ((unsigned long long)a.beam << 32 | a.token) < ((unsigned long long)b.beam << 32 | b.token));
+}
+__device__ __forceinline__ unsigned long long ordered(double x) {
+  const unsigned long long u = (unsigned long long)__double_as_longlong(x + 0.);
+  return u >> 63 ? ~u : u | 1ull << 63;
+}
+__device__ __forceinline__ double unordered(unsigned long long k) {
+  return __longlong_as_double((long long)(k >> 63 ? k & ~(1ull << 63) : ~k));
 }
 
 constexpr int kJoinCap = 1024;
 
+// Its time is that of its few 64-bit floating-point instructions one behind the other (this GPU issues one a
+// warp in 64 cycles): a logarithm a row, three sums a candidate.
 __global__ void __launch_bounds__(kThreads) beam_join_kernel(const __grid_constant__ BeamProblem p, const __grid_constant__ BeamSplit s) {
-  __shared__ double top[kMaxK], log_sum[kMaxK];
+  __shared__ double top[kMaxK], log_sum[kMaxK], score[kMaxK];
   __shared__ Scored list[kJoinCap], warp_best[kWarps];
+  __shared__ uint32_t bound;  // of the keys' upper halves
   __shared__ int count;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = p.k;
   const long g = blockIdx.x;
   const Cand *cands = reinterpret_cast<const Cand *>(s.cands) + g * p.W * s.runs * k;
+  if (tid == 0) count = 0, bound = 0;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the runs' kernel is through
   for (int w = warp; w < p.W; w += kWarps) {
-    const float *st = s.stats + (g * p.W + w) * s.runs * 2;
-    float t = -INFINITY;
-    for (int r = lane; r < s.runs; r += 32) t = fmaxf(t, st[2 * r]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
-    double z = 0.;
+    const float2 *st = reinterpret_cast<const float2 *>(s.stats) + (g * p.W + w) * s.runs;
+    float t = -INFINITY, z = 0.f;
+    for (int r = lane; r < s.runs; r += 32) t = fmaxf(t, st[r].x);
+    t = unordered(__reduce_max_sync(0xffffffffu, ordered(t)));
     for (int r = lane; r < s.runs; r += 32)
-      if (st[2 * r] > -INFINITY) z += (double)st[2 * r + 1] * (st[2 * r] == t ? 1. : exp((double)st[2 * r] - (double)t));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-    if (lane == 0) top[w] = t, log_sum[w] = log(z);
+      if (st[r].x > -INFINITY) z += st[r].y * exp_under(st[r].x, t);
+    z = warp_sum(z);
+    if (lane == 0) top[w] = t, log_sum[w] = log((double)z), score[w] = p.scores[g * p.W + w];
   }
-  if (tid == 0) count = 0;
   __syncthreads();
-  const int lists = p.W * s.runs;
-  auto scored = [&](int l, int i) {
-    const Cand c = cands[(long)l * k + i];
-    if (c.key == 0) return Scored{0., -1};
-    const int w = l / s.runs;
-    const double score = c.key == kMinusInf ? -INFINITY
-                                            : (double)p.scores[g * p.W + w] + (((double)unordered(c.key) - top[w]) - log_sum[w]);
-    return Scored{score, (long)w * p.V + c.token};
+  const unsigned per_row = s.runs * k, all = p.W * per_row;
+  auto scored = [&](unsigned i) {
+    const Cand c = cands[i];
+    if (c.key == 0) return Scored{0, ~0u, ~0u};
+    const unsigned w = i / per_row;
+    const double x = c.key == kMinusInf ? -INFINITY : score[w] + (((double)unordered(c.key) - top[w]) - log_sum[w]);
+    return Scored{ordered(x), w, c.token};
   };
-  auto block_best = [&](Scored b) {  // the first in order of all threads'
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const Scored x{__shfl_xor_sync(0xffffffffu, b.score, o), __shfl_xor_sync(0xffffffffu, b.flat, o)};
-      if (before(x, b)) b = x;
-    }
-    __syncthreads();
-    if (lane == 0) warp_best[warp] = b;
-    __syncthreads();
-    b = warp_best[0];
-    for (int w = 1; w < kWarps; ++w)
-      if (before(warp_best[w], b)) b = warp_best[w];
-    return b;
-  };
-  // no list's last candidate may be beaten by a chosen one's successor: what comes before the best of them is enough
-  Scored bound{0., -1};
-  for (int l = tid; l < lists; l += kThreads) {
-    const Scored x = scored(l, k - 1);
-    if (before(x, bound)) bound = x;
-  }
-  bound = block_best(bound);
-  for (int i = tid; i < lists * k; i += kThreads) {
-    const Scored x = scored(i / k, i % k);
-    if (x.flat >= 0 && !before(bound, x)) {
+  // at least k continuations reach the best of the lists' last ones; the first kThreads continuations stay in registers
+  const Scored mine = tid < all ? scored(tid) : Scored{0, ~0u, ~0u};
+  for (unsigned i = tid; i < all; i += kThreads)
+    if (i % k == k - 1) atomicMax(&bound, (uint32_t)((i < kThreads ? mine : scored(i)).key >> 32));
+  __syncthreads();
+  for (unsigned i = tid; i < all; i += kThreads) {
+    const Scored x = i < kThreads ? mine : scored(i);
+    if (x.key && (uint32_t)(x.key >> 32) >= bound) {
       const int n = atomicAdd(&count, 1);
       if (n < kJoinCap) list[n] = x;
     }
@@ -343,8 +386,7 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const __grid_consta
   const int n = count;
   auto put = [&](int r, const Scored &x) {
     const long o = g * k + r;
-    const int w = (int)(x.flat / p.V);
-    p.out_scores[o] = (float)x.score, p.parents[o] = w, p.tokens[o] = (int)(x.flat - (long)w * p.V);
+    p.out_scores[o] = (float)unordered(x.key), p.parents[o] = (int)x.beam, p.tokens[o] = (int)x.token;
   };
   if (n <= kJoinCap) {
     for (int i = tid; i < n; i += kThreads) {
@@ -355,15 +397,27 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const __grid_consta
     }
     return;
   }
-  Scored prev{INFINITY, -2};
+  Scored prev{~0ull, 0, 0};
   for (int r = 0; r < k; ++r) {  // one after another, from the lists themselves
-    Scored b{0., -1};
-    for (int i = tid; i < lists * k; i += kThreads) {
-      const Scored x = scored(i / k, i % k);
-      if ((prev.flat == -2 || before(prev, x)) && before(x, b)) b = x;
+    Scored b{0, ~0u, ~0u};
+    for (unsigned i = tid; i < all; i += kThreads) {
+      const Scored x = scored(i);
+      if (x.key && before(prev, x) && before(x, b)) b = x;
     }
-    prev = block_best(b);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const Scored x{__shfl_xor_sync(0xffffffffu, b.key, o), __shfl_xor_sync(0xffffffffu, b.beam, o),
+                     __shfl_xor_sync(0xffffffffu, b.token, o)};
+      if (before(x, b)) b = x;
+    }
+    if (lane == 0) warp_best[warp] = b;
+    __syncthreads();
+    b = warp_best[0];
+    for (int w = 1; w < kWarps; ++w)
+      if (before(warp_best[w], b)) b = warp_best[w];
+    prev = b;
     if (tid == 0) put(r, prev);
+    __syncthreads();
   }
 }
 
@@ -442,12 +496,12 @@ cudaError_t launched(cudaError_t e, LaunchTimer &timer) {
 
 }  // namespace
 
-// Runs of a row: enough blocks for four an SM, of whole chunks (a row may begin up to 16 bytes behind its first chunk's
-// start).
-BeamSplit beam_split(int G, int W, int k, long V, la_dtype dt) {
+// Runs of a row, of whole chunks: enough blocks for three an SM (each starts with its own bounds and ends with a join;
+// six an SM took 80 us for 68 at 512 rows of 131072 in bf16).
+BeamSplit beam_split(int G, int W, int k, long V) {
   BeamSplit s{};
-  const long chunks = (V + 16 / (dt == LA_F32 ? 4 : 2) - 1 + kChunk - 1) / kChunk;
-  const long rows = (long)G * W, want = 4L * std::max(1, device_info(-1).sm_count);
+  const long chunks = (V + kChunk - 1) / kChunk;
+  const long rows = (long)G * W, want = 3L * std::max(1, device_info(-1).sm_count);
   const long runs = std::max(1L, std::min(chunks, (want + rows - 1) / rows));
   s.run_chunks = (int)((chunks + runs - 1) / runs);
   s.runs = (int)((chunks + s.run_chunks - 1) / s.run_chunks);
@@ -456,7 +510,7 @@ BeamSplit beam_split(int G, int W, int k, long V, la_dtype dt) {
 }
 
 cudaError_t launch_beam_select(const BeamProblem &p) {
-  BeamSplit s = beam_split(p.G, p.W, p.k, p.V, p.dt);
+  BeamSplit s = beam_split(p.G, p.W, p.k, p.V);
   s.cands = p.ws;
   s.stats = (float *)((char *)p.ws + (size_t)p.G * p.W * s.runs * p.k * 8);
   const unsigned blocks = (unsigned)((long)p.G * p.W * s.runs);
@@ -470,8 +524,17 @@ cudaError_t launch_beam_select(const BeamProblem &p) {
     if (e != cudaSuccess) return e;
   }
   LaunchTimer timer(kKBeamSelect, p.stream);
-  beam_join_kernel<<<(unsigned)p.G, kThreads, 0, p.stream>>>(p, s);
-  return launched(cudaGetLastError(), timer);
+  // launched early (programmatic dependent launch); it waits for the runs before it reads
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute early[1];
+  early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)p.G);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = p.stream;
+  cfg.attrs = early;
+  cfg.numAttrs = 1;
+  return launched(cudaLaunchKernelEx(&cfg, beam_join_kernel, p, s), timer);
 }
 
 // Few beams: a block for every pool of a child's row, so that one child's copies do not wait for each other.

@@ -351,7 +351,7 @@ struct ReorderProblem {
   int G, W, n_slots;
   cudaStream_t stream;
 };
-BeamSplit beam_split(int G, int W, int k, long V, la_dtype dt);
+BeamSplit beam_split(int G, int W, int k, long V);
 cudaError_t launch_beam_select(const BeamProblem &p);
 cudaError_t launch_beam_reorder(const ReorderProblem &p);
 cudaError_t read_and_clear_beam_status(unsigned int *value);

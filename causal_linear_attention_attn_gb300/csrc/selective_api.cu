@@ -264,7 +264,7 @@ la_status la_selective_scan_step(const void *x, long ldx, const void *delta, lon
 
 size_t la_beam_select_workspace(int G, int W, int k, int V, la_dtype dt) {
   if (beam_sizes(G, W, k, V, dt) != LA_OK || G == 0) return 0;
-  return beam_split(G, W, k, V, dt).bytes;
+  return beam_split(G, W, k, V).bytes;
 }
 
 la_status la_beam_select(const void *logits, long ld, const float *scores, const unsigned char *finished,
@@ -278,7 +278,7 @@ la_status la_beam_select(const void *logits, long ld, const float *scores, const
   if (!aligned({logits}, 16) || !aligned({workspace}, 256) || !aligned({scores, out_scores, parents, tokens}, 4))
     return LA_ERR_MISALIGNED;
   if ((st = api_device()) != LA_OK) return st;
-  if (!workspace || workspace_bytes < beam_split(G, W, k, V, dt).bytes) return LA_ERR_INVALID_VALUE;
+  if (!workspace || workspace_bytes < beam_split(G, W, k, V).bytes) return LA_ERR_INVALID_VALUE;
   return api_status(launch_beam_select(
       {logits, ld, scores, finished, out_scores, parents, tokens, G, W, k, V, eos, dt, workspace, (cudaStream_t)stream}));
 }
@@ -308,7 +308,7 @@ la_status la_beam_reorder(void *const *pools, const size_t *row_bytes, int n_poo
     for (int i = 0; i < p.pools; ++i) p.pool[i] = pools[at + i], p.row_bytes[i] = (long)row_bytes[at + i];
     p.first = at == 0;
     p.slots = slots, p.parents = parents, p.new_slots = new_slots;
-    p.G = G, p.W = W, p.n_slots = n_slots, p.stream = (cudaStream_t)stream;
+    p.G = G, p.W = W, p.n_slots = n_pools ? n_slots : 0x7fffffff, p.stream = (cudaStream_t)stream;
     if ((st = api_status(launch_beam_reorder(p))) != LA_OK) return st;
   }
   return LA_OK;
