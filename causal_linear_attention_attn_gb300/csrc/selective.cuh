@@ -39,6 +39,19 @@ __device__ __forceinline__ float2 softplus2(float2 v) {
   return __ffma2_rn(p, e, make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
 }
 
+// Where two channels' steps are: eight lanes that write four neighbours each meet no bank twice.
+__device__ __forceinline__ int step_slot(int pair) { return pair ^ (pair >> 3 & 3); }
+
+// Named barriers between kinds of warps: all kThreads threads, some of which wait.
+template <int kThreads>
+__device__ __forceinline__ void bar_sync(int id) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kThreads) : "memory");
+}
+template <int kThreads>
+__device__ __forceinline__ void bar_arrive(int id) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(kThreads) : "memory");
+}
+
 // Sums over the lanes of aligned groups of kLanes (a power of two) of kVals values a lane, which end up
 // spread over the group: each round halves the lanes that still add the same values and the values a lane holds, so
 // kVals values cost about kVals shuffles and not kVals log2(kLanes).  `stride`: lanes of a group are that far apart.

@@ -6,15 +6,17 @@
 //   dx = D dy + delta s1,  ddt = (x s1 + s2) softplus'(dt + bias),  dz = dout y silu'(z)
 //   dA_n = sum_{b,t} G (a h_{t-1}) delta,  dD = sum dy x,  dbias = sum ddt,  dS0 = a_0 G_0.
 //
-// The states are not kept by the forward: a pass of the scan leaves the state in front of every chunk, and
-// this kernel goes through the chunks from the last to the first.  In each it runs the recurrence again, with
-// the scan's layout (a lane: four components of a channel), keeping a_t h_{t-1} of the chunk's tokens in shared
-// memory (16 bytes a lane and token, read back by the lane that wrote it), then walks back with G in registers.
+// The states are not kept by the forward: a pass of the scan leaves the state in front of every chunk of 16 tokens, and
+// this kernel goes through the chunks from the last to the first, with the scan's layout (a lane: four components, of
+// d_state = 64 eight, of two channels) and three kinds of warps, a chunk apart:
+//   1. around: rows in, steps, dy, B and C to shared memory; later dx, ddt, dz out, and dB, dC added over the warps;
+//   2. forward: the recurrence again, leaving a_t h_{t-1} of every token in shared memory;
+//   3. backward: G in registers, everything that depends on it.  A lane reads the a h that its like wrote.
 // Sums over the components are spread over a channel's lanes; the sums of dB and dC over channels are
-// spread over a warp's channels, added over the block's warps, and leave as one partial sum a block of 32
-// channels, which a last kernel adds in order.  No atomics: the gradient is the same from run to run.
+// spread over a warp's channels, added over the block's warps, and leave as one partial sum a block of channels, which a
+// last kernel adds in order.  No atomics: the gradient is the same from run to run.
 //
-// Three exponentials and about twenty issue slots a component, channel and token bound it.
+// Two exponentials and about twenty issue slots a component, channel and token bound it, and shared memory's port.
 #include <algorithm>
 
 #include "internal.h"
@@ -23,32 +25,58 @@
 namespace la {
 namespace {
 
-constexpr int kCols = 32;        // channels a block
-constexpr int kRow = kCols + 8;  // floats between tokens of the sums' places
+constexpr int kAround = 128;  // threads of the first kind
 
-// Tokens a chunk: a h of a token takes 128 ds bytes of shared memory, and two blocks an SM fit (ds = 64: one).
-constexpr int chunk_tokens(int ds) { return ds <= 16 ? 32 : ds == 32 ? 16 : 8; }
+// Tokens a chunk and channels a block: as many as keep the a h of two chunks within shared memory.
+constexpr int grad_tokens(int ds) { return ds == 64 ? 8 : 16; }
+constexpr int grad_cols(int ds) { return ds <= 16 ? 64 : 32; }
+
+template <int DS>
+struct Layout {
+  static constexpr int kTok = grad_tokens(DS), kCols = grad_cols(DS), kRow = kCols + 8;  // floats between tokens of the sums' places
+  static constexpr int kSN = DS == 64 ? 8 : 4;                   // components a lane
+  static constexpr int kLanes = DS / kSN, kScan = kCols / 2 * kLanes, kWarps = kScan / 32;
+  static constexpr int kThreads = kAround + 2 * kScan;
+};
 
 template <int DS>
 struct Smem {
-  static constexpr int kTok = chunk_tokens(DS), kThreads = 8 * DS;
-  float4 ah[kTok][kThreads];
-  float2 steps[kTok][kCols];  // delta; delta x
-  float dy[kTok][kCols];
-  float B[kTok][DS], C[kTok][DS];
-  float s1[kTok][kRow], s2[kTok][kRow], y[kTok][kRow];
-  float bc[kTok][kThreads / 32][2 * DS];  // dB, dC of each warp's channels
+  using L = Layout<DS>;
+  static constexpr int kTok = L::kTok;
+  float4 ah[2][kTok][L::kSN / 2][L::kScan];
+  struct In {
+    float4 steps[kTok][L::kCols / 2];  // of two channels: delta, delta x; at step_slot
+    float dy[kTok][L::kCols];
+    float B[kTok][DS], C[kTok][DS];
+  } in[3];
+  struct Out {
+    float s1[kTok][L::kRow], s2[kTok][L::kRow], y[kTok][L::kRow];
+    float bc[kTok][L::kWarps][2 * DS];  // dB, dC of each warp's channels
+  } out[2];
 };
 
+// Barriers between the kinds of warps.
+enum Bar { kIn = 1, kAhFull = 4, kAhFree = 6, kOutFull = 8, kOutFree = 10, kOwn = 12 };
+
+// A sum that carries its rounding errors along.
+__device__ __forceinline__ void add_carry(float2 &s, float2 &e, float2 x) {
+  const float2 t = __fadd2_rn(s, x), b = __fadd2_rn(t, __fmul2_rn(s, both(-1.f)));
+  const float2 rest = __fadd2_rn(s, __fmul2_rn(__fadd2_rn(t, __fmul2_rn(b, both(-1.f))), both(-1.f)));
+  e = __fadd2_rn(e, __fadd2_rn(rest, __fadd2_rn(x, __fmul2_rn(b, both(-1.f)))));
+  s = t;
+}
+
 template <typename T, int DS, bool kGate>
-__global__ void __launch_bounds__(8 * DS) scan_grad_kernel(const __grid_constant__ ScanGradProblem g, const __grid_constant__ ScanSplit s) {
-  constexpr int kThreads = 8 * DS, kLanes = DS / 4, kPerWarp = 32 / kLanes, kTok = Smem<DS>::kTok;
-  constexpr int kGroups = (kTok * 4 + kThreads - 1) / kThreads;
-  constexpr int kStep = kLanes < 4 ? 4 : kLanes > kTok ? kTok : kLanes;
+__global__ void __launch_bounds__(Layout<DS>::kThreads) scan_grad_kernel(const __grid_constant__ ScanGradProblem g, const __grid_constant__ ScanSplit s) {
+  using L = Layout<DS>;
+  constexpr int kTok = L::kTok, kCols = L::kCols, kScan = L::kScan, kLanes = L::kLanes, kSN = L::kSN, kPerWarp = 32 / kLanes;
+  constexpr int kPairs = kSN / 2;                                // of components, a channel
+  constexpr int kStep = kLanes < 4 ? 4 : kLanes;  // tokens whose sums over components are spread together
+  constexpr int kBatch = 16 / kSN;                 // the same for sums over channels: the more, the fewer waits
   extern __shared__ __align__(16) unsigned char raw_smem[];
   Smem<DS> &m = *reinterpret_cast<Smem<DS> *>(raw_smem);
   const ScanProblem &p = g.p;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
   const int nb = (p.D + kCols - 1) / kCols;
   const int cb = blockIdx.x % nb;
   const long rest = blockIdx.x / nb;
@@ -56,241 +84,343 @@ __global__ void __launch_bounds__(8 * DS) scan_grad_kernel(const __grid_constant
   const long b = rest / s.segs;
   const long n = row_length(p.lengths, b, p.N);
   const long begin = (long)seg * s.len, stop = min(begin + s.len, p.N), end = min(stop, n);
+  const int chunks = end > begin ? (int)((end - begin + kTok - 1) / kTok) : 0;
+  auto first_of = [&](int i) { return begin + (long)(chunks - 1 - i) * kTok; };  // the i-th chunk from the end
+  const long state = (long)p.D * DS;
+  float *columns = s.columns + (b * s.segs + seg) * (long)p.D * (DS + 2);
 
-  const int q = lane % kLanes, num = lane / kLanes, ch = warp * kPerWarp + num;
-  const int c = cb * kCols + ch;
-  const long at = (long)c * DS + 4 * q, state = (long)p.D * DS;
+  if (tid < kAround) {
+    constexpr int kPerRow = kCols / 8;  // threads a token
+    const int row = tid / kPerRow, col = tid % kPerRow * 8, c8 = cb * kCols + col;
+    const bool live = c8 < p.D && row < kTok;
+    float2 bias[4], skip[4], dD[4], dbias[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      bias[e] = live && p.dt_bias ? reinterpret_cast<const float2 *>(p.dt_bias + c8)[e] : both(0.f);
+      skip[e] = live && p.Dskip ? reinterpret_cast<const float2 *>(p.Dskip + c8)[e] : both(0.f);
+      dD[e] = dbias[e] = both(0.f);
+    }
+    const T *x = (const T *)p.x + b * p.N * p.ldx + c8, *dt = (const T *)p.delta + b * p.N * p.ldt + c8;
+    const T *z = kGate ? (const T *)p.z + b * p.N * p.ldz + c8 : nullptr;
+    const long out0 = b * p.N * p.D + c8;
+    const T *dout = (const T *)g.dout + out0;
+    if (live) {  // tokens past the row's end: zero gradients
+      const float2 zero[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
+      for (long t = max(begin, end) + row; t < stop; t += kTok) {
+        put8((T *)g.dx + out0 + t * p.D, zero), put8((T *)g.ddt + out0 + t * p.D, zero);
+        if (kGate) put8((T *)g.dz + out0 + t * p.D, zero);
+      }
+    }
+    // rows of B and C, eight components a piece
+    constexpr int kPieces = 2 * kTok * DS / 8, kEach = (kPieces + kAround - 1) / kAround, kPR = DS / 8;
+    struct Rows {
+      Raw<T> x, t, z, d;
+    } next, done;  // of the chunk that goes in next; of the one that comes out (read again, from L2: there is no place)
+    Raw<T> rb[kEach];
+    auto rows_of = [&](Rows &r, long t) {
+      r.x.zero(), r.t.zero(), r.z.zero(), r.d.zero();
+      if (live && t < end) {
+        r.x.load(x + t * p.ldx), r.t.load(dt + t * p.ldt), r.d.load(dout + t * p.D);
+        if (kGate) r.z.load(z + t * p.ldz);
+      }
+    };
+    auto load = [&](long t0) {
+      rows_of(next, t0 + row);
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int k = tid + i * kAround, which = k >= kPieces / 2, j = which ? k - kPieces / 2 : k;
+        rb[i].zero();
+        if (k < kPieces && t0 + j / kPR < end)
+          rb[i].load((which ? (const T *)p.Cm + (b * p.N + t0 + j / kPR) * p.ldc : (const T *)p.Bm + (b * p.N + t0 + j / kPR) * p.ldb) +
+                     j % kPR * 8);
+      }
+    };
+    if (chunks) load(first_of(0));
+    int at = 0;  // i mod 3
+    for (int i = 0; i < chunks + 2; ++i) {
+      if (i < chunks) {
+        typename Smem<DS>::In &to = m.in[at];
+        if (row < kTok) {
+          const bool in = first_of(i) + row < end;
+          float2 xv[4], tv[4], dv[4], zv[4];
+          next.x.get(xv), next.t.get(tv), next.d.get(dv);
+          if (kGate) next.z.get(zv);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float2 d = __fadd2_rn(tv[e], bias[e]);
+            if (p.softplus) d = softplus2(d);
+            float2 u = __fmul2_rn(d, xv[e]);
+            if (!in) d = u = both(0.f);
+            to.steps[row][step_slot(col / 2 + e)] = make_float4(d.x, u.x, d.y, u.y);
+            if (kGate) dv[e] = __fmul2_rn(dv[e], __fmul2_rn(zv[e], Sigmoid2(zv[e]).s));
+            *reinterpret_cast<float2 *>(&to.dy[row][col + 2 * e]) = in ? dv[e] : both(0.f);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+          const int k = tid + j * kAround;
+          float2 v[4];
+          rb[j].get(v);
+          if (k < kPieces) put8((k >= kPieces / 2 ? &to.C[0][0] + (k - kPieces / 2) * 8 : &to.B[0][0] + k * 8), v);
+        }
+        if (i + 1 < chunks) load(first_of(i + 1));
+        bar_arrive<kAround + kScan>(kIn + at);
+      }
+      if (i >= 2) {
+        const int o = i - 2;
+        const long t0 = first_of(o), t = t0 + row;
+        rows_of(done, t);
+        bar_sync<kAround + kScan>(kOutFull + (o & 1));
+        const typename Smem<DS>::Out &from = m.out[o & 1];
+        const typename Smem<DS>::In &in = m.in[at == 2 ? 0 : at + 1];
+        if (live && t < end) {
+          float2 xv[4], tv[4], dv[4], zv[4], ox[4], ot[4], oz[4];
+          done.x.get(xv), done.t.get(tv), done.d.get(dv);
+          if (kGate) done.z.get(zv);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 s1 = *reinterpret_cast<const float2 *>(&from.s1[row][col + 2 * e]);
+            const float2 s2 = *reinterpret_cast<const float2 *>(&from.s2[row][col + 2 * e]);
+            const float2 dy = *reinterpret_cast<const float2 *>(&in.dy[row][col + 2 * e]);
+            const float4 st = in.steps[row][step_slot(col / 2 + e)];
+            ox[e] = __ffma2_rn(make_float2(st.x, st.z), s1, __fmul2_rn(skip[e], dy));
+            ot[e] = __ffma2_rn(xv[e], s1, __fmul2_rn(s2, both(0.693147181f)));  // A carries log2 e
+            if (p.softplus) ot[e] = __fmul2_rn(ot[e], Sigmoid2(__fadd2_rn(tv[e], bias[e])).s);
+            dD[e] = __ffma2_rn(dy, xv[e], dD[e]);
+            dbias[e] = __fadd2_rn(dbias[e], ot[e]);
+            if (kGate) {
+              const float2 y = __ffma2_rn(skip[e], xv[e], *reinterpret_cast<const float2 *>(&from.y[row][col + 2 * e]));
+              const Sigmoid2 sg(zv[e]);
+              const float2 slope = __ffma2_rn(__fmul2_rn(zv[e], sg.s), sg.one_less(), sg.s);
+              oz[e] = __fmul2_rn(__fmul2_rn(dv[e], y), slope);
+            }
+          }
+          const long to = out0 + t * p.D;
+          put8((T *)g.dx + to, ox), put8((T *)g.ddt + to, ot);
+          if (kGate) put8((T *)g.dz + to, oz);
+        }
+        for (int j = tid; j < kTok * 2 * DS; j += kAround) {
+          const int r = j / (2 * DS), k = j % (2 * DS);
+          float v = from.bc[r][0][k];
+#pragma unroll
+          for (int w = 1; w < L::kWarps; ++w) v += from.bc[r][w][k];
+          if (t0 + r < end) s.bc[((long)cb * p.B * p.N + b * p.N + t0 + r) * (2 * DS) + k] = v;
+        }
+        if (i < chunks) bar_arrive<kAround + kScan>(kOutFree + (o & 1));
+      }
+      at = at == 2 ? 0 : at + 1;
+    }
+    // dD and the bias's gradient: threads of the same channels in order
+    bar_sync<kAround>(kOwn);
+    float *part = &m.out[0].s1[0][0];  // [dD, dbias][kAround][8]; all chunks are through
+    static_assert(sizeof(typename Smem<DS>::Out) >= 2 * kAround * 8 * sizeof(float), "place for the sums");
+    if (row < kTok) {
+      put8(part + tid * 8, dD);
+      put8(part + (kAround + tid) * 8, dbias);
+    }
+    bar_sync<kAround>(kOwn);
+    for (int j = tid; j < 2 * kCols; j += kAround) {
+      const int which = j / kCols, c = j % kCols;
+      if (cb * kCols + c >= p.D) continue;
+      float v = 0.f;
+      for (int r = 0; r < kTok; ++r) v += part[(which * kAround + r * kPerRow + c / 8) * 8 + c % 8];
+      columns[state + (long)which * p.D + cb * kCols + c] = v;
+    }
+    return;
+  }
+
+  const bool forward = tid < kAround + kScan;
+  const int me = tid - kAround - (forward ? 0 : kScan), warp = me >> 5;
+  const int q = lane % kLanes, num = lane / kLanes, ch = (warp * kPerWarp + num) * 2;
+  const int c = cb * kCols + ch, slot = step_slot(ch / 2);  // and the next channel; D is even
   const bool mine = c < p.D;
-  float2 A[2] = {both(0.f), both(0.f)}, G[2] = {both(0.f), both(0.f)}, dA[2] = {both(0.f), both(0.f)};
-  if (mine) {
-    const float4 a = *reinterpret_cast<const float4 *>(p.A + at);
-    A[0] = __fmul2_rn(make_float2(a.x, a.y), both(kLog2e)), A[1] = __fmul2_rn(make_float2(a.z, a.w), both(kLog2e));
-    const float *from = s.segs > 1 ? s.rev_starts + (b * s.segs + seg) * state : g.dS ? g.dS + b * state : nullptr;
-    if (from) {
-      const float4 v = *reinterpret_cast<const float4 *>(from + at);
-      G[0] = make_float2(v.x, v.y), G[1] = make_float2(v.z, v.w);
-    }
-  }
-
-  const int c8 = cb * kCols + (tid & 3) * 8;
-  const bool live = c8 < p.D;
-  float2 bias[4], skip[4], dD[4], dbias[4];
+  const long at = (long)c * DS + kSN * q;  // in a state
+  float2 A[2][kPairs];
+  auto get = [&](float2 (&v)[2][kPairs], const float *from) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    bias[e] = live && p.dt_bias ? reinterpret_cast<const float2 *>(p.dt_bias + c8)[e] : both(0.f);
-    skip[e] = live && p.Dskip ? reinterpret_cast<const float2 *>(p.Dskip + c8)[e] : both(0.f);
-    dD[e] = dbias[e] = both(0.f);
-  }
-  const T *x = (const T *)p.x + b * p.N * p.ldx + c8, *dt = (const T *)p.delta + b * p.N * p.ldt + c8;
-  const T *z = kGate ? (const T *)p.z + b * p.N * p.ldz + c8 : nullptr;
-  const T *dout = (const T *)g.dout + b * p.N * p.D + c8;
-  const long out0 = b * p.N * p.D + c8;
-  // tokens past the row's end: zero gradients
-  for (long i = tid; i < (stop - max(begin, end)) * 4; i += kThreads) {
-    const long o = out0 + (max(begin, end) + (i >> 2)) * p.D;
-    const float2 zero[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
-    if (!live) break;
-    put8((T *)g.dx + o, zero), put8((T *)g.ddt + o, zero);
-    if (kGate) put8((T *)g.dz + o, zero);
-  }
-
-  Raw<T> rx[kGroups], rt[kGroups], rz[kGate ? kGroups : 1], rd[kGroups], rb;
-  constexpr int kPieces = kTok * DS / 8, kPerRow = DS / 8;
-  const bool with_c = tid >= kPieces;
-  const int piece = with_c ? tid - kPieces : tid, brow = piece / kPerRow, bcol = piece % kPerRow * 8;
-  const bool has_bc = tid < 2 * kPieces;
-  const T *bc = with_c ? (const T *)p.Cm + b * p.N * p.ldc + bcol : (const T *)p.Bm + b * p.N * p.ldb + bcol;
-  const long ldbc = with_c ? p.ldc : p.ldb;
-  float4 h0 = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto load = [&](long t0) {
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int i = 0; i < kGroups; ++i) {
-      const int k = tid + i * kThreads;
-      const long t = t0 + (k >> 2);
-      rx[i].zero(), rt[i].zero(), rd[i].zero();
-      if (kGate) rz[i].zero();
-      if (k < kTok * 4 && live && t < end) {
-        rx[i].load(x + t * p.ldx), rt[i].load(dt + t * p.ldt), rd[i].load(dout + t * p.D);
-        if (kGate) rz[i].load(z + t * p.ldz);
+      for (int e = 0; e < kPairs; e += 2) {
+        const float4 f = mine && from ? *reinterpret_cast<const float4 *>(from + at + i * DS + 2 * e) : make_float4(0.f, 0.f, 0.f, 0.f);
+        v[i][e] = make_float2(f.x, f.y), v[i][e + 1] = make_float2(f.z, f.w);
       }
-    }
-    rb.zero();
-    if (has_bc && t0 + brow < end) rb.load(bc + (t0 + brow) * ldbc);
-    if (mine) h0 = *reinterpret_cast<const float4 *>(s.chunk_states + (b * s.all_chunks + t0 / kTok) * state + at);
   };
-  const long chunks = end > begin ? (end - begin + kTok - 1) / kTok : 0;
-  if (chunks) load(begin + (chunks - 1) * kTok);
-  for (long k = chunks - 1; k >= 0; --k) {
-    const long t0 = begin + k * kTok;
-    Raw<T> kx[kGroups], kt[kGroups], kz[kGate ? kGroups : 1], kd[kGroups];
+  auto put = [&](float *to, const float2 (&v)[2][kPairs]) {
 #pragma unroll
-    for (int i = 0; i < kGroups; ++i) {
-      const int j = tid + i * kThreads;
-      if (j >= kTok * 4) break;
-      const bool in = t0 + (j >> 2) < end;
-      kx[i] = rx[i], kt[i] = rt[i], kd[i] = rd[i];
-      float2 xv[4], tv[4], dv[4], zv[4];
-      rx[i].get(xv), rt[i].get(tv), rd[i].get(dv);
-      if (kGate) kz[i] = rz[i], rz[i].get(zv);
-      const int row = j >> 2, col = (tid & 3) * 8;
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float2 d = __fadd2_rn(tv[e], bias[e]);
-        if (p.softplus) d = softplus2(d);
-        float2 u = __fmul2_rn(d, xv[e]);
-        if (!in) d = u = both(0.f);
-        reinterpret_cast<float4 *>(&m.steps[row][col])[e] = make_float4(d.x, u.x, d.y, u.y);
-        if (kGate) dv[e] = __fmul2_rn(dv[e], __fmul2_rn(zv[e], Sigmoid2(zv[e]).s));
-        reinterpret_cast<float2 *>(&m.dy[row][col])[e] = in ? dv[e] : both(0.f);
-      }
+      for (int e = 0; e < kPairs; e += 2) st4(to + at + i * DS + 2 * e, v[i][e].x, v[i][e].y, v[i][e + 1].x, v[i][e + 1].y);
+  };
+  auto read = [&](float2 (&v)[kPairs], const float *from) {
+#pragma unroll
+    for (int e = 0; e < kPairs; e += 2) {
+      const float4 f = *reinterpret_cast<const float4 *>(from + 2 * e);
+      v[e] = make_float2(f.x, f.y), v[e + 1] = make_float2(f.z, f.w);
     }
-    if (has_bc) {
-      float2 v[4];
-      rb.get(v);
-      put8(with_c ? &m.C[brow][bcol] : &m.B[brow][bcol], v);
-    }
-    float2 h[2] = {make_float2(h0.x, h0.y), make_float2(h0.z, h0.w)};
-    if (k > 0) load(t0 - kTok);
-    __syncthreads();
-    // the chunk's states again
-#pragma unroll 1
-    for (int i0 = 0; i0 < kTok; i0 += kStep) {
-      float y[kStep];
+  };
+  get(A, p.A);
 #pragma unroll
-      for (int j = 0; j < kStep; ++j) {
-        const int i = i0 + j;
-        const float2 d = m.steps[i][ch];
-        const float4 bv = *reinterpret_cast<const float4 *>(&m.B[i][4 * q]);
-        const float2 a0 = __fmul2_rn(exp2_approx(__fmul2_rn(both(d.x), A[0])), h[0]);
-        const float2 a1 = __fmul2_rn(exp2_approx(__fmul2_rn(both(d.x), A[1])), h[1]);
-        m.ah[i][tid] = make_float4(a0.x, a0.y, a1.x, a1.y);
-        h[0] = __ffma2_rn(both(d.y), make_float2(bv.x, bv.y), a0);
-        h[1] = __ffma2_rn(both(d.y), make_float2(bv.z, bv.w), a1);
-        if (kGate) {
-          const float4 cv = *reinterpret_cast<const float4 *>(&m.C[i][4 * q]);
-          const float2 yy = __ffma2_rn(h[1], make_float2(cv.z, cv.w), __fmul2_rn(h[0], make_float2(cv.x, cv.y)));
-          y[j] = yy.x + yy.y;
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int e = 0; e < kPairs; ++e) A[i][e] = __fmul2_rn(A[i][e], both(kLog2e));
+
+  if (forward) {
+    float2 h[2][kPairs], next[2][kPairs];
+    auto states_of = [&](int i) { return s.chunk_states + (b * s.all_chunks + first_of(i) / kTok) * state; };
+    if (chunks) get(next, states_of(0));
+    int buf = 0;
+    for (int i = 0; i < chunks; ++i) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int e = 0; e < kPairs; ++e) h[k][e] = next[k][e];
+      if (i + 1 < chunks) get(next, states_of(i + 1));
+      bar_sync<kAround + kScan>(kIn + buf);
+      if (i >= 2) bar_sync<2 * kScan>(kAhFree + (i & 1));
+      const typename Smem<DS>::In &in = m.in[buf];
+      auto &ah = m.ah[i & 1];
+#pragma unroll
+      for (int t = 0; t < kTok; ++t) {
+        const float4 d = in.steps[t][slot];
+        float2 B[kPairs];
+        read(B, &in.B[t][kSN * q]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float2 dd = both(k ? d.z : d.x), u = both(k ? d.w : d.y);
+          float2 v[kPairs];
+#pragma unroll
+          for (int e = 0; e < kPairs; ++e) {
+            v[e] = __fmul2_rn(exp2_approx(__fmul2_rn(dd, A[k][e])), h[k][e]);
+            h[k][e] = __ffma2_rn(u, B[e], v[e]);
+          }
+#pragma unroll
+          for (int e = 0; e < kPairs; e += 2) ah[t][(k * kPairs + e) / 2][me] = make_float4(v[e].x, v[e].y, v[e + 1].x, v[e + 1].y);
         }
       }
-      if (kGate) {
-        spread_sum<kLanes, kStep, 1>(y, q);
-#pragma unroll
-        for (int v = 0; v < (kStep > kLanes ? kStep / kLanes : 1); ++v)
-          if (q < kStep) m.y[i0 + v * kLanes + q][ch] = y[v];
-      }
+      bar_arrive<2 * kScan>(kAhFull + (i & 1));
+      buf = buf == 2 ? 0 : buf + 1;
     }
-    // and back
+    return;
+  }
+  float2 G[2][kPairs], dA[2][kPairs], lost[2][kPairs];
+  get(G, s.segs > 1 ? s.rev_starts + (b * s.segs + seg) * state : g.dS ? g.dS + b * state : nullptr);
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int e = 0; e < kPairs; ++e) dA[k][e] = lost[k][e] = both(0.f);
+  int buf = 0;
+  for (int i = 0; i < chunks; ++i) {
+    bar_sync<2 * kScan>(kAhFull + (i & 1));
+    if (i >= 2) bar_sync<kAround + kScan>(kOutFree + (i & 1));
+    const typename Smem<DS>::In &in = m.in[buf];
+    typename Smem<DS>::Out &out = m.out[i & 1];
+    const auto &ah = m.ah[i & 1];
+    float2 part[2][kPairs];  // of dA
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int e = 0; e < kPairs; ++e) part[k][e] = both(0.f);
+    // a token's values are on their way while the one behind it is worked on (the compiler does not move these loads
+    // across the stores of sums)
+    struct Token {
+      float4 d;
+      float2 dy, B[kPairs], C[kPairs], ah[2][kPairs];
+    } now, then;
+    auto fetch = [&](Token &v, int t) {
+      v.d = in.steps[t][slot];
+      v.dy = *reinterpret_cast<const float2 *>(&in.dy[t][ch]);
+      read(v.B, &in.B[t][kSN * q]);
+      read(v.C, &in.C[t][kSN * q]);
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int e = 0; e < kPairs; e += 2) {
+          const float4 f = ah[t][(k * kPairs + e) / 2][me];
+          v.ah[k][e] = make_float2(f.x, f.y), v.ah[k][e + 1] = make_float2(f.z, f.w);
+        }
+    };
+    fetch(now, kTok - 1);
 #pragma unroll 1
     for (int i0 = kTok - kStep; i0 >= 0; i0 -= kStep) {
-      float s1[kStep], s2[kStep];
+      float s1[2 * kStep], s2[2 * kStep], y[2 * kStep];  // of the first channel, of the second
+      float sums[kBatch * 2 * kSN];                      // of dB and dC
 #pragma unroll
       for (int j = kStep - 1; j >= 0; --j) {
-        const int i = i0 + j;
-        const float2 d = m.steps[i][ch];
-        const float dy = m.dy[i][ch];
-        const float4 bv = *reinterpret_cast<const float4 *>(&m.B[i][4 * q]);
-        const float4 cv = *reinterpret_cast<const float4 *>(&m.C[i][4 * q]);
-        const float4 av = m.ah[i][tid];
-        const float2 b0 = make_float2(bv.x, bv.y), b1 = make_float2(bv.z, bv.w);
-        const float2 ah0 = make_float2(av.x, av.y), ah1 = make_float2(av.z, av.w);
-        G[0] = __ffma2_rn(make_float2(cv.x, cv.y), both(dy), G[0]);
-        G[1] = __ffma2_rn(make_float2(cv.z, cv.w), both(dy), G[1]);
-        const float2 B0 = __fmul2_rn(G[0], both(d.y)), B1 = __fmul2_rn(G[1], both(d.y));
-        const float2 C0 = __fmul2_rn(__ffma2_rn(both(d.y), b0, ah0), both(dy));
-        const float2 C1 = __fmul2_rn(__ffma2_rn(both(d.y), b1, ah1), both(dy));
-        const float2 t1 = __ffma2_rn(G[1], b1, __fmul2_rn(G[0], b0));
-        const float2 w0 = __fmul2_rn(G[0], ah0), w1 = __fmul2_rn(G[1], ah1);
-        const float2 t2 = __ffma2_rn(w1, A[1], __fmul2_rn(w0, A[0]));
-        s1[j] = t1.x + t1.y, s2[j] = t2.x + t2.y;
-        dA[0] = __ffma2_rn(w0, both(d.x), dA[0]), dA[1] = __ffma2_rn(w1, both(d.x), dA[1]);
-        G[0] = __fmul2_rn(exp2_approx(__fmul2_rn(both(d.x), A[0])), G[0]);
-        G[1] = __fmul2_rn(exp2_approx(__fmul2_rn(both(d.x), A[1])), G[1]);
-        float v[8] = {B0.x, B0.y, B1.x, B1.y, C0.x, C0.y, C1.x, C1.y};
-        spread_sum<kPerWarp, 8, kLanes>(v, num);
-        // value k of a lane's four components' dB (k < 4) and dC
+        const int t = i0 + j;
+        if (t > 0) fetch(then, t - 1);
+        const float4 d = now.d;
+        const float2 dy = now.dy;
+        const auto &B = now.B, &C = now.C;
+        float2 dB[kPairs], dC[kPairs];
 #pragma unroll
-        for (int r = 0; r < (kPerWarp < 8 ? 8 / kPerWarp : 1); ++r) {
-          const int k8 = num + r * kPerWarp;
-          if (k8 < 8) m.bc[i][warp][(k8 >> 2) * DS + 4 * q + (k8 & 3)] = v[r];
+        for (int k = 0; k < 2; ++k) {
+          const float2 dd = both(k ? d.z : d.x), u = both(k ? d.w : d.y), dyk = both(k ? dy.y : dy.x);
+          const auto &v = now.ah[k];
+          float2 t1 = both(0.f), t2 = both(0.f), t3 = both(0.f);
+#pragma unroll
+          for (int e = 0; e < kPairs; ++e) {
+            G[k][e] = __ffma2_rn(C[e], dyk, G[k][e]);
+            const float2 h = __ffma2_rn(u, B[e], v[e]);
+            dB[e] = k ? __ffma2_rn(G[k][e], u, dB[e]) : __fmul2_rn(G[k][e], u);
+            dC[e] = k ? __ffma2_rn(h, dyk, dC[e]) : __fmul2_rn(h, dyk);
+            t1 = e ? __ffma2_rn(G[k][e], B[e], t1) : __fmul2_rn(G[k][e], B[e]);
+            if (kGate) t3 = e ? __ffma2_rn(h, C[e], t3) : __fmul2_rn(h, C[e]);
+            const float2 w = __fmul2_rn(G[k][e], v[e]);
+            t2 = e ? __ffma2_rn(w, A[k][e], t2) : __fmul2_rn(w, A[k][e]);
+            part[k][e] = __ffma2_rn(w, dd, part[k][e]);
+            G[k][e] = __fmul2_rn(exp2_approx(__fmul2_rn(dd, A[k][e])), G[k][e]);
+          }
+          s1[k * kStep + j] = t1.x + t1.y, s2[k * kStep + j] = t2.x + t2.y;
+          if (kGate) y[k * kStep + j] = t3.x + t3.y;
         }
-      }
-      spread_sum<kLanes, kStep, 1>(s1, q);
-      spread_sum<kLanes, kStep, 1>(s2, q);
+        float *v = sums + j % kBatch * 2 * kSN;
 #pragma unroll
-      for (int v = 0; v < (kStep > kLanes ? kStep / kLanes : 1); ++v)
-        if (q < kStep) m.s1[i0 + v * kLanes + q][ch] = s1[v], m.s2[i0 + v * kLanes + q][ch] = s2[v];
-    }
-    __syncthreads();
+        for (int e = 0; e < kPairs; ++e)
+          v[2 * e] = dB[e].x, v[2 * e + 1] = dB[e].y, v[kSN + 2 * e] = dC[e].x, v[kSN + 2 * e + 1] = dC[e].y;
+        if (j % kBatch == 0) {
+          spread_sum<kPerWarp, kBatch * 2 * kSN, kLanes>(sums, num);
 #pragma unroll
-    for (int i = 0; i < kGroups; ++i) {
-      const int j = tid + i * kThreads, row = j >> 2, col = (tid & 3) * 8;
-      const long t = t0 + row;
-      if (j >= kTok * 4 || !live || t >= end) break;
-      float2 xv[4], tv[4], dv[4], zv[4], ox[4], ot[4], oz[4];
-      kx[i].get(xv), kt[i].get(tv), kd[i].get(dv);
-      if (kGate) kz[i].get(zv);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 s1 = *reinterpret_cast<const float2 *>(&m.s1[row][col + 2 * e]);
-        const float2 s2 = *reinterpret_cast<const float2 *>(&m.s2[row][col + 2 * e]);
-        const float2 dy = *reinterpret_cast<const float2 *>(&m.dy[row][col + 2 * e]);
-        const float4 st = reinterpret_cast<const float4 *>(&m.steps[row][col])[e];
-        ox[e] = __ffma2_rn(make_float2(st.x, st.z), s1, __fmul2_rn(skip[e], dy));
-        ot[e] = __ffma2_rn(xv[e], s1, __fmul2_rn(s2, both(0.693147181f)));  // A carries log2 e
-        if (p.softplus) ot[e] = __fmul2_rn(ot[e], Sigmoid2(__fadd2_rn(tv[e], bias[e])).s);
-        dD[e] = __ffma2_rn(dy, xv[e], dD[e]);
-        dbias[e] = __fadd2_rn(dbias[e], ot[e]);
-        if (kGate) {
-          const float2 y = __ffma2_rn(skip[e], xv[e], *reinterpret_cast<const float2 *>(&m.y[row][col + 2 * e]));
-          const Sigmoid2 sg(zv[e]);
-          const float2 slope = __ffma2_rn(__fmul2_rn(zv[e], sg.s), sg.one_less(), sg.s);
-          oz[e] = __fmul2_rn(__fmul2_rn(dv[e], y), slope);
+          for (int r = 0; r < kBatch * 2 * kSN / kPerWarp; ++r) {
+            const int k = num + r * kPerWarp, of = k / (2 * kSN), n8 = k % (2 * kSN);  // token; dB's components, then dC's
+            out.bc[t + of][warp][n8 / kSN * DS + kSN * q + n8 % kSN] = sums[r];
+          }
         }
+        now = then;
       }
-      const long o = out0 + t * p.D;
-      put8((T *)g.dx + o, ox), put8((T *)g.ddt + o, ot);
-      if (kGate) put8((T *)g.dz + o, oz);
-    }
-    for (int i = tid; i < kTok * 2 * DS; i += kThreads) {
-      const int row = i / (2 * DS), col = i % (2 * DS);
-      float v = m.bc[row][0][col];
+      spread_sum<kLanes, 2 * kStep, 1>(s1, q);
+      spread_sum<kLanes, 2 * kStep, 1>(s2, q);
+      if (kGate) spread_sum<kLanes, 2 * kStep, 1>(y, q);
+      constexpr int kHave = kStep / kLanes;
 #pragma unroll
-      for (int w = 1; w < kThreads / 32; ++w) v += m.bc[row][w][col];
-      if (t0 + row < end) s.bc[((long)cb * p.B * p.N + b * p.N + t0 + row) * (2 * DS) + col] = v;
+      for (int v = 0; v < kHave; ++v) {
+        const int t = i0 + v * kLanes + q;
+        *reinterpret_cast<float2 *>(&out.s1[t][ch]) = make_float2(s1[v], s1[kHave + v]);
+        *reinterpret_cast<float2 *>(&out.s2[t][ch]) = make_float2(s2[v], s2[kHave + v]);
+        if (kGate) *reinterpret_cast<float2 *>(&out.y[t][ch]) = make_float2(y[v], y[kHave + v]);
+      }
     }
-    __syncthreads();
+    if (i + 2 < chunks) bar_arrive<2 * kScan>(kAhFree + (i & 1));
+    bar_arrive<kAround + kScan>(kOutFull + (i & 1));
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int e = 0; e < kPairs; ++e) add_carry(dA[k][e], lost[k][e], part[k][e]);
+    buf = buf == 2 ? 0 : buf + 1;
   }
-  if (seg == 0 && g.dS0 && mine) *reinterpret_cast<float4 *>(g.dS0 + b * state + at) = make_float4(G[0].x, G[0].y, G[1].x, G[1].y);
-  float *to = s.columns + (b * s.segs + seg) * (long)p.D * (DS + 2);
-  if (mine) *reinterpret_cast<float4 *>(to + at) = make_float4(dA[0].x, dA[0].y, dA[1].x, dA[1].y);
-  __syncthreads();
-  float *part = reinterpret_cast<float *>(raw_smem);  // [warp][dD, dbias][32 channels]
+  if (!mine) return;
+  if (seg == 0 && g.dS0) put(g.dS0 + b * state, G);
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
+  for (int k = 0; k < 2; ++k)
 #pragma unroll
-    for (int o = 4; o < 32; o <<= 1) {
-      dD[e].x += __shfl_xor_sync(0xffffffffu, dD[e].x, o), dD[e].y += __shfl_xor_sync(0xffffffffu, dD[e].y, o);
-      dbias[e].x += __shfl_xor_sync(0xffffffffu, dbias[e].x, o), dbias[e].y += __shfl_xor_sync(0xffffffffu, dbias[e].y, o);
-    }
-    if (lane < 4) {
-      float *at8 = part + warp * 2 * kCols + lane * 8 + 2 * e;
-      at8[0] = dD[e].x, at8[1] = dD[e].y, at8[kCols] = dbias[e].x, at8[kCols + 1] = dbias[e].y;
-    }
-  }
-  __syncthreads();
-  if (tid < 2 * kCols && cb * kCols + tid % kCols < p.D) {
-    float v = part[tid];
-#pragma unroll
-    for (int w = 1; w < kThreads / 32; ++w) v += part[w * 2 * kCols + tid];
-    to[state + (long)(tid / kCols) * p.D + cb * kCols + tid % kCols] = v;
-  }
+    for (int e = 0; e < kPairs; ++e) dA[k][e] = __fadd2_rn(dA[k][e], lost[k][e]);
+  put(columns, dA);
 }
 
 // dB and dC from the partial sums of the blocks of channels: a thread a token and component.
 template <typename T>
 __global__ void __launch_bounds__(256) scan_bc_kernel(const __grid_constant__ ScanGradProblem g, const __grid_constant__ ScanSplit s) {
   const ScanProblem &p = g.p;
-  const int ds2 = 2 * p.ds, nb = (p.D + kCols - 1) / kCols;
+  const int cols = p.ds <= 16 ? 64 : 32, ds2 = 2 * p.ds, nb = (p.D + cols - 1) / cols;  // (grad_cols)
   const long rows = (long)p.B * p.N, all = rows * ds2, i = (long)blockIdx.x * 256 + threadIdx.x;
   if (i >= all) return;
   const long row = i / ds2, b = row / p.N;
@@ -318,11 +448,12 @@ cudaError_t launch_grad(const ScanGradProblem &g, const ScanSplit &s) {
   const void *fn = p.z ? (const void *)scan_grad_kernel<T, DS, true> : (const void *)scan_grad_kernel<T, DS, false>;
   cudaError_t e = ensure_smem_optin(fn, sizeof(Smem<DS>));
   if (e != cudaSuccess) return e;
+  constexpr int kCols = grad_cols(DS);
   const long blocks = (long)p.B * s.segs * ((p.D + kCols - 1) / kCols);
   {
     LaunchTimer timer(kKSelectiveBackward, p.stream);
     void *args[] = {const_cast<ScanGradProblem *>(&g), const_cast<ScanSplit *>(&s)};
-    e = cudaLaunchKernel(fn, dim3((unsigned)blocks), dim3(8 * DS), args, sizeof(Smem<DS>), p.stream);
+    e = cudaLaunchKernel(fn, dim3((unsigned)blocks), dim3(Layout<DS>::kThreads), args, sizeof(Smem<DS>), p.stream);
     timer.done(e);
     if (e != cudaSuccess) return e;
     count_launch();
@@ -362,14 +493,15 @@ Parts parts(const ScanProblem &p, const ScanSplit &s) {
   q.rev_starts = take(split * state);
   q.rev_total = take(split * p.D);
   q.chunk_states = take((size_t)p.B * s.all_chunks * state);
-  q.bc = take((size_t)((p.D + kCols - 1) / kCols) * p.B * p.N * 2 * p.ds);
+  const int cols = grad_cols(p.ds);
+  q.bc = take((size_t)((p.D + cols - 1) / cols) * p.B * p.N * 2 * p.ds);
   q.columns = take(rows * p.D * (p.ds + 2));
   q.all = o;
   return q;
 }
 ScanSplit grad_split(const ScanProblem &p) {
   ScanSplit s = scan_split(p);
-  s.chunk = chunk_tokens(p.ds);
+  s.chunk = grad_tokens(p.ds);
   s.all_chunks = (p.N + s.chunk - 1) / s.chunk;
   return s;
 }

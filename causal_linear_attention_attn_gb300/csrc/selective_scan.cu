@@ -41,19 +41,6 @@ struct Smem {
   float sums[kMode == kOutputs ? kTok : 1][kRow];
 };
 
-// Where two channels' steps are: eight lanes that write four neighbours each meet no bank twice.
-__device__ __forceinline__ int step_slot(int pair) { return pair ^ (pair >> 3 & 3); }
-
-// Named barriers: chunk k's inputs are in place (k even, odd); its recurrence is through.
-template <int kThreads>
-__device__ __forceinline__ void bar_sync(int id) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kThreads) : "memory");
-}
-template <int kThreads>
-__device__ __forceinline__ void bar_arrive(int id) {
-  asm volatile("bar.arrive %0, %1;" ::"r"(id), "n"(kThreads) : "memory");
-}
-
 // kOutputs: out, and the last segment's end state to S.  kEnds: each segment's end state from zero and sum of
 // delta.  kStates: the state in front of each chunk of s.chunk tokens.  kReverseEnds: the same as kEnds for the
 // recurrence of the state's gradient, from a segment's last token to its first: G <- a_t (G + C_t dy_t).
