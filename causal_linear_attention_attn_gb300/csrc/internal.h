@@ -295,8 +295,10 @@ struct ScanStepProblem {
   la_dtype dt;
   cudaStream_t stream;
 };
-ScanSplit scan_split(const ScanProblem &p);
+ScanSplit scan_split(const ScanProblem &p, int cols, int per_sm);
 size_t scan_workspace(const ScanProblem &p);
+// What a call of these sizes needs at most, with lengths or without (need: scan_workspace or scan_grad_workspace).
+size_t scan_workspace_any(ScanProblem p, size_t (*need)(const ScanProblem &));
 cudaError_t launch_selective_scan(const ScanProblem &p);
 cudaError_t launch_scan_starts(const ScanProblem &p, const ScanSplit &s);
 cudaError_t launch_scan_reverse_starts(const ScanProblem &p, const ScanSplit &s, const float *dS);

@@ -207,7 +207,7 @@ size_t la_selective_scan_workspace(int B, int N, int D, int d_state, la_dtype dt
   if (scan_sizes(B, N, D, d_state, dt) != LA_OK || B == 0 || N == 0) return 0;
   ScanProblem p{};
   p.B = B, p.N = N, p.D = D, p.ds = d_state, p.dt = dt;
-  return backward ? scan_grad_workspace(p) : scan_workspace(p);
+  return scan_workspace_any(p, backward ? scan_grad_workspace : scan_workspace);
 }
 
 la_status la_selective_scan_backward(const void *x, long ldx, const void *delta, long ld_delta, const float *A,

@@ -55,6 +55,10 @@ struct Smem {
   } out[2];
 };
 
+// Where channel c's sums and dy are in a token's row: eight threads that read eight channels each, four at a
+// time, meet no bank twice.
+__device__ __forceinline__ int row_place(int c) { return c ^ (c >> 3 & 4); }
+
 // Barriers between the kinds of warps.
 enum Bar { kIn = 1, kAhFull = 4, kAhFree = 6, kOutFull = 8, kOutFree = 10, kOwn = 12 };
 
@@ -153,8 +157,10 @@ __global__ void __launch_bounds__(Layout<DS>::kThreads) scan_grad_kernel(const _
             if (!in) d = u = both(0.f);
             to.steps[row][step_slot(col / 2 + e)] = make_float4(d.x, u.x, d.y, u.y);
             if (kGate) dv[e] = __fmul2_rn(dv[e], __fmul2_rn(zv[e], Sigmoid2(zv[e]).s));
-            *reinterpret_cast<float2 *>(&to.dy[row][col + 2 * e]) = in ? dv[e] : both(0.f);
+            if (!in) dv[e] = both(0.f);
           }
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) st4(&to.dy[row][row_place(col + 2 * e)], dv[e].x, dv[e].y, dv[e + 1].x, dv[e + 1].y);
         }
 #pragma unroll
         for (int j = 0; j < kEach; ++j) {
@@ -174,14 +180,21 @@ __global__ void __launch_bounds__(Layout<DS>::kThreads) scan_grad_kernel(const _
         const typename Smem<DS>::Out &from = m.out[o & 1];
         const typename Smem<DS>::In &in = m.in[at == 2 ? 0 : at + 1];
         if (live && t < end) {
-          float2 xv[4], tv[4], dv[4], zv[4], ox[4], ot[4], oz[4];
+          float2 xv[4], tv[4], dv[4], zv[4], ox[4], ot[4], oz[4], s1v[4], s2v[4], yv[4], dyv[4];
+          auto row8 = [&](float2 (&v)[4], const float *of) {
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+              const float4 f = *reinterpret_cast<const float4 *>(of + row_place(col + 2 * e));
+              v[e] = make_float2(f.x, f.y), v[e + 1] = make_float2(f.z, f.w);
+            }
+          };
+          row8(s1v, from.s1[row]), row8(s2v, from.s2[row]), row8(dyv, in.dy[row]);
+          if (kGate) row8(yv, from.y[row]);
           done.x.get(xv), done.t.get(tv), done.d.get(dv);
           if (kGate) done.z.get(zv);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float2 s1 = *reinterpret_cast<const float2 *>(&from.s1[row][col + 2 * e]);
-            const float2 s2 = *reinterpret_cast<const float2 *>(&from.s2[row][col + 2 * e]);
-            const float2 dy = *reinterpret_cast<const float2 *>(&in.dy[row][col + 2 * e]);
+            const float2 s1 = s1v[e], s2 = s2v[e], dy = dyv[e];
             const float4 st = in.steps[row][step_slot(col / 2 + e)];
             ox[e] = __ffma2_rn(make_float2(st.x, st.z), s1, __fmul2_rn(skip[e], dy));
             ot[e] = __ffma2_rn(xv[e], s1, __fmul2_rn(s2, both(0.693147181f)));  // A carries log2 e
@@ -189,7 +202,7 @@ __global__ void __launch_bounds__(Layout<DS>::kThreads) scan_grad_kernel(const _
             dD[e] = __ffma2_rn(dy, xv[e], dD[e]);
             dbias[e] = __fadd2_rn(dbias[e], ot[e]);
             if (kGate) {
-              const float2 y = __ffma2_rn(skip[e], xv[e], *reinterpret_cast<const float2 *>(&from.y[row][col + 2 * e]));
+              const float2 y = __ffma2_rn(skip[e], xv[e], yv[e]);
               const Sigmoid2 sg(zv[e]);
               const float2 slope = __ffma2_rn(__fmul2_rn(zv[e], sg.s), sg.one_less(), sg.s);
               oz[e] = __fmul2_rn(__fmul2_rn(dv[e], y), slope);
@@ -232,7 +245,7 @@ __global__ void __launch_bounds__(Layout<DS>::kThreads) scan_grad_kernel(const _
   const bool forward = tid < kAround + kScan;
   const int me = tid - kAround - (forward ? 0 : kScan), warp = me >> 5;
   const int q = lane % kLanes, num = lane / kLanes, ch = (warp * kPerWarp + num) * 2;
-  const int c = cb * kCols + ch, slot = step_slot(ch / 2);  // and the next channel; D is even
+  const int c = cb * kCols + ch, slot = step_slot(ch / 2), place = row_place(ch);  // and the next channel; D is even
   const bool mine = c < p.D;
   const long at = (long)c * DS + kSN * q;  // in a state
   float2 A[2][kPairs];
@@ -328,7 +341,7 @@ __global__ void __launch_bounds__(Layout<DS>::kThreads) scan_grad_kernel(const _
     } now, then;
     auto fetch = [&](Token &v, int t) {
       v.d = in.steps[t][slot];
-      v.dy = *reinterpret_cast<const float2 *>(&in.dy[t][ch]);
+      v.dy = *reinterpret_cast<const float2 *>(&in.dy[t][place]);
       read(v.B, &in.B[t][kSN * q]);
       read(v.C, &in.C[t][kSN * q]);
 #pragma unroll
@@ -394,9 +407,9 @@ __global__ void __launch_bounds__(Layout<DS>::kThreads) scan_grad_kernel(const _
 #pragma unroll
       for (int v = 0; v < kHave; ++v) {
         const int t = i0 + v * kLanes + q;
-        *reinterpret_cast<float2 *>(&out.s1[t][ch]) = make_float2(s1[v], s1[kHave + v]);
-        *reinterpret_cast<float2 *>(&out.s2[t][ch]) = make_float2(s2[v], s2[kHave + v]);
-        if (kGate) *reinterpret_cast<float2 *>(&out.y[t][ch]) = make_float2(y[v], y[kHave + v]);
+        *reinterpret_cast<float2 *>(&out.s1[t][place]) = make_float2(s1[v], s1[kHave + v]);
+        *reinterpret_cast<float2 *>(&out.s2[t][place]) = make_float2(s2[v], s2[kHave + v]);
+        if (kGate) *reinterpret_cast<float2 *>(&out.y[t][place]) = make_float2(y[v], y[kHave + v]);
       }
     }
     if (i + 2 < chunks) bar_arrive<2 * kScan>(kAhFree + (i & 1));
@@ -500,7 +513,7 @@ Parts parts(const ScanProblem &p, const ScanSplit &s) {
   return q;
 }
 ScanSplit grad_split(const ScanProblem &p) {
-  ScanSplit s = scan_split(p);
+  ScanSplit s = scan_split(p, grad_cols(p.ds), 1);
   s.chunk = grad_tokens(p.ds);
   s.all_chunks = (p.N + s.chunk - 1) / s.chunk;
   return s;
