@@ -25,7 +25,6 @@ namespace la {
 namespace {
 
 constexpr int kTok = 32;         // tokens a chunk
-constexpr int kAround = 128;     // threads around the recurrence: (token, eight channels) in turns
 
 // Channels a block: as many as keep it within 400 threads.
 constexpr int scan_cols(int ds) { return ds == 64 ? 32 : 64; }
@@ -44,7 +43,8 @@ struct Smem {
 // kOutputs: out, and the last segment's end state to S.  kEnds: each segment's end state from zero and sum of
 // delta.  kStates: the state in front of each chunk of s.chunk tokens.  kReverseEnds: the same as kEnds for the
 // recurrence of the state's gradient, from a segment's last token to its first: G <- a_t (G + C_t dy_t).
-template <typename T, int DS, int kMode>
+// kAround: threads around the recurrence, (token, eight channels) in turns.
+template <typename T, int DS, int kMode, int kAround>
 __global__ void __launch_bounds__(scan_cols(DS) * DS / 8 + kAround) scan_kernel(const __grid_constant__ ScanProblem p, const __grid_constant__ ScanSplit s) {
   constexpr int kCols = Smem<DS, kMode>::kCols, kTurns = kTok * kCols / 8 / kAround;
   constexpr int kScan = kCols * DS / 8, kThreads = kScan + kAround, kLanes = DS / 4, kPerWarp = 64 / kLanes;
@@ -78,35 +78,50 @@ __global__ void __launch_bounds__(scan_cols(DS) * DS / 8 + kAround) scan_kernel(
     const T *x = (const T *)p.x + b * p.N * p.ldx + c8, *dt = (const T *)p.delta + b * p.N * p.ldt + c8;
     const T *z = p.z ? (const T *)p.z + b * p.N * p.ldz + c8 : nullptr;
     T *out = (T *)p.out + b * p.N * p.D + c8;
-    constexpr bool kNeedZ = kMode == kOutputs || kRev;
     // rows of B (and C), eight components a piece
     constexpr int kPerRow = DS / 8, kOne = kTok * kPerRow, kPieces = kMode == kOutputs ? 2 * kOne : kOne;
     constexpr int kEach = (kPieces + kAround - 1) / kAround;
     const T *Bm = (const T *)(kRev ? p.Cm : p.Bm) + b * p.N * (kRev ? p.ldc : p.ldb), *Cm = (const T *)p.Cm + b * p.N * p.ldc;
-    Raw<T> rx[kTurns], rt[kTurns], rz[kTurns], rb[kEach], kx[kTurns], kz[kTurns];
-    auto load = [&](long t0) {
+    // Rows of the chunk that goes in, and of the next one, which are on their way all the while (an iteration's time is
+    // about the latency of HBM: asked for only behind this chunk's work they cost 488 us for 390); x and z of the chunk
+    // that comes out are read again, from L2.
+    struct Rows {
+      Raw<T> x[kTurns], t[kTurns], z[kTurns], b[kEach];
+    } now, next;
+    Raw<T> ox[kTurns], oz[kTurns];
+    auto load = [&](Rows &r, long t0) {
 #pragma unroll
       for (int u = 0; u < kTurns; ++u) {
         const long t = t0 + row0 + u * kRows;
-        rx[u].zero(), rt[u].zero(), rz[u].zero();
+        r.x[u].zero(), r.t[u].zero(), r.z[u].zero();
         if (live && t < end) {
-          rx[u].load(x + t * p.ldx), rt[u].load(dt + t * p.ldt);
-          if (kNeedZ && z) rz[u].load(z + t * p.ldz);
+          r.x[u].load(x + t * p.ldx), r.t[u].load(dt + t * p.ldt);
+          if (kRev && z) r.z[u].load(z + t * p.ldz);
         }
       }
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
         const int k = at + i * kAround, which = k >= kOne, j = which ? k - kOne : k;
-        rb[i].zero();
+        r.b[i].zero();
         if (k < kPieces && t0 + j / kPerRow < end)
-          rb[i].load((which ? Cm : Bm) + (t0 + j / kPerRow) * (which ? p.ldc : kRev ? p.ldc : p.ldb) + j % kPerRow * 8);
+          r.b[i].load((which ? Cm : Bm) + (t0 + j / kPerRow) * (which ? p.ldc : kRev ? p.ldc : p.ldb) + j % kPerRow * 8);
       }
     };
-    if (chunks) load(first_of(0));
+    if (chunks) load(next, first_of(0));
     for (int k = 0; k <= chunks; ++k) {
-      Raw<T> px[kTurns], pz[kTurns];  // of the chunk whose sums come next
+      if (kMode == kOutputs && k > 0) {
 #pragma unroll
-      for (int u = 0; u < kTurns; ++u) px[u] = kx[u], pz[u] = kz[u];
+        for (int u = 0; u < kTurns; ++u) {
+          const long t = first_of(k - 1) + row0 + u * kRows;
+          ox[u].zero(), oz[u].zero();
+          if (live && t < end) {
+            if (p.Dskip) ox[u].load(x + t * p.ldx);
+            if (z) oz[u].load(z + t * p.ldz);
+          }
+        }
+      }
+      now = next;
+      if (k + 1 < chunks) load(next, first_of(k + 1));
       if (k < chunks) {
         Smem<DS, kMode> &to = m[k & 1];
 #pragma unroll
@@ -114,9 +129,8 @@ __global__ void __launch_bounds__(scan_cols(DS) * DS / 8 + kAround) scan_kernel(
           const int row = row0 + u * kRows;
           const bool in = first_of(k) + row < end;
           float2 xv[4], tv[4], zv[4];
-          rx[u].get(xv), rt[u].get(tv);
-          if (kRev) rz[u].get(zv);
-          kx[u] = rx[u], kz[u] = rz[u];
+          now.x[u].get(xv), now.t[u].get(tv);
+          if (kRev) now.z[u].get(zv);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             float2 d = __fadd2_rn(tv[e], bias[e]);
@@ -133,10 +147,9 @@ __global__ void __launch_bounds__(scan_cols(DS) * DS / 8 + kAround) scan_kernel(
         for (int i = 0; i < kEach; ++i) {
           const int q = at + i * kAround, which = q >= kOne, j = which ? q - kOne : q;
           float2 v[4];
-          rb[i].get(v);
+          now.b[i].get(v);
           if (q < kPieces) put8((which ? &to.C[0][0] : &to.B[0][0]) + j * 8, v);
         }
-        if (k + 1 < chunks) load(first_of(k + 1));
         bar_arrive<kThreads>(1 + (k & 1));
       }
       if (k > 0) {
@@ -151,7 +164,7 @@ __global__ void __launch_bounds__(scan_cols(DS) * DS / 8 + kAround) scan_kernel(
             const float4 y1 = *reinterpret_cast<const float4 *>(&from.sums[row][col + 4]);
             float2 y[4] = {make_float2(y0.x, y0.y), make_float2(y0.z, y0.w), make_float2(y1.x, y1.y), make_float2(y1.z, y1.w)};
             float2 xv[4], zv[4];
-            px[u].get(xv), pz[u].get(zv);
+            ox[u].get(xv), oz[u].get(zv);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               y[e] = __ffma2_rn(skip[e], xv[e], y[e]);
@@ -315,24 +328,33 @@ __global__ void __launch_bounds__(256) scan_join_kernel(const __grid_constant__ 
   }
 }
 
-template <typename T, int DS>
-cudaError_t launch_mode(const ScanProblem &p, ScanSplit s, int mode) {
-  s.launched = mode == kEnds || mode == kReverseEnds ? s.segs - 1 : s.segs;
-  constexpr int kCols = scan_cols(DS);
-  const long blocks = (long)p.B * s.launched * ((p.D + kCols - 1) / kCols);
-  const void *fn = mode == kOutputs ? (const void *)scan_kernel<T, DS, kOutputs>
-                   : mode == kEnds  ? (const void *)scan_kernel<T, DS, kEnds>
-                   : mode == kStates ? (const void *)scan_kernel<T, DS, kStates>
-                                     : (const void *)scan_kernel<T, DS, kReverseEnds>;
-  const int smem = 2 * (int)(mode == kOutputs ? sizeof(Smem<DS, kOutputs>) : sizeof(Smem<DS, kEnds>));
-  cudaError_t e = smem > 48 * 1024 ? ensure_smem_optin(fn, smem) : cudaSuccess;
+template <typename T, int DS, int kMode, int kAround>
+cudaError_t launch_kernel(const ScanProblem &p, const ScanSplit &s, long blocks) {
+  const void *fn = (const void *)scan_kernel<T, DS, kMode, kAround>;
+  constexpr int kSmem = 2 * (int)sizeof(Smem<DS, kMode>);
+  cudaError_t e = kSmem > 48 * 1024 ? ensure_smem_optin(fn, kSmem) : cudaSuccess;
   if (e != cudaSuccess) return e;
-  LaunchTimer timer(mode == kOutputs ? kKSelectiveScan : kKSelectiveState, p.stream);
-  void *args[] = {const_cast<ScanProblem *>(&p), &s};
-  e = cudaLaunchKernel(fn, dim3((unsigned)blocks), dim3(kCols * DS / 8 + kAround), args, smem, p.stream);
+  LaunchTimer timer(kMode == kOutputs ? kKSelectiveScan : kKSelectiveState, p.stream);
+  void *args[] = {const_cast<ScanProblem *>(&p), const_cast<ScanSplit *>(&s)};
+  e = cudaLaunchKernel(fn, dim3((unsigned)blocks), dim3(scan_cols(DS) * DS / 8 + kAround), args, kSmem, p.stream);
   timer.done(e);
   if (e == cudaSuccess) count_launch();
   return e;
+}
+
+// Outputs: where a block an SM is all there is, the work around its recurrence gets twice the warps (4 x 8192 x 2048 x 16:
+// 445 us to 413); with more blocks an SM their registers are worth more (16 x 2048 tokens: 347 us, with them 415).
+template <typename T, int DS>
+cudaError_t launch_mode(const ScanProblem &p, ScanSplit s, int mode) {
+  s.launched = mode == kEnds || mode == kReverseEnds ? s.segs - 1 : s.segs;
+  const long blocks = (long)p.B * s.launched * ((p.D + scan_cols(DS) - 1) / scan_cols(DS));
+  if (mode == kEnds) return launch_kernel<T, DS, kEnds, 128>(p, s, blocks);
+  if (mode == kStates) return launch_kernel<T, DS, kStates, 128>(p, s, blocks);
+  if (mode == kReverseEnds) return launch_kernel<T, DS, kReverseEnds, 128>(p, s, blocks);
+  if constexpr (scan_cols(DS) == 64) {
+    if (blocks <= device_info(-1).sm_count) return launch_kernel<T, DS, kOutputs, 256>(p, s, blocks);
+  }
+  return launch_kernel<T, DS, kOutputs, 128>(p, s, blocks);
 }
 
 template <typename T>
