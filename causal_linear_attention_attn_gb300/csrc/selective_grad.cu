@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(Layout<DS>::kThreads) scan_grad_kernel(const _
           float2 v[kPairs];
 #pragma unroll
           for (int e = 0; e < kPairs; ++e) {
-            v[e] = __fmul2_rn(exp2_approx(__fmul2_rn(dd, A[k][e])), h[k][e]);
+            v[e] = __fmul2_rn(decay(dd, A[k][e]), h[k][e]);
             h[k][e] = __ffma2_rn(u, B[e], v[e]);
           }
 #pragma unroll
@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(Layout<DS>::kThreads) scan_grad_kernel(const _
             const float2 w = __fmul2_rn(G[k][e], v[e]);
             t2 = e ? __ffma2_rn(w, A[k][e], t2) : __fmul2_rn(w, A[k][e]);
             part[k][e] = __ffma2_rn(w, dd, part[k][e]);
-            G[k][e] = __fmul2_rn(exp2_approx(__fmul2_rn(dd, A[k][e])), G[k][e]);
+            G[k][e] = __fmul2_rn(decay(dd, A[k][e]), G[k][e]);
           }
           s1[k * kStep + j] = t1.x + t1.y, s2[k * kStep + j] = t2.x + t2.y;
           if (kGate) y[k * kStep + j] = t3.x + t3.y;

@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(scan_cols(DS) * DS / 8 + kAround) scan_kernel(
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) a[j][i] = exp2_approx(__fmul2_rn(both(i < 2 ? now.d[j].x : now.d[j].z), A[i]));
+          for (int i = 0; i < 4; ++i) a[j][i] = decay(both(i < 2 ? now.d[j].x : now.d[j].z), A[i]);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           if (kMode == kStates && (f + j) % 8 == 0) {

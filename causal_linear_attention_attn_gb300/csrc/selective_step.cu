@@ -95,10 +95,10 @@ __global__ void __launch_bounds__(kThreads, 3) scan_step_kernel(const __grid_con
       if (in && !skip_row) {
         const float d2 = it.d2, du = it.du;
         float4 &s = h[r][u];
-        s.x = fmaf(exp2_approx(d2 * A[u].x), s.x, du * B.x);
-        s.y = fmaf(exp2_approx(d2 * A[u].y), s.y, du * B.y);
-        s.z = fmaf(exp2_approx(d2 * A[u].z), s.z, du * B.z);
-        s.w = fmaf(exp2_approx(d2 * A[u].w), s.w, du * B.w);
+        s.x = fmaf(exp2_approx(fmaf(d2, A[u].x, kLean)), s.x, du * B.x);
+        s.y = fmaf(exp2_approx(fmaf(d2, A[u].y, kLean)), s.y, du * B.y);
+        s.z = fmaf(exp2_approx(fmaf(d2, A[u].z, kLean)), s.z, du * B.z);
+        s.w = fmaf(exp2_approx(fmaf(d2, A[u].w, kLean)), s.w, du * B.w);
         __stcs(S + u * kThreads, s);
         y = fmaf(s.x, C.x, fmaf(s.y, C.y, fmaf(s.z, C.z, s.w * C.w)));
       }
