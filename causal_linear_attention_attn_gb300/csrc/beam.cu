@@ -7,15 +7,16 @@
 //
 // A block takes a run of one row in chunks of 4096 values, its warps an eighth of each, without waiting for one
 // another: a warp keeps 512 values in registers while the next ones are on their way, adds up their exponentials
-// against its running maximum, and keeps a list of candidates for its k best.  The bound that lets values into
-// the list is its k-th best so far; before there is one, the k-th largest of the lanes' largest values, sorted across
-// the lanes, is a value that at least k reach.  Lists are ranked by counting (every candidate against every other), not
+// against its running maximum, and keeps a list of candidates for its k best.  The bound that lets values into the
+// lists is the block's k-th best of the first chunk, or a warp's so far if that is better; before there is one, the k-th
+// largest of the lanes' largest values, sorted across the lanes, is a value that at least k reach.  Lists are ranked by counting (every candidate against every other), not
 // extracted one after another.  A second kernel, a block a group, joins the runs of a row and the rows of the group the
-// same way in 64 bits.
+// same way in 64 bits.  512 rows of 131072 in bf16 in 66 us, 2.0 TB/s: issue slots bound it (67 % taken, 300 instructions
+// per 512 values).  With barriers a chunk and a bound a warp it took 307 us, with 32 values a lane (fewer warps) 88.
 //
 // Reordering.  A beam's first child keeps the slot of its state in every pool; its other children get the
 // slots of the group's childless beams, with a copy.  So the states move no more than they must, in place:
-// what is read (kept slots) and what is written (freed ones) never meet.
+// what is read (kept slots) and what is written (freed ones) never meet.  192 rows of 573 KB in 39 us, 5.6 TB/s.
 #include <algorithm>
 
 #include "internal.h"

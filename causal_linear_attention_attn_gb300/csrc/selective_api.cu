@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <initializer_list>
+#include <utility>
 
 #include "internal.h"
 #include "linattn.h"
@@ -61,7 +62,7 @@ la_status scan_sizes(int B, long N, int D, int ds, la_dtype dt) {
   const la_status st = sizes(B, N, D, dt);
   if (st != LA_OK) return st;
   if (ds != 8 && ds != 16 && ds != 32 && ds != 64) return LA_ERR_UNSUPPORTED;
-  return (long)B * D * ds > 0x7fffffffL * 64 || (long)B * N * ds > 0x7fffffffL * 64 ? LA_ERR_INVALID_VALUE : LA_OK;
+  return (long)D * ds > 0x7fffffffL || (long)B * N * ds > 0x7fffffffL * 64 ? LA_ERR_INVALID_VALUE : LA_OK;
 }
 
 // A carried state that no token changes: zero, or as it is.

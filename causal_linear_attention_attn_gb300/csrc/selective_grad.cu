@@ -16,7 +16,10 @@
 // spread over a warp's channels, added over the block's warps, and leave as one partial sum a block of channels, which a
 // last kernel adds in order.  No atomics: the gradient is the same from run to run.
 //
-// Two exponentials and about twenty issue slots a component, channel and token bound it, and shared memory's port.
+// Two exponentials and about twenty issue slots a component, channel and token bound it, and shared memory's port:
+// 4 x 4096 x 2048 x 16 in bf16 in 880 us, 660 of them here (62 % of the issue slots and 70 % of the port on the 128 SMs
+// that have a block), 195 in the scan of states, 28 in the sums.  With one kind of warps and one channel a lane it
+// took 1337 us; with results out before the next rows in, 944.
 #include <algorithm>
 
 #include "internal.h"

@@ -457,7 +457,8 @@ LA_API size_t la_group_norm_workspace(int B, int H, int N, int d);
  * are not written.  D a multiple of 8, K in {2, 3, 4}.
  * la_short_conv_with_state starts from the window in S and updates it in
  * place.  Sums in fp32.  Pointers 16-byte aligned (lengths 4), ldx >= D and a
- * multiple of 16 bytes.  N == 0 leaves the carried window (zeros without one).
+ * multiple of 16 bytes.  out and S must not overlap an input.  N == 0 leaves the
+ * carried window (zeros without one).
  */
 LA_API la_status la_short_conv(const void *x, long ldx, const float *weight, const float *bias, const int *lengths,
                                void *out, void *S, int B, int N, int D, int K, int silu, la_dtype dt, void *stream);
@@ -485,7 +486,7 @@ LA_API size_t la_short_conv_workspace(int B, int N, int D, int K);
  * One token of la_short_conv per batch row, on windows that live in a pool S
  * [n_slots,K-1,D], dtype dt, read and written in place: row b works on
  * S[slots[b]].  x: [B,D], rows ldx apart; out: [B,D].  slots as in
- * la_gated_decode_step (unused, bad and repeated ones too).
+ * la_gated_decode_step (unused, bad and repeated ones too).  Allocates nothing.
  */
 LA_API la_status la_short_conv_step(const void *x, long ldx, const float *weight, const float *bias, void *S,
                                     const int *slots, void *out, int B, int n_slots, int D, int K, int silu, la_dtype dt,
@@ -506,9 +507,10 @@ LA_API la_status la_short_conv_step(const void *x, long ldx, const float *weight
  * la_short_conv.  la_selective_scan_with_state starts from S and updates it in
  * place.  Steps, states and sums in fp32.  D a multiple of 8, d_state in {8, 16,
  * 32, 64}; pointers 16-byte aligned (lengths 4), every ld at least its row and a
- * multiple of 16 bytes.  workspace: la_selective_scan_workspace(..., 0) bytes,
- * 256-byte aligned (NULL if that is 0).  N == 0 leaves the carried state (zeros
- * without one).
+ * multiple of 16 bytes.  out and S must not overlap an input.  workspace:
+ * la_selective_scan_workspace(..., 0) bytes, 256-byte aligned (NULL if that is 0);
+ * calls that may run at the same time need one each.  N == 0 leaves the carried
+ * state (zeros without one).
  */
 LA_API la_status la_selective_scan(const void *x, long ldx, const void *delta, long ld_delta, const float *A,
                                    const void *Bm, long ldb, const void *Cm, long ldc, const float *Dskip, const void *z,

@@ -136,6 +136,7 @@ def scan_common(call):
         assert call(**{n: least - 8}) == INVALID and call(**{n: least + 4}) == MISALIGNED and call(**{n: 1 << 33}) == INVALID
     assert call(ds=12) == UNSUPPORTED and call(ds=128) == UNSUPPORTED and call(ds=0) == INVALID
     assert call(C=36) == UNSUPPORTED and call(dt=7) == UNSUPPORTED and call(B=-1) == INVALID
+    assert call(C=1 << 26, ds=32, ldx=1 << 26, ldt=1 << 26, ldz=1 << 26) == INVALID  # a state of more than 31 bits count
 
 
 @pytest.mark.parametrize("fn", ["la_selective_scan", "la_selective_scan_with_state"])
