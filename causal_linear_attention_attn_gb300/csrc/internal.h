@@ -301,7 +301,7 @@ size_t scan_workspace(const ScanProblem &p);
 size_t scan_workspace_any(ScanProblem p, size_t (*need)(const ScanProblem &));
 cudaError_t launch_selective_scan(const ScanProblem &p);
 cudaError_t launch_scan_starts(const ScanProblem &p, const ScanSplit &s);
-cudaError_t launch_scan_reverse_starts(const ScanProblem &p, const ScanSplit &s, const float *dS);
+cudaError_t launch_scan_both_starts(const ScanProblem &p, const ScanSplit &s, const void *dout, const float *dS);
 cudaError_t launch_scan_states(const ScanProblem &p, const ScanSplit &s);
 size_t scan_grad_workspace(const ScanProblem &p);
 cudaError_t launch_selective_scan_grad(const ScanGradProblem &b);

@@ -537,11 +537,7 @@ cudaError_t launch_selective_scan_grad(const ScanGradProblem &g) {
   cudaError_t e = cudaSuccess;
   if (s.segs > 1) {
     s.starts = ws + at.starts, s.total = ws + at.total, s.rev_starts = ws + at.rev_starts, s.rev_total = ws + at.rev_total;
-    e = launch_scan_starts(p, s);
-    if (e != cudaSuccess) return e;
-    ScanProblem r = p;
-    r.x = g.dout, r.ldx = p.D;
-    e = launch_scan_reverse_starts(r, s, g.dS);
+    e = launch_scan_both_starts(p, s, g.dout, g.dS);
     if (e != cudaSuccess) return e;
   }
   e = launch_scan_states(p, s);

@@ -45,9 +45,9 @@ struct Smem {
 // kOutputs: out, and the last segment's end state to S.  kEnds: each segment's end state from zero and sum of
 // delta.  kStates: the state in front of each chunk of s.chunk tokens.  kReverseEnds: the same as kEnds for the
 // recurrence of the state's gradient, from a segment's last token to its first: G <- a_t (G + C_t dy_t).
-// kAround: threads around the recurrence, (token, eight channels) in turns.
+// kAround: threads around the recurrence, (token, eight channels) in turns.  `block` of the mode's blocks.
 template <typename T, int DS, int kMode, int kAround>
-__global__ void __launch_bounds__(scan_cols(DS) * DS / 8 + kAround) scan_kernel(const __grid_constant__ ScanProblem p, const __grid_constant__ ScanSplit s) {
+__device__ __forceinline__ void scan_block(const ScanProblem &p, const ScanSplit &s, unsigned block) {
   constexpr int kCols = Smem<DS, kMode>::kCols, kTurns = kTok * kCols / 8 / kAround;
   constexpr int kScan = kCols * DS / 8, kThreads = kScan + kAround, kLanes = DS / 4, kPerWarp = 64 / kLanes;
   constexpr bool kRev = kMode == kReverseEnds;
@@ -56,8 +56,8 @@ __global__ void __launch_bounds__(scan_cols(DS) * DS / 8 + kAround) scan_kernel(
   __shared__ float part[kAround / 32][Smem<DS, kMode>::kCols];
   const int tid = threadIdx.x, lane = tid & 31;
   const int nb = (p.D + kCols - 1) / kCols;
-  const int cb = blockIdx.x % nb;
-  const long rest = blockIdx.x / nb;
+  const int cb = block % nb;
+  const long rest = block / nb;
   const int seg = (int)(rest % s.launched) + (kRev ? 1 : 0);
   const long b = rest / s.launched;
   const long n = row_length(p.lengths, b, p.N);
@@ -299,15 +299,34 @@ __global__ void __launch_bounds__(scan_cols(DS) * DS / 8 + kAround) scan_kernel(
   }
 }
 
+template <typename T, int DS, int kMode, int kAround>
+__global__ void __launch_bounds__(scan_cols(DS) * DS / 8 + kAround) scan_kernel(const __grid_constant__ ScanProblem p, const __grid_constant__ ScanSplit s) {
+  scan_block<T, DS, kMode, kAround>(p, s, blockIdx.x);
+}
+
+// The ends of segments in both directions, side by side: the second half of the blocks runs q, whose x is the gradient of
+// the outputs.
+template <typename T, int DS>
+__global__ void __launch_bounds__(scan_cols(DS) * DS / 8 + 128)
+    scan_ends_kernel(const __grid_constant__ ScanProblem p, const __grid_constant__ ScanProblem q, const __grid_constant__ ScanSplit s) {
+  const unsigned half = gridDim.x / 2;
+  if (blockIdx.x < half)
+    scan_block<T, DS, kEnds, 128>(p, s, blockIdx.x);
+  else
+    scan_block<T, DS, kReverseEnds, 128>(q, s, blockIdx.x - half);
+}
+
 // Segment ends to segment starts, in place: starts[s] <- h, h <- e^{A total[s]} h + starts[s] (old), from S0; the
-// state's gradient the same way from the last segment, from dS.  A thread a component.
+// state's gradient (blockIdx.y = 1) the same way from the last segment, from dS.  A thread a component.
 __global__ void __launch_bounds__(256) scan_join_kernel(const __grid_constant__ ScanSplit s, const float *A,
-                                                        const float *S0, int B, int D, int ds, bool reverse) {
+                                                        const float *S0, const float *dS, int B, int D, int ds) {
+  const bool reverse = blockIdx.y;
   const long state = (long)D * ds, i = (long)blockIdx.x * 256 + threadIdx.x;
   if (i >= B * state) return;
   const long b = i / state, r = i - b * state, c = r / ds;
   const float a = A[r] * kLog2e;
-  float h = S0 ? S0[i] : 0.f;
+  const float *from = reverse ? dS : S0;
+  float h = from ? from[i] : 0.f;
   float *starts = (reverse ? s.rev_starts : s.starts) + b * s.segs * state + r;
   const float *total = (reverse ? s.rev_total : s.total) + b * s.segs * D + c;
   constexpr int kAhead = 8;
@@ -348,11 +367,10 @@ cudaError_t launch_kernel(const ScanProblem &p, const ScanSplit &s, long blocks)
 // 445 us to 413); with more blocks an SM their registers are worth more (16 x 2048 tokens: 347 us, with them 415).
 template <typename T, int DS>
 cudaError_t launch_mode(const ScanProblem &p, ScanSplit s, int mode) {
-  s.launched = mode == kEnds || mode == kReverseEnds ? s.segs - 1 : s.segs;
+  s.launched = mode == kEnds ? s.segs - 1 : s.segs;
   const long blocks = (long)p.B * s.launched * ((p.D + scan_cols(DS) - 1) / scan_cols(DS));
   if (mode == kEnds) return launch_kernel<T, DS, kEnds, 128>(p, s, blocks);
   if (mode == kStates) return launch_kernel<T, DS, kStates, 128>(p, s, blocks);
-  if (mode == kReverseEnds) return launch_kernel<T, DS, kReverseEnds, 128>(p, s, blocks);
   if constexpr (scan_cols(DS) == 64) {
     if (blocks <= device_info(-1).sm_count) return launch_kernel<T, DS, kOutputs, 256>(p, s, blocks);
   }
@@ -371,10 +389,31 @@ cudaError_t launch(const ScanProblem &p, const ScanSplit &s, int mode) {
   return p.dt == LA_F32 ? launch_ds<float>(p, s, mode) : launch_ds<__nv_bfloat16>(p, s, mode);
 }
 
-cudaError_t join(const ScanProblem &p, const ScanSplit &s, const float *from, bool reverse) {
+template <typename T, int DS>
+cudaError_t launch_ends(const ScanProblem &p, const ScanProblem &q, ScanSplit s) {
+  s.launched = s.segs - 1;
+  constexpr int kSmem = 2 * (int)sizeof(Smem<DS, kEnds>);
+  static_assert(kSmem <= 48 * 1024, "no opt-in needed");
+  const long blocks = 2L * p.B * s.launched * ((p.D + scan_cols(DS) - 1) / scan_cols(DS));
+  LaunchTimer timer(kKSelectiveState, p.stream);
+  scan_ends_kernel<T, DS><<<(unsigned)blocks, scan_cols(DS) * DS / 8 + 128, kSmem, p.stream>>>(p, q, s);
+  const cudaError_t e = cudaGetLastError();
+  timer.done(e);
+  if (e == cudaSuccess) count_launch();
+  return e;
+}
+template <typename T>
+cudaError_t launch_ends_ds(const ScanProblem &p, const ScanProblem &q, const ScanSplit &s) {
+  return p.ds == 8    ? launch_ends<T, 8>(p, q, s)
+         : p.ds == 16 ? launch_ends<T, 16>(p, q, s)
+         : p.ds == 32 ? launch_ends<T, 32>(p, q, s)
+                      : launch_ends<T, 64>(p, q, s);
+}
+
+cudaError_t join(const ScanProblem &p, const ScanSplit &s, const float *dS, int directions) {
   const long all = (long)p.B * p.D * p.ds;
   LaunchTimer timer(kKSelectiveState, p.stream);
-  scan_join_kernel<<<(unsigned)((all + 255) / 256), 256, 0, p.stream>>>(s, p.A, from, p.B, p.D, p.ds, reverse);
+  scan_join_kernel<<<dim3((unsigned)((all + 255) / 256), directions), 256, 0, p.stream>>>(s, p.A, p.S0, dS, p.B, p.D, p.ds);
   const cudaError_t e = cudaGetLastError();
   timer.done(e);
   if (e == cudaSuccess) count_launch();
@@ -425,12 +464,14 @@ size_t scan_workspace_any(ScanProblem p, size_t (*need)(const ScanProblem &)) {
 
 cudaError_t launch_scan_starts(const ScanProblem &p, const ScanSplit &s) {
   const cudaError_t e = launch(p, s, kEnds);
-  return e != cudaSuccess ? e : join(p, s, p.S0, false);
+  return e != cudaSuccess ? e : join(p, s, nullptr, 1);
 }
 
-cudaError_t launch_scan_reverse_starts(const ScanProblem &p, const ScanSplit &s, const float *dS) {
-  const cudaError_t e = launch(p, s, kReverseEnds);
-  return e != cudaSuccess ? e : join(p, s, dS, true);
+cudaError_t launch_scan_both_starts(const ScanProblem &p, const ScanSplit &s, const void *dout, const float *dS) {
+  ScanProblem q = p;
+  q.x = dout, q.ldx = p.D;
+  const cudaError_t e = p.dt == LA_F32 ? launch_ends_ds<float>(p, q, s) : launch_ends_ds<__nv_bfloat16>(p, q, s);
+  return e != cudaSuccess ? e : join(p, s, dS, 2);
 }
 
 cudaError_t launch_scan_states(const ScanProblem &p, const ScanSplit &s) { return launch(p, s, kStates); }

@@ -575,13 +575,17 @@ def _rows(name, t, shape, dtype, device):
     """The distance of t's rows in elements, after checking its shape, dtype and device: rows of consecutive values at
     one distance throughout (a contiguous tensor, or a part of the last dimension of one)."""
     if isinstance(t, torch.Tensor) and t.get_device() == device.index and t.dtype is dtype and t.shape == shape:
-        if t.is_contiguous():
+        strides = t.stride()
+        if strides[-1] == 1:  # (dimensions of one row have no distance)
+            rows = shape[-2]
+            if len(shape) == 2:
+                return strides[0] if rows > 1 else shape[1]
+            if rows == 1:
+                return strides[0] if shape[0] > 1 else shape[2]
+            if shape[0] == 1 or strides[0] == rows * strides[1]:
+                return strides[1]
+        if t.numel() == 0:
             return shape[-1]
-        strides = [(n, d) for n, d in zip(shape[:-1], t.stride()[:-1]) if n > 1]
-        if not strides:
-            return shape[-1]
-        if t.stride(-1) == 1 and (len(strides) == 1 or strides[0][1] == strides[1][0] * strides[1][1]):
-            return strides[-1][1]
         raise ValueError(f"{name} must be contiguous, or one part of the last dimension of a contiguous tensor")
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -853,8 +857,8 @@ def la_beam_select(logits, scores, k=None, finished=None, eos: int = 0, stream=N
     _opt("finished", finished, (G, W), torch.bool, dev)
     s, ctx = _on(dev, stream)
     try:
-        best = torch.empty(G, max(k, 0), dtype=torch.float32, device=dev)
-        parents, tokens = (torch.empty(G, max(k, 0), dtype=torch.int32, device=dev) for _ in range(2))
+        best = torch.empty((G, max(k, 0)), dtype=torch.float32, device=dev)
+        parents, tokens = (torch.empty((G, max(k, 0)), dtype=torch.int32, device=dev) for _ in range(2))
         need = _beam_workspace(dev.index, G, W, k, V, dt)
         ws = _workspace(need, dev)
         rc = lib.la_beam_select(_ptr(logits), ld, _ptr(scores), _ptr(finished), _ptr(best), _ptr(parents), _ptr(tokens), G,
