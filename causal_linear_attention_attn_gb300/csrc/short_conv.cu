@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) short_conv_kernel(const __gr
 template <typename T, int K>
 __global__ void __launch_bounds__(kGradThreads, kPerSm)
     short_conv_grad_kernel(const __grid_constant__ ConvGradProblem q, int segs, int len, float *sums) {
-  constexpr int V = kV;
+  constexpr int V = kV, kRows = sizeof(T) == 4 ? 2 : kAhead;  // (fp32: four spill registers, 222 us for 155)
   const ConvProblem &p = q.p;
   const Run me(p, (long)blockIdx.x * kGradThreads + threadIdx.x, p.D / V, segs, len);
   if (!me.live) return;
@@ -239,9 +239,9 @@ __global__ void __launch_bounds__(kGradThreads, kPerSm)
     const int carried = dS ? (int)min(me.n - me.t0, 0x3fffffffL) : 0x3fffffff;  // from that step on dS adds
     const T *xi = x + me.t0 * p.ldx, *yi = (const T *)q.dout + (me.b * p.N + me.t0) * p.D + c;
     T *o = dx + (me.t0 - (K - 1)) * p.D;
-    Row<T, V> rx[kAhead], ry[kAhead];
+    Row<T, V> rx[kRows], ry[kRows];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
+    for (int u = 0; u < kRows; ++u) {
       rx[u].zero(), ry[u].zero();
       if (u < there) rx[u].load(xi + u * p.ldx), ry[u].load(yi + (long)u * p.D);
     }
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kGradThreads, kPerSm)
       float2 gg[V / 2];
 #pragma unroll
       for (int e = 0; e < V / 2; ++e) v[K - 1][e] = rx[u].pair(e), gg[e] = ry[u].pair(e);
-      if (i + kAhead < there) {
+      if (i + kRows < there) {
         rx[u].load(xi + u * p.ldx), ry[u].load(yi + (long)u * p.D);
       } else if (!kInside) {
         rx[u].zero(), ry[u].zero();
@@ -289,17 +289,17 @@ __global__ void __launch_bounds__(kGradThreads, kPerSm)
       else if (me.seg == 0 && dS0)
         to.store(dS0 + (long)i * p.D);
     };
-    for (int i0 = 0; i0 < steps; i0 += kAhead) {
-      xi += kAhead * p.ldx, yi += (long)kAhead * p.D;
-      if (i0 >= K - 1 && i0 + kAhead <= min(count, carried)) {
+    for (int i0 = 0; i0 < steps; i0 += kRows) {
+      xi += kRows * p.ldx, yi += (long)kRows * p.D;
+      if (i0 >= K - 1 && i0 + kRows <= min(count, carried)) {
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) step(std::true_type{}, i0 + u, u);
+        for (int u = 0; u < kRows; ++u) step(std::true_type{}, i0 + u, u);
       } else {
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u)
+        for (int u = 0; u < kRows; ++u)
           if (i0 + u < steps) step(std::false_type{}, i0 + u, u);
       }
-      o += (long)kAhead * p.D;
+      o += (long)kRows * p.D;
     }
   }
   Row<T, V> none;
