@@ -10,16 +10,16 @@
 // this kernel goes through the chunks from the last to the first, with the scan's layout (a lane: four components, of
 // d_state = 64 eight, of two channels) and three kinds of warps, a chunk apart:
 //   1. around: rows in, steps, dy, B and C to shared memory; later dx, ddt, dz out, and dB, dC added over the warps;
-//   2. forward: the recurrence again, leaving a_t h_{t-1} of every token in shared memory;
-//   3. backward: G in registers, everything that depends on it.  A lane reads the a h that its like wrote.
+//   2. forward: the recurrence again, leaving a_t h_{t-1} of every token in shared memory, y, and h dy summed to dC;
+//   3. backward: G in registers, and what depends on it.  A lane reads the a h that its like wrote.
 // Sums over the components are spread over a channel's lanes; the sums of dB and dC over channels are
 // spread over a warp's channels, added over the block's warps, and leave as one partial sum a block of channels, which a
 // last kernel adds in order.  No atomics: the gradient is the same from run to run.
 //
-// Two exponentials and about twenty issue slots a component, channel and token bound it, and shared memory's port:
-// 4 x 4096 x 2048 x 16 in bf16 in 880 us, 660 of them here (62 % of the issue slots and 70 % of the port on the 128 SMs
-// that have a block), 195 in the scan of states, 28 in the sums.  With one kind of warps and one channel a lane it
-// took 1337 us; with results out before the next rows in, 944.
+// Shared memory's port bounds it (60 of its cycles a token and pair of warps, 84 % taken on the 128 SMs that have a block
+// of 4 x 4096 x 2048 x 16), and two exponentials and about twenty issue slots a component: 866 us in bf16, 650 of them
+// here, 196 in the scan of states, 28 in the sums.  With one kind of warps and one channel a lane it took 1337 us; with
+// results out before the next rows in, 944; with y and dC in the third kind of warps, 876 (8 components: 826 for 738).
 #include <algorithm>
 
 #include "internal.h"
@@ -280,6 +280,16 @@ __global__ void __launch_bounds__(Layout<DS>::kThreads) scan_grad_kernel(const _
 #pragma unroll
     for (int e = 0; e < kPairs; ++e) A[i][e] = __fmul2_rn(A[i][e], both(kLog2e));
 
+  // Sums over the warp's channels of kSN values of each of kBatch tokens from t0 on: dB (first = 0) or dC (first = DS).
+  auto put_sums = [&](float (&v)[kBatch * kSN], typename Smem<DS>::Out &out, int t0, int first) {
+    spread_sum<kPerWarp, kBatch * kSN, kLanes>(v, num);
+#pragma unroll
+    for (int r = 0; r < kBatch * kSN / kPerWarp; ++r) {
+      const int k = num + r * kPerWarp;
+      out.bc[t0 + k / kSN][warp][first + kSN * q + k % kSN] = v[r];
+    }
+  };
+
   if (forward) {
     float2 h[2][kPairs], next[2][kPairs];
     auto states_of = [&](int i) { return s.chunk_states + (b * s.all_chunks + first_of(i) / kTok) * state; };
@@ -292,25 +302,57 @@ __global__ void __launch_bounds__(Layout<DS>::kThreads) scan_grad_kernel(const _
         for (int e = 0; e < kPairs; ++e) h[k][e] = next[k][e];
       if (i + 1 < chunks) get(next, states_of(i + 1));
       bar_sync<kAround + kScan>(kIn + buf);
-      if (i >= 2) bar_sync<2 * kScan>(kAhFree + (i & 1));
+      if (i >= 2) {
+        bar_sync<2 * kScan>(kAhFree + (i & 1));
+        bar_sync<kAround + kScan>(kOutFree + (i & 1));
+      }
       const typename Smem<DS>::In &in = m.in[buf];
+      typename Smem<DS>::Out &out = m.out[i & 1];
       auto &ah = m.ah[i & 1];
+      struct Token {  // as below
+        float4 d;
+        float2 dy, B[kPairs], C[kPairs];
+      } now, then;
+      auto fetch = [&](Token &v, int t) {
+        v.d = in.steps[t][slot];
+        v.dy = *reinterpret_cast<const float2 *>(&in.dy[t][place]);
+        read(v.B, &in.B[t][kSN * q]);
+        read(v.C, &in.C[t][kSN * q]);
+      };
+      fetch(now, 0);
+#pragma unroll 4
+      for (int i0 = 0; i0 < kTok; i0 += kStep) {
+        float y[2 * kStep], sums[kBatch * kSN];  // of the two channels; of dC
 #pragma unroll
-      for (int t = 0; t < kTok; ++t) {
-        const float4 d = in.steps[t][slot];
-        float2 B[kPairs];
-        read(B, &in.B[t][kSN * q]);
+        for (int j = 0; j < kStep; ++j) {
+          const int t = i0 + j;
+          if (t + 1 < kTok) fetch(then, t + 1);
+          float2 dC[kPairs];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float2 dd = both(k ? d.z : d.x), u = both(k ? d.w : d.y);
-          float2 v[kPairs];
+          for (int k = 0; k < 2; ++k) {
+            const float2 dd = both(k ? now.d.z : now.d.x), u = both(k ? now.d.w : now.d.y), dyk = both(k ? now.dy.y : now.dy.x);
+            float2 v[kPairs], t3 = both(0.f);
 #pragma unroll
-          for (int e = 0; e < kPairs; ++e) {
-            v[e] = __fmul2_rn(decay(dd, A[k][e]), h[k][e]);
-            h[k][e] = __ffma2_rn(u, B[e], v[e]);
+            for (int e = 0; e < kPairs; ++e) {
+              v[e] = __fmul2_rn(decay(dd, A[k][e]), h[k][e]);
+              h[k][e] = __ffma2_rn(u, now.B[e], v[e]);
+              dC[e] = k ? __ffma2_rn(h[k][e], dyk, dC[e]) : __fmul2_rn(h[k][e], dyk);
+              if (kGate) t3 = e ? __ffma2_rn(h[k][e], now.C[e], t3) : __fmul2_rn(h[k][e], now.C[e]);
+            }
+            if (kGate) y[k * kStep + j] = t3.x + t3.y;
+#pragma unroll
+            for (int e = 0; e < kPairs; e += 2) ah[t][(k * kPairs + e) / 2][me] = make_float4(v[e].x, v[e].y, v[e + 1].x, v[e + 1].y);
           }
 #pragma unroll
-          for (int e = 0; e < kPairs; e += 2) ah[t][(k * kPairs + e) / 2][me] = make_float4(v[e].x, v[e].y, v[e + 1].x, v[e + 1].y);
+          for (int e = 0; e < kPairs; ++e) sums[j % kBatch * kSN + 2 * e] = dC[e].x, sums[j % kBatch * kSN + 2 * e + 1] = dC[e].y;
+          if (j % kBatch == kBatch - 1) put_sums(sums, out, t - (kBatch - 1), DS);
+          now = then;
+        }
+        if (kGate) {
+          spread_sum<kLanes, 2 * kStep, 1>(y, q);
+          constexpr int kHave = kStep / kLanes;
+#pragma unroll
+          for (int v = 0; v < kHave; ++v) *reinterpret_cast<float2 *>(&out.y[i0 + v * kLanes + q][place]) = make_float2(y[v], y[kHave + v]);
         }
       }
       bar_arrive<2 * kScan>(kAhFull + (i & 1));
@@ -327,7 +369,6 @@ __global__ void __launch_bounds__(Layout<DS>::kThreads) scan_grad_kernel(const _
   int buf = 0;
   for (int i = 0; i < chunks; ++i) {
     bar_sync<2 * kScan>(kAhFull + (i & 1));
-    if (i >= 2) bar_sync<kAround + kScan>(kOutFree + (i & 1));
     const typename Smem<DS>::In &in = m.in[buf];
     typename Smem<DS>::Out &out = m.out[i & 1];
     const auto &ah = m.ah[i & 1];
@@ -358,8 +399,8 @@ __global__ void __launch_bounds__(Layout<DS>::kThreads) scan_grad_kernel(const _
     fetch(now, kTok - 1);
 #pragma unroll 1
     for (int i0 = kTok - kStep; i0 >= 0; i0 -= kStep) {
-      float s1[2 * kStep], s2[2 * kStep], y[2 * kStep];  // of the first channel, of the second
-      float sums[kBatch * 2 * kSN];                      // of dB and dC
+      float s1[2 * kStep], s2[2 * kStep];  // of the first channel, of the second
+      float sums[kBatch * kSN];            // of dB
 #pragma unroll
       for (int j = kStep - 1; j >= 0; --j) {
         const int t = i0 + j;
@@ -367,52 +408,37 @@ __global__ void __launch_bounds__(Layout<DS>::kThreads) scan_grad_kernel(const _
         const float4 d = now.d;
         const float2 dy = now.dy;
         const auto &B = now.B, &C = now.C;
-        float2 dB[kPairs], dC[kPairs];
+        float2 dB[kPairs];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const float2 dd = both(k ? d.z : d.x), u = both(k ? d.w : d.y), dyk = both(k ? dy.y : dy.x);
           const auto &v = now.ah[k];
-          float2 t1 = both(0.f), t2 = both(0.f), t3 = both(0.f);
+          float2 t1 = both(0.f), t2 = both(0.f);
 #pragma unroll
           for (int e = 0; e < kPairs; ++e) {
             G[k][e] = __ffma2_rn(C[e], dyk, G[k][e]);
-            const float2 h = __ffma2_rn(u, B[e], v[e]);
             dB[e] = k ? __ffma2_rn(G[k][e], u, dB[e]) : __fmul2_rn(G[k][e], u);
-            dC[e] = k ? __ffma2_rn(h, dyk, dC[e]) : __fmul2_rn(h, dyk);
             t1 = e ? __ffma2_rn(G[k][e], B[e], t1) : __fmul2_rn(G[k][e], B[e]);
-            if (kGate) t3 = e ? __ffma2_rn(h, C[e], t3) : __fmul2_rn(h, C[e]);
             const float2 w = __fmul2_rn(G[k][e], v[e]);
             t2 = e ? __ffma2_rn(w, A[k][e], t2) : __fmul2_rn(w, A[k][e]);
             part[k][e] = __ffma2_rn(w, dd, part[k][e]);
             G[k][e] = __fmul2_rn(decay(dd, A[k][e]), G[k][e]);
           }
           s1[k * kStep + j] = t1.x + t1.y, s2[k * kStep + j] = t2.x + t2.y;
-          if (kGate) y[k * kStep + j] = t3.x + t3.y;
         }
-        float *v = sums + j % kBatch * 2 * kSN;
 #pragma unroll
-        for (int e = 0; e < kPairs; ++e)
-          v[2 * e] = dB[e].x, v[2 * e + 1] = dB[e].y, v[kSN + 2 * e] = dC[e].x, v[kSN + 2 * e + 1] = dC[e].y;
-        if (j % kBatch == 0) {
-          spread_sum<kPerWarp, kBatch * 2 * kSN, kLanes>(sums, num);
-#pragma unroll
-          for (int r = 0; r < kBatch * 2 * kSN / kPerWarp; ++r) {
-            const int k = num + r * kPerWarp, of = k / (2 * kSN), n8 = k % (2 * kSN);  // token; dB's components, then dC's
-            out.bc[t + of][warp][n8 / kSN * DS + kSN * q + n8 % kSN] = sums[r];
-          }
-        }
+        for (int e = 0; e < kPairs; ++e) sums[j % kBatch * kSN + 2 * e] = dB[e].x, sums[j % kBatch * kSN + 2 * e + 1] = dB[e].y;
+        if (j % kBatch == 0) put_sums(sums, out, t, 0);
         now = then;
       }
       spread_sum<kLanes, 2 * kStep, 1>(s1, q);
       spread_sum<kLanes, 2 * kStep, 1>(s2, q);
-      if (kGate) spread_sum<kLanes, 2 * kStep, 1>(y, q);
       constexpr int kHave = kStep / kLanes;
 #pragma unroll
       for (int v = 0; v < kHave; ++v) {
         const int t = i0 + v * kLanes + q;
         *reinterpret_cast<float2 *>(&out.s1[t][place]) = make_float2(s1[v], s1[kHave + v]);
         *reinterpret_cast<float2 *>(&out.s2[t][place]) = make_float2(s2[v], s2[kHave + v]);
-        if (kGate) *reinterpret_cast<float2 *>(&out.y[t][place]) = make_float2(y[v], y[kHave + v]);
       }
     }
     if (i + 2 < chunks) bar_arrive<2 * kScan>(kAhFree + (i & 1));
