@@ -19,7 +19,16 @@ __device__ __forceinline__ float exp2_approx(float x) {
 }
 __device__ __forceinline__ float2 exp2_approx(float2 x) { return make_float2(exp2_approx(x.x), exp2_approx(x.y)); }
 
-// A state's decay e^{delta A}, A times log2 e.  The instruction's results are low on average, measured over each
+// A log2 e.  A = -inf, a component that forgets at once, becomes the lowest finite number: a token without a step, padding
+// among them, still changes nothing.
+__device__ __forceinline__ float rate(float A) {
+  constexpr float kLowest = -3.402823466e38f;
+  const float r = A * kLog2e;
+  return r < kLowest ? kLowest : r;
+}
+__device__ __forceinline__ float2 rate(float2 A) { return make_float2(rate(A.x), rate(A.y)); }
+
+// A state's decay e^{delta A}, A as rate(A).  The instruction's results are low on average, measured over each
 // power of two of the exponent: by 0.5e-8 to 2.6e-8 of their value above 2^-1/8, 5e-8 below.  A state that remembers a
 // thousand tokens is a product of as many, so the exponent leans up by what centres those (2^kLean is still exactly 1: a
 // token without a step changes nothing).  2 x 4096 x 512 x 16: the gradient of A is

@@ -16,7 +16,7 @@
 // spread over a warp's channels, added over the block's warps, and leave as one partial sum a block of channels, which a
 // last kernel adds in order.  No atomics: the gradient is the same from run to run.
 //
-// Shared memory's port bounds it (60 of its cycles a token and pair of warps, 84 % taken on the 128 SMs that have a block
+// Shared memory's port bounds it (60 of its cycles a token and pair of warps, 81 % taken on the 128 SMs that have a block
 // of 4 x 4096 x 2048 x 16), and two exponentials and about twenty issue slots a component: 866 us in bf16, 650 of them
 // here, 196 in the scan of states, 28 in the sums.  With one kind of warps and one channel a lane it took 1337 us; with
 // results out before the next rows in, 944; with y and dC in the third kind of warps, 876 (8 components: 826 for 738).
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(Layout<DS>::kThreads) scan_grad_kernel(const _
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int e = 0; e < kPairs; ++e) A[i][e] = __fmul2_rn(A[i][e], both(kLog2e));
+    for (int e = 0; e < kPairs; ++e) A[i][e] = rate(A[i][e]);
 
   // Sums over the warp's channels of kSN values of each of kBatch tokens from t0 on: dB (first = 0) or dC (first = DS).
   auto put_sums = [&](float (&v)[kBatch * kSN], typename Smem<DS>::Out &out, int t0, int first) {

@@ -227,7 +227,7 @@ __device__ __forceinline__ void scan_block(const ScanProblem &p, const ScanSplit
     if (from) get(h, from);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) A[i] = __fmul2_rn(A[i], both(kLog2e));
+  for (int i = 0; i < 4; ++i) A[i] = rate(A[i]);
   for (int k = 0; k < chunks; ++k) {
     Smem<DS, kMode> &in = m[k & 1];
     const long t0 = first_of(k);
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(256) scan_join_kernel(const __grid_constant__ 
   const long state = (long)D * ds, i = (long)blockIdx.x * 256 + threadIdx.x;
   if (i >= B * state) return;
   const long b = i / state, r = i - b * state, c = r / ds;
-  const float a = A[r] * kLog2e;
+  const float a = rate(A[r]);
   const float *from = reverse ? dS : S0;
   float h = from ? from[i] : 0.f;
   float *starts = (reverse ? s.rev_starts : s.starts) + b * s.segs * state + r;

@@ -26,7 +26,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_step_kernel(const __grid_con
   constexpr int kLanes = DS / 4;
   constexpr int kCols = kThreads * kPer / kLanes;  // channels a block
   struct Item {
-    float d2, du, gate, skip;  // delta log2 e, delta x, silu(z), D x
+    float d, du, gate, skip;  // delta, delta x, silu(z), D x
   };
   __shared__ Item items[kRows][kCols];
   __shared__ __align__(16) float bc[kRows][2][DS];
@@ -61,13 +61,15 @@ __global__ void __launch_bounds__(kThreads, 3) scan_step_kernel(const __grid_con
     float d = ldf((const T *)p.delta + b * p.ldt + c) + (p.dt_bias ? p.dt_bias[c] : 0.f);
     const float z = p.z ? ldf((const T *)p.z + b * p.ldz + c) : 0.f;
     if (p.softplus) d = softplus2(both(d)).x;
-    items[r][j] = Item{d * kLog2e, d * x, p.z ? z * Sigmoid2(both(z)).s.x : 1.f, p.Dskip ? p.Dskip[c] * x : 0.f};
+    items[r][j] = Item{d, d * x, p.z ? z * Sigmoid2(both(z)).s.x : 1.f, p.Dskip ? p.Dskip[c] * x : 0.f};
   }
   for (int i = threadIdx.x; i < kRows * 2 * DS; i += kThreads) {
     const int r = i / (2 * DS), j = i % (2 * DS);
     const long b = b0 + r;
     if (b < p.B) bc[r][j / DS][j % DS] = j < DS ? ldf((const T *)p.Bm + b * p.ldb + j) : ldf((const T *)p.Cm + b * p.ldc + j - DS);
   }
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) A[u] = make_float4(rate(A[u].x), rate(A[u].y), rate(A[u].z), rate(A[u].w));
   __syncthreads();
   if (p.slots) {
     for (int o = threadIdx.x; o < min(b0 + kRows, p.B) - 1; o += kThreads) {
@@ -94,12 +96,12 @@ __global__ void __launch_bounds__(kThreads, 3) scan_step_kernel(const __grid_con
       float y = 0.f;
       const Item &it = items[r][(threadIdx.x + u * kThreads) / kLanes];
       if (in && !skip_row) {
-        const float d2 = it.d2, du = it.du;
+        const float d = it.d, du = it.du;
         float4 &s = h[r][u];
-        s.x = fmaf(exp2_approx(fmaf(d2, A[u].x, kLean)), s.x, du * B.x);
-        s.y = fmaf(exp2_approx(fmaf(d2, A[u].y, kLean)), s.y, du * B.y);
-        s.z = fmaf(exp2_approx(fmaf(d2, A[u].z, kLean)), s.z, du * B.z);
-        s.w = fmaf(exp2_approx(fmaf(d2, A[u].w, kLean)), s.w, du * B.w);
+        s.x = fmaf(exp2_approx(fmaf(d, A[u].x, kLean)), s.x, du * B.x);
+        s.y = fmaf(exp2_approx(fmaf(d, A[u].y, kLean)), s.y, du * B.y);
+        s.z = fmaf(exp2_approx(fmaf(d, A[u].z, kLean)), s.z, du * B.z);
+        s.w = fmaf(exp2_approx(fmaf(d, A[u].w, kLean)), s.w, du * B.w);
         __stcs(S + u * kThreads, s);
         y = fmaf(s.x, C.x, fmaf(s.y, C.y, fmaf(s.z, C.z, s.w * C.w)));
       }

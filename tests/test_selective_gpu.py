@@ -298,3 +298,24 @@ def test_pool_of_more_elements_than_31_bits_count(cuda_lib):
     within(o, ref[:, 0], bound[:, 0], "out")
     within(pool[at.long()], S, Sb, "S")
     assert pool[: slots - 1].count_nonzero() == pool[1].count_nonzero(), "a state outside the batch was touched"
+
+
+@pytest.mark.parametrize("ds", [8, 16, 32, 64])
+@pytest.mark.parametrize("N", [1, 70, 600])
+def test_components_that_forget_at_once(cuda_lib, ds, N):
+    """A = -inf is e^{delta A} = 0 at every token with a step, as a very low A is, and none in the padding."""
+    lengths = torch.tensor([N, N // 2, 0], dtype=torch.int32, device="cuda")
+    d = make(3, N, 24, ds, F32, seed=ds + N, state=True)
+    low, inf = dict(d, A=d["A"].clone()), dict(d, A=d["A"].clone())
+    low["A"][::3, ::2], inf["A"][::3, ::2] = -1e38, -float("inf")
+    for lens in (None, lengths):
+        a, b = run(cuda_lib, low, lens), run(cuda_lib, inf, lens)
+        assert torch.equal(a[0].nan_to_num(7.0), b[0].nan_to_num(7.0)) and torch.equal(a[1], b[1]) and b[1].isfinite().all()
+        for n, x in grads(cuda_lib, inf, lens).items():
+            assert x.isfinite().all(), n
+            assert torch.equal(x, grads(cuda_lib, low, lens)[n]), n
+    pools = [d["S0"].clone(), d["S0"].clone()]
+    t = lambda e: ([e["x"][:, 0].contiguous(), e["dt"][:, 0].contiguous(), e["A"], e["Bm"][:, 0].contiguous(),  # noqa: E731
+                    e["Cm"][:, 0].contiguous()], {"D": e["D"], "z": e["z"][:, 0].contiguous(), "dt_bias": e["dt_bias"]})
+    outs = [cuda_lib.la_selective_scan_step(*t(e)[0], S, **t(e)[1]) for e, S in zip((low, inf), pools)]
+    assert torch.equal(*outs) and torch.equal(*pools)
