@@ -27,6 +27,11 @@ bool overlap(const void *a, const void *b, size_t bytes) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return a && b && (x < y ? y - x : x - y) < bytes;
 }
+// Memory of `an` bytes at a and of `bn` at b.
+bool meets(const void *a, size_t an, const void *b, size_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + bn && y < x + an;
+}
 int bytes_of(la_dtype dt) { return dt == LA_F32 ? 4 : 2; }
 
 // Rows of `width` values, `ld` apart: long enough and 16-byte aligned, and the whole tensor addressable.
@@ -42,6 +47,18 @@ la_status all_rows_ok(std::initializer_list<std::pair<long, long>> rows, la_dtyp
     if (s != LA_OK) st = s;
   }
   return st;
+}
+
+struct Input {
+  const void *at;
+  long ld, width;
+};
+// Whether an output of `rows` rows of D values meets an input's rows.
+bool over_inputs(const void *out, long rows, long D, la_dtype dt, std::initializer_list<Input> inputs) {
+  const size_t size = bytes_of(dt);
+  for (const Input &i : inputs)
+    if (meets(out, rows * D * size, i.at, ((rows - 1) * i.ld + i.width) * size)) return true;
+  return false;
 }
 
 // Every launch counts its blocks, of at least eight channels and a token each, in 31 bits.
@@ -86,6 +103,7 @@ la_status conv(const void *x, long ldx, const float *weight, const float *bias, 
   if ((st = rows_ok(ldx, D, dt)) != LA_OK) return st;
   if (!aligned({x, weight, bias, out, S}, 16) || !aligned({lengths}, 4)) return LA_ERR_MISALIGNED;
   if (N == 0) return empty(S, (size_t)B * (K - 1) * D * bytes_of(dt), from_state, stream);
+  if (over_inputs(out, (long)B * N, D, dt, {{x, ldx, D}})) return LA_ERR_INVALID_VALUE;
   if ((st = api_device()) != LA_OK) return st;
   return api_status(launch_short_conv(
       {x, ldx, weight, bias, lengths, from_state, out, S, B, N, D, K, silu != 0, dt, (cudaStream_t)stream}));
@@ -103,6 +121,8 @@ la_status scan(const void *x, long ldx, const void *delta, long ldt, const float
   if (!aligned({x, delta, A, Bm, Cm, Dskip, z, dt_bias, out, S}, 16) || !aligned({ws}, 256) || !aligned({lengths}, 4))
     return LA_ERR_MISALIGNED;
   if (N == 0) return empty(S, sizeof(float) * (size_t)B * D * ds, from_state, stream);
+  if (over_inputs(out, (long)B * N, D, dt, {{x, ldx, D}, {delta, ldt, D}, {z, ldz, D}, {Bm, ldb, ds}, {Cm, ldc, ds}}))
+    return LA_ERR_INVALID_VALUE;
   if ((st = api_device()) != LA_OK) return st;
   const ScanProblem p{x, delta, z, Bm, Cm, ldx, ldt, ldz, ldb, ldc, A, Dskip, dt_bias, lengths, from_state ? S : nullptr,
                       out, S, B, N, D, ds, softplus != 0, dt, ws, (cudaStream_t)stream};
@@ -181,6 +201,7 @@ la_status la_short_conv_step(const void *x, long ldx, const float *weight, const
   if (missing({x, weight, out}) || (!S && n_slots > 0)) return LA_ERR_INVALID_VALUE;
   if ((st = rows_ok(ldx, D, dt)) != LA_OK) return st;
   if (!aligned({x, weight, bias, S, out}, 16) || !aligned({slots}, 4)) return LA_ERR_MISALIGNED;
+  if (over_inputs(out, B, D, dt, {{x, ldx, D}})) return LA_ERR_INVALID_VALUE;
   if ((st = api_device()) != LA_OK) return st;
   return api_status(launch_short_conv_step(
       {x, ldx, weight, bias, S, slots, out, B, D, K, n_slots, silu != 0, dt, (cudaStream_t)stream}));
@@ -258,6 +279,8 @@ la_status la_selective_scan_step(const void *x, long ldx, const void *delta, lon
   if (missing({x, delta, A, Bm, Cm, out}) || (!S && n_slots > 0)) return LA_ERR_INVALID_VALUE;
   if ((st = all_rows_ok({{ldx, D}, {ld_delta, D}, {ldb, d_state}, {ldc, d_state}, {z ? ldz : ldx, D}}, dt)) != LA_OK) return st;
   if (!aligned({x, delta, A, Bm, Cm, Dskip, z, dt_bias, S, out}, 16) || !aligned({slots}, 4)) return LA_ERR_MISALIGNED;
+  if (over_inputs(out, B, D, dt, {{x, ldx, D}, {delta, ld_delta, D}, {z, ldz, D}, {Bm, ldb, d_state}, {Cm, ldc, d_state}}))
+    return LA_ERR_INVALID_VALUE;
   if ((st = api_device()) != LA_OK) return st;
   return api_status(launch_selective_step({x, delta, z, Bm, Cm, ldx, ld_delta, ldz, ldb, ldc, A, Dskip, dt_bias, S, slots,
                                            out, B, D, d_state, n_slots, softplus != 0, dt, (cudaStream_t)stream}));
@@ -278,6 +301,8 @@ la_status la_beam_select(const void *logits, long ld, const float *scores, const
   if (missing({logits, scores, out_scores, parents, tokens})) return LA_ERR_INVALID_VALUE;
   if (!aligned({logits}, 16) || !aligned({workspace}, 256) || !aligned({scores, out_scores, parents, tokens}, 4))
     return LA_ERR_MISALIGNED;
+  for (const void *out : {(const void *)out_scores, (const void *)parents, (const void *)tokens})
+    if (meets(out, 4 * (size_t)G * k, scores, 4 * (size_t)G * W)) return LA_ERR_INVALID_VALUE;
   if ((st = api_device()) != LA_OK) return st;
   if (!workspace || workspace_bytes < beam_split(G, W, k, V).bytes) return LA_ERR_INVALID_VALUE;
   return api_status(launch_beam_select(

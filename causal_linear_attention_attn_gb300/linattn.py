@@ -645,8 +645,8 @@ def la_short_conv(x, weight, bias=None, silu: bool = True, lengths=None, out=Non
 
     x [B, N, D] (float32 or bfloat16, D a multiple of 8; a part of the last dimension of a wider tensor will do); weight
     [D, K] (the last one is the current token's), bias [D], float32.  lengths [B] int32: tokens past a row's length take
-    no part and their rows of a given ``out`` are not written; without ``out`` they are zero.  Returns (out [B, N, D],
-    S [B, K-1, D] the last inputs), both in x's dtype.
+    no part and their rows of a given ``out`` (not over an input) are not written; without ``out`` they are zero.
+    Returns (out [B, N, D], S [B, K-1, D] the last inputs), both in x's dtype.
     """
     return _short_conv_call("la_short_conv", x, weight, S, bias, silu, lengths, out, stream)
 

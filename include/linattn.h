@@ -486,7 +486,8 @@ LA_API size_t la_short_conv_workspace(int B, int N, int D, int K);
  * One token of la_short_conv per batch row, on windows that live in a pool S
  * [n_slots,K-1,D], dtype dt, read and written in place: row b works on
  * S[slots[b]].  x: [B,D], rows ldx apart; out: [B,D].  slots as in
- * la_gated_decode_step (unused, bad and repeated ones too).  Allocates nothing.
+ * la_gated_decode_step (unused, bad and repeated ones too).  out must not overlap
+ * x.  Allocates nothing.
  */
 LA_API la_status la_short_conv_step(const void *x, long ldx, const float *weight, const float *bias, void *S,
                                     const int *slots, void *out, int B, int n_slots, int D, int K, int silu, la_dtype dt,
@@ -551,7 +552,8 @@ LA_API la_status la_selective_scan_backward(const void *x, long ldx, const void 
  * One token of la_selective_scan per batch row, on states that live in a pool S
  * [n_slots,D,d_state] float32, read and written in place: row b works on
  * S[slots[b]].  x, delta, z: [B,D]; Bm, Cm: [B,d_state]; rows ld* apart; out
- * [B,D].  slots as in la_gated_decode_step (unused, bad and repeated ones too).
+ * [B,D], not over an input.  slots as in la_gated_decode_step (unused, bad and
+ * repeated ones too).
  */
 LA_API la_status la_selective_scan_step(const void *x, long ldx, const void *delta, long ld_delta, const float *A,
                                         const void *Bm, long ldb, const void *Cm, long ldc, const float *Dskip,
@@ -573,7 +575,8 @@ LA_API la_status la_selective_scan_step(const void *x, long ldx, const void *del
  * score -inf.  Infinite logits count as the largest finite number.  1 <= k <=
  * min(64, W V), W <= 64, 0 <= eos < V, ld >= V.  logits 16-byte aligned, the other
  * pointers 4 (finished 1).  workspace: la_beam_select_workspace bytes, 256-byte
- * aligned; calls that may run at the same time need one each.
+ * aligned; calls that may run at the same time need one each.  No output may
+ * overlap an input.
  */
 LA_API la_status la_beam_select(const void *logits, long ld, const float *scores, const unsigned char *finished,
                                 float *out_scores, int *parents, int *tokens, int G, int W, int k, int V, int eos,

@@ -192,6 +192,30 @@ def test_reorder_refusals():
     assert call(G=0, slots=None) == OK and call(G=-1) == INVALID and call(n=-1) == INVALID and call(slots=P + 2) == MISALIGNED
 
 
+def test_outputs_over_inputs_are_refused():
+    """An output may lie right behind an input, not over a part of it (rows that are a part of wider ones included)."""
+    far = lambda i: P + (i << 24)  # noqa: E731
+    conv = caller("la_short_conv", x=P, ldx=128, w=far(1), b=None, lengths=None, out=far(2), S=far(3), B=2, N=8, D=64, K=4,
+                  silu=1, dt=1, stream=None)
+    size = 15 * 256 + 128
+    for out in (P, P + size - 16, P - 2 * 8 * 128 + 16):
+        assert conv(out=out) == INVALID
+    step = caller("la_short_conv_step", x=P, ldx=64, w=far(1), b=None, S=far(2), slots=None, out=P, B=2, n=4, D=64, K=4,
+                  silu=1, dt=1, stream=None)
+    assert step() == INVALID
+    apart = {n: far(i) for i, n in enumerate(("x", "delta", "A", "Bm", "Cm", "D", "z", "bias"))}
+    scan = caller("la_selective_scan", **(SCAN | apart), lengths=None, out=far(9), S=far(10), B=1, **TAIL, ws=far(11),
+                  bytes=1 << 40, stream=None)
+    one = caller("la_selective_scan_step", **(SCAN | apart), S=far(9), slots=None, out=far(10), B=1, n=4,
+                 **{k: v for k, v in TAIL.items() if k != "N"}, stream=None)
+    for n in ("x", "delta", "Bm", "Cm", "z"):
+        assert scan(out=apart[n]) == INVALID and one(out=apart[n]) == INVALID
+    select = caller("la_beam_select", logits=P, ld=100, scores=far(1), finished=None, best=far(2), parents=far(3),
+                    tokens=far(4), G=3, W=4, k=2, V=100, eos=3, dt=1, ws=far(5), bytes=1 << 40, stream=None)
+    for n in ("best", "parents", "tokens"):
+        assert select(**{n: far(1) + 44}) == INVALID and select(**{n: far(1) - 20}) == INVALID
+
+
 def test_workspaces():
     w = L.lib.la_selective_scan_workspace
     assert w(0, 8, 64, 16, 1, 1) == 0 and w(1, 8, 60, 16, 1, 0) == 0 and w(1, 8, 64, 16, 1, 1) > 0
