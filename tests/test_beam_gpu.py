@@ -255,3 +255,38 @@ def test_a_layer_served_by_beam_search(cuda_lib):
     assert (logits.reshape(G * W, V).double() - ref).abs().max() < 1e-3
     assert (scores.reshape(-1).double() - total).abs().max() < 2e-3
     assert all(len({tuple(h) for h in history[i].tolist()}) == W for i in range(G)), "a hypothesis twice"
+
+
+def test_a_serving_step_on_another_stream_and_in_a_graph(cuda_lib):
+    """Selection, reordering and both steps: the same bits and pools on a given stream and replayed twice."""
+    L, G, W, V, D, ds, K = cuda_lib, 2, 4, 5003, 40, 16, 4
+    g = torch.Generator(device="cuda").manual_seed(5)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    logits, scores, x, dt, Bm, Cm = r(G, W, V), r(G, W), r(G * W, D), r(G * W, D), r(G * W, ds), r(G * W, ds)
+    w, A, n = r(D, K), -torch.exp(r(D, ds)), G * W + 1
+    first = [r(n, K - 1, D), r(n, D, ds)]
+    slots = torch.randperm(n, generator=g, device="cuda")[: G * W].reshape(G, W).int()
+
+    def step(pools, stream=None):
+        best, parents, tokens = L.la_beam_select(logits, scores, stream=stream)
+        new = L.la_beam_reorder(pools, slots, parents, stream=stream)
+        u = L.la_short_conv_step(x, w, pools[0], slots=new.reshape(-1), stream=stream)
+        out = L.la_selective_scan_step(u, dt, A, Bm, Cm, pools[1], slots=new.reshape(-1), stream=stream)
+        return [best, parents, tokens, new, u, out, *pools]
+
+    want = step([p.clone() for p in first])
+    pools, other = [p.clone() for p in first], torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    got = step(pools, stream=other)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(pools)
+    for _ in range(2):
+        for p, f in zip(pools, first):
+            p.copy_(f)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert L.device_status() == 0
