@@ -1,9 +1,9 @@
 // Selective state space scan: outputs, and the states in front of chunks or at the ends of segments.
 //
-// Formulas in selective.cuh.  A lane owns four state components of two channels, ds/4 neighbouring lanes a pair of
-// channels: the states stay in registers while the lane walks over the tokens.  (Every load from shared memory costs its
-// port the lanes' bytes, broadcast or not: with two channels a lane B and C are read half as often as with one, which
-// had the port 72 % taken and took 516 us for 488.)  A block takes 64 channels (ds = 64: 32) and goes through the
+// Formulas in selective.cuh.  A lane owns four state components (or two: launch_mode) of two channels, ds/4 (ds/2)
+// neighbouring lanes a pair of channels: the states stay in registers while the lane walks over the tokens.  (Every load
+// from shared memory costs its port the lanes' bytes, broadcast or not: with two channels a lane B and C are read half as
+// often as with one, which had the port 72 % taken and took 516 us for 488.)  A block takes 64 channels (ds = 64: 32) and goes through the
 // tokens in chunks of 32, on two kinds of warps a chunk apart:
 //   - around the recurrence, threads as (token, eight channels): rows in, delta = softplus(dt + bias) and delta x to shared
 //     memory, B and C in 32 bits beside them; a chunk later + D x, times silu(z), rows out;
@@ -31,6 +31,9 @@ constexpr int kTok = 32;         // tokens a chunk
 // Channels a block: as many as keep it within 400 threads.
 constexpr int scan_cols(int ds) { return ds == 64 ? 32 : 64; }
 
+// Threads of the recurrence with `comp` components of two channels each.
+constexpr int scan_threads(int ds, int comp) { return scan_cols(ds) / 2 * ds / comp; }
+
 enum Mode { kOutputs, kEnds, kStates, kReverseEnds };
 
 template <int DS, int kMode>
@@ -45,11 +48,13 @@ struct Smem {
 // kOutputs: out, and the last segment's end state to S.  kEnds: each segment's end state from zero and sum of
 // delta.  kStates: the state in front of each chunk of s.chunk tokens.  kReverseEnds: the same as kEnds for the
 // recurrence of the state's gradient, from a segment's last token to its first: G <- a_t (G + C_t dy_t).
-// kAround: threads around the recurrence, (token, eight channels) in turns.  `block` of the mode's blocks.
-template <typename T, int DS, int kMode, int kAround>
+// kAround: threads around the recurrence, (token, eight channels) in turns.  kComp: components a lane.  `block`
+// of the mode's blocks.
+template <typename T, int DS, int kMode, int kAround, int kComp>
 __device__ __forceinline__ void scan_block(const ScanProblem &p, const ScanSplit &s, unsigned block) {
   constexpr int kCols = Smem<DS, kMode>::kCols, kTurns = kTok * kCols / 8 / kAround;
-  constexpr int kScan = kCols * DS / 8, kThreads = kScan + kAround, kLanes = DS / 4, kPerWarp = 64 / kLanes;
+  constexpr int kScan = kCols / 2 * DS / kComp, kThreads = kScan + kAround, kLanes = DS / kComp, kPerWarp = 64 / kLanes;
+  constexpr int kP = kComp / 2;  // pairs of components
   constexpr bool kRev = kMode == kReverseEnds;
   extern __shared__ __align__(16) unsigned char raw_smem[];
   Smem<DS, kMode> *m = reinterpret_cast<Smem<DS, kMode> *>(raw_smem);
@@ -204,22 +209,32 @@ __device__ __forceinline__ void scan_block(const ScanProblem &p, const ScanSplit
   const int c = cb * kCols + ch;  // and the next one; D is even
   const int slot = step_slot(ch / 2);
   const bool mine = c < p.D;
-  const long at = (long)c * DS + 4 * q;  // in a state
+  const long at = (long)c * DS + kComp * q;  // in a state
   const long state = (long)p.D * DS;
-  float2 A[4], h[4];  // two channels of two pairs
-  auto get = [&](float2 (&v)[4], const float *from) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float4 f = *reinterpret_cast<const float4 *>(from + at + i * DS);
-      v[2 * i] = make_float2(f.x, f.y), v[2 * i + 1] = make_float2(f.z, f.w);
+  float2 A[2 * kP], h[2 * kP];  // of the first channel, of the second
+  auto read = [](float2 *v, const float *from) {  // kComp values at once
+    if constexpr (kP == 2) {
+      const float4 f = *reinterpret_cast<const float4 *>(from);
+      v[0] = make_float2(f.x, f.y), v[1] = make_float2(f.z, f.w);
+    } else {
+      v[0] = *reinterpret_cast<const float2 *>(from);
     }
+  };
+  auto get = [&](float2 (&v)[2 * kP], const float *from) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) read(&v[kP * i], from + at + i * DS);
   };
   auto put = [&](float *to) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) st4(to + at + i * DS, h[2 * i].x, h[2 * i].y, h[2 * i + 1].x, h[2 * i + 1].y);
+    for (int i = 0; i < 2; ++i) {
+      if constexpr (kP == 2)
+        st4(to + at + i * DS, h[2 * i].x, h[2 * i].y, h[2 * i + 1].x, h[2 * i + 1].y);
+      else
+        *reinterpret_cast<float2 *>(to + at + i * DS) = h[i];
+    }
   };
 #pragma unroll
-  for (int i = 0; i < 4; ++i) A[i] = h[i] = both(0.f);
+  for (int i = 0; i < 2 * kP; ++i) A[i] = h[i] = both(0.f);
   if (mine) {
     get(A, p.A);
     const float *from = nullptr;
@@ -227,22 +242,23 @@ __device__ __forceinline__ void scan_block(const ScanProblem &p, const ScanSplit
     if (from) get(h, from);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) A[i] = rate(A[i]);
+  for (int i = 0; i < 2 * kP; ++i) A[i] = rate(A[i]);
   for (int k = 0; k < chunks; ++k) {
     Smem<DS, kMode> &in = m[k & 1];
     const long t0 = first_of(k);
     bar_sync<kThreads>(1 + (k & 1));
     // two tokens' values ahead of their use: the compiler does not move loads across the stores of sums
     struct Two {
-      float4 d[2], b[2], c[kMode == kOutputs ? 2 : 1];
+      float4 d[2];
+      float2 b[2][kP], c[kMode == kOutputs ? 2 : 1][kP];
     };
     auto token = [](int i) { return kRev ? kTok - 1 - i : i; };
     auto fetch = [&](Two &v, int i0) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         v.d[j] = in.steps[token(i0 + j)][slot];
-        v.b[j] = *reinterpret_cast<const float4 *>(&in.B[token(i0 + j)][4 * q]);
-        if (kMode == kOutputs) v.c[j] = *reinterpret_cast<const float4 *>(&in.C[token(i0 + j)][4 * q]);
+        read(v.b[j], &in.B[token(i0 + j)][kComp * q]);
+        if (kMode == kOutputs) read(v.c[j], &in.C[token(i0 + j)][kComp * q]);
       }
     };
     constexpr int kStep = kLanes < 4 ? 4 : kLanes;
@@ -254,28 +270,27 @@ __device__ __forceinline__ void scan_block(const ScanProblem &p, const ScanSplit
 #pragma unroll
       for (int f = 0; f < kStep; f += 2) {
         if (i0 + f + 2 < kTok) fetch(then, i0 + f + 2);
-        float2 a[2][4];
+        float2 a[2][2 * kP];
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) a[j][i] = decay(both(i < 2 ? now.d[j].x : now.d[j].z), A[i]);
+          for (int i = 0; i < 2 * kP; ++i) a[j][i] = decay(both(i < kP ? now.d[j].x : now.d[j].z), A[i]);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           if (kMode == kStates && (f + j) % 8 == 0) {
             const int i = i0 + f + j;
             if (i % s.chunk == 0 && mine && t0 + i < end) put(s.chunk_states + (b * s.all_chunks + (t0 + i) / s.chunk) * state);
           }
-          const float2 bv[2] = {make_float2(now.b[j].x, now.b[j].y), make_float2(now.b[j].z, now.b[j].w)};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 u = both(i < 2 ? now.d[j].y : now.d[j].w);
-            h[i] = kRev ? __fmul2_rn(a[j][i], __ffma2_rn(u, bv[i & 1], h[i])) : __ffma2_rn(a[j][i], h[i], __fmul2_rn(u, bv[i & 1]));
+          for (int i = 0; i < 2 * kP; ++i) {
+            const float2 u = both(i < kP ? now.d[j].y : now.d[j].w), bv = now.b[j][i % kP];
+            h[i] = kRev ? __fmul2_rn(a[j][i], __ffma2_rn(u, bv, h[i])) : __ffma2_rn(a[j][i], h[i], __fmul2_rn(u, bv));
           }
           if (kMode == kOutputs) {
-            const float2 cv[2] = {make_float2(now.c[j].x, now.c[j].y), make_float2(now.c[j].z, now.c[j].w)};
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const float2 yy = __ffma2_rn(h[2 * i + 1], cv[1], __fmul2_rn(h[2 * i], cv[0]));
+              float2 yy = __fmul2_rn(h[kP * i], now.c[j][0]);
+              if (kP == 2) yy = __ffma2_rn(h[kP * i + kP - 1], now.c[j][kP - 1], yy);
               y[i * kStep + f + j] = yy.x + yy.y;
             }
           }
@@ -299,21 +314,21 @@ __device__ __forceinline__ void scan_block(const ScanProblem &p, const ScanSplit
   }
 }
 
-template <typename T, int DS, int kMode, int kAround>
-__global__ void __launch_bounds__(scan_cols(DS) * DS / 8 + kAround) scan_kernel(const __grid_constant__ ScanProblem p, const __grid_constant__ ScanSplit s) {
-  scan_block<T, DS, kMode, kAround>(p, s, blockIdx.x);
+template <typename T, int DS, int kMode, int kAround, int kComp>
+__global__ void __launch_bounds__(scan_threads(DS, kComp) + kAround) scan_kernel(const __grid_constant__ ScanProblem p, const __grid_constant__ ScanSplit s) {
+  scan_block<T, DS, kMode, kAround, kComp>(p, s, blockIdx.x);
 }
 
 // The ends of segments in both directions, side by side: the second half of the blocks runs q, whose x is the gradient of
 // the outputs.
 template <typename T, int DS>
-__global__ void __launch_bounds__(scan_cols(DS) * DS / 8 + 128)
+__global__ void __launch_bounds__(scan_threads(DS, 4) + 128)
     scan_ends_kernel(const __grid_constant__ ScanProblem p, const __grid_constant__ ScanProblem q, const __grid_constant__ ScanSplit s) {
   const unsigned half = gridDim.x / 2;
   if (blockIdx.x < half)
-    scan_block<T, DS, kEnds, 128>(p, s, blockIdx.x);
+    scan_block<T, DS, kEnds, 128, 4>(p, s, blockIdx.x);
   else
-    scan_block<T, DS, kReverseEnds, 128>(q, s, blockIdx.x - half);
+    scan_block<T, DS, kReverseEnds, 128, 4>(q, s, blockIdx.x - half);
 }
 
 // Segment ends to segment starts, in place: starts[s] <- h, h <- e^{A total[s]} h + starts[s] (old), from S0; the
@@ -349,15 +364,15 @@ __global__ void __launch_bounds__(256) scan_join_kernel(const __grid_constant__ 
   }
 }
 
-template <typename T, int DS, int kMode, int kAround>
+template <typename T, int DS, int kMode, int kAround, int kComp>
 cudaError_t launch_kernel(const ScanProblem &p, const ScanSplit &s, long blocks) {
-  const void *fn = (const void *)scan_kernel<T, DS, kMode, kAround>;
+  const void *fn = (const void *)scan_kernel<T, DS, kMode, kAround, kComp>;
   constexpr int kSmem = 2 * (int)sizeof(Smem<DS, kMode>);
   cudaError_t e = kSmem > 48 * 1024 ? ensure_smem_optin(fn, kSmem) : cudaSuccess;
   if (e != cudaSuccess) return e;
   LaunchTimer timer(kMode == kOutputs ? kKSelectiveScan : kKSelectiveState, p.stream);
   void *args[] = {const_cast<ScanProblem *>(&p), const_cast<ScanSplit *>(&s)};
-  e = cudaLaunchKernel(fn, dim3((unsigned)blocks), dim3(scan_cols(DS) * DS / 8 + kAround), args, kSmem, p.stream);
+  e = cudaLaunchKernel(fn, dim3((unsigned)blocks), dim3(scan_threads(DS, kComp) + kAround), args, kSmem, p.stream);
   timer.done(e);
   if (e == cudaSuccess) count_launch();
   return e;
@@ -365,16 +380,24 @@ cudaError_t launch_kernel(const ScanProblem &p, const ScanSplit &s, long blocks)
 
 // Outputs: where a block an SM is all there is, the work around its recurrence gets twice the warps (4 x 8192 x 2048 x 16:
 // 445 us to 413); with more blocks an SM their registers are worth more (16 x 2048 tokens: 347 us, with them 415).
+// With a block an SM, two components a lane instead of four are twice the warps of the recurrence: states in front of
+// chunks, 4 x 4096 x 2048 x 16, 198 us to 163, outputs of 8 components 357 to 340; outputs of 16 need the steps
+// and C twice as often from shared memory then (413 us, with two 453).  With two blocks an SM four are as good or better
+// (states of 16 x 1024 tokens 159 us, with two 167; outputs of 8 components in fp32 287, with two 472).
 template <typename T, int DS>
 cudaError_t launch_mode(const ScanProblem &p, ScanSplit s, int mode) {
   s.launched = mode == kEnds ? s.segs - 1 : s.segs;
   const long blocks = (long)p.B * s.launched * ((p.D + scan_cols(DS) - 1) / scan_cols(DS));
-  if (mode == kEnds) return launch_kernel<T, DS, kEnds, 128>(p, s, blocks);
-  if (mode == kStates) return launch_kernel<T, DS, kStates, 128>(p, s, blocks);
+  if (mode == kEnds) return launch_kernel<T, DS, kEnds, 128, 4>(p, s, blocks);
+  const bool one = blocks <= device_info(-1).sm_count;
   if constexpr (scan_cols(DS) == 64) {
-    if (blocks <= device_info(-1).sm_count) return launch_kernel<T, DS, kOutputs, 256>(p, s, blocks);
+    if (one && mode == kOutputs) return launch_kernel<T, DS, kOutputs, 256, DS == 8 ? 2 : 4>(p, s, blocks);
   }
-  return launch_kernel<T, DS, kOutputs, 128>(p, s, blocks);
+  if constexpr (DS <= 16) {
+    if (one && mode == kStates) return launch_kernel<T, DS, kStates, 128, 2>(p, s, blocks);
+  }
+  if (mode == kStates) return launch_kernel<T, DS, kStates, 128, 4>(p, s, blocks);
+  return launch_kernel<T, DS, kOutputs, 128, 4>(p, s, blocks);
 }
 
 template <typename T>
@@ -396,7 +419,7 @@ cudaError_t launch_ends(const ScanProblem &p, const ScanProblem &q, ScanSplit s)
   static_assert(kSmem <= 48 * 1024, "no opt-in needed");
   const long blocks = 2L * p.B * s.launched * ((p.D + scan_cols(DS) - 1) / scan_cols(DS));
   LaunchTimer timer(kKSelectiveState, p.stream);
-  scan_ends_kernel<T, DS><<<(unsigned)blocks, scan_cols(DS) * DS / 8 + 128, kSmem, p.stream>>>(p, q, s);
+  scan_ends_kernel<T, DS><<<(unsigned)blocks, scan_threads(DS, 4) + 128, kSmem, p.stream>>>(p, q, s);
   const cudaError_t e = cudaGetLastError();
   timer.done(e);
   if (e == cudaSuccess) count_launch();
