@@ -232,7 +232,9 @@ __global__ void __launch_bounds__(kThreads, 4) beam_rows_kernel(const __grid_con
     }
     mine = clean(mine);
     top = new_top;
-    const uint32_t key = *(volatile uint32_t *)&m.bound;
+    // one lane's reading for the whole warp: other warps raise the bound, and lanes that went apart above may read at
+    // different times, which the shuffles below do not bear
+    const uint32_t key = __shfl_sync(0xffffffffu, *(volatile uint32_t *)&m.bound, 0);
     float bound = key ? unordered(key) : -INFINITY;
     if (bound == -INFINITY) {  // one from these values alone: at least k reach it
       float x = mine;
