@@ -331,6 +331,14 @@ __global__ void __launch_bounds__(scan_threads(DS, 4) + 128)
     scan_block<T, DS, kReverseEnds, 128, 4>(q, s, blockIdx.x - half);
 }
 
+// 2^exponent h + v.  A segment that grows (negative steps, A > 0) may do so beyond 2^128 while the state it starts from, zero
+// or small, has a finite product: the power is split then, and its whole part goes straight into the product's exponent.
+__device__ __forceinline__ float grown(float exponent, float h, float v) {
+  if (!(exponent > 126.f)) return fmaf(exp2f(exponent), h, v);
+  const float whole = rintf(fminf(exponent, 1024.f));  // (2^1024 takes the smallest number beyond the largest)
+  return ldexpf(exp2f(fminf(exponent, 1024.f) - whole) * h, (int)whole) + v;
+}
+
 // Segment ends to segment starts, in place: starts[s] <- h, h <- e^{A total[s]} h + starts[s] (old), from S0; the
 // state's gradient (blockIdx.y = 1) the same way from the last segment, from dS.  A thread a component.
 __global__ void __launch_bounds__(256) scan_join_kernel(const __grid_constant__ ScanSplit s, const float *A,
@@ -359,7 +367,7 @@ __global__ void __launch_bounds__(256) scan_join_kernel(const __grid_constant__ 
       const int k = reverse ? s.segs - 1 - (k0 + u) : k0 + u;
       if (k0 + u >= s.segs) break;
       starts[k * state] = h;
-      h = fmaf(exp2f(a * d[u]), h, v[u]);
+      h = grown(a * d[u], h, v[u]);
     }
   }
 }
