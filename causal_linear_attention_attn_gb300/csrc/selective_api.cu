@@ -30,7 +30,7 @@ bool overlap(const void *a, const void *b, size_t bytes) {
 // Memory of `an` bytes at a and of `bn` at b.
 bool meets(const void *a, size_t an, const void *b, size_t bn) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && x < y + bn && y < x + an;
+  return a && b && an && bn && x < y + bn && y < x + an;
 }
 int bytes_of(la_dtype dt) { return dt == LA_F32 ? 4 : 2; }
 
@@ -49,15 +49,24 @@ la_status all_rows_ok(std::initializer_list<std::pair<long, long>> rows, la_dtyp
   return st;
 }
 
-struct Input {
+// Memory that a call reads or writes; null: none.
+struct Span {
   const void *at;
-  long ld, width;
+  size_t bytes;
 };
-// Whether an output of `rows` rows of D values meets an input's rows.
-bool over_inputs(const void *out, long rows, long D, la_dtype dt, std::initializer_list<Input> inputs) {
-  const size_t size = bytes_of(dt);
-  for (const Input &i : inputs)
-    if (meets(out, rows * D * size, i.at, ((rows - 1) * i.ld + i.width) * size)) return true;
+// `count` rows (one at least) of `width` values, `ld` apart.
+Span rows(const void *at, long count, long ld, long width, la_dtype dt) {
+  return {at, ((count - 1) * (size_t)ld + width) * bytes_of(dt)};
+}
+Span floats(const void *at, long count) { return {at, sizeof(float) * (size_t)count}; }
+// Whether an output meets an input or another output.
+bool over(std::initializer_list<Span> outputs, std::initializer_list<Span> inputs) {
+  for (const Span *o = outputs.begin(); o != outputs.end(); ++o) {
+    for (const Span &i : inputs)
+      if (meets(o->at, o->bytes, i.at, i.bytes)) return true;
+    for (const Span *q = outputs.begin(); q != o; ++q)
+      if (meets(o->at, o->bytes, q->at, q->bytes)) return true;
+  }
   return false;
 }
 
@@ -103,7 +112,10 @@ la_status conv(const void *x, long ldx, const float *weight, const float *bias, 
   if ((st = rows_ok(ldx, D, dt)) != LA_OK) return st;
   if (!aligned({x, weight, bias, out, S}, 16) || !aligned({lengths}, 4)) return LA_ERR_MISALIGNED;
   if (N == 0) return empty(S, (size_t)B * (K - 1) * D * bytes_of(dt), from_state, stream);
-  if (over_inputs(out, (long)B * N, D, dt, {{x, ldx, D}})) return LA_ERR_INVALID_VALUE;
+  const long tokens = (long)B * N;
+  if (over({rows(out, tokens, D, D, dt), rows(S, (long)B * (K - 1), D, D, dt)},
+           {rows(x, tokens, ldx, D, dt), floats(weight, (long)D * K), floats(bias, D), floats(lengths, B)}))
+    return LA_ERR_INVALID_VALUE;
   if ((st = api_device()) != LA_OK) return st;
   return api_status(launch_short_conv(
       {x, ldx, weight, bias, lengths, from_state, out, S, B, N, D, K, silu != 0, dt, (cudaStream_t)stream}));
@@ -121,7 +133,11 @@ la_status scan(const void *x, long ldx, const void *delta, long ldt, const float
   if (!aligned({x, delta, A, Bm, Cm, Dskip, z, dt_bias, out, S}, 16) || !aligned({ws}, 256) || !aligned({lengths}, 4))
     return LA_ERR_MISALIGNED;
   if (N == 0) return empty(S, sizeof(float) * (size_t)B * D * ds, from_state, stream);
-  if (over_inputs(out, (long)B * N, D, dt, {{x, ldx, D}, {delta, ldt, D}, {z, ldz, D}, {Bm, ldb, ds}, {Cm, ldc, ds}}))
+  const long tokens = (long)B * N;
+  if (over({rows(out, tokens, D, D, dt), floats(S, (long)B * D * ds)},
+           {rows(x, tokens, ldx, D, dt), rows(delta, tokens, ldt, D, dt), rows(z, tokens, ldz, D, dt),
+            rows(Bm, tokens, ldb, ds, dt), rows(Cm, tokens, ldc, ds, dt), floats(A, (long)D * ds), floats(Dskip, D),
+            floats(dt_bias, D), floats(lengths, B)}))
     return LA_ERR_INVALID_VALUE;
   if ((st = api_device()) != LA_OK) return st;
   const ScanProblem p{x, delta, z, Bm, Cm, ldx, ldt, ldz, ldb, ldc, A, Dskip, dt_bias, lengths, from_state ? S : nullptr,
@@ -174,9 +190,13 @@ la_status la_short_conv_backward(const void *x, long ldx, const float *weight, c
       !aligned({lengths, dweight, dbias}, 4))
     return LA_ERR_MISALIGNED;
   const size_t window = (size_t)B * (K - 1) * D * bytes_of(dt);
-  // runs of tokens read and write windows in no order
-  if (N > 0 && (overlap(S0, dS0, window) || overlap(dS, dS0, window))) return LA_ERR_INVALID_VALUE;
   if (dS != dS0 && overlap(dS, dS0, window)) return LA_ERR_INVALID_VALUE;
+  // a run of tokens reads what belongs to the ones beside it, and runs are in no order
+  const long tokens = (long)B * N;
+  if (tokens > 0 && over({rows(dx, tokens, D, D, dt), {dS0, window}, floats(dweight, (long)D * K), floats(dbias, D)},
+                         {rows(x, tokens, ldx, D, dt), rows(dout, tokens, D, D, dt), {S0, window}, {dS, window},
+                          floats(weight, (long)D * K), floats(bias, D), floats(lengths, B)}))
+    return LA_ERR_INVALID_VALUE;
   cudaStream_t s = (cudaStream_t)stream;
   if ((st = api_device()) != LA_OK) return st;
   if (B == 0 || N == 0) {  // the sums are empty, the window passes through
@@ -201,7 +221,9 @@ la_status la_short_conv_step(const void *x, long ldx, const float *weight, const
   if (missing({x, weight, out}) || (!S && n_slots > 0)) return LA_ERR_INVALID_VALUE;
   if ((st = rows_ok(ldx, D, dt)) != LA_OK) return st;
   if (!aligned({x, weight, bias, S, out}, 16) || !aligned({slots}, 4)) return LA_ERR_MISALIGNED;
-  if (over_inputs(out, B, D, dt, {{x, ldx, D}})) return LA_ERR_INVALID_VALUE;
+  if (over({rows(out, B, D, D, dt), {S, (size_t)n_slots * (K - 1) * D * bytes_of(dt)}},
+           {rows(x, B, ldx, D, dt), floats(weight, (long)D * K), floats(bias, D), floats(slots, B)}))
+    return LA_ERR_INVALID_VALUE;
   if ((st = api_device()) != LA_OK) return st;
   return api_status(launch_short_conv_step(
       {x, ldx, weight, bias, S, slots, out, B, D, K, n_slots, silu != 0, dt, (cudaStream_t)stream}));
@@ -249,8 +271,19 @@ la_status la_selective_scan_backward(const void *x, long ldx, const void *delta,
       !aligned({workspace}, 256) || !aligned({lengths, dA, dDskip, ddt_bias}, 4))
     return LA_ERR_MISALIGNED;
   const size_t bytes = sizeof(float) * (size_t)B * D * d_state;
-  // the state and its gradient are walked in opposite directions, neither waits for the other
-  if ((N > 0 && overlap(S0, dS0, bytes)) || (dS != dS0 && overlap(dS, dS0, bytes))) return LA_ERR_INVALID_VALUE;
+  if (dS != dS0 && overlap(dS, dS0, bytes)) return LA_ERR_INVALID_VALUE;
+  // rows are read again when a chunk's results go out, by every block of channels at its own pace; the state and its
+  // gradient are walked in opposite directions, neither waits for the other
+  const long tokens = (long)B * N;
+  if (tokens > 0 &&
+      over({rows(dx, tokens, D, D, dt), rows(ddelta, tokens, D, D, dt), rows(dz, tokens, D, D, dt),
+            rows(dB, tokens, d_state, d_state, dt), rows(dC, tokens, d_state, d_state, dt), floats(dA, (long)D * d_state),
+            floats(dDskip, D), floats(ddt_bias, D), {dS0, bytes}},
+           {rows(x, tokens, ldx, D, dt), rows(delta, tokens, ld_delta, D, dt), rows(z, tokens, ldz, D, dt),
+            rows(Bm, tokens, ldb, d_state, dt), rows(Cm, tokens, ldc, d_state, dt), rows(dout, tokens, D, D, dt),
+            floats(A, (long)D * d_state), floats(Dskip, D), floats(dt_bias, D), floats(lengths, B), {S0, bytes},
+            {dS == dS0 ? nullptr : dS, bytes}}))
+    return LA_ERR_INVALID_VALUE;
   cudaStream_t s = (cudaStream_t)stream;
   if ((st = api_device()) != LA_OK) return st;
   if (B == 0 || N == 0) {  // the sums are empty, the state passes through
@@ -279,7 +312,9 @@ la_status la_selective_scan_step(const void *x, long ldx, const void *delta, lon
   if (missing({x, delta, A, Bm, Cm, out}) || (!S && n_slots > 0)) return LA_ERR_INVALID_VALUE;
   if ((st = all_rows_ok({{ldx, D}, {ld_delta, D}, {ldb, d_state}, {ldc, d_state}, {z ? ldz : ldx, D}}, dt)) != LA_OK) return st;
   if (!aligned({x, delta, A, Bm, Cm, Dskip, z, dt_bias, S, out}, 16) || !aligned({slots}, 4)) return LA_ERR_MISALIGNED;
-  if (over_inputs(out, B, D, dt, {{x, ldx, D}, {delta, ld_delta, D}, {z, ldz, D}, {Bm, ldb, d_state}, {Cm, ldc, d_state}}))
+  if (over({rows(out, B, D, D, dt), floats(S, (long)n_slots * D * d_state)},
+           {rows(x, B, ldx, D, dt), rows(delta, B, ld_delta, D, dt), rows(z, B, ldz, D, dt), rows(Bm, B, ldb, d_state, dt),
+            rows(Cm, B, ldc, d_state, dt), floats(A, (long)D * d_state), floats(Dskip, D), floats(dt_bias, D), floats(slots, B)}))
     return LA_ERR_INVALID_VALUE;
   if ((st = api_device()) != LA_OK) return st;
   return api_status(launch_selective_step({x, delta, z, Bm, Cm, ldx, ld_delta, ldz, ldb, ldc, A, Dskip, dt_bias, S, slots,
@@ -301,8 +336,10 @@ la_status la_beam_select(const void *logits, long ld, const float *scores, const
   if (missing({logits, scores, out_scores, parents, tokens})) return LA_ERR_INVALID_VALUE;
   if (!aligned({logits}, 16) || !aligned({workspace}, 256) || !aligned({scores, out_scores, parents, tokens}, 4))
     return LA_ERR_MISALIGNED;
-  for (const void *out : {(const void *)out_scores, (const void *)parents, (const void *)tokens})
-    if (meets(out, 4 * (size_t)G * k, scores, 4 * (size_t)G * W)) return LA_ERR_INVALID_VALUE;
+  const long beams = (long)G * W, chosen = (long)G * k;
+  if (over({floats(out_scores, chosen), floats(parents, chosen), floats(tokens, chosen)},
+           {rows(logits, beams, ld, V, dt), floats(scores, beams), {finished, (size_t)beams}}))
+    return LA_ERR_INVALID_VALUE;
   if ((st = api_device()) != LA_OK) return st;
   if (!workspace || workspace_bytes < beam_split(G, W, k, V).bytes) return LA_ERR_INVALID_VALUE;
   return api_status(launch_beam_select(
@@ -315,8 +352,8 @@ la_status la_beam_reorder(void *const *pools, const size_t *row_bytes, int n_poo
   if (W > 64) return LA_ERR_UNSUPPORTED;
   if (G > (1 << 24)) return LA_ERR_INVALID_VALUE;
   if (G == 0) return LA_OK;
-  if (missing({slots, parents, new_slots}) || overlap(slots, new_slots, sizeof(int) * (size_t)G * W) ||
-      overlap(parents, new_slots, sizeof(int) * (size_t)G * W))
+  const Span slots_of = floats(slots, (long)G * W), parents_of = floats(parents, (long)G * W);
+  if (missing({slots, parents, new_slots}) || over({floats(new_slots, (long)G * W)}, {slots_of, parents_of}))
     return LA_ERR_INVALID_VALUE;
   if (!aligned({slots, parents, new_slots}, 4)) return LA_ERR_MISALIGNED;
   for (int i = 0; i < n_pools; ++i) {
@@ -325,6 +362,8 @@ la_status la_beam_reorder(void *const *pools, const size_t *row_bytes, int n_poo
     if (row_bytes[i] > (size_t)1 << 40 || (long)G * W * (long)(row_bytes[i] / 32768 + 1) * kMaxPools > 0x7fffffffL)
       return LA_ERR_INVALID_VALUE;
     if (!aligned({pools[i]}, 16) || row_bytes[i] % 16) return LA_ERR_MISALIGNED;
+    if (over({{pools[i], row_bytes[i] * n_slots}, floats(new_slots, (long)G * W)}, {slots_of, parents_of}))
+      return LA_ERR_INVALID_VALUE;
   }
   la_status st = api_device();
   if (st != LA_OK) return st;

@@ -457,8 +457,8 @@ LA_API size_t la_group_norm_workspace(int B, int H, int N, int d);
  * are not written.  D a multiple of 8, K in {2, 3, 4}.
  * la_short_conv_with_state starts from the window in S and updates it in
  * place.  Sums in fp32.  Pointers 16-byte aligned (lengths 4), ldx >= D and a
- * multiple of 16 bytes.  out and S must not overlap an input.  N == 0 leaves the
- * carried window (zeros without one).
+ * multiple of 16 bytes.  out and S must overlap neither an input nor each other.
+ * N == 0 leaves the carried window (zeros without one).
  */
 LA_API la_status la_short_conv(const void *x, long ldx, const float *weight, const float *bias, const int *lengths,
                                void *out, void *S, int B, int N, int D, int K, int silu, la_dtype dt, void *stream);
@@ -469,10 +469,10 @@ LA_API la_status la_short_conv_with_state(const void *x, long ldx, const float *
 /*
  * Gradient of la_short_conv(_with_state): dout [B,N,D], dtype dt, contiguous;
  * S0 (NULL = zero) the forward's window, dS (NULL = zero) the gradient of the
- * one it left, both [B,K-1,D], dtype dt.  Written: dx [B,N,D] and dS0 (nullable;
- * it may be neither S0 nor overlap dS) of dtype dt; dweight [D,K], dbias [D]
- * float32, each nullable, added in a fixed order.  Rows t >= lengths[b] of dx are
- * zero.  workspace: la_short_conv_workspace bytes, 256-byte aligned, when dweight
+ * one it left, both [B,K-1,D], dtype dt.  Written: dx [B,N,D] and dS0 (nullable)
+ * of dtype dt; dweight [D,K], dbias [D] float32, each nullable, added in a fixed
+ * order.  Rows t >= lengths[b] of dx are zero.  No output may overlap an input
+ * (dS0: neither S0 nor dS) or another output.  workspace: la_short_conv_workspace bytes, 256-byte aligned, when dweight
  * or dbias is wanted (NULL otherwise); calls that may run at the same time need
  * one each.
  */
@@ -486,8 +486,8 @@ LA_API size_t la_short_conv_workspace(int B, int N, int D, int K);
  * One token of la_short_conv per batch row, on windows that live in a pool S
  * [n_slots,K-1,D], dtype dt, read and written in place: row b works on
  * S[slots[b]].  x: [B,D], rows ldx apart; out: [B,D].  slots as in
- * la_gated_decode_step (unused, bad and repeated ones too).  out must not overlap
- * x.  Allocates nothing.
+ * la_gated_decode_step (unused, bad and repeated ones too).  out and S must overlap
+ * neither an input nor each other.  Allocates nothing.
  */
 LA_API la_status la_short_conv_step(const void *x, long ldx, const float *weight, const float *bias, void *S,
                                     const int *slots, void *out, int B, int n_slots, int D, int K, int silu, la_dtype dt,
@@ -508,7 +508,7 @@ LA_API la_status la_short_conv_step(const void *x, long ldx, const float *weight
  * la_short_conv.  la_selective_scan_with_state starts from S and updates it in
  * place.  Steps, states and sums in fp32.  D a multiple of 8, d_state in {8, 16,
  * 32, 64}; pointers 16-byte aligned (lengths 4), every ld at least its row and a
- * multiple of 16 bytes.  out and S must not overlap an input.  workspace:
+ * multiple of 16 bytes.  out and S must overlap neither an input nor each other.  workspace:
  * la_selective_scan_workspace(..., 0) bytes, 256-byte aligned (NULL if that is 0);
  * calls that may run at the same time need one each.  N == 0 leaves the carried
  * state (zeros without one).
@@ -537,7 +537,7 @@ LA_API size_t la_selective_scan_workspace(int B, int N, int D, int d_state, la_d
  * exactly when z is), dtype dt; dA [D,d_state], dDskip, ddt_bias [D], dS0
  * [B,D,d_state] (which may be dS itself), float32, each nullable.  Rows t >=
  * lengths[b] are zero.  All sums in a fixed order.  No output may overlap an input
- * otherwise.  workspace: la_selective_scan_workspace(..., 1) bytes, 256-byte
+ * or another output otherwise.  workspace: la_selective_scan_workspace(..., 1) bytes, 256-byte
  * aligned; calls that may run at the same time need one each.
  */
 LA_API la_status la_selective_scan_backward(const void *x, long ldx, const void *delta, long ld_delta, const float *A,
@@ -552,8 +552,8 @@ LA_API la_status la_selective_scan_backward(const void *x, long ldx, const void 
  * One token of la_selective_scan per batch row, on states that live in a pool S
  * [n_slots,D,d_state] float32, read and written in place: row b works on
  * S[slots[b]].  x, delta, z: [B,D]; Bm, Cm: [B,d_state]; rows ld* apart; out
- * [B,D], not over an input.  slots as in la_gated_decode_step (unused, bad and
- * repeated ones too).
+ * [B,D].  slots as in la_gated_decode_step (unused, bad and repeated ones too).  out
+ * and S must overlap neither an input nor each other.
  */
 LA_API la_status la_selective_scan_step(const void *x, long ldx, const void *delta, long ld_delta, const float *A,
                                         const void *Bm, long ldb, const void *Cm, long ldc, const float *Dskip,
@@ -576,7 +576,7 @@ LA_API la_status la_selective_scan_step(const void *x, long ldx, const void *del
  * min(64, W V), W <= 64, 0 <= eos < V, ld >= V.  logits 16-byte aligned, the other
  * pointers 4 (finished 1).  workspace: la_beam_select_workspace bytes, 256-byte
  * aligned; calls that may run at the same time need one each.  No output may
- * overlap an input.
+ * overlap an input or another output.
  */
 LA_API la_status la_beam_select(const void *logits, long ld, const float *scores, const unsigned char *finished,
                                 float *out_scores, int *parents, int *tokens, int G, int W, int k, int V, int eos,
@@ -591,7 +591,8 @@ LA_API size_t la_beam_select_workspace(int G, int W, int k, int V, la_dtype dt);
  * first, and a copy of their parent's row there, in place, in each of n_pools
  * pools (host arrays of device pointers [n_slots, row_bytes] and row sizes, a
  * multiple of 16 bytes each; pools 16-byte aligned).  new_slots [G,W] int32,
- * written, not overlapping slots.  A negative parent takes a childless beam's slot
+ * written, not overlapping slots, parents or a pool, nor may a pool overlap these.
+ * A negative parent takes a childless beam's slot
  * without a copy, and nothing is copied from or to a negative slot.  A parent >= W,
  * a slot >= n_slots that a copy reads or writes, and a slot to be written that
  * another beam of the call has too: no copy, and the next la_device_status returns
