@@ -33,6 +33,11 @@ constexpr int kAhead = 4;  // rows in flight a thread
 // each thread that is resident (128 registers; 512 threads 96 us, 1024 104, 2048 123; three blocks of more
 // registers 122).
 constexpr int kPerSm = 4, kCutThreads = 4096, kCutThreadsGrad = 512;
+// A run of the gradient adds its tokens' shares of dweight and dbias one behind the other: at most so many, whatever the
+// batch (a sum of thousands loses the low bits of every share).  Blocks that end early cost large batches less than runs
+// of theirs that end late: in bf16, 16 x 8192 x 2048 and 64 x 8192 x 2048 take 359 and 1290 us, 368 and 1331 with 256
+// tokens, 421 and 1360 with 1024, 421 and 1555 with no limit.
+constexpr long kMostGrad = 512;
 
 // V consecutive channels as loaded.
 template <typename T, int V>
@@ -355,17 +360,20 @@ __global__ void __launch_bounds__(kThreads) short_conv_step_kernel(const __grid_
   o.store((T *)p.out + (long)b * p.D + c);
 }
 
-// Runs of tokens: at least kMinRun, so that their K - 1 extra rows cost at most a fifth more reads, from L2.
+// Runs of tokens: at least kMinRun, so that the rows a run shares with its neighbours cost at most a fifth more reads, from
+// L2 (the gradient, K - 1 rows of x on both sides and of dout behind: 9 for 32, 28 %); at most `most`.
 constexpr int kMinRun = 16;
-int run_length(const ConvProblem &p, int per_sm) {
+int run_length(const ConvProblem &p, int per_sm, long most) {
   const long threads = (long)std::max(1, device_info(-1).sm_count) * per_sm;
   const long len = ((long)p.B * (p.D / kV) * p.N + threads - 1) / threads;
-  return (int)std::max<long>(kMinRun, std::min<long>(len, p.N));
+  return (int)std::max<long>(kMinRun, std::min({len, p.N, most}));
 }
+int forward_run(const ConvProblem &p) { return run_length(p, kCutThreads, p.N); }
+int gradient_run(const ConvProblem &p) { return run_length(p, kCutThreadsGrad, kMostGrad); }
 
 template <typename T, int K>
 cudaError_t launch_fwd(const ConvProblem &p) {
-  const int len = run_length(p, kCutThreads), segs = (int)((p.N + len - 1) / len);
+  const int len = forward_run(p), segs = (int)((p.N + len - 1) / len);
   const long units = (long)p.B * segs * (p.D / kV);
   LaunchTimer timer(kKShortConv, p.stream);
   short_conv_kernel<T, K><<<(unsigned)((units + kThreads - 1) / kThreads), kThreads, 0, p.stream>>>(p, segs, len);
@@ -378,7 +386,7 @@ cudaError_t launch_fwd(const ConvProblem &p) {
 template <typename T, int K>
 cudaError_t launch_grad(const ConvGradProblem &q) {
   const ConvProblem &p = q.p;
-  const int len = run_length(p, kCutThreadsGrad), segs = (int)((p.N + len - 1) / len);
+  const int len = gradient_run(p), segs = (int)((p.N + len - 1) / len);
   const long units = (long)p.B * segs * (p.D / kV);
   const bool sums = q.dweight || q.dbias;
   LaunchTimer timer(kKShortConvBackward, p.stream);
@@ -418,7 +426,7 @@ cudaError_t launch_short_conv(const ConvProblem &p) {
 }
 
 size_t short_conv_grad_workspace(const ConvProblem &p) {
-  const int len = run_length(p, kCutThreadsGrad);
+  const int len = gradient_run(p);
   return sizeof(float) * (size_t)p.B * ((p.N + len - 1) / len) * (p.K + 1) * p.D;
 }
 
