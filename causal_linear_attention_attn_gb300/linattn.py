@@ -844,7 +844,9 @@ def la_beam_select(logits, scores, k=None, finished=None, eos: int = 0, stream=N
     """The k (default W) best continuations of each group's W beams by score + log_softmax(logits), best first.
 
     logits [G, W, V] (float32 or bfloat16; a part of the last dimension of a wider tensor will do), scores [G, W] float32
-    accumulated log probabilities (-inf: an unused beam).  Compared in 64 bits; ties go to the lowest beam and token.
+    accumulated log probabilities (-inf: an unused beam).  Ties go to the lowest beam and token.  Within a beam the logits
+    decide; between beams scores are compared in 64 bits, with a float32 sum of exponentials for each beam: continuations
+    of different beams within about 1e-6 may change places.
     finished [G, W] bool: such a beam has one continuation, token ``eos``, and keeps its score.  Logits of -inf or NaN are
     chosen only where nothing else is left.  W and k up to 64.  Returns (scores float32, parents int32, tokens int32),
     each [G, k].
