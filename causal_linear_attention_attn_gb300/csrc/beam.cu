@@ -32,7 +32,8 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kPer = 16;                  // values a thread and chunk
-constexpr int kChunk = kThreads * kPer;   // values a chunk
+constexpr int kChunk = kBeamChunk;        // values a chunk
+static_assert(kChunk == kThreads * kPer, "a chunk is a block's values");
 constexpr int kCap = 256;                 // candidates of a warp
 constexpr int kMaxK = 64;
 
@@ -428,7 +429,7 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const __grid_consta
 
 // A block takes a piece of one child's row, in every pool or (few beams) in one.  Which child copies from
 // where to where every block works out from its group's parents, a thread a beam.
-constexpr long kPiece = 32768;  // bytes
+constexpr long kPiece = kReorderPiece;
 
 __device__ __forceinline__ int nth_bit(unsigned long long x, int n) {
   for (; n > 0; --n) x &= x - 1;

@@ -342,6 +342,8 @@ struct BeamSplit {
   void *cands;
   float *stats;
 };
+constexpr int kBeamChunk = 4096;         // values of a row that a block of the selection takes at a time
+constexpr long kReorderPiece = 32768;    // bytes of a row that a block of the reordering copies
 constexpr int kMaxPools = 64;
 struct ReorderProblem {
   void *pool[kMaxPools];

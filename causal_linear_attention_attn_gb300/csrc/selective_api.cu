@@ -151,7 +151,7 @@ la_status beam_sizes(int G, int W, int k, long V, la_dtype dt) {
   if (G < 0 || W <= 0 || V <= 0 || k <= 0 || k > (long)W * V) return LA_ERR_INVALID_VALUE;
   if (dt != LA_F32 && dt != LA_BF16) return LA_ERR_UNSUPPORTED;
   if (W > 64 || k > 64) return LA_ERR_UNSUPPORTED;
-  return (long)G * W * ((V + 8191) / 8192 + 1) > 0x7fffffffL ? LA_ERR_INVALID_VALUE : LA_OK;
+  return (long)G * W * ((V + kBeamChunk - 1) / kBeamChunk + 1) > 0x7fffffffL ? LA_ERR_INVALID_VALUE : LA_OK;
 }
 
 }  // namespace
@@ -359,7 +359,7 @@ la_status la_beam_reorder(void *const *pools, const size_t *row_bytes, int n_poo
   for (int i = 0; i < n_pools; ++i) {
     if (!pools[i] && row_bytes[i] > 0 && n_slots > 0) return LA_ERR_INVALID_VALUE;
     // blocks of the largest row are counted in 31 bits
-    if (row_bytes[i] > (size_t)1 << 40 || (long)G * W * (long)(row_bytes[i] / 32768 + 1) * kMaxPools > 0x7fffffffL)
+    if (row_bytes[i] > (size_t)1 << 40 || (long)G * W * (long)(row_bytes[i] / kReorderPiece + 1) * kMaxPools > 0x7fffffffL)
       return LA_ERR_INVALID_VALUE;
     if (!aligned({pools[i]}, 16) || row_bytes[i] % 16) return LA_ERR_MISALIGNED;
     if (over({{pools[i], row_bytes[i] * n_slots}, floats(new_slots, (long)G * W)}, {slots_of, parents_of}))

@@ -33,7 +33,7 @@ constexpr int kAround = 128;  // threads of the first kind
 
 // Tokens a chunk and channels a block: as many as keep the a h of two chunks within shared memory.
 constexpr int grad_tokens(int ds) { return ds == 64 ? 8 : 16; }
-constexpr int grad_cols(int ds) { return ds <= 16 ? 64 : 32; }
+__host__ __device__ constexpr int grad_cols(int ds) { return ds <= 16 ? 64 : 32; }
 
 template <int DS>
 struct Layout {
@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(Layout<DS>::kThreads) scan_grad_kernel(const _
 template <typename T>
 __global__ void __launch_bounds__(256) scan_bc_kernel(const __grid_constant__ ScanGradProblem g, const __grid_constant__ ScanSplit s) {
   const ScanProblem &p = g.p;
-  const int cols = p.ds <= 16 ? 64 : 32, ds2 = 2 * p.ds, nb = (p.D + cols - 1) / cols;  // (grad_cols)
+  const int cols = grad_cols(p.ds), ds2 = 2 * p.ds, nb = (p.D + cols - 1) / cols;
   const long rows = (long)p.B * p.N, all = rows * ds2, i = (long)blockIdx.x * 256 + threadIdx.x;
   if (i >= all) return;
   const long row = i / ds2, b = row / p.N;

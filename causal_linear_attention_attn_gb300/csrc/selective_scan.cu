@@ -28,7 +28,7 @@ namespace {
 
 constexpr int kTok = 32;         // tokens a chunk
 
-// Channels a block: as many as keep it within 400 threads.
+// Channels a block: as many as keep it within 512 threads.
 constexpr int scan_cols(int ds) { return ds == 64 ? 32 : 64; }
 
 // Threads of the recurrence with `comp` components of two channels each.
