@@ -17,8 +17,8 @@
 // last kernel adds in order.  No atomics: the gradient is the same from run to run.
 //
 // Shared memory's port bounds it (60 of its cycles a token and pair of warps, 81 % taken on the 128 SMs that have a block
-// of 4 x 4096 x 2048 x 16), and two exponentials and about twenty issue slots a component: 833 us in bf16, 650 of them
-// here, 163 in the scan of states, 28 in the sums.  With one kind of warps and one channel a lane it took 1337 us; with
+// of 4 x 4096 x 2048 x 16), and two exponentials and about twenty issue slots a component: 833 us in bf16 (launches timed
+// one by one: 650 here, 163 in the scan of states, 28 in the sums).  With one kind of warps and one channel a lane it took 1337 us; with
 // results out before the next rows in, 944.  With y and dC in the third kind of warps 8 components took 826 us for 738,
 // 16 876 for 866 (both with 35 us more in the scan of states than now).
 #include <algorithm>

@@ -9,8 +9,8 @@
 // last K values of g) stays in registers, every row is loaded once a run, plus K - 1 rows in front of it
 // (which another thread reads too, so they come from L2) and, in the gradient, K - 1 behind it.  Four
 // rows are in flight.  HBM bounds it, x and y (gradient: x, dy, dx) once each, beside instruction issue: steps inside a
-// run have no checks and no 64-bit products.  In bf16, K = 4: 4 x up to 8192 x 2048 forward in 40 us (4.6 TB/s), 4 x 8192 x
-// 2048 of the gradient in 95 us (4.2 TB/s; with checks at every step 330).
+// run have no checks and no 64-bit products.  In bf16, K = 4: 4 x up to 8192 x 2048 forward in 42 us (4.5 TB/s), 4 x 8192 x
+// 2048 of the gradient in 95 us (4.3 TB/s; with checks at every step 330).
 //
 // Column sums dw, db leave each run once and are added in a fixed order by a second kernel.
 #include <algorithm>
